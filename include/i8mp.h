@@ -365,6 +365,43 @@ i8mp_status i8mp_linear_bwd_fp8_colmax(const uint16_t* dY, const uint16_t* X, co
                                        const float* colmax_x, const float* colmax_w, void* ws,
                                        size_t ws_bytes, void* stream);
 
+/* ---- operators around the linears --------------------------------------- */
+
+/* Element types of the operators that take more than bf16. */
+typedef enum { I8MP_BF16 = 0, I8MP_FP16 = 1, I8MP_FP32 = 2 } i8mp_dtype;
+
+/*
+ * Rotary positions of query and key heads.  Pair i (i < rot / 2) of a head is
+ * (a, b) = elements (i, i + rot / 2) for I8MP_PAIRS_HALF and (2i, 2i + 1) for
+ * I8MP_PAIRS_INTERLEAVED; with t = pos * freqs[i],
+ *   a' = a cos t - b sin t,  b' = a sin t + b cos t     (inverse: t = -pos * freqs[i])
+ * and elements rot .. D - 1 are copied.  Scaling for long contexts is the
+ * caller's choice of freqs.  The angle is formed and reduced in 64 bits, the
+ * rotation computed in fp32 and rounded once.  The inverse is the backward:
+ * it takes the outputs' gradients to the inputs'.
+ *   q, k: heads [B][S][heads][D], elements of one head adjacent, any strides of
+ *         the other dimensions (counted in elements, >= 0), so views of a packed
+ *         projection are taken as they are.  k may be NULL (or heads = 0).
+ *         y may be x with the same strides (in place); otherwise no output may
+ *         overlap an input or the other output (views that share a packed token
+ *         row without sharing elements are fine), and no output may overlap itself.
+ *   D, rot: even, 2 <= rot <= D <= 4096.
+ *   pos: int64 (pos_bits = 64) or int32 (32), element [b][s] at b * pos_b + s * pos_s
+ *   freqs: double [rot / 2], 8-byte aligned
+ */
+typedef enum { I8MP_PAIRS_HALF = 0, I8MP_PAIRS_INTERLEAVED = 1 } i8mp_pairs;
+typedef struct {
+  const void* x;
+  void* y;
+  int32_t heads;
+  int64_t x_b, x_s, x_h; /* strides of x */
+  int64_t y_b, y_s, y_h; /* strides of y */
+} i8mp_heads;
+i8mp_status i8mp_rotary(const i8mp_heads* q, const i8mp_heads* k, int64_t B, int64_t S, int32_t D,
+                        int32_t rot, int32_t dtype, int32_t pairs, int32_t inverse, const void* pos,
+                        int32_t pos_bits, int64_t pos_b, int64_t pos_s, const double* freqs,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,6 +27,7 @@ __all__ = [
     "quantize_colwise_fp8", "fp8_scaled_mm", "fp8_mm_f32", "linear_fwd_fp8", "linear_bwd_fp8",
     "linear_fwd_fp8_colmax",
     "quantize_colwise_noalloc", "STATIC_SCRATCH_BYTES", "mfma_rate_probe", "EXPORTED_SYMBOLS",
+    "rotary", "rotary_frequencies",
 ]
 
 RNE, SR = 0, 1
@@ -46,6 +47,7 @@ EXPORTED_SYMBOLS = (
     "i8mp_fp8_scaled_mm", "i8mp_fp8_mm_f32", "i8mp_linear_fwd_fp8", "i8mp_linear_bwd_fp8",
     "i8mp_linear_fwd_fp8_colmax", "i8mp_linear_bwd_fp8_colmax",
     "i8mp_quantize_colwise_noalloc", "i8mp_mfma_rate_probe",
+    "i8mp_rotary",
 )
 
 
@@ -57,6 +59,11 @@ class I8mpError(RuntimeError):
 
 class _Opts(ctypes.Structure):
     _fields_ = [("round", ctypes.c_int32), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int32)] + [
+        (n, ctypes.c_int64) for n in ("x_b", "x_s", "x_h", "y_b", "y_s", "y_h")]
 
 
 def _load() -> ctypes.CDLL:
@@ -95,6 +102,8 @@ def _load() -> ctypes.CDLL:
         "i8mp_linear_bwd_fp8_colmax": ([p, p, p, p, p, i64, i64, i64, p, p, p, sz, p], i32),
         "i8mp_quantize_colwise_noalloc": ([p, i64, i64, i64, p, i64, p, i32, u64, u64, p], i32),
         "i8mp_mfma_rate_probe": ([p, i64, i64, p, p], i32),
+        "i8mp_rotary": ([ctypes.POINTER(_Heads), ctypes.POINTER(_Heads), i64, i64, i32, i32, i32, i32, i32, p, i32,
+                         i64, i64, p, p], i32),
     }
     for name, (args, res) in sigs.items():
         f = getattr(L, name)
@@ -660,3 +669,8 @@ def linear_bwd_fp8(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, want_dx: 
                                             _ptr(colmax_w), _ptr(workspace), workspace.numel(), _stream(dev))
     _check(st, "i8mp_linear_bwd_fp8_colmax")
     return (dX if want_dx else None), (dW if want_dw else None)
+
+
+# --------------------------------------------------------------------------- operators around the linears
+
+from .operators import rotary, rotary_frequencies  # noqa: E402

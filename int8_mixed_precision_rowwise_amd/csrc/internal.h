@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/i8mp.h"
+
 namespace i8mp {
 
 // Row-wise quantization (round: 0 = RNE, 1 = SR).
@@ -173,5 +175,11 @@ hipError_t launch_philox(uint64_t seed, uint64_t offset, int64_t n_blocks, uint3
 constexpr int kMfmaProbeWorkgroups = 256;
 hipError_t launch_mfma_rate_probe(const int8_t* codes, int64_t bytes, int64_t rounds, int32_t* sink,
                                   hipStream_t stream);
+
+// Rotary positions of q and k (heads 0: none); see i8mp_rotary.
+typedef i8mp_heads RotaryTensor;
+hipError_t launch_rotary(const RotaryTensor& q, const RotaryTensor& k, int64_t B, int64_t S, int D, int rot, int dtype,
+                         bool half, bool inverse, const void* pos, int pos32, int64_t pos_b, int64_t pos_s,
+                         const double* freqs, hipStream_t stream);
 
 }  // namespace i8mp

@@ -1,0 +1,225 @@
+// Rotary positions of query and key heads, and their inverse (which is also
+// the backward: the rotation is orthogonal, so its gradient is the rotation by
+// the negative angle).
+//
+// Pair i of a head is (a, b); with t = position * freqs[i]
+//   a' = a cos t - b sin t,   b' = a sin t + b cos t.
+// "half" pairs are elements (i, i + rot / 2), "interleaved" ones (2i, 2i + 1);
+// elements from rot on are copied.
+//
+// The angle of a position 10^6 out needs more than the 24 bits of a float: it
+// is formed and reduced in 64 bits (t * 2/pi = n + f, n the nearest integer,
+// |f| <= 1/2), and only the remainder f * pi/2 goes to fp32, where the Taylor
+// polynomials of sine (to y^9) and cosine (to y^10) on [-pi/4, pi/4] are off
+// by less than 2^-28.
+//
+// A pass reads and writes every head once and computes next to nothing, so it
+// is bound by memory (by the launch, for one token per sequence).  The cosines
+// and sines of a token serve all its heads: a workgroup takes a few whole
+// tokens (or part of one token's heads), computes their table into LDS, then
+// streams the heads with the widest access that the pairs' layout allows.
+#include "internal.h"
+
+namespace i8mp {
+namespace {
+
+constexpr int kRotThreads = 256;
+
+struct RotKernelArgs {
+  RotaryTensor t[2];  // q, k
+  int64_t tokens, S;
+  const void* pos;
+  int64_t pos_b, pos_s;
+  const double* freqs;
+  int pos32, D, rot;
+  float sign;
+  int tpw;           // tokens per workgroup
+  int rows_per_y;    // heads per workgroup along grid y (all of them unless tpw = 1)
+  int slots;         // work items per head
+  int rot_slots;     // of them, items that rotate
+  int dslot, drow;   // kRotThreads = drow * slots + dslot
+};
+
+// fp32 cosine and sine of an angle given in 64 bits.
+__device__ __forceinline__ float2 cos_sin(double angle) {
+  const double turns = angle * 0.63661977236758134308;  // 2 / pi
+  const double n = __builtin_rint(turns);
+  const double f = __builtin_fma(angle, 0.63661977236758134308, -n);
+  const float y = (float)(f * 1.57079632679489661923);
+  // the quarter modulo 4 by a 64-bit remainder: exact for every n
+  const int quarter = (int)(n - 4.0 * __builtin_floor(n * 0.25));
+  const float y2 = y * y;
+  float s = 1.0f / 362880.0f;
+  s = __builtin_fmaf(s, y2, -1.0f / 5040.0f);
+  s = __builtin_fmaf(s, y2, 1.0f / 120.0f);
+  s = __builtin_fmaf(s, y2, -1.0f / 6.0f);
+  s = __builtin_fmaf(s * y2, y, y);
+  float c = -1.0f / 3628800.0f;
+  c = __builtin_fmaf(c, y2, 1.0f / 40320.0f);
+  c = __builtin_fmaf(c, y2, -1.0f / 720.0f);
+  c = __builtin_fmaf(c, y2, 1.0f / 24.0f);
+  c = __builtin_fmaf(c, y2, -0.5f);
+  c = __builtin_fmaf(c, y2, 1.0f);
+  const float cc = (quarter & 1) ? s : c, ss = (quarter & 1) ? c : s;
+  return make_float2(quarter == 1 || quarter == 2 ? -cc : cc, quarter >= 2 ? -ss : ss);
+}
+
+// V elements of type T, read and written in one access (WIDE) or one by one.
+template <typename T, int V, bool WIDE>
+struct Pack {
+  struct __attribute__((aligned(WIDE ? sizeof(T) * V : sizeof(T)))) Mem { T v[V]; };
+  static __device__ __forceinline__ void load(const T* p, T (&x)[V]) {
+    const Mem m = *reinterpret_cast<const Mem*>(p);
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = m.v[j];
+  }
+  static __device__ __forceinline__ void store(T* p, const T (&x)[V]) {
+    Mem m;
+#pragma unroll
+    for (int j = 0; j < V; ++j) m.v[j] = x[j];
+    *reinterpret_cast<Mem*>(p) = m;
+  }
+};
+
+// Every element is read before its pair's outputs are written, by the same
+// thread, so the outputs may be the inputs themselves.
+template <typename T, int V, bool WIDE, bool HALF>
+__global__ __launch_bounds__(kRotThreads) void rotary_kernel(RotKernelArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float2 table[];  // [tokens][rot / 2]: cosine, sine
+  typedef Pack<T, V, WIDE> P;
+  const int t = threadIdx.x;
+  const int half = a.rot / 2;
+  const int64_t token0 = (int64_t)blockIdx.x * a.tpw;
+  const int tokens = (int)min((int64_t)a.tpw, a.tokens - token0);
+  for (int i = t; i < tokens * half; i += kRotThreads) {
+    const int tb = i / half, pair = i - tb * half;
+    const int64_t token = token0 + tb, b = token / a.S, s = token - b * a.S;
+    const int64_t at = b * a.pos_b + s * a.pos_s;
+    const int64_t p = a.pos32 ? (int64_t) static_cast<const int32_t*>(a.pos)[at] : static_cast<const int64_t*>(a.pos)[at];
+    float2 cs = cos_sin((double)p * a.freqs[pair]);
+    cs.y *= a.sign;
+    table[i] = cs;
+  }
+  __syncthreads();
+  const int heads = a.t[0].heads + a.t[1].heads;
+  const int row0 = (int)blockIdx.y * a.rows_per_y;
+  const int rows = min(a.rows_per_y, heads - row0);
+  int row = t / a.slots, slot = t - row * a.slots;
+  int tb = row / rows;
+  row -= tb * rows;
+  while (tb < tokens) {
+    const int64_t token = token0 + tb, b = token / a.S, s = token - b * a.S;
+    const int which = row0 + row >= a.t[0].heads;
+    const int h = row0 + row - (which ? a.t[0].heads : 0);
+    const RotaryTensor& r = a.t[which];
+    const T* x = static_cast<const T*>(r.x) + b * r.x_b + s * r.x_s + h * r.x_h;
+    T* y = static_cast<T*>(r.y) + b * r.y_b + s * r.y_s + h * r.y_h;
+    const float2* cs = table + tb * half;
+    if (slot >= a.rot_slots) {  // past the rotated part: copied
+      const int e = a.rot + (slot - a.rot_slots) * V;
+      T v[V];
+      P::load(x + e, v);
+      P::store(y + e, v);
+    } else if constexpr (HALF) {
+      const int e = slot * V;
+      T u[V], v[V];
+      P::load(x + e, u);
+      P::load(x + e + half, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float2 k = cs[e + j];
+        const float p = (float)u[j], q = (float)v[j];
+        u[j] = (T)__builtin_fmaf(p, k.x, -(q * k.y));
+        v[j] = (T)__builtin_fmaf(p, k.y, q * k.x);
+      }
+      P::store(y + e, u);
+      P::store(y + e + half, v);
+    } else {
+      const int e = slot * V;
+      T v[V];
+      P::load(x + e, v);
+#pragma unroll
+      for (int j = 0; j + 1 < V; j += 2) {
+        const float2 k = cs[(e + j) / 2];
+        const float p = (float)v[j], q = (float)v[j + 1];
+        v[j] = (T)__builtin_fmaf(p, k.x, -(q * k.y));
+        v[j + 1] = (T)__builtin_fmaf(p, k.y, q * k.x);
+      }
+      P::store(y + e, v);
+    }
+    slot += a.dslot;
+    row += a.drow;
+    if (slot >= a.slots) slot -= a.slots, ++row;
+    while (row >= rows) row -= rows, ++tb;
+  }
+}
+
+template <typename T, int V, bool WIDE>
+void launch_pairs(const RotKernelArgs& a, bool half, dim3 grid, size_t lds, hipStream_t stream) {
+  if (half)
+    rotary_kernel<T, V, WIDE, true><<<grid, kRotThreads, lds, stream>>>(a);
+  else if constexpr (V >= 2)
+    rotary_kernel<T, V, WIDE, false><<<grid, kRotThreads, lds, stream>>>(a);
+}
+
+template <typename T>
+hipError_t launch_typed(RotKernelArgs a, bool half, hipStream_t stream) {
+  // Elements per access: the widest power of two, up to 16 bytes, that divides
+  // the rotated part (each half of it for half pairs), the head and every
+  // stride, with aligned bases.
+  constexpr int kWidest = 16 / (int)sizeof(T);
+  int64_t any = a.D | (half ? a.rot / 2 : a.rot);
+  for (const RotaryTensor& r : a.t)
+    if (r.heads > 0) {
+      any |= r.x_b | r.x_s | r.x_h | r.y_b | r.y_s | r.y_h;
+      any |= (int64_t)((reinterpret_cast<uintptr_t>(r.x) | reinterpret_cast<uintptr_t>(r.y)) / sizeof(T));
+    }
+  int v = kWidest;
+  while (v > 1 && any % v) v /= 2;
+  const bool wide = half || v >= 2;
+  if (!wide) v = 2;  // interleaved pairs at an odd address or stride: element by element
+  a.rot_slots = (half ? a.rot / 2 : a.rot) / v;
+  a.slots = a.rot_slots + (a.D - a.rot) / v;
+  const int heads = a.t[0].heads + a.t[1].heads;
+  // Workgroups of about 1024 items while that leaves 2048 of them (8 a CU);
+  // with fewer tokens one token each, and with few of those the heads are
+  // split so that one item falls to each thread.
+  const int64_t items = (int64_t)heads * a.slots;
+  a.tpw = (int)max((int64_t)1, min(min((int64_t)16, 1024 / items), a.tokens / 2048));
+  a.tpw = (int)min((int64_t)a.tpw, max((int64_t)1, (int64_t)32768 / max(1, a.rot / 2 * 8)));
+  a.rows_per_y = heads;
+  if (a.tpw == 1 && a.tokens < 1024) a.rows_per_y = (int)max((int64_t)1, min((int64_t)heads, (int64_t)kRotThreads / a.slots));
+  a.drow = kRotThreads / a.slots;
+  a.dslot = kRotThreads - a.drow * a.slots;
+  const dim3 grid((unsigned)((a.tokens + a.tpw - 1) / a.tpw), (unsigned)((heads + a.rows_per_y - 1) / a.rows_per_y));
+  const size_t lds = (size_t)a.tpw * (a.rot / 2) * sizeof(float2);
+  if constexpr (kWidest >= 8) {
+    if (v == 8) launch_pairs<T, 8, true>(a, half, grid, lds, stream);
+  }
+  if (v == 4) launch_pairs<T, 4, true>(a, half, grid, lds, stream);
+  if (v == 2 && wide) launch_pairs<T, 2, true>(a, half, grid, lds, stream);
+  if (v == 2 && !wide) launch_pairs<T, 2, false>(a, half, grid, lds, stream);
+  if (v == 1) launch_pairs<T, 1, true>(a, half, grid, lds, stream);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rotary(const RotaryTensor& q, const RotaryTensor& k, int64_t B, int64_t S, int D, int rot, int dtype,
+                         bool half, bool inverse, const void* pos, int pos32, int64_t pos_b, int64_t pos_s,
+                         const double* freqs, hipStream_t stream) {
+  RotKernelArgs a{};
+  a.t[0] = q, a.t[1] = k;
+  a.tokens = B * S, a.S = S;
+  a.pos = pos, a.pos32 = pos32, a.pos_b = pos_b, a.pos_s = pos_s;
+  a.freqs = freqs;
+  a.D = D, a.rot = rot;
+  a.sign = inverse ? -1.0f : 1.0f;
+  switch (dtype) {
+    case I8MP_BF16: return launch_typed<__bf16>(a, half, stream);
+    case I8MP_FP16: return launch_typed<_Float16>(a, half, stream);
+    default: return launch_typed<float>(a, half, stream);
+  }
+}
+
+}  // namespace i8mp

@@ -1,0 +1,143 @@
+"""Operators around the INT8 mixed-precision linears, bound like the linears.
+
+Rotary positions of query and key heads (``rotary``), with the tensors'
+checks, the current stream and the errors of the package's other calls; every
+step of the computation runs in the library's HIP kernels.  ``training`` holds
+their autograd forms.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+import int8_mixed_precision_rowwise_amd as _pkg
+
+__all__ = ["rotary", "rotary_frequencies"]
+
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_PAIRS = {"half": 0, "interleaved": 1}
+
+
+def _on(dev: torch.device):
+    """(device guard or None, raw stream): the guard only where another GPU is current."""
+    guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return guard, torch.cuda.current_stream(dev).cuda_stream
+
+
+def _call(dev: torch.device, name: str, *args):
+    """lib.<name>(*args, stream) on dev's current stream, its status checked."""
+    guard, stream = _on(dev)
+    f = getattr(_pkg.lib, name)
+    if guard is None:
+        st = f(*args, stream)
+    else:
+        with guard:
+            st = f(*args, stream)
+    if st:
+        raise _pkg.I8mpError(st, name)
+
+
+# --------------------------------------------------------------------------- rotary positions
+
+
+def rotary_frequencies(rot: int, theta: float = 10000.0, factor: float = 1.0, original_length: int | None = None,
+                       low: float = 1.0, high: float = 4.0, device=None) -> torch.Tensor:
+    """float64 [rot / 2] frequencies theta ** (-2 i / rot) for ``rotary``.
+
+    ``factor`` > 1 stretches positions for contexts longer than the trained
+    one.  Alone it divides every frequency.  With ``original_length`` (the
+    trained context) a frequency is left alone where that context holds at
+    least ``high`` of its turns, divided where it holds at most ``low``, and
+    in between the two are mixed linearly in the number of turns."""
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and at least 2, got {rot}")
+    if not (theta > 0 and factor > 0):
+        raise ValueError(f"theta and factor must be positive, got {theta} and {factor}")
+    f = theta ** (-2.0 * torch.arange(rot // 2, dtype=torch.float64) / rot)
+    if original_length is None:
+        f = f / factor
+    else:
+        if not (original_length > 0 and 0 < low < high):
+            raise ValueError(f"original_length > 0 and 0 < low < high expected, got {original_length}, {low}, {high}")
+        turns = original_length * f / (2 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    return f.to(device) if device is not None else f
+
+
+def _heads(t, name: str, dtype, lead=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: torch.Tensor expected, got {type(t).__name__}")
+    if t.dtype != dtype or dtype not in _DTYPE:
+        raise TypeError(f"{name}: {'bfloat16, float16 or float32' if dtype not in _DTYPE else dtype} tensor expected, got {t.dtype}")
+    if t.dim() != 4:
+        raise ValueError(f"{name}: 4-D tensor [batch, positions, heads, head size] expected, got {t.dim()}-D")
+    if lead is not None and (t.shape[0], t.shape[1], t.shape[3]) != lead:
+        raise ValueError(f"{name}: shape {(lead[0], lead[1], 'heads', lead[2])} expected, got {tuple(t.shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: elements of a head must be adjacent (stride 1)")
+    return t
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, freqs: torch.Tensor,
+           pairs: str = "half", inverse: bool = False, out_q: torch.Tensor | None = None,
+           out_k: torch.Tensor | None = None):
+    """Query and key heads turned by their positions: (q', k').
+
+    q [B, S, HQ, D] and k [B, S, HK, D] (bf16, fp16 or fp32; k may be None) may
+    be views of a packed projection: only a head's own elements have to be
+    adjacent.  positions: int64 or int32, [B, S] or [S].  freqs: float64
+    [rot / 2], rot <= D (``rotary_frequencies``); elements from rot on are
+    copied.  pairs: "half" pairs element i with i + rot / 2, "interleaved" 2i
+    with 2i + 1.  ``inverse`` turns back, which is also the backward: it takes
+    the gradients of q' and k' to those of q and k.  out_q / out_k: where to
+    write, any strides; q and k themselves for a rotation in place."""
+    dtype = q.dtype if isinstance(q, torch.Tensor) else None
+    _heads(q, "q", dtype)
+    B, S, HQ, D = q.shape
+    HK = 0
+    if k is not None:
+        _heads(k, "k", dtype, (B, S, D))
+        HK = k.shape[2]
+    elif out_k is not None:
+        raise ValueError("out_k given without k")
+    if pairs not in _PAIRS:
+        raise ValueError(f"pairs must be 'half' or 'interleaved', got {pairs!r}")
+    if not isinstance(freqs, torch.Tensor) or freqs.dtype != torch.float64:
+        raise TypeError("freqs: torch.float64 tensor expected")
+    if freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError(f"freqs: contiguous 1-D tensor expected, got shape {tuple(freqs.shape)}")
+    rot = 2 * freqs.shape[0]
+    if D % 2 or D > 4096 or not 2 <= rot <= D:
+        raise ValueError(f"an even head size of at most 4096 and 1 to {D // 2} frequencies expected, got {D} and {rot // 2}")
+    if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int64, torch.int32):
+        raise TypeError("positions: torch.int64 or torch.int32 tensor expected")
+    if tuple(positions.shape) not in ((B, S), (S,)):
+        raise ValueError(f"positions: shape {(B, S)} or {(S,)} expected, got {tuple(positions.shape)}")
+    if out_q is not None:
+        _heads(out_q, "out_q", dtype, (B, S, D))
+        if out_q.shape[2] != HQ:
+            raise ValueError(f"out_q: {HQ} heads expected, got {out_q.shape[2]}")
+    if out_k is not None:
+        _heads(out_k, "out_k", dtype, (B, S, D))
+        if out_k.shape[2] != HK:
+            raise ValueError(f"out_k: {HK} heads expected, got {out_k.shape[2]}")
+    dev = _pkg._device(q, k, positions, freqs, out_q, out_k)
+    if out_q is None:
+        out_q = torch.empty((B, S, HQ, D), dtype=dtype, device=dev)
+    if k is not None and out_k is None:
+        out_k = torch.empty((B, S, HK, D), dtype=dtype, device=dev)
+    xb, xs, xh, _ = q.stride()
+    yb, ys, yh, _ = out_q.stride()
+    hq = _pkg._Heads(q.data_ptr(), out_q.data_ptr(), HQ, xb, xs, xh, yb, ys, yh)
+    hk = None
+    if k is not None:
+        xb, xs, xh, _ = k.stride()
+        yb, ys, yh, _ = out_k.stride()
+        hk = _pkg._Heads(k.data_ptr(), out_k.data_ptr(), HK, xb, xs, xh, yb, ys, yh)
+    pb, ps = positions.stride() if positions.dim() == 2 else (0, positions.stride(0))
+    _call(dev, "i8mp_rotary", hq, hk, B, S, D, rot, _DTYPE[dtype], _PAIRS[pairs], int(inverse), positions.data_ptr(),
+          64 if positions.dtype == torch.int64 else 32, pb, ps, freqs.data_ptr())
+    return out_q, out_k

@@ -43,10 +43,11 @@ from typing import Callable, Optional
 import torch
 
 from . import linear_bwd, linear_bwd_fp8, linear_fwd, linear_fwd_colmax, linear_fwd_fp8, linear_fwd_fp8_colmax
+from . import operators as _ops
 
 __all__ = ["Int8MixedPrecisionConfig", "Int8MixedPrecisionLinearFunction",
            "Int8MixedPrecisionLinear", "swap_linear_modules", "STEP_STRIDE", "STEPS_PER_KEY",
-           "module_seed", "step_key_offset", "sr_checkpoint_contexts"]
+           "module_seed", "step_key_offset", "sr_checkpoint_contexts", "RotaryFunction", "rotary"]
 
 STEP_STRIDE = 8 << 40  # Philox blocks reserved per linear step (6 passes of 2**40 each, rounded up)
 STEPS_PER_KEY = (1 << 64) // STEP_STRIDE  # steps whose offsets fit the 64-bit block counter
@@ -290,3 +291,32 @@ def swap_linear_modules(model: torch.nn.Module, config: Optional[Int8MixedPrecis
         lin = getattr(parent, child)
         setattr(parent, child, Int8MixedPrecisionLinear.from_linear(lin, config, module_seed(config.seed, index)))
     return model
+
+
+class RotaryFunction(torch.autograd.Function):
+    """Positions turned into q and k (operators.rotary); the backward turns the
+    gradients back."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, freqs, pairs):
+        ctx.save_for_backward(positions, freqs)
+        ctx.pairs = pairs
+        ctx.set_materialize_grads(False)
+        return _ops.rotary(q, k, positions, freqs, pairs)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        positions, freqs = ctx.saved_tensors
+        d = [None if g is None else g if g.dim() == 4 and (g.shape[3] <= 1 or g.stride(3) == 1) else g.contiguous()
+             for g in (dq, dk)]
+        if d[0] is None:
+            d = [None, None if d[1] is None else _ops.rotary(d[1], None, positions, freqs, ctx.pairs, inverse=True)[0]]
+        else:
+            d = _ops.rotary(d[0], d[1], positions, freqs, ctx.pairs, inverse=True)
+        return d[0], d[1], None, None, None
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, freqs: torch.Tensor,
+           pairs: str = "half"):
+    """operators.rotary with a gradient: (q', k')."""
+    return RotaryFunction.apply(q, k, positions, freqs, pairs)

@@ -402,6 +402,65 @@ i8mp_status i8mp_rotary(const i8mp_heads* q, const i8mp_heads* k, int64_t B, int
                         int32_t pos_bits, int64_t pos_b, int64_t pos_s, const double* freqs,
                         void* stream);
 
+/*
+ * Loss of a student's logits x [T x V] against a teacher's kept top logits.
+ * Row r keeps the classes idx[r][j] (j < kept; negative or >= V: no entry; the
+ * others distinct) with the teacher's logits teacher[r][j].  With temperature
+ * tau, q = softmax(x / tau), and p over the kept classes either their softmax
+ * (lse NULL) or exp(teacher / tau - lse[r]), lse being the log-sum-exp of all
+ * the teacher's logits / tau; then what is left, p_rest = max(0, 1 - sum p),
+ * is one more class, whose student is q_rest = the sum of q over the rest:
+ *   loss[r] = tau^2 (sum p log(p / q) + p_rest log(p_rest / q_rest))
+ *             + ce_weight (log sum exp x - x[label[r]])
+ * A row that keeps nothing has no first part; a label equal to ignore_index,
+ * or none of the V classes, no second.  The gradient of sum_r grad[r] loss[r] is
+ * written in the logits' type, rounded once from fp32.
+ * Logits of -inf are classes the student cannot choose; their gradient is that
+ * of a probability of zero.  A row holding +inf or NaN gives NaN.
+ *   logits, dlogits: bf16, fp16 or fp32 (dtype), rows of any alignment; only
+ *     whole 16-byte chunks that hold part of a row are read, and dlogits is
+ *     written inside its rows
+ *   teacher: bf16, fp16 or fp32 (teacher_dtype) and idx: int32 or int64
+ *     (idx_bits), [T x kept]; 0 <= kept <= I8MP_DISTILL_MAX_KEPT
+ *   lse: fp32 [T] or NULL; labels: int32 or int64 (label_bits) [T], or NULL
+ *   grad: fp32, row r's at r * grad_s (0: one for all rows)
+ *   loss: fp32 [T]
+ *   stats: double [T x I8MP_DISTILL_STATS], 8-byte aligned: what
+ *     i8mp_distill_bwd needs of the forward (with the same other arguments)
+ *   ws: at least i8mp_distill_workspace_bytes(...) bytes, 256-aligned
+ * i8mp_distill_fwd writes the loss and, unless NULL, the statistics;
+ * i8mp_distill_bwd the gradient from them; i8mp_distill_step loss and gradient
+ * with one read of the logits.  Sums are added in a fixed order: the same call
+ * gives the same bits.
+ */
+#define I8MP_DISTILL_MAX_KEPT 1024
+#define I8MP_DISTILL_STATS 8
+typedef struct {
+  const void* logits;
+  int64_t T, V, ld;
+  int32_t dtype;
+  const void* teacher;
+  int64_t teacher_ld;
+  int32_t teacher_dtype;
+  const void* idx;
+  int64_t idx_ld;
+  int32_t idx_bits;
+  int32_t kept;
+  float temperature;
+  const float* lse;
+  const void* labels;
+  int32_t label_bits;
+  int64_t ignore_index;
+  float ce_weight;
+} i8mp_distill;
+size_t i8mp_distill_workspace_bytes(int64_t T, int64_t V, int32_t kept, int32_t dtype);
+i8mp_status i8mp_distill_fwd(const i8mp_distill* p, float* loss, double* stats, void* ws, size_t ws_bytes,
+                             void* stream);
+i8mp_status i8mp_distill_bwd(const i8mp_distill* p, const double* stats, const float* grad, int64_t grad_s,
+                             void* dlogits, int64_t d_ld, void* stream);
+i8mp_status i8mp_distill_step(const i8mp_distill* p, const float* grad, int64_t grad_s, float* loss,
+                              void* dlogits, int64_t d_ld, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,7 @@ __all__ = [
     "quantize_colwise_fp8", "fp8_scaled_mm", "fp8_mm_f32", "linear_fwd_fp8", "linear_bwd_fp8",
     "linear_fwd_fp8_colmax",
     "quantize_colwise_noalloc", "STATIC_SCRATCH_BYTES", "mfma_rate_probe", "EXPORTED_SYMBOLS",
-    "rotary", "rotary_frequencies",
+    "rotary", "rotary_frequencies", "distill_loss", "distill_loss_bwd", "distill_loss_and_grad",
 ]
 
 RNE, SR = 0, 1
@@ -47,7 +47,7 @@ EXPORTED_SYMBOLS = (
     "i8mp_fp8_scaled_mm", "i8mp_fp8_mm_f32", "i8mp_linear_fwd_fp8", "i8mp_linear_bwd_fp8",
     "i8mp_linear_fwd_fp8_colmax", "i8mp_linear_bwd_fp8_colmax",
     "i8mp_quantize_colwise_noalloc", "i8mp_mfma_rate_probe",
-    "i8mp_rotary",
+    "i8mp_rotary", "i8mp_distill_workspace_bytes", "i8mp_distill_fwd", "i8mp_distill_bwd", "i8mp_distill_step",
 )
 
 
@@ -64,6 +64,15 @@ class _Opts(ctypes.Structure):
 class _Heads(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int32)] + [
         (n, ctypes.c_int64) for n in ("x_b", "x_s", "x_h", "y_b", "y_s", "y_h")]
+
+
+class _Distill(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("T", ctypes.c_int64), ("V", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("teacher", ctypes.c_void_p), ("teacher_ld", ctypes.c_int64),
+                ("teacher_dtype", ctypes.c_int32), ("idx", ctypes.c_void_p), ("idx_ld", ctypes.c_int64),
+                ("idx_bits", ctypes.c_int32), ("kept", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("lse", ctypes.c_void_p), ("labels", ctypes.c_void_p), ("label_bits", ctypes.c_int32),
+                ("ignore_index", ctypes.c_int64), ("ce_weight", ctypes.c_float)]
 
 
 def _load() -> ctypes.CDLL:
@@ -104,6 +113,10 @@ def _load() -> ctypes.CDLL:
         "i8mp_mfma_rate_probe": ([p, i64, i64, p, p], i32),
         "i8mp_rotary": ([ctypes.POINTER(_Heads), ctypes.POINTER(_Heads), i64, i64, i32, i32, i32, i32, i32, p, i32,
                          i64, i64, p, p], i32),
+        "i8mp_distill_workspace_bytes": ([i64, i64, i32, i32], sz),
+        "i8mp_distill_fwd": ([ctypes.POINTER(_Distill), p, p, p, sz, p], i32),
+        "i8mp_distill_bwd": ([ctypes.POINTER(_Distill), p, p, i64, p, i64, p], i32),
+        "i8mp_distill_step": ([ctypes.POINTER(_Distill), p, i64, p, p, i64, p, sz, p], i32),
     }
     for name, (args, res) in sigs.items():
         f = getattr(L, name)
@@ -673,4 +686,5 @@ def linear_bwd_fp8(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, want_dx: 
 
 # --------------------------------------------------------------------------- operators around the linears
 
-from .operators import rotary, rotary_frequencies  # noqa: E402
+from .operators import (distill_loss, distill_loss_and_grad, distill_loss_bwd, rotary,  # noqa: E402
+                        rotary_frequencies)

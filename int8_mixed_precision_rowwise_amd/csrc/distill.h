@@ -1,0 +1,872 @@
+// Loss of a student's logits against a teacher's kept top logits, and its
+// gradient: kernels, templated on the logits' type (distill_bf16.hip,
+// distill_fp16.hip and distill_fp32.hip instantiate them).
+//
+// For one row x of V logits, temperature tau, kept entries j with logits t_j:
+//   q = softmax(x / tau),  p_j = exp(t_j / tau - z)
+// z = log sum_j exp(t_j / tau), or the whole teacher's log-sum-exp, when the
+// mass p_rest = max(0, 1 - sum p_j) that is left is one more class, whose
+// student is q_rest = sum of q over the entries not kept;
+//   loss = tau^2 [sum_j p_j log(p_j / q_j) + p_rest log(p_rest / q_rest)]
+//          + ce (log sum exp(x) - x_label)
+//   dx_i = g tau [mass q_i - p_i]                     (i kept; mass = sum p_j + p_rest)
+//        = g tau q_i [mass - p_rest / q_rest]         (i not kept)
+//          + g ce (softmax(x)_i - [i = label]).
+//
+// A step has to read every logit and write every gradient once, and nothing
+// else of size: it is bound by memory as long as a row is read once.  So one
+// workgroup holds a whole row in registers between the sums and the gradient
+// (a row of 131064 16-bit logits is half a CU's registers).  The sums are
+// taken while the row arrives, each thread rescaling its own to the maximum it
+// has seen so far; the kept entries are left out of them (their elements are
+// set to -inf in the registers) and are evaluated one per thread in 64 bits,
+// which keeps q_rest and mass q_j - p_j free of cancellation.  A table in LDS
+// from each 16-byte chunk of the row to the kept entries inside it tells a
+// thread which of its elements they are.
+//
+// Rows too long for that, and calls with too few rows to fill the chip, take
+// two launches over (segment, row): partial sums, then the gradient with each
+// workgroup joining its row's partial sums itself.  The gradient alone (the
+// backward of an earlier forward) is the second of them with the sums given.
+//
+// Exponentials are 2^(c (x - m)) with m the row's maximum and c = log2(e) / tau
+// rounded to fp32, the same c in the 64-bit part, so that its rounding only
+// scales the temperature by 2^-24.  (c x - c m in one fused operation would
+// save one of about ten per element, but the rounding of c m then decides the
+// result where a whole row is masked with the type's lowest value.)  fp32 logits
+// carry the product's low part too.
+#pragma once
+
+#include "internal.h"
+
+namespace i8mp {
+namespace distill {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
+
+// What a row's gradient needs besides its logits and kept entries.
+struct RowStats {
+  double ref;      // the maximum m of the logits (0 if all are -inf)
+  double total;    // sum of exp((x - m) / tau)
+  double total1;   // sum of exp(x - m)
+  double outside;  // mass - p_rest / q_rest
+  double mass;
+  double z;        // p_j = exp(t_j / tau - z)
+  double spare[2];
+};
+static_assert(sizeof(RowStats) == 8 * I8MP_DISTILL_STATS, "one row of the caller's statistics");
+
+struct Partial {  // sums of one segment without its kept entries, relative to its own maximum
+  float max, sum, sum1;
+  float pad;
+};
+
+// One LDS-only workgroup barrier: loads in flight from memory stay in flight.
+__device__ __forceinline__ void lds_sync() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The row's element type: 16-byte chunks of E elements.
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__bf16> {
+  static constexpr int E = 8;
+  static constexpr uint32_t kNegInf = 0xFF80u;
+  static __device__ __forceinline__ float get(const v4i& v, int e) {
+    const uint32_t w = (uint32_t)v[e >> 1];
+    return __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
+  }
+};
+template <>
+struct Elem<_Float16> {
+  static constexpr int E = 8;
+  static constexpr uint32_t kNegInf = 0xFC00u;
+  static __device__ __forceinline__ float get(const v4i& v, int e) {
+    const uint32_t w = (uint32_t)v[e >> 1];
+    return (float)__builtin_bit_cast(_Float16, (unsigned short)((e & 1) ? (w >> 16) : (w & 0xFFFFu)));
+  }
+};
+template <>
+struct Elem<float> {
+  static constexpr int E = 4;
+  static constexpr uint32_t kNegInf = 0xFF800000u;
+  static __device__ __forceinline__ float get(const v4i& v, int e) { return __uint_as_float((uint32_t)v[e]); }
+};
+
+// Elements whose bit is set in mask become -inf.
+template <typename T>
+__device__ __forceinline__ void drop(v4i& v, uint32_t mask) {
+  constexpr int E = Elem<T>::E;
+  constexpr uint32_t inf = Elem<T>::kNegInf;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (!(mask >> e & 1)) continue;
+    if constexpr (E == 4)
+      v[e] = (int)inf;
+    else
+      v[e >> 1] = (e & 1) ? (int)(((uint32_t)v[e >> 1] & 0xFFFFu) | (inf << 16)) : (int)(((uint32_t)v[e >> 1] & 0xFFFF0000u) | inf);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float pick(const v4i& v, int e) {
+  float x = Elem<T>::get(v, 0);
+#pragma unroll
+  for (int i = 1; i < Elem<T>::E; ++i) x = e == i ? Elem<T>::get(v, i) : x;
+  return x;
+}
+
+// A row as 16-byte chunks of memory: chunk c holds elements c E - shift ...;
+// elements before the row and behind it (in its first and last chunk) are
+// read as -inf and never written.
+template <typename T>
+struct Row {
+  const v4i* chunks;
+  int shift;    // elements of the first chunk that lie before the row
+  int nchunks;
+  int V;
+  __device__ __forceinline__ Row(const void* base, int64_t row, int64_t ld, int V_) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(base) + (uintptr_t)(row * ld) * sizeof(T);
+    chunks = reinterpret_cast<const v4i*>(a & ~(uintptr_t)15);
+    shift = (int)(a & 15) / (int)sizeof(T);
+    V = V_;
+    nchunks = (V + shift + Elem<T>::E - 1) / Elem<T>::E;
+  }
+  // Elements of chunk c outside the row.
+  __device__ __forceinline__ uint32_t outside(int c) const {
+    constexpr int E = Elem<T>::E;
+    uint32_t m = 0;
+    if (c == 0) m = (1u << shift) - 1;
+    const int left = V + shift - c * E;  // elements up to the row's end
+    if (left < E) m |= ~0u << (left > 0 ? left : 0);
+    return m;
+  }
+  __device__ __forceinline__ v4i load(int c) const {
+    v4i v = chunks[c];
+    if (c == 0 || c == nchunks - 1) drop<T>(v, outside(c));
+    return v;
+  }
+};
+
+__device__ __forceinline__ v4i all_neg_inf(int elem_bytes, uint32_t inf) {
+  const int w = elem_bytes == 4 ? (int)inf : (int)(inf | (inf << 16));
+  return (v4i){w, w, w, w};
+}
+
+// Exponentials of a row relative to one reference.  MODE 0: one temperature
+// (no hard labels, or tau = 1); 1: tau = 2, exp(x) as the square; 2: two.
+template <typename T, int MODE>
+struct Expo {
+  static constexpr bool kPrecise = sizeof(T) == 4;
+  float c, c_lo, c1, c1_lo;  // log2(e) / tau and log2(e), with their low parts
+  float r;                   // the reference m
+  __device__ __forceinline__ Expo(const DistillArgs& a) : c(a.c), c_lo(a.c_lo), c1(a.c1), c1_lo(a.c1_lo), r(0) {}
+  __device__ __forceinline__ void at(float max) { r = max == -__builtin_inff() ? 0.0f : max; }  // all -inf: every exponential is 0
+  __device__ __forceinline__ static float precise(float y, float c, float c_lo) {
+    const float h = y * c;
+    const float l = __builtin_fmaf(y, c_lo, __builtin_fmaf(y, c, -h));
+    const float e = exp2_fast(h);
+    // y = -inf: h is -inf and l a NaN
+    return h < -150.0f ? 0.0f : __builtin_fmaf(e, l * (float)kLn2, e);
+  }
+  // exp(y / tau) and, given that, exp(y), for y = x - m
+  __device__ __forceinline__ float e(float y) const {
+    if constexpr (kPrecise) return precise(y, c, c_lo);
+    else return exp2_fast(y * c);
+  }
+  __device__ __forceinline__ float e1(float y, float e) const {
+    if constexpr (MODE == 1) return e * e;
+    if constexpr (kPrecise) return precise(y, c1, c1_lo);
+    else return exp2_fast(y * c1);
+  }
+  // log2 of the same exponentials in 64 bits
+  __device__ __forceinline__ double log2e(double y, const DistillArgs& a) const { return y * (kPrecise ? a.cd : (double)c); }
+  __device__ __forceinline__ double log2e1(double y, const DistillArgs& a) const {
+    if constexpr (MODE == 0) return log2e(y, a);
+    if constexpr (MODE == 1) return 2 * log2e(y, a);
+    return y * (kPrecise ? kLog2e : (double)c1);
+  }
+};
+
+// 2^y in 64 bits: the Taylor polynomial of degree 10 of exp on |z| <= ln(2) / 2
+// is off by less than 1e-12 relative, far inside what the sums' fp32 part has.
+__device__ __forceinline__ double exp2_d(double y) {
+  const double n = __builtin_rint(y), z = (y - n) * kLn2;
+  double p = 1.0 / 3628800;
+  p = __builtin_fma(p, z, 1.0 / 362880);
+  p = __builtin_fma(p, z, 1.0 / 40320);
+  p = __builtin_fma(p, z, 1.0 / 5040);
+  p = __builtin_fma(p, z, 1.0 / 720);
+  p = __builtin_fma(p, z, 1.0 / 120);
+  p = __builtin_fma(p, z, 1.0 / 24);
+  p = __builtin_fma(p, z, 1.0 / 6);
+  p = __builtin_fma(p, z, 0.5);
+  p = __builtin_fma(p, z, 1.0);
+  p = __builtin_fma(p, z, 1.0);
+  // -inf (where the polynomial is a NaN) and what underflows give 0; beyond the range: infinity
+  return y < -1100 ? 0 : y > 1100 ? (double)__builtin_inff() : __builtin_amdgcn_ldexp(p, (int)n);
+}
+
+__device__ __forceinline__ float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
+
+template <typename F>
+__device__ __forceinline__ F wave_sum(F v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
+  return v;
+}
+
+__device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t row, int j) {
+  const int64_t at = row * a.t_ld + j;
+  switch (a.t_dtype) {
+    case I8MP_BF16: return __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.teacher)[at] << 16);
+    case I8MP_FP16: return (float)static_cast<const _Float16*>(a.teacher)[at];
+    default: return static_cast<const float*>(a.teacher)[at];
+  }
+}
+
+// The class of kept entry j of a row, or -1 (also for classes the vocabulary does not have).
+__device__ __forceinline__ int kept_at(const DistillArgs& a, int64_t row, int j) {
+  const int64_t at = row * a.i_ld + j;
+  const int64_t i = a.idx64 ? static_cast<const int64_t*>(a.idx)[at] : (int64_t) static_cast<const int32_t*>(a.idx)[at];
+  return i >= 0 && i < a.V ? (int)i : -1;
+}
+__device__ __forceinline__ int label_at(const DistillArgs& a, int64_t row) {
+  if (!a.labels) return -1;
+  const int64_t i = a.lab64 ? static_cast<const int64_t*>(a.labels)[row] : (int64_t) static_cast<const int32_t*>(a.labels)[row];
+  return i != a.ignore && i >= 0 && i < a.V ? (int)i : -1;
+}
+
+// What the joined sums of a row give: the loss and the statistics.
+// sums over kept entries: W = sum w_j, A = sum w_j (ln w_j - ln e_j), e and e1;
+// w_j = exp(t_j / tau - zref), kept: how many there are.
+struct Joined {
+  double out, out1;  // sums over the entries not kept
+  double W, A, e, e1;
+  double zref;
+  int kept;
+};
+__device__ __forceinline__ RowStats join(const DistillArgs& a, const Joined& s, double ref, int mode) {
+  RowStats st;
+  st.ref = ref, st.spare[0] = st.spare[1] = 0;
+  st.total = s.out + s.e;
+  st.total1 = mode == 0 ? st.total : s.out1 + s.e1;
+  if (s.kept == 0) {
+    st.outside = st.mass = 0;
+  } else if (a.lse) {
+    const double p_rest = s.W < 1 ? 1 - s.W : s.W >= 1 ? 0 : s.W;  // a NaN stays one
+    st.mass = s.W + p_rest;
+    st.outside = p_rest == 0 ? st.mass : st.mass - p_rest * st.total / s.out;
+  } else {
+    st.mass = st.outside = 1;
+  }
+  st.z = 0;
+  return st;
+}
+// p_j = exp(t_j / tau - z): the one statistic that takes a logarithm.
+__device__ __forceinline__ double teacher_norm(const DistillArgs& a, const Joined& s) {
+  return s.kept == 0 ? 0 : a.lse ? s.zref : s.zref + log(s.W);
+}
+__device__ __forceinline__ float row_loss(const DistillArgs& a, const Joined& s, const RowStats& st, double label_log2e1,
+                                          bool has_label) {
+  double loss = 0;
+  if (s.kept > 0) {
+    const double lt = log(st.total);
+    if (a.lse) {
+      const double p_rest = st.mass - s.W;
+      loss = s.A + s.W * lt;
+      if (!(p_rest == 0)) loss += p_rest * (log(p_rest) - log(s.out) + lt);
+    } else {
+      loss = s.A / s.W - log(s.W) + lt;
+    }
+    loss *= (double)a.tau * (double)a.tau;
+  }
+  if (has_label) loss += (double)a.ce * (log(st.total1) - label_log2e1 * kLn2);
+  return (float)loss;
+}
+
+// The gradient's factors of a row, formed in 64 bits.
+struct Factors {
+  float out, out1;    // not kept: out * e + out1 * e1
+  float kept, p, c1;  // kept: kept * e_j + c1 * e1_j - p * w_j
+  float label;        // subtracted at the label
+};
+// w_scale: p_j = w_scale * w_j for the w_j in the slots.
+__device__ __forceinline__ Factors factors(const DistillArgs& a, const RowStats& st, double w_scale, int64_t row, bool has_label,
+                                           int mode) {
+  const double g = (double)a.grad[row * a.grad_s], gt = g * (double)a.tau;
+  const double label = has_label ? g * (double)a.ce : 0, c1 = has_label ? label / st.total1 : 0;
+  const double out = st.outside == 0 && st.mass == 0 ? 0 : gt * st.outside / st.total;
+  Factors f;
+  f.label = (float)label;
+  f.c1 = f.out1 = (float)c1;
+  f.kept = (float)(st.mass == 0 ? 0 : gt * st.mass / st.total);
+  f.p = (float)(gt * w_scale);
+  f.out = (float)(mode == 0 ? out + c1 : out);
+  return f;
+}
+__device__ __forceinline__ Factors uniform(const Factors& f) {
+  return {uniform(f.out), uniform(f.out1), uniform(f.kept), uniform(f.p), uniform(f.c1), uniform(f.label)};
+}
+
+template <typename T, int MODE>
+__device__ __forceinline__ float outside_grad(const Expo<T, MODE>& ex, const Factors& f, float x) {
+  const float e = ex.e(x - ex.r);
+  if constexpr (MODE == 0) return e * f.out;
+  const float e1 = ex.e1(x - ex.r, e);
+  return __builtin_fmaf(e1, f.out1, e * f.out);
+}
+
+// Entry slots of one row in LDS: the chain to the chunk's next entry with the
+// element inside its chunk, then x_j, later e_j, e1_j and p_j.
+template <int KM>
+struct Slots {
+  int link[KM + 1];
+  float x[KM + 1], x1[KM + 1], p[KM + 1];  // the label's slot is number k; its p: 1 + the kept entry of its class, or 0
+};
+template <typename S>
+__device__ __forceinline__ void insert(int* first, S& s, int chunk, int elem, int j) {
+  s.link[j] = atomicExch(first + chunk, j + 1) << 3 | elem;
+}
+
+// Gradient of one chunk, kept entries and the label put in from its chain.
+template <typename T, int MODE, typename S>
+__device__ __forceinline__ void grad_chunk(const Row<T>& row, const DistillArgs& a, const Expo<T, MODE>& ex, const Factors& f,
+                                           const S& s, v4i v, int chain, int c, T* __restrict__ d) {
+  constexpr int E = Elem<T>::E;
+  float y[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = outside_grad<T, MODE>(ex, f, Elem<T>::get(v, e));
+  if (chain) {
+    int lab = -1;
+    for (int j = chain; j;) {
+      const int link = s.link[j - 1], at = link & 7;
+      if (j - 1 == a.k) {
+        lab = at;
+      } else {
+        float value = __builtin_fmaf(f.kept, s.x[j - 1], -(f.p * s.p[j - 1]));
+        if (f.label != 0) value += __builtin_fmaf(f.c1, s.x1[j - 1], s.p[a.k] == (float)j ? -f.label : 0.0f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = at == e ? value : y[e];
+      }
+      j = link >> 3;
+    }
+    if (lab >= 0 && s.p[a.k] == 0.0f) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = lab == e ? y[e] - f.label : y[e];
+    }
+  }
+  T o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = (T)y[e];
+  T* at = d + (int64_t)c * E - row.shift;
+  const uint32_t skip = (c == 0 || c == row.nchunks - 1) ? row.outside(c) : 0;
+  if (!skip && a.d_aligned) {
+    __builtin_nontemporal_store(__builtin_bit_cast(v4i, o), reinterpret_cast<v4i*>(at));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (!(skip >> e & 1)) at[e] = o[e];
+  }
+}
+
+// Running sums of one thread: four fp32 sums relative to the maximum so far,
+// so none adds more than a few dozen terms before they are joined.
+template <typename T, int MODE>
+struct Running {
+  static constexpr int E = Elem<T>::E, S = 4;
+  float max = -__builtin_inff();
+  float s[S], s1[MODE ? S : 1];
+  __device__ __forceinline__ Running() {
+#pragma unroll
+    for (int e = 0; e < S; ++e) s[e] = 0;
+#pragma unroll
+    for (int e = 0; e < (MODE ? S : 1); ++e) s1[e] = 0;
+  }
+  // floor: a maximum of elements that v no longer holds (kept entries)
+  template <int N>
+  __device__ __forceinline__ void add(const v4i (&v)[N], float floor, Expo<T, MODE>& ex, const DistillArgs& a) {
+    float m = fmaxf(max, floor);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) m = fmaxf(m, Elem<T>::get(v[i], e));
+    rescale(m, ex, a);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float x = Elem<T>::get(v[i], e) - ex.r;
+        const float y = ex.e(x);
+        s[e % S] += y;
+        if constexpr (MODE == 1) s1[e % S] = __builtin_fmaf(y, y, s1[e % S]);
+        if constexpr (MODE == 2) s1[e % S] += ex.e1(x, y);
+      }
+  }
+  __device__ __forceinline__ void rescale(float m, Expo<T, MODE>& ex, const DistillArgs& a) {
+    const float r = ex.r;
+    ex.at(m);
+    float f = ex.e(r - ex.r), f1 = 1;
+    if constexpr (MODE != 0) f1 = ex.e1(r - ex.r, f);
+    if (max == -__builtin_inff()) f = f1 = 1;  // nothing summed yet
+    max = m;
+#pragma unroll
+    for (int e = 0; e < S; ++e) s[e] *= f;
+    if constexpr (MODE != 0) {
+#pragma unroll
+      for (int e = 0; e < S; ++e) s1[e] *= f1;
+    }
+  }
+  __device__ __forceinline__ float sum() const { return (s[0] + s[1]) + (s[2] + s[3]); }
+  __device__ __forceinline__ float sum1() const {
+    if constexpr (MODE == 0) return 0;
+    else return (s1[0] + s1[1]) + (s1[2] + s1[3]);
+  }
+};
+
+// Elements of v that its chain names: their values go to their slots, kept
+// ones are dropped from v; returns the largest dropped value.
+template <typename T, typename S>
+__device__ __forceinline__ float take_out(v4i& v, int chain, S& s, int k) {
+  float floor = -__builtin_inff();
+  uint32_t mask = 0;
+  for (int j = chain; j;) {
+    const int link = s.link[j - 1];
+    const float x = pick<T>(v, link & 7);
+    s.x[j - 1] = x;
+    if (j - 1 < k) {
+      mask |= 1u << (link & 7);
+      floor = fmaxf(floor, x);
+    }
+    j = link >> 3;
+  }
+  drop<T>(v, mask);
+  return floor;
+}
+
+// ---- one workgroup a row, the row in registers -----------------------------
+
+template <int NT, int KM>
+struct RowLds {
+  Slots<KM> slots;
+  double sums[NT / 64][6];
+  float wmax[NT / 64];
+  int kept[NT / 64];
+  int label_slot;  // 1 + the kept entry that is the label's class, or 0
+  int row_kept;
+  double zref;
+  RowStats st;
+  Factors f;
+};
+
+constexpr int row_waves(int nt, int nv) { return nv <= 8 ? (nt == 1024 ? 8 : 6) : 4; }  // waves a SIMD
+
+template <typename T, int NT, int NV, int KM, int MODE>
+__global__ __launch_bounds__(NT, row_waves(NT, NV)) void distill_rows(DistillArgs a) {
+  constexpr int W = NT / 64, E = Elem<T>::E, GROUP = 2;
+  constexpr int KPT = (KM + NT - 1) / NT;
+  __shared__ __attribute__((aligned(16))) int first[NT * NV];
+  __shared__ RowLds<NT, KM> l;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int64_t row = blockIdx.x;
+  const int V = (int)a.V, k = a.k;
+  const Row<T> x(a.logits, row, a.ld, V);
+  const int label = label_at(a, row);
+
+  // kept entries first: they are needed before the row has arrived
+  int id[KPT];
+  float tv[KPT];
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    const int j = t + i * NT;
+    id[i] = j < k ? kept_at(a, row, j) : -1;
+    tv[i] = id[i] >= 0 ? teacher_at(a, row, j) : 0.0f;
+  }
+  v4i v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = i * NT + t;
+    v[i] = c < x.nchunks ? x.chunks[c] : all_neg_inf(sizeof(T), Elem<T>::kNegInf);
+  }
+  for (int c = t; c < x.nchunks; c += NT) first[c] = 0;
+  if (t == 0) l.label_slot = 0;
+  float tmax = -__builtin_inff();
+  int kept = 0;
+#pragma unroll
+  for (int i = 0; i < KPT; ++i)
+    if (id[i] >= 0) tmax = fmaxf(tmax, tv[i]), ++kept;
+  if (wave * 64 < k) {
+    tmax = wave_max(tmax);
+    kept = wave_sum(kept);
+  }
+  if (lane == 0) l.wmax[wave] = tmax, l.kept[wave] = kept;
+  lds_sync();
+#pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    const int j = t + i * NT;
+    if (j >= k) continue;
+    if (id[i] >= 0) {
+      const int at = id[i] + x.shift;
+      l.slots.p[j] = tv[i];
+      insert(first, l.slots, at / E, at % E, j);
+      if (id[i] == label) l.label_slot = j + 1;
+    } else {
+      l.slots.link[j] = -1;
+    }
+  }
+  if (t == 0) {
+    if (label >= 0) insert(first, l.slots, (label + x.shift) / E, (label + x.shift) % E, k);
+    float tm = l.wmax[0];
+    int n = l.kept[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) tm = fmaxf(tm, l.wmax[w]), n += l.kept[w];
+    l.zref = a.lse ? (double)a.lse[row] : (double)tm * a.itau;
+    l.row_kept = n;
+  }
+  lds_sync();
+
+  Expo<T, MODE> ex(a);
+  Running<T, MODE> run;
+#pragma unroll
+  for (int g = 0; g < NV; g += GROUP) {
+    if (g * NT >= x.nchunks) break;  // the whole workgroup
+    float floor = -__builtin_inff();
+    v4i u[GROUP];
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+      const int c = (g + i) * NT + t;
+      if (c < x.nchunks) {
+        if (c == 0 || c == x.nchunks - 1) drop<T>(v[g + i], x.outside(c));
+        const int chain = first[c];
+        if (chain) floor = fmaxf(floor, take_out<T>(v[g + i], chain, l.slots, k));
+      }
+      u[i] = v[g + i];
+    }
+    run.add(u, floor, ex, a);
+  }
+  const float wm = wave_max(run.max);
+  if (lane == 0) l.wmax[wave] = wm;
+  lds_sync();
+  float m = l.wmax[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) m = fmaxf(m, l.wmax[w]);
+  run.rescale(uniform(m), ex, a);
+  ex.r = uniform(ex.r);
+
+  // sums of this wave; the kept entries in 64 bits
+  const float ws = wave_sum(run.sum()), ws1 = MODE ? wave_sum(run.sum1()) : 0;
+  if (wave * 64 < k) {
+    double q[4] = {0, 0, 0, 0};
+    const double zref = l.zref;
+#pragma unroll 1
+    for (int j = t; j < k; j += NT) {
+      if (l.slots.link[j] < 0) continue;
+      const double lw = (double)l.slots.p[j] * a.itau - zref, w = exp2_d(lw * kLog2e);
+      const double xj = (double)l.slots.x[j] - (double)ex.r, y = ex.log2e(xj, a), e = exp2_d(y);
+      const double e1 = MODE == 0 ? e : MODE == 1 ? e * e : exp2_d(ex.log2e1(xj, a));
+      q[0] += w;
+      if (!(w == 0)) q[1] += w * (lw - y * kLn2);
+      q[2] += e;
+      q[3] += e1;
+      l.slots.x[j] = (float)e;
+      l.slots.x1[j] = (float)e1;
+      l.slots.p[j] = (float)w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double b = wave_sum(q[i]);
+      if (lane == 0) l.sums[wave][2 + i] = b;
+    }
+  } else if (lane == 0) {
+#pragma unroll
+    for (int i = 2; i < 6; ++i) l.sums[wave][i] = 0;
+  }
+  if (lane == 0) l.sums[wave][0] = (double)ws, l.sums[wave][1] = (double)ws1;
+  lds_sync();
+  if (wave == 0) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      double b = lane < W ? l.sums[lane][i] : 0.0;
+#pragma unroll
+      for (int off = 1; off < W; off <<= 1) b += __shfl_xor(b, off);
+      if (lane == 0) l.sums[0][i] = b;
+    }
+    if (lane == 0) {
+      const Joined s = {l.sums[0][0], l.sums[0][1], l.sums[0][2], l.sums[0][3], l.sums[0][4], l.sums[0][5], l.zref, l.row_kept};
+      l.st = join(a, s, (double)ex.r, MODE);
+      // the slots hold w_j = exp(t_j / tau - zref)
+      if (a.d) l.f = factors(a, l.st, s.kept == 0 ? 0 : a.lse ? 1 : 1 / s.W, row, label >= 0, MODE);
+      l.slots.p[k] = (float)l.label_slot;
+    }
+  }
+  lds_sync();
+  if (a.d) {
+    const Factors f = uniform(l.f);
+    T* d = static_cast<T*>(a.d) + row * a.d_ld;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * NT + t;
+      if (c < x.nchunks) grad_chunk<T, MODE>(x, a, ex, f, l.slots, v[i], first[c], c, d);
+    }
+  }
+  if (t == 0) {
+    const Joined s = {l.sums[0][0], l.sums[0][1], l.sums[0][2], l.sums[0][3], l.sums[0][4], l.sums[0][5], l.zref, l.row_kept};
+    RowStats st = l.st;
+    st.z = teacher_norm(a, s);
+    if (a.loss) a.loss[row] = row_loss(a, s, st, label >= 0 ? ex.log2e1((double)l.slots.x[k] - (double)ex.r, a) : 0, label >= 0);
+    if (a.stats) static_cast<RowStats*>(a.stats)[row] = st;
+  }
+}
+
+// ---- segments of rows ------------------------------------------------------
+
+constexpr int kSegThreads = 512;
+constexpr int kSegChunks = 4096;  // at most, so that the table of a segment takes 16 KiB
+
+struct SegLds {
+  int first[kSegChunks];
+  Slots<kDistillMaxKept> slots;
+  double sums[kSegThreads / 64][6];
+  float wmax[kSegThreads / 64];
+  int kept[kSegThreads / 64];
+  int label_slot;
+};
+
+// Kept entries (and the label) of chunks [c0, c1) go into the table.
+template <typename T>
+__device__ __forceinline__ void seg_table(SegLds& l, const DistillArgs& a, const Row<T>& x, int64_t row, int label, int c0,
+                                          int c1) {
+  constexpr int E = Elem<T>::E;
+  const int t = threadIdx.x;
+  for (int c = t; c < c1 - c0; c += kSegThreads) l.first[c] = 0;
+  if (t == 0) l.label_slot = 0;
+  __syncthreads();
+  for (int j = t; j <= a.k; j += kSegThreads) {
+    const int id = j < a.k ? kept_at(a, row, j) : label;
+    if (id < 0) continue;
+    if (j < a.k && id == label) l.label_slot = j + 1;
+    const int at = id + x.shift, c = at / E;
+    if (c >= c0 && c < c1) insert(l.first, l.slots, c - c0, at % E, j);
+  }
+  __syncthreads();
+}
+
+template <typename T, int MODE>
+__global__ __launch_bounds__(kSegThreads) void distill_partial(DistillArgs a) {
+  constexpr int W = kSegThreads / 64, GROUP = 4;
+  __shared__ __attribute__((aligned(16))) SegLds l;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int seg = (int)(blockIdx.x % a.segs);
+  const int64_t row = blockIdx.x / a.segs;
+  const Row<T> x(a.logits, row, a.ld, (int)a.V);
+  const int c0 = seg * a.seg_chunks, c1 = min(x.nchunks, c0 + a.seg_chunks);
+  seg_table<T>(l, a, x, row, -1, c0, c1);
+  Expo<T, MODE> ex(a);
+  Running<T, MODE> run;
+  for (int g = c0 + t; g < c1; g += GROUP * kSegThreads) {
+    v4i v[GROUP];
+    float floor = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+      const int c = g + i * kSegThreads;
+      v[i] = c < c1 ? x.load(c) : all_neg_inf(sizeof(T), Elem<T>::kNegInf);
+    }
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+      const int c = g + i * kSegThreads;
+      const int chain = c < c1 ? l.first[c - c0] : 0;
+      if (chain) floor = fmaxf(floor, take_out<T>(v[i], chain, l.slots, a.k));
+    }
+    run.add(v, floor, ex, a);
+  }
+  const float wm = wave_max(run.max);
+  if (lane == 0) l.wmax[wave] = wm;
+  __syncthreads();
+  float m = l.wmax[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) m = fmaxf(m, l.wmax[w]);
+  run.rescale(m, ex, a);
+  const float s = wave_sum(run.sum()), s1 = MODE ? wave_sum(run.sum1()) : 0;
+  if (lane == 0) l.sums[wave][0] = s, l.sums[wave][1] = s1;
+  __syncthreads();
+  if (t == 0) {
+    double b = 0, b1 = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) b += l.sums[w][0], b1 += l.sums[w][1];
+    static_cast<Partial*>(a.partial)[blockIdx.x] = {m, (float)b, (float)b1, 0.0f};
+  }
+}
+
+// A row's partial sums and kept entries joined, by the whole workgroup; every
+// thread returns the statistics, thread 0 writes the loss if `write`.
+template <typename T, int MODE>
+__device__ __forceinline__ RowStats seg_join(SegLds& l, const DistillArgs& a, int64_t row, int label, bool write,
+                                             Expo<T, MODE>& ex) {
+  constexpr int W = kSegThreads / 64;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const T* x = static_cast<const T*>(a.logits) + row * a.ld;
+  const Partial* part = static_cast<const Partial*>(a.partial) + row * a.segs;
+  float tmax = -__builtin_inff(), m = -__builtin_inff();
+  int kept = 0;
+  for (int j = t; j < a.k; j += kSegThreads)
+    if (kept_at(a, row, j) >= 0) tmax = fmaxf(tmax, teacher_at(a, row, j)), ++kept;
+  for (int i = t; i < a.segs; i += kSegThreads) m = fmaxf(m, part[i].max);
+  tmax = wave_max(tmax), m = wave_max(m), kept = wave_sum(kept);
+  if (lane == 0) l.wmax[wave] = tmax, l.sums[wave][0] = m, l.kept[wave] = kept;
+  __syncthreads();
+  tmax = m = -__builtin_inff(), kept = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) tmax = fmaxf(tmax, l.wmax[w]), m = fmaxf(m, (float)l.sums[w][0]), kept += l.kept[w];
+  __syncthreads();
+  ex.at(m);
+  double q[6] = {0, 0, 0, 0, 0, 0};
+  for (int i = t; i < a.segs; i += kSegThreads) {
+    const Partial p = part[i];
+    Expo<T, MODE> own(a);
+    own.at(p.max);
+    const double to = (double)own.r - (double)ex.r, y = ex.log2e(to, a), y1 = ex.log2e1(to, a);
+    q[0] += p.sum == 0 ? 0 : (double)p.sum * exp2_d(y);
+    if (MODE) q[1] += p.sum1 == 0 ? 0 : (double)p.sum1 * exp2_d(y1);
+  }
+  const double itau = a.itau, zref = a.lse ? (double)a.lse[row] : (double)tmax * itau;
+  for (int j = t; j < a.k; j += kSegThreads) {
+    const int id = kept_at(a, row, j);
+    if (id < 0) continue;
+    const double lw = (double)teacher_at(a, row, j) * itau - zref, w = exp2_d(lw * kLog2e), xj = (double)(float)x[id] - (double)ex.r;
+    const double y = ex.log2e(xj, a), e = exp2_d(y);
+    q[2] += w;
+    if (!(w == 0)) q[3] += w * (lw - y * kLn2);
+    q[4] += e;
+    q[5] += MODE == 0 ? e : exp2_d(ex.log2e1(xj, a));
+  }
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    q[i] = wave_sum(q[i]);
+    if (lane == 0) l.sums[wave][i] = q[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    q[i] = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) q[i] += l.sums[w][i];
+  }
+  __syncthreads();
+  const Joined s = {q[0], q[1], q[2], q[3], q[4], q[5], zref, kept};
+  RowStats st = join(a, s, (double)ex.r, MODE);
+  st.z = teacher_norm(a, s);
+  if (write && t == 0) {
+    if (a.loss) a.loss[row] = row_loss(a, s, st, label >= 0 ? ex.log2e1((double)(float)x[label] - (double)ex.r, a) : 0, label >= 0);
+    if (a.stats) static_cast<RowStats*>(a.stats)[row] = st;
+  }
+  return st;
+}
+
+template <typename T, int MODE>
+__global__ __launch_bounds__(kSegThreads) void distill_finish(DistillArgs a) {
+  __shared__ __attribute__((aligned(16))) SegLds l;
+  const int64_t row = blockIdx.x;
+  Expo<T, MODE> ex(a);
+  seg_join<T, MODE>(l, a, row, label_at(a, row), true, ex);
+}
+
+// GIVEN: the row's statistics come from an earlier forward.
+template <typename T, int MODE, bool GIVEN>
+__global__ __launch_bounds__(kSegThreads) void distill_grad(DistillArgs a) {
+  constexpr int GROUP = 4;
+  __shared__ __attribute__((aligned(16))) SegLds l;
+  const int t = threadIdx.x;
+  const int seg = (int)(blockIdx.x % a.segs);
+  const int64_t row = blockIdx.x / a.segs;
+  const Row<T> x(a.logits, row, a.ld, (int)a.V);
+  const int c0 = seg * a.seg_chunks, c1 = min(x.nchunks, c0 + a.seg_chunks);
+  const int label = label_at(a, row);
+  Expo<T, MODE> ex(a);
+  RowStats st;
+  if constexpr (GIVEN) {
+    st = static_cast<const RowStats*>(a.stats)[row];
+    ex.r = (float)st.ref;
+  } else {
+    st = seg_join<T, MODE>(l, a, row, label, seg == 0, ex);
+  }
+  seg_table<T>(l, a, x, row, label, c0, c1);
+  const Factors f = uniform(factors(a, st, 1, row, label >= 0, MODE));
+  const T* xr = static_cast<const T*>(a.logits) + row * a.ld;
+  for (int j = t; j < a.k; j += kSegThreads) {
+    const int id = kept_at(a, row, j);
+    if (id < 0) continue;
+    const int c = (id + x.shift) / Elem<T>::E;
+    if (c < c0 || c >= c1) continue;
+    const double xj = (double)(float)xr[id] - (double)ex.r;
+    l.slots.x[j] = (float)exp2_d(ex.log2e(xj, a));
+    l.slots.x1[j] = MODE == 0 ? l.slots.x[j] : (float)exp2_d(ex.log2e1(xj, a));
+    l.slots.p[j] = (float)exp2_d(((double)teacher_at(a, row, j) * a.itau - st.z) * kLog2e);
+  }
+  if (t == 0) l.slots.p[a.k] = (float)l.label_slot;
+  __syncthreads();
+  T* d = static_cast<T*>(a.d) + row * a.d_ld;
+  for (int g = c0 + t; g < c1; g += GROUP * kSegThreads) {
+    v4i v[GROUP];
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+      const int c = g + i * kSegThreads;
+      if (c < c1) v[i] = x.load(c);
+    }
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) {
+      const int c = g + i * kSegThreads;
+      if (c < c1) grad_chunk<T, MODE>(x, a, ex, f, l.slots, v[i], l.first[c - c0], c, d);
+    }
+  }
+}
+
+// ---- launches ---------------------------------------------------------------
+
+template <typename T, int MODE>
+hipError_t launch_mode(const DistillArgs& a, hipStream_t stream) {
+  switch (a.plan) {
+    case kRows64x8: distill_rows<T, 64, 8, 256, MODE><<<(unsigned)a.T, 64, 0, stream>>>(a); break;
+    case kRows256x8: distill_rows<T, 256, 8, 256, MODE><<<(unsigned)a.T, 256, 0, stream>>>(a); break;
+    case kRows512x8: distill_rows<T, 512, 8, kDistillMaxKept, MODE><<<(unsigned)a.T, 512, 0, stream>>>(a); break;
+    case kRows1024x8: distill_rows<T, 1024, 8, kDistillMaxKept, MODE><<<(unsigned)a.T, 1024, 0, stream>>>(a); break;
+    case kRows1024x16: distill_rows<T, 1024, 16, kDistillMaxKept, MODE><<<(unsigned)a.T, 1024, 0, stream>>>(a); break;
+    default: {
+      const dim3 grid((unsigned)(a.T * a.segs));
+      if (a.given) {
+        distill_grad<T, MODE, true><<<grid, kSegThreads, 0, stream>>>(a);
+        break;
+      }
+      distill_partial<T, MODE><<<grid, kSegThreads, 0, stream>>>(a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      if (a.d)
+        distill_grad<T, MODE, false><<<grid, kSegThreads, 0, stream>>>(a);
+      else
+        distill_finish<T, MODE><<<(unsigned)a.T, kSegThreads, 0, stream>>>(a);
+    }
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_typed(const DistillArgs& a, hipStream_t stream) {
+  if (!a.labels || a.tau == 1.0f) return launch_mode<T, 0>(a, stream);
+  if (a.tau == 2.0f) return launch_mode<T, 1>(a, stream);
+  return launch_mode<T, 2>(a, stream);
+}
+
+}  // namespace distill
+}  // namespace i8mp

@@ -182,4 +182,31 @@ hipError_t launch_rotary(const RotaryTensor& q, const RotaryTensor& k, int64_t B
                          bool half, bool inverse, const void* pos, int pos32, int64_t pos_b, int64_t pos_s,
                          const double* freqs, hipStream_t stream);
 
+// Distillation from a teacher's top logits; see i8mp_distill_*.
+constexpr int kDistillMaxKept = I8MP_DISTILL_MAX_KEPT;
+// A row in one workgroup's registers (threads x 16-byte chunks a thread), or
+// segments of rows in two launches.
+enum DistillPlan { kRows64x8, kRows256x8, kRows512x8, kRows1024x8, kRows1024x16, kSegments };
+struct DistillArgs {
+  const void *logits, *teacher, *idx, *labels;
+  const float *lse, *grad;
+  float* loss;
+  void *stats, *d, *partial;
+  int64_t T, V, ld, t_ld, i_ld, d_ld, grad_s, ignore;
+  double cd, itau;           // log2(e) / tau and 1 / tau
+  float tau, ce;
+  float c, c_lo, c1, c1_lo;  // log2(e) / tau and log2(e) in fp32, and what that leaves out
+  int k, t_dtype, idx64, lab64;
+  int d_aligned;             // a gradient row starts where its logits row does, modulo 16 bytes
+  int given;                 // stats hold the sums of an earlier forward
+  int plan, segs, seg_chunks;
+};
+// The plan for T rows of V logits of `elem` bytes (any alignment) with k kept
+// entries, and the bytes of partial sums it needs.
+void distill_plan(DistillArgs& a, int elem);
+size_t distill_workspace_bytes(int64_t T, int64_t V, int k, int elem);
+hipError_t launch_distill_bf16(const DistillArgs& a, hipStream_t stream);
+hipError_t launch_distill_fp16(const DistillArgs& a, hipStream_t stream);
+hipError_t launch_distill_fp32(const DistillArgs& a, hipStream_t stream);
+
 }  // namespace i8mp

@@ -5,9 +5,53 @@
 #include "internal.h"
 
 #include <algorithm>
+#include <cmath>
 #include <utility>
 
 using namespace i8mp::checks;
+
+namespace i8mp {
+
+// Workgroups of at least this many over (segment, row) fill the chip twice.
+constexpr int64_t kDistillFill = 1024;
+constexpr int64_t kDistillSegMin = 512, kDistillSegMax = 4096;  // chunks of 16 bytes
+
+static void distill_segments(int64_t T, int64_t chunks, int* segs, int* seg_chunks) {
+  const int64_t want = (kDistillFill + T - 1) / T;
+  int64_t per = (chunks + want - 1) / want;
+  per = std::min(std::max(per, kDistillSegMin), kDistillSegMax);
+  *segs = (int)((chunks + per - 1) / per);
+  *seg_chunks = (int)per;
+}
+
+// 16-byte chunks that a row of V elements can touch at any alignment.
+static int64_t distill_chunks(int64_t V, int elem) { return (V * elem + 15 + elem - 1) / 16 + 1; }
+
+// A row in one workgroup's registers is read once; segments read it twice but
+// spread few rows over the chip.
+static int distill_shape(int64_t T, int64_t V, int k, int elem) {
+  const int64_t chunks = distill_chunks(V, elem);
+  if (chunks > 16384 || (T < 128 && chunks > 4 * kDistillSegMin)) return kSegments;
+  if (k <= 256) {
+    if (chunks <= 512) return kRows64x8;
+    if (chunks <= 2048) return kRows256x8;
+  }
+  return chunks <= 4096 ? kRows512x8 : chunks <= 8192 ? kRows1024x8 : kRows1024x16;
+}
+
+void distill_plan(DistillArgs& a, int elem) {
+  a.plan = a.given ? kSegments : distill_shape(a.T, a.V, a.k, elem);
+  distill_segments(a.T, distill_chunks(a.V, elem), &a.segs, &a.seg_chunks);
+}
+
+size_t distill_workspace_bytes(int64_t T, int64_t V, int k, int elem) {
+  if (distill_shape(T, V, k, elem) != kSegments) return 0;
+  int segs, per;
+  distill_segments(T, distill_chunks(V, elem), &segs, &per);
+  return (size_t)T * (size_t)segs * 16;
+}
+
+}  // namespace i8mp
 
 namespace {
 
@@ -66,9 +110,130 @@ bool heads_disjoint(const HeadsView& a, const HeadsView& c, int64_t B, int64_t S
   return off >= lo_ext && (B * S == 1 || off + hi_ext <= period);
 }
 
+// Checks of the loss's inputs; fills `a` (not its outputs).
+i8mp_status distill_inputs(const i8mp_distill* p, i8mp::DistillArgs& a) {
+  if (!p || !dtype_ok(p->dtype) || !dtype_ok(p->teacher_dtype)) return I8MP_EINVAL;
+  if (!dims_ok(p->T, p->V) || p->T >= (int64_t(1) << 31) || p->V > (int64_t(1) << 30)) return I8MP_EINVAL;
+  if (p->kept < 0 || p->kept > I8MP_DISTILL_MAX_KEPT) return I8MP_EINVAL;
+  if (!(p->temperature > 0) || !std::isfinite(p->temperature) || !std::isfinite(p->ce_weight)) return I8MP_EINVAL;
+  const int64_t elem = dtype_bytes(p->dtype), t_elem = dtype_bytes(p->teacher_dtype);
+  if (!elementwise_ok(p->logits, p->T, p->V, p->ld, elem)) return I8MP_EINVAL;
+  if (p->T > 0 && p->V > 0 && p->T > kMaxDim / (p->ld > 0 ? p->ld : 1)) return I8MP_EINVAL;
+  const bool hard = p->labels && p->ce_weight != 0;
+  if (p->T > 0 && p->kept > 0) {
+    if (p->idx_bits != 32 && p->idx_bits != 64) return I8MP_EINVAL;
+    if (!elementwise_ok(p->teacher, p->T, p->kept, p->teacher_ld, t_elem)) return I8MP_EINVAL;
+    if (!elementwise_ok(p->idx, p->T, p->kept, p->idx_ld, p->idx_bits / 8)) return I8MP_EINVAL;
+    if (p->teacher_ld > kMaxDim / p->T || p->idx_ld > kMaxDim / p->T) return I8MP_EINVAL;
+  }
+  if (p->lse && !vec_ok(p->lse, p->T)) return I8MP_EINVAL;
+  if (hard && ((p->label_bits != 32 && p->label_bits != 64) || !aligned(p->labels, (uintptr_t)p->label_bits / 8))) return I8MP_EINVAL;
+  a.logits = p->logits, a.teacher = p->teacher, a.idx = p->idx, a.lse = p->lse;
+  a.labels = hard ? p->labels : nullptr;
+  a.T = p->T, a.V = p->V, a.ld = p->ld, a.t_ld = p->teacher_ld, a.i_ld = p->idx_ld;
+  a.ignore = p->ignore_index;
+  a.tau = p->temperature, a.ce = p->ce_weight;
+  const double log2e = 1.4426950408889634074;
+  a.itau = 1.0 / (double)a.tau;
+  a.cd = log2e * a.itau;
+  a.c = (float)a.cd, a.c_lo = (float)(a.cd - (double)a.c);
+  a.c1 = (float)log2e, a.c1_lo = (float)(log2e - (double)a.c1);
+  a.k = p->kept, a.t_dtype = p->teacher_dtype;
+  a.idx64 = p->idx_bits == 64, a.lab64 = p->label_bits == 64;
+  return I8MP_OK;
+}
+
+// Whether the written range w overlaps anything the loss reads.
+bool distill_reads(const i8mp_distill* p, Range w) {
+  const int64_t T = p->T;
+  return overlap(w, mat_range(p->logits, T, p->V, p->ld, dtype_bytes(p->dtype))) ||
+         overlap(w, mat_range(p->teacher, T, p->kept, p->teacher_ld, dtype_bytes(p->teacher_dtype))) ||
+         overlap(w, mat_range(p->idx, T, p->kept, p->idx_ld, p->idx_bits / 8)) || overlap(w, vec_range(p->lse, T, 4)) ||
+         overlap(w, vec_range(p->labels, T, p->label_bits / 8));
+}
+
+i8mp_status distill_run(const i8mp_distill* p, i8mp::DistillArgs& a, void* stream) {
+  const i8mp_status st = device_check();
+  if (st != I8MP_OK) return st;
+  const int elem = (int)dtype_bytes(p->dtype);
+  if (a.d)
+    a.d_aligned = (reinterpret_cast<uintptr_t>(a.d) - reinterpret_cast<uintptr_t>(a.logits)) % 16 == 0 &&
+                  (a.d_ld - a.ld) * elem % 16 == 0;
+  i8mp::distill_plan(a, elem);
+  const hipStream_t s = as_stream(stream);
+  return hip_status(p->dtype == I8MP_BF16   ? i8mp::launch_distill_bf16(a, s)
+                    : p->dtype == I8MP_FP16 ? i8mp::launch_distill_fp16(a, s)
+                                            : i8mp::launch_distill_fp32(a, s));
+}
+
+i8mp_status distill_forward(const i8mp_distill* p, float* loss, double* stats, const float* grad, int64_t grad_s,
+                            void* d, int64_t d_ld, void* ws, size_t ws_bytes, void* stream, bool step) {
+  i8mp::DistillArgs a{};
+  i8mp_status st = distill_inputs(p, a);
+  if (st != I8MP_OK) return st;
+  const int64_t elem = dtype_bytes(p->dtype);
+  if (!vec_ok(loss, p->T) || (stats && !aligned(stats, 8))) return I8MP_EINVAL;
+  const Range rl = vec_range(loss, p->T, 4), rs = vec_range(stats, p->T * I8MP_DISTILL_STATS, 8);
+  Range rd, rg;
+  if (step) {
+    if (!elementwise_ok(d, p->T, p->V, d_ld, elem) || (p->T > 0 && d_ld > kMaxDim / p->T)) return I8MP_EINVAL;
+    if (grad_s < 0 || grad_s >= kMaxDim || (p->T > 0 && (!grad || !aligned(grad, 4) || grad_s > kMaxDim / p->T))) return I8MP_EINVAL;
+    rd = mat_range(d, p->T, p->V, d_ld, elem);
+    rg = p->T > 0 ? vec_range(grad, (p->T - 1) * grad_s + 1, 4) : Range{};
+  }
+  if (p->T == 0) return I8MP_OK;
+  if (p->V == 0) return I8MP_EINVAL;
+  const size_t need = i8mp_distill_workspace_bytes(p->T, p->V, p->kept, p->dtype);
+  if (need && (!ws || !aligned(ws, kAlign) || ws_bytes < need)) return I8MP_EWORKSPACE;
+  const Range rw = need ? vec_range(ws, (int64_t)need, 1) : Range{};
+  const Range out[4] = {rl, rs, rd, rw};
+  for (int i = 0; i < 4; ++i) {
+    if (distill_reads(p, out[i]) || overlap(out[i], rg)) return I8MP_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return I8MP_EINVAL;
+  }
+  a.loss = loss, a.stats = stats, a.grad = grad, a.grad_s = grad_s, a.d = d, a.d_ld = d_ld, a.partial = ws;
+  return distill_run(p, a, stream);
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t i8mp_distill_workspace_bytes(int64_t T, int64_t V, int32_t kept, int32_t dtype) {
+  if (!dims_ok(T, V) || T == 0 || V == 0 || T >= (int64_t(1) << 31) || V > (int64_t(1) << 30) || kept < 0 || !dtype_ok(dtype)) return 0;
+  return up(i8mp::distill_workspace_bytes(T, V, kept, (int)dtype_bytes(dtype)));
+}
+
+i8mp_status i8mp_distill_fwd(const i8mp_distill* p, float* loss, double* stats, void* ws, size_t ws_bytes,
+                             void* stream) {
+  return distill_forward(p, loss, stats, nullptr, 0, nullptr, 0, ws, ws_bytes, stream, false);
+}
+
+i8mp_status i8mp_distill_step(const i8mp_distill* p, const float* grad, int64_t grad_s, float* loss,
+                              void* dlogits, int64_t d_ld, void* ws, size_t ws_bytes, void* stream) {
+  return distill_forward(p, loss, nullptr, grad, grad_s, dlogits, d_ld, ws, ws_bytes, stream, true);
+}
+
+i8mp_status i8mp_distill_bwd(const i8mp_distill* p, const double* stats, const float* grad, int64_t grad_s,
+                             void* dlogits, int64_t d_ld, void* stream) {
+  i8mp::DistillArgs a{};
+  i8mp_status st = distill_inputs(p, a);
+  if (st != I8MP_OK) return st;
+  const int64_t T = p->T, elem = dtype_bytes(p->dtype);
+  if (!elementwise_ok(dlogits, T, p->V, d_ld, elem) || (T > 0 && d_ld > kMaxDim / T)) return I8MP_EINVAL;
+  if (T > 0 && (!stats || !aligned(stats, 8))) return I8MP_EINVAL;
+  if (grad_s < 0 || grad_s >= kMaxDim || (T > 0 && (!grad || !aligned(grad, 4) || grad_s > kMaxDim / T))) return I8MP_EINVAL;
+  if (T == 0) return I8MP_OK;
+  if (p->V == 0) return I8MP_EINVAL;
+  const Range rd = mat_range(dlogits, T, p->V, d_ld, elem);
+  if (distill_reads(p, rd) || overlap(rd, vec_range(grad, (T - 1) * grad_s + 1, 4)) ||
+      overlap(rd, vec_range(stats, T * I8MP_DISTILL_STATS, 8)))
+    return I8MP_EINVAL;
+  a.stats = const_cast<double*>(stats), a.given = 1;
+  a.grad = grad, a.grad_s = grad_s, a.d = dlogits, a.d_ld = d_ld;
+  return distill_run(p, a, stream);
+}
 
 i8mp_status i8mp_rotary(const i8mp_heads* q, const i8mp_heads* k, int64_t B, int64_t S, int32_t D,
                         int32_t rot, int32_t dtype, int32_t pairs, int32_t inverse, const void* pos,

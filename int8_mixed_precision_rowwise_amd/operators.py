@@ -1,8 +1,10 @@
 """Operators around the INT8 mixed-precision linears, bound like the linears.
 
-Rotary positions of query and key heads (``rotary``), with the tensors'
-checks, the current stream and the errors of the package's other calls; every
-step of the computation runs in the library's HIP kernels.  ``training`` holds
+Rotary positions of query and key heads (``rotary``) and the loss of a
+student's logits against a teacher's top logits (``distill_loss``,
+``distill_loss_bwd``, ``distill_loss_and_grad``), with the tensors' checks, the
+current stream and the errors of the package's other calls; every step of the
+computation runs in the library's HIP kernels.  ``training`` holds
 their autograd forms.
 """
 from __future__ import annotations
@@ -14,7 +16,7 @@ import torch
 
 import int8_mixed_precision_rowwise_amd as _pkg
 
-__all__ = ["rotary", "rotary_frequencies"]
+__all__ = ["rotary", "rotary_frequencies", "distill_loss", "distill_loss_bwd", "distill_loss_and_grad"]
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _PAIRS = {"half": 0, "interleaved": 1}
@@ -141,3 +143,149 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, fre
     _call(dev, "i8mp_rotary", hq, hk, B, S, D, rot, _DTYPE[dtype], _PAIRS[pairs], int(inverse), positions.data_ptr(),
           64 if positions.dtype == torch.int64 else 32, pb, ps, freqs.data_ptr())
     return out_q, out_k
+
+
+# --------------------------------------------------------------------------- distillation loss
+
+DISTILL_STATS = 8
+DISTILL_MAX_KEPT = 1024
+
+
+def _ld2(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _rows(t, name: str, dtypes, shape=None):
+    """2-D tensor of one of `dtypes` with adjacent columns (any row stride that spans a row)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: torch.Tensor expected, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {' or '.join(str(d) for d in dtypes)} tensor expected, got {t.dtype}")
+    return _pkg._mat(t, name, t.dtype, shape)
+
+
+def _per_row(t, name: str, dtypes, T: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: torch.Tensor expected, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {' or '.join(str(d) for d in dtypes)} tensor expected, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != T:
+        raise ValueError(f"{name}: 1-D tensor of {T} elements expected, got shape {tuple(t.shape)}")
+
+
+def _distill(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index, grad=None, stats=None,
+             out=None, workspace=None, backward=False):
+    """Checks of the loss's inputs: (the C structure, device, T, V)."""
+    _rows(logits, "logits", tuple(_DTYPE))
+    T, V = logits.shape
+    _rows(teacher, "teacher", tuple(_DTYPE))
+    if teacher.shape[0] != T:
+        raise ValueError(f"teacher: {T} rows expected (logits are {tuple(logits.shape)}), got {tuple(teacher.shape)}")
+    k = teacher.shape[1]
+    _rows(idx, "idx", (torch.int32, torch.int64), (T, k))
+    if k > DISTILL_MAX_KEPT:
+        raise ValueError(f"teacher: at most {DISTILL_MAX_KEPT} kept entries a row, got {k}")
+    if V == 0 and T > 0:
+        raise ValueError("logits: rows without classes")
+    if not (0 < temperature < math.inf):
+        raise ValueError(f"temperature must be positive and finite, got {temperature}")
+    if not math.isfinite(ce_weight):
+        raise ValueError(f"ce_weight must be finite, got {ce_weight}")
+    if teacher_lse is not None:
+        _pkg._vec(teacher_lse, "teacher_lse", T)
+    if labels is not None:
+        _per_row(labels, "labels", (torch.int64, torch.int32), T)
+        if T > 1 and labels.stride(0) != 1:
+            raise ValueError("labels: contiguous tensor expected")
+    elif ce_weight:
+        raise ValueError("ce_weight given without labels")
+    if backward:
+        _per_row(grad, "grad", (torch.float32,), T)
+        if stats is not None:
+            _pkg._mat(stats, "stats", torch.float64, (T, DISTILL_STATS), dense=True)
+        if out is not None:
+            _pkg._mat(out, "out", logits.dtype, (T, V))
+    if workspace is not None:
+        _pkg._workspace(workspace)
+    dev = _pkg._device(logits, teacher, idx, teacher_lse, labels, grad, stats, out, workspace)
+    p = _pkg._Distill(logits.data_ptr(), T, V, _ld2(logits), _DTYPE[logits.dtype], teacher.data_ptr(), _ld2(teacher),
+                      _DTYPE[teacher.dtype], idx.data_ptr(), _ld2(idx), 64 if idx.dtype == torch.int64 else 32, k,
+                      temperature, None if teacher_lse is None else teacher_lse.data_ptr(),
+                      None if labels is None else labels.data_ptr(),
+                      0 if labels is None else 64 if labels.dtype == torch.int64 else 32, ignore_index, ce_weight)
+    return p, dev, T, V
+
+
+def _distill_ws(p, dev, workspace):
+    need = _pkg.lib.i8mp_distill_workspace_bytes(p.T, p.V, p.kept, p.dtype)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+
+
+def _grad_out(logits, out, dev):
+    """Where the gradient goes: rows as far apart as the logits', so that both sides start at the same place in a chunk."""
+    if out is not None:
+        return out
+    T, V = logits.shape
+    ld = _ld2(logits)
+    if ld == V or ld > 2 * V:
+        return torch.empty((T, V), dtype=logits.dtype, device=dev)
+    return torch.empty((T, ld), dtype=logits.dtype, device=dev)[:, :V]
+
+
+def distill_loss(logits: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor, temperature: float = 1.0,
+                 teacher_lse: torch.Tensor | None = None, labels: torch.Tensor | None = None, ce_weight: float = 0.0,
+                 ignore_index: int = -100, workspace: torch.Tensor | None = None):
+    """Loss of each row of a student's logits against a teacher's kept top logits: (loss fp32 [T], stats).
+
+    logits [T, V] (bf16, fp16 or fp32); teacher [T, k] (the same types) the
+    teacher's logits of the classes idx [T, k] (int32 or int64; negative: no
+    entry; distinct within a row; at most 1024).  With q = softmax(logits /
+    temperature) and p the softmax of teacher / temperature over the kept
+    classes, the loss is temperature^2 KL(p || q).  teacher_lse (fp32 [T], the
+    log-sum-exp of all the teacher's logits / temperature) makes p the
+    teacher's own probabilities and the classes not kept one more class.
+    labels ([T], int64 or int32) with ce_weight add ce_weight times the cross
+    entropy; rows labelled ignore_index (or outside the classes) add none, and
+    rows without kept entries have no other part.  stats: float64 [T, 8], what
+    distill_loss_bwd needs."""
+    p, dev, T, _ = _distill(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index, workspace=workspace)
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    stats = torch.empty((T, DISTILL_STATS), dtype=torch.float64, device=dev)
+    ws, n = _distill_ws(p, dev, workspace)
+    _call(dev, "i8mp_distill_fwd", p, loss.data_ptr(), stats.data_ptr(), ws, n)
+    return loss, stats
+
+
+def distill_loss_bwd(logits: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor, stats: torch.Tensor,
+                     grad: torch.Tensor, temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                     labels: torch.Tensor | None = None, ce_weight: float = 0.0, ignore_index: int = -100,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of sum(grad * loss) at the logits, in their type, from distill_loss's stats.
+
+    grad: fp32 [T], any stride (an expanded scalar too); the other arguments as
+    in the forward."""
+    if not isinstance(stats, torch.Tensor):
+        raise TypeError(f"stats: torch.Tensor expected, got {type(stats).__name__}")
+    p, dev, T, V = _distill(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index, grad, stats, out,
+                            backward=True)
+    d = _grad_out(logits, out, dev)
+    _call(dev, "i8mp_distill_bwd", p, stats.data_ptr(), grad.data_ptr(), grad.stride(0), d.data_ptr(), _ld2(d))
+    return d
+
+
+def distill_loss_and_grad(logits: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor, grad: torch.Tensor,
+                          temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                          labels: torch.Tensor | None = None, ce_weight: float = 0.0, ignore_index: int = -100,
+                          out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """distill_loss and the gradient of sum(grad * loss) at the logits with one
+    read of them: (loss, dlogits).  For training, where the rows' weights (1 / T
+    for a mean) are known before the loss is."""
+    p, dev, T, V = _distill(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index, grad, None, out,
+                            workspace, backward=True)
+    d = _grad_out(logits, out, dev)
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    ws, n = _distill_ws(p, dev, workspace)
+    _call(dev, "i8mp_distill_step", p, grad.data_ptr(), grad.stride(0), loss.data_ptr(), d.data_ptr(), _ld2(d), ws, n)
+    return loss, d

@@ -47,7 +47,7 @@ from . import operators as _ops
 
 __all__ = ["Int8MixedPrecisionConfig", "Int8MixedPrecisionLinearFunction",
            "Int8MixedPrecisionLinear", "swap_linear_modules", "STEP_STRIDE", "STEPS_PER_KEY",
-           "module_seed", "step_key_offset", "sr_checkpoint_contexts", "RotaryFunction", "rotary"]
+           "module_seed", "step_key_offset", "sr_checkpoint_contexts", "RotaryFunction", "rotary", "DistillFunction", "distill_loss"]
 
 STEP_STRIDE = 8 << 40  # Philox blocks reserved per linear step (6 passes of 2**40 each, rounded up)
 STEPS_PER_KEY = (1 << 64) // STEP_STRIDE  # steps whose offsets fit the 64-bit block counter
@@ -320,3 +320,29 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, 
            pairs: str = "half"):
     """operators.rotary with a gradient: (q', k')."""
     return RotaryFunction.apply(q, k, positions, freqs, pairs)
+
+
+class DistillFunction(torch.autograd.Function):
+    """Rows' losses against a teacher's kept logits (operators.distill_loss);
+    the backward reads the logits again with the forward's statistics."""
+
+    @staticmethod
+    def forward(ctx, logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index):
+        loss, stats = _ops.distill_loss(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index)
+        ctx.save_for_backward(logits, teacher, idx, teacher_lse, labels, stats)
+        ctx.args = temperature, ce_weight, ignore_index
+        return loss
+
+    @staticmethod
+    def backward(ctx, grad):
+        logits, teacher, idx, lse, labels, stats = ctx.saved_tensors
+        temperature, ce, ignore = ctx.args
+        d = _ops.distill_loss_bwd(logits, teacher, idx, stats, grad, temperature, lse, labels, ce, ignore)
+        return d, None, None, None, None, None, None, None
+
+
+def distill_loss(logits: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor, temperature: float = 1.0,
+                 teacher_lse: Optional[torch.Tensor] = None, labels: Optional[torch.Tensor] = None,
+                 ce_weight: float = 0.0, ignore_index: int = -100) -> torch.Tensor:
+    """operators.distill_loss with a gradient at the logits: loss fp32 [T]."""
+    return DistillFunction.apply(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index)

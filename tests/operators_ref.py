@@ -38,3 +38,51 @@ def rotary_scale(x, freqs, pairs):
     first, second = (slice(0, r // 2), slice(r // 2, r)) if pairs == "half" else (slice(0, r, 2), slice(1, r, 2))
     out[..., first] = out[..., second] = x[..., first] + x[..., second]
     return out
+
+
+def distill(logits, teacher, idx, temperature, lse=None, labels=None, ce=0.0, ignore=-100, grad=None):
+    """(loss, gradient or None, scale) in 64 bits; scale: what the gradient's
+    terms add up to before they cancel."""
+    x, t = logits.detach().to("cpu", F64), teacher.detach().to("cpu", F64) / temperature
+    idx = idx.cpu().long()
+    T, V = x.shape
+    loss, d, scale = torch.zeros(T, dtype=F64), torch.zeros(T, V, dtype=F64), torch.zeros(T, V, dtype=F64)
+    for r in range(T):
+        ok = (idx[r] >= 0) & (idx[r] < V)
+        at = idx[r][ok]
+        logq = torch.log_softmax(x[r] / temperature, 0)
+        if at.numel():
+            p = torch.exp(t[r][ok] - float(lse[r])) if lse is not None else torch.softmax(t[r][ok], 0)
+            target = torch.zeros(V, dtype=F64)
+            target[at] = p
+            kl = torch.special.xlogy(p, p).sum() - torch.where(p > 0, p * logq[at], 0.0).sum()
+            factor = torch.full((V,), float(p.sum()), dtype=F64)
+            if lse is not None:
+                left = max(0.0, 1.0 - float(p.sum()))
+                away = torch.ones(V, dtype=torch.bool)
+                away[at] = False
+                factor += left
+                if left > 0:
+                    log_left = torch.logsumexp(logq[away], 0)
+                    kl = kl + left * (math.log(left) - log_left)
+                    factor[away] -= left / torch.exp(log_left)
+            else:
+                factor[:] = 1.0
+            loss[r] = temperature ** 2 * kl
+            q = logq.exp()
+            d[r] = temperature * (factor * q - target)
+            scale[r] = temperature * (factor.abs() * q + target)
+            if lse is not None and left > 0:
+                scale[r][away] = temperature * (1.0 + left / torch.exp(log_left)) * q[away]
+        lab = int(labels[r]) if labels is not None else ignore
+        if ce and lab != ignore and 0 <= lab < V:
+            logp = torch.log_softmax(x[r], 0)
+            loss[r] -= ce * logp[lab]
+            hot = torch.zeros(V, dtype=F64)
+            hot[lab] = 1.0
+            d[r] += ce * (logp.exp() - hot)
+            scale[r] += abs(ce) * (logp.exp() + hot)
+    if grad is None:
+        return loss, None, None
+    g = grad.detach().to("cpu", F64)[:, None]
+    return loss, d * g, scale * g.abs()

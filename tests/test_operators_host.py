@@ -134,3 +134,120 @@ def test_rotary_frequencies():
                 dict(rot=8, original_length=10, low=4.0, high=1.0)):
         with pytest.raises(ValueError):
             i8.rotary_frequencies(**bad)
+
+
+# ------------------------------------------------------------------ distillation loss
+
+
+def test_distill_binding_checks(lib):
+    x, te, ix, g, st = t(4, 30), t(4, 5), t(4, 5, dtype=i32), t(4, dtype=f32), t(4, 8, dtype=f64)
+    with pytest.raises(ValueError, match="device tensors"):
+        i8.distill_loss_and_grad(x, te, ix, g)  # right but for the device
+    with pytest.raises(TypeError, match="logits"):
+        i8.distill_loss(x.double(), te, ix)
+    with pytest.raises(ValueError, match="logits: 2-D"):
+        i8.distill_loss(x[0], te, ix)
+    with pytest.raises(ValueError, match="logits: columns"):
+        i8.distill_loss(t(30, 4).t(), te, ix)
+    with pytest.raises(ValueError, match="classes"):
+        i8.distill_loss(t(4, 0), te, ix)
+    with pytest.raises(ValueError, match="teacher: 4 rows"):
+        i8.distill_loss(x, t(3, 5), ix)
+    with pytest.raises(TypeError, match="idx"):
+        i8.distill_loss(x, te, ix.float())
+    with pytest.raises(ValueError, match="idx: shape"):
+        i8.distill_loss(x, te, t(4, 6, dtype=i32))
+    with pytest.raises(ValueError, match="1024"):
+        i8.distill_loss(x, t(4, 1025), t(4, 1025, dtype=i32))
+    for tau in (0.0, -1.0, math.inf, math.nan):
+        with pytest.raises(ValueError, match="temperature"):
+            i8.distill_loss(x, te, ix, temperature=tau)
+    with pytest.raises(ValueError, match="ce_weight"):
+        i8.distill_loss(x, te, ix, ce_weight=math.nan)
+    with pytest.raises(ValueError, match="without labels"):
+        i8.distill_loss(x, te, ix, ce_weight=0.5)
+    with pytest.raises(TypeError, match="labels"):
+        i8.distill_loss(x, te, ix, labels=g, ce_weight=0.5)
+    with pytest.raises(ValueError, match="labels"):
+        i8.distill_loss(x, te, ix, labels=t(3, dtype=i64), ce_weight=0.5)
+    with pytest.raises(TypeError, match="teacher_lse"):
+        i8.distill_loss(x, te, ix, teacher_lse=g.double())
+    with pytest.raises(TypeError, match="grad"):
+        i8.distill_loss_and_grad(x, te, ix, g.double())
+    with pytest.raises(TypeError, match="grad"):
+        i8.distill_loss_and_grad(x, te, ix, None)
+    with pytest.raises(ValueError, match="grad"):
+        i8.distill_loss_bwd(x, te, ix, st, t(5, dtype=f32))
+    with pytest.raises(ValueError, match="stats"):
+        i8.distill_loss_bwd(x, te, ix, t(4, 7, dtype=f64), g)
+    with pytest.raises(TypeError, match="stats"):
+        i8.distill_loss_bwd(x, te, ix, None, g)
+    with pytest.raises(ValueError, match="out"):
+        i8.distill_loss_bwd(x, te, ix, st, g, out=t(4, 31))
+    with pytest.raises(TypeError, match="workspace"):
+        i8.distill_loss(x, te, ix, workspace=g)
+
+
+def _dist(call="step", grad=1 << 33, grad_s=1, loss=1 << 34, d=1 << 35, d_ld=130, stats=1 << 36, ws=1 << 37, n=1 << 20, **over):
+    a = dict(logits=1 << 20, T=300, V=130, ld=130, dtype=0, teacher=1 << 30, teacher_ld=5, teacher_dtype=0, idx=1 << 31,
+             idx_ld=5, idx_bits=32, kept=5, temperature=1.0, lse=None, labels=None, label_bits=0, ignore_index=-100, ce_weight=0.0)
+    p = i8._Distill(**{**a, **over})
+    if call == "step":
+        return L.i8mp_distill_step(p, grad, grad_s, loss, d, d_ld, ws, n, None)
+    if call == "fwd":
+        return L.i8mp_distill_fwd(p, loss, stats, ws, n, None)
+    return L.i8mp_distill_bwd(p, stats, grad, grad_s, d, d_ld, None)
+
+
+def test_distill_abi_validation():
+    for call in ("step", "fwd", "bwd"):
+        assert accepted(lambda: _dist(call))
+        assert accepted(lambda: _dist(call, logits=(1 << 20) + 2, ld=133, d_ld=137))  # any alignment of elements
+        for bad in (dict(dtype=3), dict(teacher_dtype=-1), dict(T=-1), dict(T=1 << 31), dict(V=0), dict(V=(1 << 30) + 1, ld=1 << 31),
+                    dict(ld=129), dict(logits=None), dict(logits=(1 << 20) + 1), dict(kept=-1), dict(kept=1025), dict(teacher=None),
+                    dict(teacher_ld=4), dict(idx=None), dict(idx_ld=4), dict(idx_bits=16), dict(idx=(1 << 31) + 2),
+                    dict(temperature=0.0), dict(temperature=math.nan), dict(ce_weight=math.inf), dict(lse=3),
+                    dict(labels=1 << 32, ce_weight=1.0, label_bits=8), dict(labels=(1 << 32) + 4, ce_weight=1.0, label_bits=64)):
+            assert _dist(call, **bad) == EINVAL, (call, bad)
+        assert _dist(call, T=0, logits=None, teacher=None, idx=None) == 0  # nothing to do
+        assert accepted(lambda: _dist(call, kept=0, teacher=None, idx=None))
+    for call in ("step", "bwd"):
+        for bad in (dict(d=None), dict(d=1 << 20), dict(d=(1 << 20) + 260), dict(d=(1 << 35) + 1), dict(d_ld=129), dict(grad=None),
+                    dict(grad=(1 << 33) + 2), dict(grad_s=-1), dict(grad=1 << 35), dict(d=1 << 30), dict(d=1 << 31)):
+            assert _dist(call, **bad) == EINVAL, (call, bad)
+        assert accepted(lambda: _dist(call, grad_s=0))
+    for bad in (dict(loss=None), dict(loss=1 << 35), dict(loss=1 << 20)):
+        assert _dist("step", **bad) == EINVAL, bad
+    for bad in (dict(stats=4), dict(stats=1 << 34)):
+        assert _dist("fwd", **bad) == EINVAL, bad
+    assert accepted(lambda: _dist("fwd", stats=None))
+    assert _dist("bwd", stats=None) == EINVAL and _dist("bwd", stats=1 << 35) == EINVAL
+    # a few long rows are split: they need a workspace
+    long = dict(T=2, V=40000, ld=40000, d_ld=40000)
+    need = L.i8mp_distill_workspace_bytes(2, 40000, 5, 0)
+    assert need > 0 and need % 256 == 0
+    for call in ("step", "fwd"):
+        assert _dist(call, ws=None, **long) == EWORKSPACE
+        assert _dist(call, ws=(1 << 37) + 8, **long) == EWORKSPACE
+        assert _dist(call, n=need - 1, **long) == EWORKSPACE
+        assert accepted(lambda: _dist(call, n=need, **long))
+        assert _dist(call, ws=1 << 34, **long) == EINVAL
+    assert L.i8mp_distill_workspace_bytes(-1, 5, 5, 0) == 0 and L.i8mp_distill_workspace_bytes(5, 5, 5, 9) == 0
+
+
+def test_distill_reference_gradient_is_the_derivative():
+    from tests import operators_ref as ref
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(6, 40, generator=g, dtype=f64)
+    te = torch.randn(6, 7, generator=g, dtype=f64)
+    ix = torch.stack([torch.randperm(40, generator=g)[:7] for _ in range(6)])
+    ix[1, 3:] = -1
+    ix[2] = -1
+    lab = torch.tensor([0, 5, -100, 7, int(ix[4, 2]), 39])
+    for tau, rest, ce in ((1.0, False, 0.0), (2.0, True, 0.5), (1.5, False, 1.0)):
+        lse = torch.logsumexp(te / tau, 1) + 0.1 if rest else None
+        _, d, _ = ref.distill(x, te, ix, tau, lse, lab, ce, grad=torch.ones(6))
+        v = torch.randn(6, 40, generator=g, dtype=f64)
+        h = 1e-5
+        up, down = (ref.distill(x + s * h * v, te, ix, tau, lse, lab, ce)[0] for s in (1, -1))
+        assert torch.allclose((up - down) / (2 * h), (d * v).sum(1), rtol=1e-7, atol=1e-8)

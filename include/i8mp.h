@@ -403,6 +403,79 @@ i8mp_status i8mp_rotary(const i8mp_heads* q, const i8mp_heads* k, int64_t B, int
                         void* stream);
 
 /*
+ * A linear layer with bias, activation and residual in its GEMM's epilogue:
+ *   z = X @ W.T + bias,  Y = act(z) + residual
+ * X and W quantized row-wise over K as in i8mp_linear_fwd; z, the activation
+ * and the sum are fp32, Y and Z (z kept for the backward; NULL: not) are rounded
+ * once.  GELU is z Phi(z); GELU_TANH z (1 + tanh(sqrt(2 / pi)(z + 0.044715 z^3))) / 2;
+ * SILU z / (1 + exp(-z)).
+ *   bias: bf16 [N] or NULL; residual: bf16 [M x N] or NULL
+ *   Y, Z: bf16 [M x N], any alignment of elements (rows of 16-byte aligned starts
+ *     leave in whole 16-byte stores)
+ */
+typedef enum {
+  I8MP_ACT_NONE = 0, I8MP_ACT_RELU = 1, I8MP_ACT_GELU = 2, I8MP_ACT_GELU_TANH = 3, I8MP_ACT_SILU = 4
+} i8mp_activation;
+typedef struct {
+  int64_t M, N, K;
+  const uint16_t* X;
+  int64_t ldx;
+  const uint16_t* W;
+  int64_t ldw;
+  int32_t activation;
+  const uint16_t* bias;
+  const uint16_t* residual;
+  int64_t ld_residual;
+  uint16_t* Y;
+  int64_t ldy;
+  uint16_t* Z;
+  int64_t ldz;
+} i8mp_linear_act;
+/* Bytes of workspace of the forward (backward = 0) or the backward (1). */
+size_t i8mp_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward);
+/* colmax_x, colmax_w: as in i8mp_linear_fwd_colmax (either may be NULL). */
+i8mp_status i8mp_linear_act_fwd(const i8mp_linear_act* p, const i8mp_linear_opts* opts, float* colmax_x,
+                                float* colmax_w, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The same forward over weights quantized once (serving): Wq int8 [N x K] codes
+ * with scales w_scale [N], for instance from i8mp_quantize_rowwise; p->W and
+ * p->ldw are not read.  X is quantized to nearest.  Up to 64 rows take a kernel
+ * for few tokens.
+ */
+size_t i8mp_linear_wq_workspace_bytes(int64_t M, int64_t N, int64_t K);
+i8mp_status i8mp_linear_wq_fwd(const i8mp_linear_act* p, const int8_t* Wq, int64_t ldwq, const float* w_scale,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward of i8mp_linear_act_fwd (the residual's gradient is dY itself): with
+ * g = dY act'(Z) in fp32 and dZ = bf16(g),
+ *   dX = dZ @ W, dW = dZ.T @ X (quantized and scaled as in i8mp_linear_bwd),
+ *   dbias = column sums of g (fp32 [N], added in a fixed order).
+ * Any of dX, dW, dbias may be NULL.  Z (bf16 [M x N]) is not read without an
+ * activation.  colmax_x, colmax_w: from the forward, or NULL.
+ */
+typedef struct {
+  int64_t M, N, K;
+  const uint16_t* dY;
+  int64_t lddy;
+  const uint16_t* Z;
+  int64_t ldz;
+  const uint16_t* X;
+  int64_t ldx;
+  const uint16_t* W;
+  int64_t ldw;
+  int32_t activation;
+  uint16_t* dX;
+  int64_t lddx;
+  uint16_t* dW;
+  int64_t lddw;
+  float* dbias;
+} i8mp_linear_act_grad;
+i8mp_status i8mp_linear_act_bwd(const i8mp_linear_act_grad* p, const i8mp_linear_opts* opts, const float* colmax_x,
+                                const float* colmax_w, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Loss of a student's logits x [T x V] against a teacher's kept top logits.
  * Row r keeps the classes idx[r][j] (j < kept; negative or >= V: no entry; the
  * others distinct) with the teacher's logits teacher[r][j].  With temperature

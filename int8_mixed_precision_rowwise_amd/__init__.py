@@ -28,6 +28,8 @@ __all__ = [
     "linear_fwd_fp8_colmax",
     "quantize_colwise_noalloc", "STATIC_SCRATCH_BYTES", "mfma_rate_probe", "EXPORTED_SYMBOLS",
     "rotary", "rotary_frequencies", "distill_loss", "distill_loss_bwd", "distill_loss_and_grad",
+    "linear_act_fwd", "linear_act_fwd_train", "linear_act_bwd", "linear_wq_fwd", "linear_act_workspace_bytes",
+    "linear_wq_workspace_bytes", "ACTIVATIONS",
 ]
 
 RNE, SR = 0, 1
@@ -48,6 +50,8 @@ EXPORTED_SYMBOLS = (
     "i8mp_linear_fwd_fp8_colmax", "i8mp_linear_bwd_fp8_colmax",
     "i8mp_quantize_colwise_noalloc", "i8mp_mfma_rate_probe",
     "i8mp_rotary", "i8mp_distill_workspace_bytes", "i8mp_distill_fwd", "i8mp_distill_bwd", "i8mp_distill_step",
+    "i8mp_linear_act_workspace_bytes", "i8mp_linear_act_fwd", "i8mp_linear_wq_workspace_bytes", "i8mp_linear_wq_fwd",
+    "i8mp_linear_act_bwd",
 )
 
 
@@ -73,6 +77,21 @@ class _Distill(ctypes.Structure):
                 ("idx_bits", ctypes.c_int32), ("kept", ctypes.c_int32), ("temperature", ctypes.c_float),
                 ("lse", ctypes.c_void_p), ("labels", ctypes.c_void_p), ("label_bits", ctypes.c_int32),
                 ("ignore_index", ctypes.c_int64), ("ce_weight", ctypes.c_float)]
+
+
+class _LinearAct(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("X", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("W", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("activation", ctypes.c_int32),
+                ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("Z", ctypes.c_void_p), ("ldz", ctypes.c_int64)]
+
+
+class _LinearActGrad(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("dY", ctypes.c_void_p),
+                ("lddy", ctypes.c_int64), ("Z", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("X", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("W", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("activation", ctypes.c_int32),
+                ("dX", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dW", ctypes.c_void_p), ("lddw", ctypes.c_int64),
+                ("dbias", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -113,6 +132,11 @@ def _load() -> ctypes.CDLL:
         "i8mp_mfma_rate_probe": ([p, i64, i64, p, p], i32),
         "i8mp_rotary": ([ctypes.POINTER(_Heads), ctypes.POINTER(_Heads), i64, i64, i32, i32, i32, i32, i32, p, i32,
                          i64, i64, p, p], i32),
+        "i8mp_linear_act_workspace_bytes": ([i64, i64, i64, i32], sz),
+        "i8mp_linear_act_fwd": ([ctypes.POINTER(_LinearAct), ctypes.POINTER(_Opts), p, p, p, sz, p], i32),
+        "i8mp_linear_wq_workspace_bytes": ([i64, i64, i64], sz),
+        "i8mp_linear_wq_fwd": ([ctypes.POINTER(_LinearAct), p, i64, p, p, sz, p], i32),
+        "i8mp_linear_act_bwd": ([ctypes.POINTER(_LinearActGrad), ctypes.POINTER(_Opts), p, p, p, sz, p], i32),
         "i8mp_distill_workspace_bytes": ([i64, i64, i32, i32], sz),
         "i8mp_distill_fwd": ([ctypes.POINTER(_Distill), p, p, p, sz, p], i32),
         "i8mp_distill_bwd": ([ctypes.POINTER(_Distill), p, p, i64, p, i64, p], i32),
@@ -686,5 +710,6 @@ def linear_bwd_fp8(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, want_dx: 
 
 # --------------------------------------------------------------------------- operators around the linears
 
-from .operators import (distill_loss, distill_loss_and_grad, distill_loss_bwd, rotary,  # noqa: E402
-                        rotary_frequencies)
+from .operators import (ACTIVATIONS, distill_loss, distill_loss_and_grad, distill_loss_bwd,  # noqa: E402
+                        linear_act_bwd, linear_act_fwd, linear_act_fwd_train, linear_act_workspace_bytes, linear_wq_fwd,
+                        linear_wq_workspace_bytes, rotary, rotary_frequencies)

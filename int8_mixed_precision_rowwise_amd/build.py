@@ -22,8 +22,10 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB_PATH = os.path.join(HERE, "libi8mp.so")
 SOURCES = ["i8mp_api.cpp", "operators_api.cpp", "quantize.hip", "gemm.hip", "rotary.hip",
-           "distill_bf16.hip", "distill_fp16.hip", "distill_fp32.hip"]
-HEADERS = ["internal.h", "checks.h", "philox.h", "distill.h", os.path.join("..", "..", "include", "i8mp.h")]
+           "distill_bf16.hip", "distill_fp16.hip", "distill_fp32.hip", "linear_act.hip", "linear_act_bwd.hip",
+           "skinny.hip"]
+HEADERS = ["internal.h", "checks.h", "philox.h", "distill.h", "quant_device.h", "gemm_pipelined.h", "activation.h",
+           os.path.join("..", "..", "include", "i8mp.h")]
 
 HIP_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -182,6 +182,54 @@ hipError_t launch_rotary(const RotaryTensor& q, const RotaryTensor& k, int64_t B
                          bool half, bool inverse, const void* pos, int pos32, int64_t pos_b, int64_t pos_s,
                          const double* freqs, hipStream_t stream);
 
+// What a linear's GEMM does to z = acc * sa * sb + bias before it stores
+// act(z) + residual (activations: i8mp_activation).
+struct Epilogue {
+  int act;
+  const uint16_t* bias;      // bf16 [N], or null
+  const uint16_t* residual;  // bf16 [M x N] in 16-byte aligned rows, or null
+  int64_t ld_residual;
+  uint16_t* z;               // where z is kept (bf16 [M x N]), or null
+  int64_t ld_z;
+};
+// NT INT8 GEMM with that epilogue.  K > 0 is a multiple of 16; where a
+// contraction was padded to one, A's padding holds zeros (launch_zero_padding:
+// bytes [cols, ld) of each row).  ws: gemm_split_workspace_bytes(0, ...), or null
+// when that is 0; side as in launch_gemm_split.
+hipError_t launch_zero_padding(int8_t* q, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream);
+hipError_t launch_gemm_epilogue(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* sa,
+                                const int8_t* B, int64_t ldb, const float* sb, uint16_t* C, int64_t ldc, const Epilogue& e,
+                                void* ws, const ColmaxJob* side, hipStream_t stream);
+// The int32 partial planes alone of an NT contraction that gemm_split_workspace_bytes splits.
+hipError_t launch_gemm_partials(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* B,
+                                int64_t ldb, void* P, const ColmaxJob* side, hipStream_t stream);
+
+// The same product and epilogue for at most kSkinnyRows rows of A (any K;
+// nothing has to be padded).
+constexpr int64_t kSkinnyRows = 64;
+hipError_t launch_skinny(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* sa, const int8_t* B,
+                         int64_t ldb, const float* sb, uint16_t* C, int64_t ldc, const Epilogue& e, hipStream_t stream);
+
+// dZ = dY act'(Z) of a backward, its codes along rows and down columns (either
+// may be null) with their scales, and the column sums of the unrounded values.
+struct ActBwdArgs {
+  const uint16_t *dY, *Z;
+  uint16_t* dZ;  // rows of a multiple of 8 elements; dY itself without an activation
+  int64_t lddy, ldz, lddz, M, N;
+  int64_t np, mp;  // N and M padded to 16: pitch of the codes, rows of the column codes (padding is zero)
+  int8_t *row_codes, *col_codes;
+  float *row_scale, *col_scale, *dbias;
+  uint16_t *segmax, *band_max;
+  float* band_sum;
+  uint64_t seed, row_offset, col_offset;
+  int64_t rows_per_band, rows_per_block;
+  int tiles, bands;
+};
+void act_bwd_plan(ActBwdArgs& a);  // np, mp and the launch shapes from M and N
+size_t act_bwd_segmax_bytes(const ActBwdArgs& a);
+size_t act_bwd_band_elems(const ActBwdArgs& a);  // of band_max and of band_sum
+hipError_t launch_act_bwd(const ActBwdArgs& a, int act, int round, hipStream_t stream);
+
 // Distillation from a teacher's top logits; see i8mp_distill_*.
 constexpr int kDistillMaxKept = I8MP_DISTILL_MAX_KEPT;
 // A row in one workgroup's registers (threads x 16-byte chunks a thread), or

@@ -110,6 +110,112 @@ bool heads_disjoint(const HeadsView& a, const HeadsView& c, int64_t B, int64_t S
   return off >= lo_ext && (B * S == 1 || off + hi_ext <= period);
 }
 
+bool act_ok(int32_t act) { return act >= I8MP_ACT_NONE && act <= I8MP_ACT_SILU; }
+uint64_t pass_offset(uint64_t offset, int j) { return offset + ((uint64_t)j << 40); }
+bool opts_ok(const i8mp_linear_opts* o) { return o && (o->round == I8MP_RNE || o->round == I8MP_SR); }
+// Sizes whose buffers' byte counts stay far from overflow.
+bool linear_dims_ok(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kArea = int64_t(1) << 50;
+  const int64_t m = M + 16, n = N + 16, k = K + 16;
+  return dims_ok(M, N, K) && m <= kArea / n && m <= kArea / k && n <= kArea / k;
+}
+
+// The contraction a GEMM runs over: padded to whole 16-byte chunks.
+int64_t padded_k(int64_t K) { return K > 0 ? pad16(K) : 16; }
+
+struct ActFwdWs {
+  int8_t *qx, *qw;
+  float *sx, *sw;
+  void *part_x, *part_w, *split;
+};
+size_t carve_act_fwd(void* ws, int64_t M, int64_t N, int64_t K, bool weights, ActFwdWs* out) {
+  Carver c{static_cast<char*>(ws)};
+  const int64_t kp = padded_k(K);
+  ActFwdWs w{};
+  w.qx = static_cast<int8_t*>(c.take((size_t)(M * kp)));
+  w.sx = static_cast<float*>(c.take((size_t)M * 4));
+  if (weights) {
+    w.qw = static_cast<int8_t*>(c.take((size_t)(N * kp)));
+    w.sw = static_cast<float*>(c.take((size_t)N * 4));
+    w.part_x = c.take(i8mp::rowwise_colmax_workspace_bytes(M, K));
+    w.part_w = c.take(i8mp::rowwise_colmax_workspace_bytes(N, K));
+  }
+  const size_t split = i8mp::gemm_split_workspace_bytes(I8MP_NT, M, N, kp, kp, kp);
+  w.split = split ? c.take(split) : nullptr;
+  if (out) *out = w;
+  return c.used;
+}
+
+struct ActBwdWs {
+  uint16_t* dz;
+  int8_t *q_row, *q_col, *qw, *qx;
+  float *s_row, *s_col, *sw, *sx, *band_sum;
+  uint16_t *segmax, *band_max;
+  void *col, *split;
+};
+size_t carve_act_bwd(void* ws, int64_t M, int64_t N, int64_t K, ActBwdWs* out) {
+  Carver c{static_cast<char*>(ws)};
+  i8mp::ActBwdArgs a{};
+  a.M = M, a.N = N;
+  i8mp::act_bwd_plan(a);
+  const int64_t kp = pad16(K);
+  ActBwdWs w{};
+  w.dz = static_cast<uint16_t*>(c.take((size_t)(M * a.np) * 2));
+  w.q_row = static_cast<int8_t*>(c.take((size_t)(M * a.np)));
+  w.q_col = static_cast<int8_t*>(c.take((size_t)(a.mp * a.np)));
+  w.qw = static_cast<int8_t*>(c.take((size_t)(a.np * kp)));
+  w.qx = static_cast<int8_t*>(c.take((size_t)(a.mp * kp)));
+  w.s_row = static_cast<float*>(c.take((size_t)M * 4));
+  w.s_col = static_cast<float*>(c.take((size_t)N * 4));
+  w.sw = static_cast<float*>(c.take((size_t)K * 4));
+  w.sx = static_cast<float*>(c.take((size_t)K * 4));
+  w.segmax = static_cast<uint16_t*>(c.take(i8mp::act_bwd_segmax_bytes(a)));
+  w.band_max = static_cast<uint16_t*>(c.take(i8mp::act_bwd_band_elems(a) * 2));
+  w.band_sum = static_cast<float*>(c.take(i8mp::act_bwd_band_elems(a) * 4));
+  w.col = c.take(std::max(i8mp::colwise_workspace_bytes(N, K), i8mp::colwise_workspace_bytes(M, K)));
+  const size_t split = std::max(i8mp::gemm_split_workspace_bytes(I8MP_NN, M, K, a.np, a.np, kp),
+                                i8mp::gemm_split_workspace_bytes(I8MP_TN, N, K, a.mp, a.np, kp));
+  w.split = split ? c.take(split) : nullptr;
+  if (out) *out = w;
+  return c.used;
+}
+
+// Checks of a forward's X, epilogue and outputs; its ranges for the overlap checks.
+i8mp_status act_fwd_checks(const i8mp_linear_act* p, Range (&out)[2], Range (&in)[3]) {
+  if (!p || !act_ok(p->activation) || !linear_dims_ok(p->M, p->N, p->K)) return I8MP_EINVAL;
+  const int64_t M = p->M, N = p->N, K = p->K;
+  if (K > I8MP_MAX_CONTRACTION) return I8MP_ERANGE;
+  if (!chunked_ok(p->X, M, K, p->ldx, 2) || !elementwise_ok(p->Y, M, N, p->ldy, 2)) return I8MP_EINVAL;
+  if (p->residual && !chunked_ok(p->residual, M, N, p->ld_residual, 2)) return I8MP_EINVAL;
+  if (p->Z && !elementwise_ok(p->Z, M, N, p->ldz, 2)) return I8MP_EINVAL;
+  if (p->bias && !aligned(p->bias, 2)) return I8MP_EINVAL;
+  for (int64_t ld : {p->ldx, p->ldy, p->residual ? p->ld_residual : 0, p->Z ? p->ldz : 0})
+    if (M > 0 && ld > kMaxDim / M) return I8MP_EINVAL;
+  out[0] = mat_range(p->Y, M, N, p->ldy, 2);
+  out[1] = mat_range(p->Z, M, N, p->ldz, 2);
+  in[0] = mat_range(p->X, M, K, p->ldx, 2);
+  in[1] = mat_range(p->residual, M, N, p->ld_residual, 2);
+  in[2] = vec_range(p->bias, N, 2);
+  return I8MP_OK;
+}
+
+i8mp::Epilogue epilogue_of(const i8mp_linear_act* p) {
+  return {p->activation, p->bias, p->residual, p->ld_residual, p->Z, p->ldz};
+}
+
+// Codes of X (rounded as asked) times codes of W, with the epilogue.
+hipError_t act_product(const i8mp_linear_act* p, int8_t* qx, const float* sx, const int8_t* qw, int64_t ldqw,
+                       const float* sw, void* split, i8mp::ColmaxJob* side, hipStream_t s) {
+  const int64_t M = p->M, N = p->N, K = p->K, kp = padded_k(K);
+  if (M <= i8mp::kSkinnyRows) {
+    const hipError_t e = side ? i8mp::launch_colmax_finalize(*side, s) : hipSuccess;
+    return e != hipSuccess ? e : i8mp::launch_skinny(M, N, K, qx, kp, sx, qw, ldqw, sw, p->Y, p->ldy, epilogue_of(p), s);
+  }
+  const hipError_t e = i8mp::launch_zero_padding(qx, M, K, kp, s);
+  if (e != hipSuccess) return e;
+  return i8mp::launch_gemm_epilogue(M, N, kp, qx, kp, sx, qw, ldqw, sw, p->Y, p->ldy, epilogue_of(p), split, side, s);
+}
+
 // Checks of the loss's inputs; fills `a` (not its outputs).
 i8mp_status distill_inputs(const i8mp_distill* p, i8mp::DistillArgs& a) {
   if (!p || !dtype_ok(p->dtype) || !dtype_ok(p->teacher_dtype)) return I8MP_EINVAL;
@@ -199,6 +305,177 @@ i8mp_status distill_forward(const i8mp_distill* p, float* loss, double* stats, c
 }  // namespace
 
 extern "C" {
+
+size_t i8mp_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward) {
+  if (!linear_dims_ok(M, N, K)) return 0;
+  return backward ? carve_act_bwd(nullptr, M, N, K, nullptr) : carve_act_fwd(nullptr, M, N, K, true, nullptr);
+}
+
+size_t i8mp_linear_wq_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return linear_dims_ok(M, N, K) ? carve_act_fwd(nullptr, M, N, K, false, nullptr) : 0;
+}
+
+i8mp_status i8mp_linear_act_fwd(const i8mp_linear_act* p, const i8mp_linear_opts* opts, float* colmax_x,
+                                float* colmax_w, void* ws, size_t ws_bytes, void* stream) {
+  Range out[4], in[4], o2[2], i3[3];
+  if (!opts_ok(opts)) return I8MP_EINVAL;
+  i8mp_status st = act_fwd_checks(p, o2, i3);
+  if (st != I8MP_OK) return st;
+  const int64_t M = p->M, N = p->N, K = p->K;
+  if (!chunked_ok(p->W, N, K, p->ldw, 2) || (N > 0 && p->ldw > kMaxDim / N)) return I8MP_EINVAL;
+  if ((colmax_x && !vec_ok(colmax_x, K)) || (colmax_w && !vec_ok(colmax_w, K))) return I8MP_EINVAL;
+  out[0] = o2[0], out[1] = o2[1], out[2] = vec_range(colmax_x, K, 4), out[3] = vec_range(colmax_w, K, 4);
+  in[0] = i3[0], in[1] = i3[1], in[2] = i3[2], in[3] = mat_range(p->W, N, K, p->ldw, 2);
+  for (int i = 0; i < 4; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i], r)) return I8MP_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return I8MP_EINVAL;
+  }
+  if (M == 0 || N == 0) return I8MP_OK;
+  const size_t need = carve_act_fwd(nullptr, M, N, K, true, nullptr);
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return I8MP_EWORKSPACE;
+  const Range rw = vec_range(ws, (int64_t)need, 1);
+  for (int i = 0; i < 4; ++i)
+    if (overlap(rw, out[i]) || overlap(rw, in[i])) return I8MP_EINVAL;
+  if ((st = device_check()) != I8MP_OK) return st;
+  ActFwdWs w;
+  carve_act_fwd(ws, M, N, K, true, &w);
+  const hipStream_t s = as_stream(stream);
+  const int64_t kp = padded_k(K);
+  const int r = opts->round;
+  const uint64_t ox = pass_offset(opts->offset, 0), ow = pass_offset(opts->offset, 1);
+  hipError_t e;
+  i8mp::ColmaxJob side{};  // X's and W's slab maxima, folded by the GEMM
+  if (colmax_x && colmax_w && K > 0) {
+    e = i8mp::launch_quantize_rowwise_colmax_pair(p->X, M, p->ldx, w.qx, kp, w.sx, colmax_x, ox, w.part_x, p->W, N, p->ldw,
+                                                  w.qw, kp, w.sw, colmax_w, ow, w.part_w, K, r, opts->seed, false, 0, s);
+    side.n = 2;
+    side.cols = K;
+    side.part[0] = static_cast<const uint16_t*>(w.part_x), side.part[1] = static_cast<const uint16_t*>(w.part_w);
+    side.colmax[0] = colmax_x, side.colmax[1] = colmax_w;
+    i8mp::rowwise_colmax_geometry(M, K, r, &side.slabs[0], &side.part_ld);
+    i8mp::rowwise_colmax_geometry(N, K, r, &side.slabs[1], &side.part_ld);
+  } else {
+    e = colmax_x && K > 0
+            ? i8mp::launch_quantize_rowwise_colmax(p->X, M, K, p->ldx, w.qx, kp, w.sx, colmax_x, r, opts->seed, ox, w.part_x, s)
+            : i8mp::launch_quantize_rowwise(p->X, M, K, p->ldx, w.qx, kp, w.sx, r, opts->seed, ox, s);
+    if (e == hipSuccess)
+      e = colmax_w && K > 0
+              ? i8mp::launch_quantize_rowwise_colmax(p->W, N, K, p->ldw, w.qw, kp, w.sw, colmax_w, r, opts->seed, ow, w.part_w, s)
+              : i8mp::launch_quantize_rowwise(p->W, N, K, p->ldw, w.qw, kp, w.sw, r, opts->seed, ow, s);
+  }
+  if (e == hipSuccess) e = act_product(p, w.qx, w.sx, w.qw, kp, w.sw, w.split, side.n ? &side : nullptr, s);
+  return hip_status(e);
+}
+
+i8mp_status i8mp_linear_wq_fwd(const i8mp_linear_act* p, const int8_t* Wq, int64_t ldwq, const float* w_scale,
+                               void* ws, size_t ws_bytes, void* stream) {
+  Range out[2], in[3];
+  i8mp_status st = act_fwd_checks(p, out, in);
+  if (st != I8MP_OK) return st;
+  const int64_t M = p->M, N = p->N, K = p->K;
+  if (!chunked_ok(Wq, N, K, ldwq, 1) || (N > 0 && ldwq > kMaxDim / N) || !vec_ok(w_scale, N)) return I8MP_EINVAL;
+  const Range all_in[5] = {in[0], in[1], in[2], mat_range(Wq, N, K, ldwq, 1), vec_range(w_scale, N, 4)};
+  for (const Range& r : all_in)
+    if (overlap(out[0], r) || overlap(out[1], r)) return I8MP_EINVAL;
+  if (overlap(out[0], out[1])) return I8MP_EINVAL;
+  if (M == 0 || N == 0) return I8MP_OK;
+  const size_t need = carve_act_fwd(nullptr, M, N, K, false, nullptr);
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return I8MP_EWORKSPACE;
+  const Range rw = vec_range(ws, (int64_t)need, 1);
+  for (const Range& r : all_in)
+    if (overlap(rw, r)) return I8MP_EINVAL;
+  if (overlap(rw, out[0]) || overlap(rw, out[1])) return I8MP_EINVAL;
+  if ((st = device_check()) != I8MP_OK) return st;
+  ActFwdWs w;
+  carve_act_fwd(ws, M, N, K, false, &w);
+  const hipStream_t s = as_stream(stream);
+  // without a contraction the codes of X are the padding's zeros, and W's may be anything readable
+  if (K == 0) Wq = w.qx, ldwq = 0;
+  hipError_t e = i8mp::launch_quantize_rowwise(p->X, M, K, p->ldx, w.qx, padded_k(K), w.sx, I8MP_RNE, 0, 0, s);
+  if (e == hipSuccess) e = act_product(p, w.qx, w.sx, Wq, ldwq, w_scale, w.split, nullptr, s);
+  return hip_status(e);
+}
+
+i8mp_status i8mp_linear_act_bwd(const i8mp_linear_act_grad* p, const i8mp_linear_opts* opts, const float* colmax_x,
+                                const float* colmax_w, void* ws, size_t ws_bytes, void* stream) {
+  if (!p || !opts_ok(opts) || !act_ok(p->activation) || !linear_dims_ok(p->M, p->N, p->K)) return I8MP_EINVAL;
+  const int64_t M = p->M, N = p->N, K = p->K;
+  if (p->dX && N > I8MP_MAX_CONTRACTION) return I8MP_ERANGE;
+  if (p->dW && M > I8MP_MAX_CONTRACTION) return I8MP_ERANGE;
+  const bool act = p->activation != I8MP_ACT_NONE;
+  if (!chunked_ok(p->dY, M, N, p->lddy, 2) || (act && !chunked_ok(p->Z, M, N, p->ldz, 2))) return I8MP_EINVAL;
+  if (p->dX && (!chunked_ok(p->W, N, K, p->ldw, 2) || !elementwise_ok(p->dX, M, K, p->lddx, 2))) return I8MP_EINVAL;
+  if (p->dW && (!chunked_ok(p->X, M, K, p->ldx, 2) || !elementwise_ok(p->dW, N, K, p->lddw, 2))) return I8MP_EINVAL;
+  if ((p->dbias && !vec_ok(p->dbias, N)) || (colmax_x && !vec_ok(colmax_x, K)) || (colmax_w && !vec_ok(colmax_w, K))) return I8MP_EINVAL;
+  for (int64_t ld : {p->lddy, act ? p->ldz : 0, p->dX ? p->lddx : 0, p->dW ? p->ldx : 0})
+    if (M > 0 && ld > kMaxDim / M) return I8MP_EINVAL;
+  for (int64_t ld : {p->dX ? p->ldw : 0, p->dW ? p->lddw : 0})
+    if (N > 0 && ld > kMaxDim / N) return I8MP_EINVAL;
+  const Range in[6] = {mat_range(p->dY, M, N, p->lddy, 2), act ? mat_range(p->Z, M, N, p->ldz, 2) : Range{},
+                       p->dW ? mat_range(p->X, M, K, p->ldx, 2) : Range{}, p->dX ? mat_range(p->W, N, K, p->ldw, 2) : Range{},
+                       vec_range(colmax_x, K, 4), vec_range(colmax_w, K, 4)};
+  const Range out[3] = {mat_range(p->dX, M, K, p->lddx, 2), mat_range(p->dW, N, K, p->lddw, 2), vec_range(p->dbias, N, 4)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : in)
+      if (overlap(out[i], r)) return I8MP_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return I8MP_EINVAL;
+  }
+  const bool want_dx = p->dX && M > 0 && K > 0, want_dw = p->dW && N > 0 && K > 0, want_db = p->dbias && N > 0;
+  if (!want_dx && !want_dw && !want_db) return I8MP_OK;
+  const size_t need = carve_act_bwd(nullptr, M, N, K, nullptr);
+  if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return I8MP_EWORKSPACE;
+  const Range rw = vec_range(ws, (int64_t)need, 1);
+  for (const Range& r : in)
+    if (overlap(rw, r)) return I8MP_EINVAL;
+  for (const Range& r : out)
+    if (overlap(rw, r)) return I8MP_EINVAL;
+  i8mp_status st = device_check();
+  if (st != I8MP_OK) return st;
+  ActBwdWs w;
+  carve_act_bwd(ws, M, N, K, &w);
+  const hipStream_t s = as_stream(stream);
+  const int64_t kp = pad16(K);
+  const int r = opts->round;
+  const uint64_t seed = opts->seed, off = opts->offset;
+  i8mp::ActBwdArgs a{};
+  a.M = M, a.N = N;
+  i8mp::act_bwd_plan(a);
+  hipError_t e = hipSuccess;
+  if (N > 0) {
+    a.dY = p->dY, a.lddy = p->lddy, a.Z = p->Z, a.ldz = p->ldz;
+    a.dZ = act ? w.dz : const_cast<uint16_t*>(p->dY);
+    a.lddz = act ? a.np : p->lddy;
+    a.row_codes = want_dx ? w.q_row : nullptr, a.row_scale = w.s_row;
+    a.col_codes = want_dw ? w.q_col : nullptr, a.col_scale = w.s_col;
+    a.dbias = want_db ? p->dbias : nullptr;
+    a.segmax = w.segmax, a.band_max = w.band_max, a.band_sum = w.band_sum;
+    a.seed = seed, a.row_offset = pass_offset(off, 2), a.col_offset = pass_offset(off, 4);
+    e = i8mp::launch_act_bwd(a, p->activation, r, s);
+  } else if (want_dx) {  // no columns: scales of zero
+    e = i8mp::launch_quantize_rowwise(p->dY, M, 0, p->lddy, w.q_row, 16, w.s_row, I8MP_RNE, 0, 0, s);
+  }
+  // W and X down their columns, in one launch where both column maxima are given
+  if (e == hipSuccess && want_dx && want_dw && colmax_x && colmax_w && M > 0) {
+    e = i8mp::launch_quantize_colwise_given_pair(p->W, N, K, p->ldw, colmax_w, w.qw, kp, w.sw, pass_offset(off, 3), p->X, M, K,
+                                                 p->ldx, colmax_x, w.qx, kp, w.sx, pass_offset(off, 5), r, seed, 0, s);
+  } else {
+    if (e == hipSuccess && want_dx)
+      e = colmax_w ? i8mp::launch_quantize_colwise_given(p->W, N, K, p->ldw, colmax_w, w.qw, kp, w.sw, r, seed, pass_offset(off, 3), s)
+                   : i8mp::launch_quantize_colwise(p->W, N, K, p->ldw, w.qw, kp, w.sw, r, seed, pass_offset(off, 3), w.col, s);
+    if (e == hipSuccess && want_dw)
+      e = colmax_x ? i8mp::launch_quantize_colwise_given(p->X, M, K, p->ldx, colmax_x, w.qx, kp, w.sx, r, seed, pass_offset(off, 5), s)
+                   : i8mp::launch_quantize_colwise(p->X, M, K, p->ldx, w.qx, kp, w.sx, r, seed, pass_offset(off, 5), w.col, s);
+  }
+  // contractions over N and M padded to 16: dZ's codes are zero there
+  if (e == hipSuccess && want_dx)
+    e = i8mp::launch_gemm_split(I8MP_NN, M, K, a.np, w.q_row, a.np, w.s_row, w.qw, kp, w.sw, p->dX, p->lddx, w.split, nullptr, 0, s);
+  if (e == hipSuccess && want_dw)
+    e = i8mp::launch_gemm_split(I8MP_TN, N, K, a.mp, w.q_col, a.np, w.s_col, w.qx, kp, w.sx, p->dW, p->lddw, w.split, nullptr, 0, s);
+  return hip_status(e);
+}
 
 size_t i8mp_distill_workspace_bytes(int64_t T, int64_t V, int32_t kept, int32_t dtype) {
   if (!dims_ok(T, V) || T == 0 || V == 0 || T >= (int64_t(1) << 31) || V > (int64_t(1) << 30) || kept < 0 || !dtype_ok(dtype)) return 0;

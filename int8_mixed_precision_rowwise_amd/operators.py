@@ -1,10 +1,12 @@
 """Operators around the INT8 mixed-precision linears, bound like the linears.
 
-Rotary positions of query and key heads (``rotary``) and the loss of a
-student's logits against a teacher's top logits (``distill_loss``,
-``distill_loss_bwd``, ``distill_loss_and_grad``), with the tensors' checks, the
-current stream and the errors of the package's other calls; every step of the
-computation runs in the library's HIP kernels.  ``training`` holds
+Linear layers with bias, activation and residual in the INT8 GEMM's epilogue
+(``linear_act_fwd``, ``linear_act_fwd_train``, ``linear_act_bwd``, and over weights
+quantized once ``linear_wq_fwd``), rotary positions of query and key heads
+(``rotary``) and the loss of a student's logits against a teacher's top logits
+(``distill_loss``, ``distill_loss_bwd``, ``distill_loss_and_grad``), with the
+tensors' checks, the current stream and the errors of the package's other calls;
+every step of the computation runs in the library's HIP kernels.  ``training`` holds
 their autograd forms.
 """
 from __future__ import annotations
@@ -16,7 +18,8 @@ import torch
 
 import int8_mixed_precision_rowwise_amd as _pkg
 
-__all__ = ["rotary", "rotary_frequencies", "distill_loss", "distill_loss_bwd", "distill_loss_and_grad"]
+__all__ = ["ACTIVATIONS", "linear_act_fwd", "linear_act_fwd_train", "linear_act_bwd", "linear_wq_fwd",
+           "linear_act_workspace_bytes", "linear_wq_workspace_bytes", "rotary", "rotary_frequencies", "distill_loss", "distill_loss_bwd", "distill_loss_and_grad"]
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _PAIRS = {"half": 0, "interleaved": 1}
@@ -39,6 +42,164 @@ def _call(dev: torch.device, name: str, *args):
             st = f(*args, stream)
     if st:
         raise _pkg.I8mpError(st, name)
+
+
+# --------------------------------------------------------------------------- linears with an epilogue
+
+ACTIVATIONS = ("none", "relu", "gelu", "gelu_tanh", "silu")
+_ACT = {a: i for i, a in enumerate(ACTIVATIONS)}
+_bf = torch.bfloat16
+
+
+def _ld2(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _ptr(t):
+    return None if t is None or t.numel() == 0 else t.data_ptr()
+
+
+def _new_rows(rows: int, cols: int, dev) -> torch.Tensor:
+    """bf16 [rows, cols], every row at a 16-byte boundary (dense where cols is a multiple of 8)."""
+    ld = (cols + 7) // 8 * 8
+    t = torch.empty((rows, ld), dtype=_bf, device=dev)
+    return t if ld == cols else t[:, :cols]
+
+
+def _activation(name: str) -> int:
+    if name not in _ACT:
+        raise ValueError(f"activation must be one of {ACTIVATIONS}, got {name!r}")
+    return _ACT[name]
+
+
+def linear_act_workspace_bytes(M: int, N: int, K: int, backward: bool) -> int:
+    return _pkg.lib.i8mp_linear_act_workspace_bytes(M, N, K, int(backward))
+
+
+def linear_wq_workspace_bytes(M: int, N: int, K: int) -> int:
+    return _pkg.lib.i8mp_linear_wq_workspace_bytes(M, N, K)
+
+
+def _space(workspace, need: int, dev):
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _act_forward(X, W, w_scale, bias, activation, residual, out, workspace, keep_z=False):
+    """Checks of a forward; (the C structure, device, Y, Z)."""
+    act = _activation(activation)
+    _pkg._mat(X, "X", _bf)
+    M, K = X.shape
+    if w_scale is None:
+        _pkg._mat(W, "W", _bf)
+    else:
+        _pkg._mat(W, "Wq", torch.int8)
+    if W.shape[1] != K:
+        raise ValueError(f"W: {K} columns expected (X is {tuple(X.shape)}), got {tuple(W.shape)}")
+    N = W.shape[0]
+    if w_scale is not None:
+        _pkg._vec(w_scale, "w_scale", N)
+    if bias is not None:
+        _pkg._vec(bias, "bias", N, _bf)
+    if residual is not None:
+        _pkg._mat(residual, "residual", _bf, (M, N))
+    if out is not None:
+        _pkg._mat(out, "out", _bf, (M, N))
+    if workspace is not None:
+        _pkg._workspace(workspace)
+    dev = _pkg._device(X, W, w_scale, bias, residual, out, workspace)
+    Y = _new_rows(M, N, dev) if out is None else out
+    Z = _new_rows(M, N, dev) if keep_z and act else None
+    p = _pkg._LinearAct(M, N, K, _ptr(X), _ld2(X), None if w_scale is not None else _ptr(W), _ld2(W), act, _ptr(bias),
+                        _ptr(residual), 0 if residual is None else _ld2(residual), _ptr(Y), _ld2(Y), _ptr(Z),
+                        0 if Z is None else _ld2(Z))
+    return p, dev, Y, Z
+
+
+def linear_act_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "none",
+                   residual: torch.Tensor | None = None, rounding="rne", seed: int = 0, offset: int = 0,
+                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = act(X @ W.T + bias) + residual, X [M, K] and W [N, K] quantized row-wise over K.
+
+    bf16 tensors; X, W and residual may have rows further apart than they are
+    long (16-byte aligned).  activation: one of ACTIVATIONS.  Bias, activation and
+    residual are added in fp32 and Y is rounded once.  Y's rows start every 16
+    bytes unless out is given."""
+    p, dev, Y, _ = _act_forward(X, W, None, bias, activation, residual, out, workspace)
+    ws, n = _space(workspace, linear_act_workspace_bytes(p.M, p.N, p.K, False), dev)
+    _call(dev, "i8mp_linear_act_fwd", p, _pkg._opts(rounding, seed, offset), None, None, ws, n)
+    return Y
+
+
+def linear_act_fwd_train(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "none",
+                         residual: torch.Tensor | None = None, rounding="rne", seed: int = 0, offset: int = 0,
+                         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """linear_act_fwd that also returns what linear_act_bwd needs: (Y, Z, colmax_x,
+    colmax_w), Z the pre-activation (bf16; None without an activation) and the
+    column maxima of X and W (fp32 [K])."""
+    p, dev, Y, Z = _act_forward(X, W, None, bias, activation, residual, out, workspace, keep_z=True)
+    cx = torch.empty(p.K, dtype=torch.float32, device=dev)
+    cw = torch.empty(p.K, dtype=torch.float32, device=dev)
+    ws, n = _space(workspace, linear_act_workspace_bytes(p.M, p.N, p.K, False), dev)
+    _call(dev, "i8mp_linear_act_fwd", p, _pkg._opts(rounding, seed, offset), _ptr(cx), _ptr(cw), ws, n)
+    return Y, Z, cx, cw
+
+
+def linear_wq_fwd(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, bias: torch.Tensor | None = None,
+                  activation: str = "none", residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """linear_act_fwd over weights quantized once: int8 codes Wq [N, K] and fp32 scales
+    w_scale [N], for instance from quantize_rowwise.  X is quantized to nearest."""
+    if not isinstance(w_scale, torch.Tensor):
+        raise TypeError(f"w_scale: torch.Tensor expected, got {type(w_scale).__name__}")
+    p, dev, Y, _ = _act_forward(X, Wq, w_scale, bias, activation, residual, out, workspace)
+    ws, n = _space(workspace, linear_wq_workspace_bytes(p.M, p.N, p.K), dev)
+    _call(dev, "i8mp_linear_wq_fwd", p, _ptr(Wq), _ld2(Wq), _ptr(w_scale), ws, n)
+    return Y
+
+
+def linear_act_bwd(dY: torch.Tensor, Z: torch.Tensor | None, X: torch.Tensor, W: torch.Tensor, activation: str = "none",
+                   rounding="rne", seed: int = 0, offset: int = 0, want_dx: bool = True, want_dw: bool = True,
+                   want_dbias: bool = False, dX: torch.Tensor | None = None, dW: torch.Tensor | None = None,
+                   dbias: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   colmax_x: torch.Tensor | None = None, colmax_w: torch.Tensor | None = None):
+    """Backward of linear_act_fwd: (dX, dW, dbias), None for what is not wanted.
+
+    dZ = dY act'(Z) rounded to bf16 is quantized along each contraction as in
+    linear_bwd; dbias (fp32 [N]) sums the values before that rounding.  Z: the
+    pre-activation from linear_act_fwd_train (not read without an activation).
+    The residual's gradient is dY itself."""
+    act = _activation(activation)
+    _pkg._mat(dY, "dY", _bf)
+    M, N = dY.shape
+    if act:
+        _pkg._mat(Z, "Z", _bf, (M, N))
+    else:
+        Z = None
+    _pkg._mat(W, "W", _bf)
+    if W.shape[0] != N:
+        raise ValueError(f"W: {N} rows expected (dY is {tuple(dY.shape)}), got {tuple(W.shape)}")
+    K = W.shape[1]
+    _pkg._mat(X, "X", _bf, (M, K))
+    for t, name, shape in ((dX, "dX", (M, K)), (dW, "dW", (N, K))):
+        if t is not None:
+            _pkg._mat(t, name, _bf, shape)
+    for t, name, n in ((dbias, "dbias", N), (colmax_x, "colmax_x", K), (colmax_w, "colmax_w", K)):
+        if t is not None:
+            _pkg._vec(t, name, n)
+    if workspace is not None:
+        _pkg._workspace(workspace)
+    dev = _pkg._device(dY, Z, X, W, dX, dW, dbias, workspace, colmax_x, colmax_w)
+    dX = None if not want_dx else torch.empty((M, K), dtype=_bf, device=dev) if dX is None else dX
+    dW = None if not want_dw else torch.empty((N, K), dtype=_bf, device=dev) if dW is None else dW
+    dbias = None if not want_dbias else torch.empty(N, dtype=torch.float32, device=dev) if dbias is None else dbias
+    p = _pkg._LinearActGrad(M, N, K, _ptr(dY), _ld2(dY), _ptr(Z), 0 if Z is None else _ld2(Z), _ptr(X), _ld2(X), _ptr(W),
+                            _ld2(W), act, _ptr(dX), 0 if dX is None else _ld2(dX), _ptr(dW), 0 if dW is None else _ld2(dW),
+                            _ptr(dbias))
+    ws, n = _space(workspace, linear_act_workspace_bytes(M, N, K, True), dev)
+    _call(dev, "i8mp_linear_act_bwd", p, _pkg._opts(rounding, seed, offset), _ptr(colmax_x), _ptr(colmax_w), ws, n)
+    return dX, dW, dbias
 
 
 # --------------------------------------------------------------------------- rotary positions
@@ -149,10 +310,6 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, fre
 
 DISTILL_STATS = 8
 DISTILL_MAX_KEPT = 1024
-
-
-def _ld2(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def _rows(t, name: str, dtypes, shape=None):

@@ -47,7 +47,8 @@ from . import operators as _ops
 
 __all__ = ["Int8MixedPrecisionConfig", "Int8MixedPrecisionLinearFunction",
            "Int8MixedPrecisionLinear", "swap_linear_modules", "STEP_STRIDE", "STEPS_PER_KEY",
-           "module_seed", "step_key_offset", "sr_checkpoint_contexts", "RotaryFunction", "rotary", "DistillFunction", "distill_loss"]
+           "module_seed", "step_key_offset", "sr_checkpoint_contexts", "RotaryFunction", "rotary", "DistillFunction", "distill_loss",
+           "LinearActFunction", "linear_act", "Int8MixedPrecisionActLinear"]
 
 STEP_STRIDE = 8 << 40  # Philox blocks reserved per linear step (6 passes of 2**40 each, rounded up)
 STEPS_PER_KEY = (1 << 64) // STEP_STRIDE  # steps whose offsets fit the 64-bit block counter
@@ -346,3 +347,74 @@ def distill_loss(logits: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor,
                  ce_weight: float = 0.0, ignore_index: int = -100) -> torch.Tensor:
     """operators.distill_loss with a gradient at the logits: loss fp32 [T]."""
     return DistillFunction.apply(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index)
+
+
+def _aligned_rows(t: torch.Tensor, cols: int) -> torch.Tensor:
+    """t as a matrix of `cols` columns whose rows start every 16 bytes."""
+    t = t.reshape(-1, cols)
+    if t.stride(1) == 1 and t.stride(0) % 8 == 0 and t.stride(0) >= cols and t.data_ptr() % 16 == 0:
+        return t
+    store = torch.empty((t.shape[0], max(8, (cols + 7) // 8 * 8)), dtype=t.dtype, device=t.device)
+    return store[:, :cols].copy_(t)
+
+
+class LinearActFunction(torch.autograd.Function):
+    """y = act(x @ weight.T + bias) + residual with all three GEMMs in INT8
+    (operators.linear_act_fwd_train / linear_act_bwd).  Saved for backward: input,
+    weight, the pre-activation and the column maxima of the first two."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, activation, residual, rounding, seed, offset):
+        N, K = weight.shape
+        x2, w = _aligned_rows(x, K), _aligned_rows(weight, K)
+        r2 = None if residual is None else _aligned_rows(residual, N)
+        y, z, cx, cw = _ops.linear_act_fwd_train(x2, w, bias, activation, r2, rounding, seed, offset)
+        ctx.save_for_backward(x2, w, z, cx, cw)
+        ctx.args = activation, rounding, seed, offset
+        ctx.shape, ctx.bias_dtype = x.shape, None if bias is None else bias.dtype
+        return y.reshape(*x.shape[:-1], N)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x2, w, z, cx, cw = ctx.saved_tensors
+        activation, rounding, seed, offset = ctx.args
+        dx, dw, db = _ops.linear_act_bwd(_aligned_rows(dy, w.shape[0]), z, x2, w, activation, rounding, seed, offset,
+                                         want_dx=ctx.needs_input_grad[0], want_dw=ctx.needs_input_grad[1],
+                                         want_dbias=ctx.needs_input_grad[2], colmax_x=cx, colmax_w=cw)
+        return (None if dx is None else dx.view(ctx.shape), dw, None if db is None else db.to(ctx.bias_dtype), None,
+                dy if ctx.needs_input_grad[4] else None, None, None, None)
+
+
+def linear_act(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, activation: str = "none",
+               residual: Optional[torch.Tensor] = None, rounding: str = "rne", seed: int = 0, offset: int = 0) -> torch.Tensor:
+    """operators.linear_act_fwd with a gradient: x [..., K], weight [N, K], bias [N], residual [..., N], bf16."""
+    if x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"shapes {tuple(x.shape)} and {tuple(weight.shape)} do not match")
+    if residual is not None and residual.shape != (*x.shape[:-1], weight.shape[0]):
+        raise ValueError(f"residual: shape {(*x.shape[:-1], weight.shape[0])} expected, got {tuple(residual.shape)}")
+    return LinearActFunction.apply(x, weight, bias, activation, residual, rounding, seed, offset)
+
+
+class Int8MixedPrecisionActLinear(Int8MixedPrecisionLinear):
+    """Linear layer with bias, activation and residual whose three GEMMs run in
+    INT8: forward(x, residual=None) = act(x @ weight.T + bias) + residual.  Its
+    rounding, seed and step are those of Int8MixedPrecisionLinear (the switches
+    that turn single GEMMs to BF16 or FP8 do not apply and are refused)."""
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True, activation: str = "none",
+                 config: Optional[Int8MixedPrecisionConfig] = None, seed: int = 0, device=None, dtype=torch.bfloat16):
+        super().__init__(in_features, out_features, config, seed, device, dtype)
+        c = self.config
+        if c.fp8 or not (c.output and c.grad_input and c.grad_weight):
+            raise ValueError("linear layers with an epilogue run all three GEMMs in INT8")
+        _ops._activation(activation)
+        self.activation = activation
+        if bias:
+            self.bias = torch.nn.Parameter(torch.zeros(out_features, device=device, dtype=dtype))
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+        key, offset = self._key_offset()
+        return linear_act(x, self.weight, self.bias, self.activation, residual, self.config.rounding, key, offset)
+
+    def extra_repr(self) -> str:
+        return super().extra_repr() + f", bias={self.bias is not None}, activation={self.activation}"

@@ -86,3 +86,31 @@ def distill(logits, teacher, idx, temperature, lse=None, labels=None, ce=0.0, ig
         return loss, None, None
     g = grad.detach().to("cpu", F64)[:, None]
     return loss, d * g, scale * g.abs()
+
+
+def activation(z, act):
+    """act(z) in 64 bits, from the definitions."""
+    if act == "relu":
+        return z.clamp_min(0)
+    if act == "gelu":
+        return z * 0.5 * torch.special.erfc(-z / math.sqrt(2))
+    if act == "gelu_tanh":
+        return z / (1 + torch.exp(-2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))
+    if act == "silu":
+        return z / (1 + torch.exp(-z))
+    return z
+
+
+def activation_grad(z, act):
+    if act == "relu":
+        return (z > 0).to(z.dtype)
+    if act == "gelu":
+        return 0.5 * torch.special.erfc(-z / math.sqrt(2)) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    if act == "gelu_tanh":
+        b = math.sqrt(2 / math.pi)
+        s = 1 / (1 + torch.exp(-2 * b * (z + 0.044715 * z ** 3)))
+        return s + z * s * (1 - s) * 2 * b * (1 + 3 * 0.044715 * z * z)
+    if act == "silu":
+        s = 1 / (1 + torch.exp(-z))
+        return s + z * s * (1 - s)
+    return torch.ones_like(z)

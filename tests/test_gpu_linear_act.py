@@ -1,0 +1,239 @@
+"""Linears with bias, activation and residual on the GPU.
+
+Forward: the codes are the oracle's (bit for bit), their product is exact in
+64 bits.  Tolerance: the product's conversion and two scales and the bias are at
+most four fp32 roundings (2^-22 of |product| + |bias|), passed on by an activation
+whose slope is below 1.13; the activation's own arithmetic is below 2^-16 of its
+value; the residual's sum rounds once more; then one rounding to bf16.
+
+Backward: dY holds powers of two and Z only values whose derivative keeps
+2^-14 away from a boundary between bf16 values, so dZ is known exactly and dX and
+dW are the oracle's, bit for bit.  dbias sums unrounded values whose derivative is
+off by at most 2^-15 in fp32."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from tests import operators_ref as ref
+from tests.gpu_util import padded_copy, tensor_bits
+
+pytestmark = pytest.mark.gpu
+
+i8 = pytest.importorskip("int8_mixed_precision_rowwise_amd")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+bf = torch.bfloat16
+ACTS = list(i8.ACTIVATIONS)
+ROUND = {"rne": oracle.RNE, "sr": oracle.SR}
+
+
+def randn(seed, *shape, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (scale * torch.randn(*shape, generator=g, device="cuda")).to(bf)
+
+
+def rows(t):
+    """The same matrix with every row at a 16-byte boundary."""
+    ld = max(8, (t.shape[1] + 7) // 8 * 8)
+    return t if t.shape[1] == ld else padded_copy(t, ld)
+
+
+def product(qx, sx, qw, sw):
+    return torch.from_numpy(qx.astype(np.float64) @ qw.astype(np.float64).T) * torch.outer(torch.from_numpy(sx).double(), torch.from_numpy(sw).double())
+
+
+def within(got, want, tol):
+    worst = float(((got.cpu().double() - want).abs() / tol).max())  # a NaN fails too
+    assert worst <= 1, worst
+
+
+def check_forward(p, bias, act, residual, Y, Z=None):
+    b = torch.zeros(p.shape[1], dtype=torch.float64) if bias is None else bias.cpu().double()
+    z = p + b
+    ez = 2.0 ** -22 * (p.abs() + b.abs()) + 2.0 ** -126
+    y, r = ref.activation(z, act), 0 if residual is None else residual.cpu().double()
+    ey = 1.13 * ez + (2.0 ** -16 * y.abs() if act not in ("none", "relu") else 0)
+    y = y + r
+    ey = ey + 2.0 ** -23 * y.abs()
+    half = ref.half_step(bf)
+    within(Y, y, ey + half * (y.abs() + ey))
+    if Z is not None:
+        within(Z, z, ez + half * (z.abs() + ez))
+
+
+# M, N, K: tiles of 128 with ragged edges, contractions that are no multiple of 16 (or nothing at all), tiles
+# of 256, a split contraction, and the few-token kernel
+SHAPES = [(65, 8, 16), (70, 130, 24), (200, 257, 40), (300, 513, 2048), (66, 40, 0), (2053, 4099, 72), (260, 500, 4104),
+          (1, 1, 1), (1, 1000, 4096), (13, 503, 2040), (17, 64, 8), (33, 129, 520), (49, 3, 100), (64, 129, 8200), (2, 16, 0)]
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_forward(M, N, K, act):
+    n = SHAPES.index((M, N, K)) + ACTS.index(act)
+    X, W = rows(randn(1, M, K)), rows(randn(2, N, K, scale=0.7 / max(1, K) ** 0.5 * 3))
+    bias = randn(3, N) if n % 2 else None
+    residual = rows(randn(4, M, N)) if n % 3 else None
+    rounding = "sr" if n % 4 == 3 else "rne"
+    kw = dict(bias=bias, activation=act, residual=residual, rounding=rounding, seed=77, offset=5)
+    p = torch.zeros(M, N, dtype=torch.float64)
+    if K:
+        p = product(*oracle.quantize_rowwise(tensor_bits(X), ROUND[rounding], 77, 5),
+                    *oracle.quantize_rowwise(tensor_bits(W), ROUND[rounding], 77, 5 + (1 << 40)))
+    Y = i8.linear_act_fwd(X, W, **kw)
+    check_forward(p, bias, act, residual, Y)
+    Yt, Z, cx, cw = i8.linear_act_fwd_train(X, W, **kw)
+    assert torch.equal(Y, Yt) and (Z is None) == (act == "none")
+    check_forward(p, bias, act, residual, Yt, Z)
+    if K:
+        assert torch.equal(cx, X.abs().amax(0).float()) and torch.equal(cw, W.abs().amax(0).float())
+    if rounding == "rne":  # the same codes given as weights quantized once
+        Wq, ws = i8.quantize_rowwise(W)
+        assert torch.equal(i8.linear_wq_fwd(X, Wq, ws, bias=bias, activation=act, residual=residual), Y)
+    # an output whose rows start anywhere
+    store = torch.full((M * (N + 3) + 1,), 7.0, dtype=bf, device="cuda")
+    out = store[1:].view(M, N + 3)[:, :N]
+    assert i8.linear_act_fwd(X, W, out=out, **kw) is out and torch.equal(out, Y)
+    assert bool((store[1:].view(M, N + 3)[:, N:] == 7).all()) and float(store[0]) == 7
+
+
+def test_far_activations():
+    z = torch.tensor([[-40.0, -20, -12, -6, -3, -1e-3, 0, 1e-3, 3, 6, 12, 40]], device="cuda").to(bf)
+    X = torch.full((1, 16), 1.0, dtype=bf, device="cuda")
+    for act in ACTS:  # the values as the bias of a zero product
+        for M in (1, 70):
+            Y = i8.linear_act_fwd(X.expand(M, 16).contiguous(), torch.zeros(12, 16, dtype=bf, device="cuda"), bias=z[0].contiguous(), activation=act)
+            check_forward(torch.zeros(M, 12, dtype=torch.float64), z[0], act, None, Y)
+
+
+@pytest.mark.parametrize("M", [5, 100])
+def test_rows_that_are_not_finite_stay_alone(M):
+    X, W = randn(1, M, 64), randn(2, 48, 64)
+    want = i8.linear_act_fwd(X, W, activation="silu")
+    for bad in (float("inf"), float("nan")):
+        Xb = X.clone()
+        Xb[3, 7] = bad
+        Y = i8.linear_act_fwd(Xb, W, activation="silu")
+        keep = torch.arange(M, device="cuda") != 3
+        assert not Y[3].isfinite().any() and torch.equal(Y[keep], want[keep])
+
+
+def safe_z(act):
+    """bf16 values whose derivative is known to round the same way."""
+    z = torch.arange(-6.0, 6.0, 2.0 ** -6).to(bf).unique()
+    d = ref.activation_grad(z.double(), act)
+    step = torch.exp2(torch.floor(torch.log2(d.abs().clamp_min(1e-30))) - 7)
+    off = (d.abs() / step) % 1.0
+    return z[((off - 0.5).abs() * step > 2.0 ** -14 * d.abs()) & (d.abs() > 0.05)]
+
+
+BWD = [(1, 8, 8), (17, 24, 40), (130, 520, 72), (300, 1032, 136), (1500, 64, 32), (33, 13, 21), (2070, 96, 48)]
+
+
+@pytest.mark.parametrize("rounding", ["rne", "sr"])
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,N,K", BWD)
+def test_backward(M, N, K, act, rounding):
+    g = torch.Generator().manual_seed(M + N)
+    pick = safe_z(act) if act not in ("none", "relu") else torch.arange(-3.0, 3.0, 0.25).to(bf)
+    zc = pick[torch.randint(0, len(pick), (M, N), generator=g)]
+    dyc = (torch.exp2(torch.randint(-8, 3, (M, N), generator=g).float()) * (1 - 2.0 * torch.randint(0, 2, (M, N), generator=g))).to(bf)
+    X, W, Z, dY = rows(randn(1, M, K)), rows(randn(2, N, K)), rows(zc.cuda()), rows(dyc.cuda())
+    gz = dyc.double() * ref.activation_grad(zc.double(), act)
+    dz = gz.to(bf)  # safe: rounding 64 bits to fp32 first changes nothing
+    kw = dict(rounding=rounding, seed=9, offset=123)
+    dXo, dWo = oracle.linear_bwd(tensor_bits(dz), tensor_bits(X), tensor_bits(W), ROUND[rounding], 9, 123)
+    cx, cw = X.abs().amax(0).float(), W.abs().amax(0).float()
+    zarg = None if act == "none" else Z
+    for given in (dict(), dict(colmax_x=cx, colmax_w=cw)):
+        dX, dW, db = i8.linear_act_bwd(dY, zarg, X, W, act, want_dbias=True, **given, **kw)
+        assert np.array_equal(tensor_bits(dX), dXo.reshape(M, K)) and np.array_equal(tensor_bits(dW), dWo.reshape(N, K))
+        tol = 2.0 ** -14 * gz.abs().sum(0) + 2.0 ** -126
+        within(db, gz.sum(0), tol)
+    only = [i8.linear_act_bwd(dY, zarg, X, W, act, want_dx=a, want_dw=b, want_dbias=c, **kw)
+            for a, b, c in ((1, 0, 0), (0, 1, 0), (0, 0, 1))]
+    for i, (o, w) in enumerate(zip(only, (dX, dW, db))):
+        assert torch.equal(o[i], w) and all(v is None for j, v in enumerate(o) if j != i)
+
+
+def test_empty_sizes():
+    for M, N, K in ((0, 16, 16), (16, 0, 16), (16, 16, 0)):
+        X, W = randn(1, M, K), randn(2, N, K)
+        bias = randn(3, N)
+        Y, Z, _, _ = i8.linear_act_fwd_train(X, W, bias=bias, activation="gelu")
+        assert Y.shape == (M, N)
+        if K == 0:
+            assert torch.equal(Z, bias.expand(M, N))
+        dX, dW, db = i8.linear_act_bwd(Y, Z, X, W, "gelu", want_dbias=True)
+        assert dX.shape == (M, K) and dW.shape == (N, K) and db.shape == (N,)
+        assert not dX.any() and not dW.any()
+        if M == 0:
+            assert not db.any()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_autograd_form(act):
+    """The function's gradients are the calls'; the bias gradient agrees with differences of
+    the bias (exact in the product, so only the activation's slope is measured)."""
+    from int8_mixed_precision_rowwise_amd import training
+    x, w = randn(1, 3, 33, 40).requires_grad_(), randn(2, 24, 40).requires_grad_()
+    b, res = randn(3, 24).requires_grad_(), randn(4, 3, 33, 24).requires_grad_()
+    dy = randn(5, 3, 33, 24)
+    y = training.linear_act(x, w, b, act, res)
+    y.backward(dy)
+    Y, Z, cx, cw = i8.linear_act_fwd_train(x.detach().view(99, 40), w.detach(), b.detach(), act, res.detach().view(99, 24))
+    dX, dW, db = i8.linear_act_bwd(dy.view(99, 24), Z, x.detach().view(99, 40), w.detach(), act, want_dbias=True, colmax_x=cx, colmax_w=cw)
+    assert torch.equal(y.view(99, 24), Y) and torch.equal(x.grad.view(99, 40), dX) and torch.equal(w.grad, dW)
+    assert torch.equal(b.grad, db.to(bf)) and torch.equal(res.grad, dy)
+    # the formula's derivative against differences, at the values that the kernel kept
+    z = (Z if Z is not None else Y - res.view(99, 24)).detach().cpu().double()
+    h = 1e-4
+    slope = (ref.activation(z + h, act) - ref.activation(z - h, act)) / (2 * h)
+    away = z.abs() > 1e-3  # relu's corner
+    assert torch.allclose(slope[away], ref.activation_grad(z, act)[away], atol=1e-7)
+
+
+def test_module_trains_and_resumes():
+    from int8_mixed_precision_rowwise_amd import training
+    torch.manual_seed(0)
+    cfg = training.Int8MixedPrecisionConfig(stochastic_rounding=True)
+    a = training.Int8MixedPrecisionActLinear(64, 48, activation="silu", config=cfg, seed=3, device="cuda")
+    x, r = randn(1, 20, 64), randn(2, 20, 48)
+    first = a(x, r)
+    state = a.state_dict()
+    second = a(x, r)
+    assert not torch.equal(first, second)
+    c = training.Int8MixedPrecisionActLinear(64, 48, activation="silu", config=cfg, seed=0, device="cuda")
+    c.load_state_dict(state)
+    assert torch.equal(c(x, r), second)
+    second.float().square().mean().backward()
+    assert a.weight.grad is not None and a.bias.grad is not None and bool(a.bias.grad.isfinite().all())
+
+
+@pytest.mark.parametrize("M", [8, 200])
+def test_captured_and_on_another_stream(M):
+    N, K = 96, 72
+    X, W, b, R, dY = randn(1, M, K), randn(2, N, K), randn(3, N), randn(4, M, N), randn(5, M, N)
+    Wq, ws = i8.quantize_rowwise(W)
+
+    def step():
+        Y, Z, cx, cw = i8.linear_act_fwd_train(X, W, b, "gelu", R)
+        return (Y, Z, i8.linear_wq_fwd(X, Wq, ws, b, "silu", R),
+                *i8.linear_act_bwd(dY, Z, X, W, "gelu", want_dbias=True, colmax_x=cx, colmax_w=cw))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        other = step()
+    s.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(other, step()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in range(3):
+        X.copy_(randn(10 + seed, M, K)), dY.copy_(randn(20 + seed, M, N))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(got, step()))

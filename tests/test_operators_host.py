@@ -251,3 +251,122 @@ def test_distill_reference_gradient_is_the_derivative():
         h = 1e-5
         up, down = (ref.distill(x + s * h * v, te, ix, tau, lse, lab, ce)[0] for s in (1, -1))
         assert torch.allclose((up - down) / (2 * h), (d * v).sum(1), rtol=1e-7, atol=1e-8)
+
+
+# ------------------------------------------------------------------ linears with an epilogue
+
+
+def test_linear_act_binding_checks(lib):
+    lib.i8mp_linear_act_workspace_bytes = lib.i8mp_linear_wq_workspace_bytes = lambda *a: 0
+    X, W, b, r, q, s = t(4, 16), t(8, 16), t(8), t(4, 8), t(8, 16, dtype=s8), t(8, dtype=f32)
+    for call in (lambda **k: i8.linear_act_fwd(X, W, **k), lambda **k: i8.linear_act_fwd_train(X, W, **k),
+                 lambda **k: i8.linear_wq_fwd(X, q, s, **k)):
+        with pytest.raises(ValueError, match="device tensors"):
+            call(bias=b, residual=r, activation="gelu")  # right but for the device
+        with pytest.raises(ValueError, match="activation"):
+            call(activation="tanh")
+        with pytest.raises(TypeError, match="bias"):
+            call(bias=b.float())
+        with pytest.raises(ValueError, match="bias"):
+            call(bias=t(9))
+        with pytest.raises(ValueError, match="residual"):
+            call(residual=t(4, 9))
+        with pytest.raises(TypeError, match="residual"):
+            call(residual=r.float())
+        with pytest.raises(ValueError, match="out"):
+            call(out=t(5, 8))
+        with pytest.raises(TypeError, match="workspace"):
+            call(workspace=s)
+    with pytest.raises(TypeError, match="X"):
+        i8.linear_act_fwd(X.float(), W)
+    with pytest.raises(ValueError, match="W: 16 columns"):
+        i8.linear_act_fwd(X, t(8, 24))
+    with pytest.raises(TypeError, match="Wq"):
+        i8.linear_wq_fwd(X, W, s)
+    with pytest.raises(TypeError, match="w_scale"):
+        i8.linear_wq_fwd(X, q, None)
+    with pytest.raises(ValueError, match="w_scale"):
+        i8.linear_wq_fwd(X, q, t(9, dtype=f32))
+    dY, Z = t(4, 8), t(4, 8)
+    with pytest.raises(ValueError, match="device tensors"):
+        i8.linear_act_bwd(dY, Z, X, W, "silu")
+    with pytest.raises(TypeError, match="Z"):
+        i8.linear_act_bwd(dY, None, X, W, "silu")
+    with pytest.raises(ValueError, match="Z"):
+        i8.linear_act_bwd(dY, t(4, 9), X, W, "silu")
+    with pytest.raises(ValueError, match="W: 8 rows"):
+        i8.linear_act_bwd(dY, Z, X, t(9, 16), "silu")
+    with pytest.raises(ValueError, match="X: shape"):
+        i8.linear_act_bwd(dY, Z, t(5, 16), W, "silu")
+    with pytest.raises(ValueError, match="dX"):
+        i8.linear_act_bwd(dY, Z, X, W, "silu", dX=t(4, 15))
+    with pytest.raises(TypeError, match="dbias"):
+        i8.linear_act_bwd(dY, Z, X, W, "silu", want_dbias=True, dbias=t(8))
+    with pytest.raises(ValueError, match="colmax_x"):
+        i8.linear_act_bwd(dY, Z, X, W, "silu", colmax_x=t(15, dtype=f32))
+
+
+G = 1 << 30
+
+
+def _lact(call="fwd", opts=(0, 0, 0), cx=None, cw=None, ws=40 * G, n=1 << 30, q=41 * G, ldq=64, sc=42 * G, **over):
+    a = dict(M=100, N=48, K=64, X=1 * G, ldx=64, W=2 * G, ldw=64, activation=2, bias=3 * G, residual=4 * G, ld_residual=48,
+             Y=5 * G, ldy=48, Z=6 * G, ldz=48)
+    p = i8._LinearAct(**{**a, **over})
+    o = None if opts is None else i8._Opts(*opts)
+    if call == "fwd":
+        return L.i8mp_linear_act_fwd(p, o, cx, cw, ws, n, None)
+    return L.i8mp_linear_wq_fwd(p, q, ldq, sc, ws, n, None)
+
+
+def test_linear_act_abi_validation():
+    for call in ("fwd", "wq"):
+        assert accepted(lambda: _lact(call))
+        assert accepted(lambda: _lact(call, bias=None, residual=None, Z=None, Y=5 * G + 2, ldy=51))
+        for bad in (dict(M=-1), dict(N=1 << 40), dict(activation=5), dict(activation=-1), dict(X=None), dict(X=G + 8), dict(ldx=60),
+                    dict(ldx=68), dict(Y=None), dict(Y=5 * G + 1), dict(ldy=47), dict(bias=3 * G + 1), dict(residual=4 * G + 8),
+                    dict(ld_residual=47), dict(ld_residual=52), dict(Z=6 * G + 1), dict(ldz=40), dict(Y=1 * G), dict(Y=4 * G),
+                    dict(Z=5 * G), dict(Z=1 * G + 64), dict(Y=3 * G), dict(M=1 << 30, N=1 << 30)):
+            assert _lact(call, **bad) == EINVAL, (call, bad)
+        assert _lact(call, K=133145, ldx=133152, ldw=133152, ldq=133152) == ERANGE
+        assert _lact(call, ws=None) == EWORKSPACE and _lact(call, ws=40 * G + 16) == EWORKSPACE and _lact(call, n=100) == EWORKSPACE
+        assert _lact(call, ws=5 * G) == EINVAL and _lact(call, ws=1 * G) == EINVAL
+        assert _lact(call, M=0, X=None, Y=None, Z=None, residual=None) == 0
+    assert _lact(opts=None) == EINVAL and _lact(opts=(2, 0, 0)) == EINVAL
+    assert _lact(W=None) == EINVAL and _lact(W=2 * G + 2) == EINVAL and _lact(ldw=60) == EINVAL and _lact(Y=2 * G) == EINVAL
+    assert accepted(lambda: _lact(cx=50 * G, cw=51 * G))
+    assert _lact(cx=50 * G, cw=50 * G) == EINVAL and _lact(cx=5 * G) == EINVAL and _lact(cx=50 * G + 2) == EINVAL
+    assert _lact("wq", q=None) == EINVAL and _lact("wq", q=41 * G + 4) == EINVAL and _lact("wq", ldq=60) == EINVAL
+    assert _lact("wq", sc=None) == EINVAL and _lact("wq", Y=41 * G) == EINVAL and _lact("wq", Y=42 * G) == EINVAL
+    need = L.i8mp_linear_act_workspace_bytes(100, 48, 64, 0)
+    assert accepted(lambda: _lact(n=need)) and _lact(n=need - 1) == EWORKSPACE
+    assert L.i8mp_linear_act_workspace_bytes(-1, 1, 1, 0) == 0 and L.i8mp_linear_wq_workspace_bytes(1, 1, 1 << 41) == 0
+
+
+def _lbwd(opts=(0, 0, 0), cx=None, cw=None, ws=40 * G, n=1 << 30, **over):
+    a = dict(M=100, N=48, K=64, dY=1 * G, lddy=48, Z=2 * G, ldz=48, X=3 * G, ldx=64, W=4 * G, ldw=64, activation=4, dX=5 * G,
+             lddx=64, dW=6 * G, lddw=64, dbias=7 * G)
+    return L.i8mp_linear_act_bwd(i8._LinearActGrad(**{**a, **over}), None if opts is None else i8._Opts(*opts), cx, cw, ws, n, None)
+
+
+def test_linear_act_bwd_abi_validation():
+    assert accepted(lambda: _lbwd()) and accepted(lambda: _lbwd(activation=0, Z=None))
+    assert accepted(lambda: _lbwd(dX=None, W=None)) and accepted(lambda: _lbwd(dW=None, X=None))
+    for bad in (dict(opts=None), dict(opts=(3, 0, 0)), dict(activation=9), dict(M=-1), dict(dY=None), dict(dY=G + 8), dict(lddy=44),
+                dict(Z=None), dict(ldz=44), dict(Z=2 * G + 2), dict(X=None), dict(W=None), dict(ldx=60), dict(ldw=68), dict(lddx=63),
+                dict(lddw=63), dict(dX=5 * G + 1), dict(dbias=7 * G + 2), dict(dX=6 * G), dict(dX=1 * G), dict(dW=3 * G),
+                dict(dbias=2 * G), dict(dbias=5 * G), dict(cx=8 * G + 2), dict(cw=5 * G), dict(ws=1 * G), dict(ws=7 * G)):
+        assert _lbwd(**bad) == EINVAL, bad
+    assert _lbwd(M=133145) == ERANGE and _lbwd(N=133152, lddy=133152, ldz=133152) == ERANGE
+    assert accepted(lambda: _lbwd(M=133145, dW=None))
+    need = L.i8mp_linear_act_workspace_bytes(100, 48, 64, 1)
+    assert accepted(lambda: _lbwd(n=need)) and _lbwd(n=need - 1) == EWORKSPACE and _lbwd(ws=None) == EWORKSPACE
+    assert _lbwd(dX=None, dW=None, dbias=None) == 0 and _lbwd(M=0, N=0, dY=None, Z=None) == 0
+
+
+def test_activation_derivatives_are_the_derivatives():
+    from tests import operators_ref as ref
+    z = torch.linspace(-8, 8, 999, dtype=f64) + 1e-3
+    for act in i8.ACTIVATIONS:
+        slope = (ref.activation(z + 1e-5, act) - ref.activation(z - 1e-5, act)) / 2e-5
+        assert torch.allclose(slope, ref.activation_grad(z, act), atol=1e-8)

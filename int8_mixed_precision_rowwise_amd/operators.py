@@ -23,25 +23,37 @@ __all__ = ["ACTIVATIONS", "linear_act_fwd", "linear_act_fwd_train", "linear_act_
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _PAIRS = {"half": 0, "interleaved": 1}
-
-
-def _on(dev: torch.device):
-    """(device guard or None, raw stream): the guard only where another GPU is current."""
-    guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-    return guard, torch.cuda.current_stream(dev).cuda_stream
+_POSITIONS = {torch.int64: 64, torch.int32: 32}
 
 
 def _call(dev: torch.device, name: str, *args):
     """lib.<name>(*args, stream) on dev's current stream, its status checked."""
-    guard, stream = _on(dev)
-    f = getattr(_pkg.lib, name)
-    if guard is None:
+    f, index = getattr(_pkg.lib, name), dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
         st = f(*args, stream)
-    else:
-        with guard:
+    else:  # another GPU is current
+        with torch.cuda.device(dev):
             st = f(*args, stream)
     if st:
         raise _pkg.I8mpError(st, name)
+
+
+def _on_gpu(first: torch.Tensor, *others) -> bool:
+    """Whether all the given tensors live on one GPU (the refusal's words come from _pkg._device)."""
+    dev = first.get_device()
+    if dev < 0:
+        return False
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            return False
+    return True
+
+
+# A call for a few tokens is over in a few microseconds, which is what the
+# checks below cost one after the other.  So each operator first asks whether
+# everything is as it should be, reading every property once, and only a call
+# that is not goes through the checks that find the words for it.
 
 
 # --------------------------------------------------------------------------- linears with an epilogue
@@ -88,7 +100,37 @@ def _space(workspace, need: int, dev):
 
 def _act_forward(X, W, w_scale, bias, activation, residual, out, workspace, keep_z=False):
     """Checks of a forward; (the C structure, device, Y, Z)."""
-    act = _activation(activation)
+    try:
+        (M, K), (N, KW) = X.shape, W.shape
+        sx, sw, act = X.stride(), W.stride(), _ACT[activation]
+        fine = (X.dtype == _bf and K == KW and K > 0 and M > 0 and sx[1] == 1 and sx[0] >= K and sw[1] == 1 and sw[0] >= K
+                and W.dtype == (_bf if w_scale is None else torch.int8) and _on_gpu(X, W, w_scale, bias, residual, out, workspace))
+        if w_scale is not None:
+            fine = fine and w_scale.shape == (N,) and w_scale.dtype == torch.float32 and w_scale.is_contiguous()
+        if bias is not None:
+            fine = fine and bias.shape == (N,) and bias.dtype == _bf and bias.is_contiguous()
+        for t in (residual, out):
+            if t is not None:
+                st = t.stride()
+                fine = fine and t.shape == (M, N) and t.dtype == _bf and st[1] == 1 and st[0] >= N
+        if workspace is not None:
+            fine = fine and workspace.dtype == torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous()
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _act_forward_checks(X, W, w_scale, bias, activation, residual, out, workspace)
+        (M, K), N, act = X.shape, W.shape[0], _ACT[activation]
+    dev = X.device
+    Y = _new_rows(M, N, dev) if out is None else out
+    Z = _new_rows(M, N, dev) if keep_z and act else None
+    p = _pkg._LinearAct(M, N, K, X.data_ptr(), _ld2(X), None if w_scale is not None else W.data_ptr(), _ld2(W), act, _ptr(bias),
+                        _ptr(residual), 0 if residual is None else _ld2(residual), Y.data_ptr(), _ld2(Y), _ptr(Z),
+                        0 if Z is None else _ld2(Z))
+    return p, dev, Y, Z
+
+
+def _act_forward_checks(X, W, w_scale, bias, activation, residual, out, workspace):
+    _activation(activation)
     _pkg._mat(X, "X", _bf)
     M, K = X.shape
     if w_scale is None:
@@ -108,13 +150,7 @@ def _act_forward(X, W, w_scale, bias, activation, residual, out, workspace, keep
         _pkg._mat(out, "out", _bf, (M, N))
     if workspace is not None:
         _pkg._workspace(workspace)
-    dev = _pkg._device(X, W, w_scale, bias, residual, out, workspace)
-    Y = _new_rows(M, N, dev) if out is None else out
-    Z = _new_rows(M, N, dev) if keep_z and act else None
-    p = _pkg._LinearAct(M, N, K, _ptr(X), _ld2(X), None if w_scale is not None else _ptr(W), _ld2(W), act, _ptr(bias),
-                        _ptr(residual), 0 if residual is None else _ld2(residual), _ptr(Y), _ld2(Y), _ptr(Z),
-                        0 if Z is None else _ld2(Z))
-    return p, dev, Y, Z
+    _pkg._device(X, W, w_scale, bias, residual, out, workspace)
 
 
 def linear_act_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "none",
@@ -257,6 +293,47 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, fre
     with 2i + 1.  ``inverse`` turns back, which is also the backward: it takes
     the gradients of q' and k' to those of q and k.  out_q / out_k: where to
     write, any strides; q and k themselves for a rotation in place."""
+    try:
+        B, S, HQ, D = q.shape
+        dtype, half = q.dtype, freqs.shape[0]
+        at = positions.shape
+        fine = (dtype in _DTYPE and pairs in _PAIRS and 1 <= half and 2 * half <= D <= 4096 and D % 2 == 0
+                and freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous() and positions.dtype in _POSITIONS
+                and (at == (B, S) or at == (S,)) and _on_gpu(q, k, positions, freqs, out_q, out_k))
+        xq = q.stride()
+        fine = fine and xq[3] == 1
+        HK = 0
+        if k is not None:
+            HK, xk = k.shape[2], k.stride()
+            fine = fine and k.shape == (B, S, HK, D) and k.dtype == dtype and xk[3] == 1
+        for out, heads in ((out_q, HQ), (out_k, HK if k is not None else -1)):
+            if out is not None:
+                fine = fine and out.shape == (B, S, heads, D) and out.dtype == dtype and out.stride(3) == 1
+    except (AttributeError, IndexError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _rotary_checks(q, k, positions, freqs, pairs, out_q, out_k)
+        B, S, HQ, D = q.shape
+        dtype, half, at, xq = q.dtype, freqs.shape[0], positions.shape, q.stride()
+        HK, xk = (0, None) if k is None else (k.shape[2], k.stride())
+    if out_q is None:
+        out_q = torch.empty_like(q, memory_format=torch.contiguous_format)
+    y = out_q.stride()
+    hq = _pkg._Heads(q.data_ptr(), out_q.data_ptr(), HQ, xq[0], xq[1], xq[2], y[0], y[1], y[2])
+    hk = None
+    if k is not None:
+        if out_k is None:
+            out_k = torch.empty_like(k, memory_format=torch.contiguous_format)
+        y = out_k.stride()
+        hk = _pkg._Heads(k.data_ptr(), out_k.data_ptr(), HK, xk[0], xk[1], xk[2], y[0], y[1], y[2])
+    p = positions.stride()
+    _call(q.device, "i8mp_rotary", hq, hk, B, S, D, 2 * half, _DTYPE[dtype], _PAIRS[pairs], 1 if inverse else 0, positions.data_ptr(),
+          _POSITIONS[positions.dtype], p[0] if len(at) == 2 else 0, p[-1], freqs.data_ptr())
+    return out_q, out_k
+
+
+def _rotary_checks(q, k, positions, freqs, pairs, out_q, out_k):
+    """rotary's checks one by one: raises what is wrong with the first that fails."""
     dtype = q.dtype if isinstance(q, torch.Tensor) else None
     _heads(q, "q", dtype)
     B, S, HQ, D = q.shape
@@ -287,23 +364,7 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, fre
         _heads(out_k, "out_k", dtype, (B, S, D))
         if out_k.shape[2] != HK:
             raise ValueError(f"out_k: {HK} heads expected, got {out_k.shape[2]}")
-    dev = _pkg._device(q, k, positions, freqs, out_q, out_k)
-    if out_q is None:
-        out_q = torch.empty((B, S, HQ, D), dtype=dtype, device=dev)
-    if k is not None and out_k is None:
-        out_k = torch.empty((B, S, HK, D), dtype=dtype, device=dev)
-    xb, xs, xh, _ = q.stride()
-    yb, ys, yh, _ = out_q.stride()
-    hq = _pkg._Heads(q.data_ptr(), out_q.data_ptr(), HQ, xb, xs, xh, yb, ys, yh)
-    hk = None
-    if k is not None:
-        xb, xs, xh, _ = k.stride()
-        yb, ys, yh, _ = out_k.stride()
-        hk = _pkg._Heads(k.data_ptr(), out_k.data_ptr(), HK, xb, xs, xh, yb, ys, yh)
-    pb, ps = positions.stride() if positions.dim() == 2 else (0, positions.stride(0))
-    _call(dev, "i8mp_rotary", hq, hk, B, S, D, rot, _DTYPE[dtype], _PAIRS[pairs], int(inverse), positions.data_ptr(),
-          64 if positions.dtype == torch.int64 else 32, pb, ps, freqs.data_ptr())
-    return out_q, out_k
+    _pkg._device(q, k, positions, freqs, out_q, out_k)
 
 
 # --------------------------------------------------------------------------- distillation loss
@@ -333,6 +394,43 @@ def _per_row(t, name: str, dtypes, T: int):
 def _distill(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index, grad=None, stats=None,
              out=None, workspace=None, backward=False):
     """Checks of the loss's inputs: (the C structure, device, T, V)."""
+    try:
+        (T, V), (_, k) = logits.shape, teacher.shape
+        sl, st, si = logits.stride(), teacher.stride(), idx.stride()
+        fine = (T > 0 and 0 < k <= DISTILL_MAX_KEPT and V > 0 and teacher.shape[0] == T and idx.shape == teacher.shape
+                and logits.dtype in _DTYPE and teacher.dtype in _DTYPE and idx.dtype in _POSITIONS
+                and sl[1] == 1 and st[1] == 1 and si[1] == 1 and sl[0] >= V and st[0] >= k and si[0] >= k
+                and 0 < temperature < math.inf and math.isfinite(ce_weight)
+                and _on_gpu(logits, teacher, idx, teacher_lse, labels, grad, stats, out, workspace))
+        if teacher_lse is not None:
+            fine = fine and teacher_lse.shape == (T,) and teacher_lse.dtype == torch.float32 and teacher_lse.is_contiguous()
+        if labels is not None:
+            fine = fine and labels.shape == (T,) and labels.dtype in _POSITIONS and labels.is_contiguous()
+        elif ce_weight:
+            fine = False
+        if backward:
+            fine = fine and grad.shape == (T,) and grad.dtype == torch.float32
+            if stats is not None:
+                fine = fine and stats.shape == (T, DISTILL_STATS) and stats.dtype == torch.float64 and stats.is_contiguous()
+            if out is not None:
+                so = out.stride()
+                fine = fine and out.shape == (T, V) and out.dtype == logits.dtype and so[1] == 1 and so[0] >= V
+        if workspace is not None:
+            fine = fine and workspace.dtype == torch.uint8 and workspace.dim() == 1 and workspace.is_contiguous()
+    except (AttributeError, IndexError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _distill_checks(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, grad, stats, out, workspace, backward)
+        (T, V), k = logits.shape, teacher.shape[1]
+    p = _pkg._Distill(logits.data_ptr(), T, V, _ld2(logits), _DTYPE[logits.dtype], teacher.data_ptr(), _ld2(teacher),
+                      _DTYPE[teacher.dtype], idx.data_ptr(), _ld2(idx), _POSITIONS[idx.dtype], k,
+                      temperature, None if teacher_lse is None else teacher_lse.data_ptr(),
+                      None if labels is None else labels.data_ptr(),
+                      0 if labels is None else _POSITIONS[labels.dtype], ignore_index, ce_weight)
+    return p, logits.device, T, V
+
+
+def _distill_checks(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, grad, stats, out, workspace, backward):
     _rows(logits, "logits", tuple(_DTYPE))
     T, V = logits.shape
     _rows(teacher, "teacher", tuple(_DTYPE))
@@ -364,13 +462,7 @@ def _distill(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, 
             _pkg._mat(out, "out", logits.dtype, (T, V))
     if workspace is not None:
         _pkg._workspace(workspace)
-    dev = _pkg._device(logits, teacher, idx, teacher_lse, labels, grad, stats, out, workspace)
-    p = _pkg._Distill(logits.data_ptr(), T, V, _ld2(logits), _DTYPE[logits.dtype], teacher.data_ptr(), _ld2(teacher),
-                      _DTYPE[teacher.dtype], idx.data_ptr(), _ld2(idx), 64 if idx.dtype == torch.int64 else 32, k,
-                      temperature, None if teacher_lse is None else teacher_lse.data_ptr(),
-                      None if labels is None else labels.data_ptr(),
-                      0 if labels is None else 64 if labels.dtype == torch.int64 else 32, ignore_index, ce_weight)
-    return p, dev, T, V
+    _pkg._device(logits, teacher, idx, teacher_lse, labels, grad, stats, out, workspace)
 
 
 def _distill_ws(p, dev, workspace):

@@ -55,18 +55,18 @@ __device__ __forceinline__ float activation(float z) {
   return z;
 }
 
-// exp(x): 2^(x log2(e)) with the product's low part, 0 below -100.
+// exp(x) for x <= 0: 2^(x log2(e)) with the product's low part (0 where fp32 ends).
 __device__ __forceinline__ float exp_full(float x) {
-  x = __builtin_fmaxf(x, -100.0f);
+  x = __builtin_fmaxf(x, -150.0f);
   const float h = x * kLog2eF;
   const float l = __builtin_fmaf(x, 1.9259629911266175e-8f, __builtin_fmaf(x, kLog2eF, -h));
   const float e = exp2_hw(h);
   return __builtin_fmaf(e, l * 0.69314718055994531f, e);
 }
-// 1 / d for d >= 1 (infinity gives 0).
+// 1 / d for finite d >= 1.
 __device__ __forceinline__ float rcp_full(float d) {
   const float r = __builtin_amdgcn_rcpf(d);
-  return d < 3.0e38f ? __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r) : r;
+  return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
 }
 // 1 / (1 + exp(-x)) and 1 minus that, each to its own relative accuracy.
 __device__ __forceinline__ void sigmoid_pair(float x, float& s, float& c) {
@@ -76,7 +76,7 @@ __device__ __forceinline__ void sigmoid_pair(float x, float& s, float& c) {
   c = x < 0.0f ? r : q;
 }
 
-// The derivative at z.
+// The derivative at z (NaN at an infinity, as z times 0 in the formulas has it).
 template <int ACT>
 __device__ __forceinline__ float activation_grad(float z) {
   if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;

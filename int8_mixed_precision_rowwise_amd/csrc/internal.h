@@ -219,7 +219,7 @@ struct ActBwdArgs {
   int64_t np, mp;  // N and M padded to 16: pitch of the codes, rows of the column codes (padding is zero)
   int8_t *row_codes, *col_codes;
   float *row_scale, *col_scale, *dbias;
-  uint16_t *segmax, *band_max;
+  uint16_t *segmax, *band_max, *col_max;
   float* band_sum;
   uint64_t seed, row_offset, col_offset;
   int64_t rows_per_band, rows_per_block;
@@ -228,6 +228,7 @@ struct ActBwdArgs {
 void act_bwd_plan(ActBwdArgs& a);  // np, mp and the launch shapes from M and N
 size_t act_bwd_segmax_bytes(const ActBwdArgs& a);
 size_t act_bwd_band_elems(const ActBwdArgs& a);  // of band_max and of band_sum
+size_t act_bwd_columns(const ActBwdArgs& a);     // elements of col_max
 hipError_t launch_act_bwd(const ActBwdArgs& a, int act, int round, hipStream_t stream);
 
 // Distillation from a teacher's top logits; see i8mp_distill_*.

@@ -6,10 +6,9 @@
 // The main loop is the pipelined GEMM's (gemm_pipelined.h).  As separate passes
 // bias, activation and residual would read and write the M x N output up to three
 // times more; here they cost the epilogue's arithmetic and the residual's one
-// read.  The accumulators hold z between the two outputs, which go through the
-// wave's own part of LDS one after the other to leave as whole row segments.  The
-// residual's loads go out before anything else of the epilogue, in the
-// accumulators' layout (8 bytes a lane; the four blocks of a row share its lines).
+// read.  Both outputs go through the wave's own part of LDS to leave as whole row
+// segments, and the residual comes in the same way: its loads go out before
+// anything else of the epilogue.
 //
 // Contractions that are no multiple of 16 are padded: whoever writes the first
 // operand's codes fills the padding with zeros, and the second's padding may
@@ -20,26 +19,39 @@
 namespace i8mp {
 namespace {
 
-// Whole rows of a wave's WM x WN bf16 region of LDS (chunk c of row r at chunk
-// c ^ (r mod chunks per row)) to memory.
-template <int WM, int WN>
+// Rows of a wave's ROWS x WN bf16 region of LDS (16-byte chunk c of row r at
+// chunk c ^ (r mod chunks per row)) to memory: 16 bytes a lane, or, for rows that
+// start anywhere, one element a lane and row.
+template <int ROWS, int WN, bool VEC>
 __device__ __forceinline__ void rows_out(const int8_t* mine, __bf16* __restrict__ C, int64_t ldc, int64_t mw, int64_t nw,
                                          int64_t M, int64_t N, int lane) {
-  constexpr int CPR = WN / 8, PITCH = WN * 2, RPI = 64 / CPR;
-  const int c = lane % CPR;
-#pragma unroll 4
-  for (int r0 = 0; r0 < WM; r0 += RPI) {
-    const int r = r0 + lane / CPR;
-    const uint4 v = *reinterpret_cast<const uint4*>(mine + r * PITCH + ((c ^ (r & (CPR - 1))) << 4));
-    const int64_t m = mw + r, n = nw + 8 * c;
-    if (m < M) {
-      __bf16* dst = C + m * ldc + n;
-      if (n + 8 <= N) {
-        __builtin_nontemporal_store(__builtin_bit_cast(v4i, v), reinterpret_cast<v4i*>(dst));
-      } else if (n < N) {
-        const __bf16* hv = reinterpret_cast<const __bf16*>(&v);
-        for (int e = 0; e < 8 && n + e < N; ++e) dst[e] = hv[e];
+  constexpr int CPR = WN / 8, PITCH = WN * 2;
+  if constexpr (VEC) {
+    constexpr int RPI = 64 / CPR;
+    const int c = lane % CPR;
+    const int64_t n = nw + 8 * c;
+    __bf16* dst = C + (mw + lane / CPR) * ldc + n;
+#pragma unroll
+    for (int r0 = 0; r0 < ROWS; r0 += RPI, dst += RPI * ldc) {
+      const int r = r0 + lane / CPR;
+      const uint4 v = *reinterpret_cast<const uint4*>(mine + r * PITCH + ((c ^ (r & (CPR - 1))) << 4));
+      if (mw + r < M) {
+        if (n + 8 <= N) {
+          __builtin_nontemporal_store(__builtin_bit_cast(v4i, v), reinterpret_cast<v4i*>(dst));
+        } else if (n < N) {
+          const __bf16* hv = reinterpret_cast<const __bf16*>(mine + r * PITCH + ((c ^ (r & (CPR - 1))) << 4));
+#pragma unroll 1
+          for (int e = 0; n + e < N; ++e) dst[e] = hv[e];
+        }
       }
+    }
+  } else {
+    static_assert(WN == 64, "one column a lane");
+    const int64_t n = nw + lane;
+#pragma unroll 8
+    for (int r = 0; r < ROWS; ++r) {
+      const __bf16 v = *reinterpret_cast<const __bf16*>(mine + r * PITCH + (((lane >> 3) ^ (r & (CPR - 1))) << 4) + 2 * (lane & 7));
+      if (mw + r < M && n < N) C[(mw + r) * ldc + n] = v;
     }
   }
 }
@@ -48,90 +60,85 @@ __device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 struct ActEpilogue : Epilogue {
-  template <int BM, int BN, int TM, int TN, bool VEC, int ACT, bool RES>
-  __device__ __forceinline__ void run(v4i (&acc)[TM][TN], int64_t m0, int64_t n0, int wm, int wn, int64_t M, int64_t N,
+  // The wave's rows in two halves, so that its LDS holds both outputs of one:
+  // y (where the residual's rows wait to be added) and z.
+  template <int BM, int BN, int TM, int TN, bool VEC, int ACT, bool RES, bool KEEP>
+  __device__ __forceinline__ void run(const v4i (&acc)[TM][TN], int64_t m0, int64_t n0, int wm, int wn, int64_t M, int64_t N,
                                       const float* s_lds, int8_t* stage, __bf16* __restrict__ C, int64_t ldc, int lane,
                                       int wave) const {
     constexpr int WM = 16 * TM, WN = 16 * TN, CPR = WN / 8, PITCH = WN * 2;
-    int8_t* mine = stage + wave * (WM * PITCH);
+    constexpr int ROWS = WM / 2, RPI = 64 / CPR, LOADS = ROWS / RPI;
+    int8_t* ybuf = stage + wave * (WM * PITCH);
+    int8_t* zbuf = ybuf + ROWS * PITCH;
     const int mr = lane & 15, q = lane >> 4;
     const int64_t mw = m0 + wm, nw = n0 + wn;
-    uint2 res[RES ? TM : 1][RES ? TN : 1];
-    if constexpr (RES) {
+    uint4 res[RES ? 2 * LOADS : 1];
+    if constexpr (RES) {  // whole row segments, 16 bytes a lane; rows are padded to 16 bytes
+      const int64_t n = nw + 8 * (lane % CPR);
+      const uint16_t* src = residual + (mw + lane / CPR) * ld_residual + n;
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int64_t m = mw + 16 * i + mr;
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const int64_t n4 = nw + 16 * j + 4 * q;
-          res[i][j] = m < M && n4 < N ? *reinterpret_cast<const uint2*>(residual + m * ld_residual + n4) : make_uint2(0, 0);
-        }
-      }
+      for (int k = 0; k < 2 * LOADS; ++k, src += RPI * ld_residual)
+        res[k] = n < N && mw + k * RPI + lane / CPR < M ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
     }
-    // z in the accumulators' place
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const float4 sbq = *reinterpret_cast<const float4*>(s_lds + BM + wn + 16 * j + 4 * q);
-      const float4 bq = *reinterpret_cast<const float4*>(s_lds + BM + BN + wn + 16 * j + 4 * q);
-      const float sbv[4] = {sbq.x, sbq.y, sbq.z, sbq.w}, bv[4] = {bq.x, bq.y, bq.z, bq.w};
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const float sam = s_lds[wm + 16 * i + mr];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float y = (float)acc[i][j][e] * sam;
-          acc[i][j][e] = __float_as_int(__builtin_fmaf(y, sbv[e], bv[e]));
-        }
-      }
-    }
-    // one output: f(i, j, e) in the accumulators' layout
-    auto out = [&](__bf16* __restrict__ dst, int64_t ld, auto f) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int r = 16 * i + mr;
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          __bf16 h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = (__bf16)f(i, j, e);
-          if constexpr (VEC) {
-            const int chunk = 2 * j + (q >> 1);
-            *reinterpret_cast<uint2*>(mine + r * PITCH + ((chunk ^ (r & (CPR - 1))) << 4) + 8 * (q & 1)) = __builtin_bit_cast(uint2, h);
-          } else {
-            const int64_t m = mw + r, n4 = nw + 16 * j + 4 * q;
-            if (m < M) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (n4 + e < N) dst[m * ld + n4 + e] = h[e];
-            }
-          }
-        }
-      }
-      if constexpr (VEC) {  // the region is this wave's own, and its LDS operations stay in order
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        rows_out<WM, WN>(mine, dst, ld, mw, nw, M, N, lane);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      }
-    };
-    if (z)
-      out(reinterpret_cast<__bf16*>(z), ld_z, [&](int i, int j, int e) __attribute__((always_inline)) { return __int_as_float(acc[i][j][e]); });
-    out(C, ldc, [&](int i, int j, int e) __attribute__((always_inline)) {
-      float y = activation<ACT>(__int_as_float(acc[i][j][e]));
+    for (int h = 0; h < 2; ++h) {
       if constexpr (RES) {
-        const uint32_t w = e < 2 ? res[i][j].x : res[i][j].y;
-        y += e & 1 ? hi_bf16(w) : lo_bf16(w);
+#pragma unroll
+        for (int k = 0; k < LOADS; ++k) {
+          const int r = k * RPI + lane / CPR;
+          *reinterpret_cast<uint4*>(ybuf + r * PITCH + (((lane % CPR) ^ (r & (CPR - 1))) << 4)) = res[h * LOADS + k];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
-      return y;
-    });
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const float4 sbq = *reinterpret_cast<const float4*>(s_lds + BM + wn + 16 * j + 4 * q);
+        const float4 bq = *reinterpret_cast<const float4*>(s_lds + BM + BN + wn + 16 * j + 4 * q);
+        const float sbv[4] = {sbq.x, sbq.y, sbq.z, sbq.w}, bv[4] = {bq.x, bq.y, bq.z, bq.w};
+#pragma unroll
+        for (int ii = 0; ii < TM / 2; ++ii) {
+          const int i = h * (TM / 2) + ii, r = 16 * ii + mr;
+          const float sam = s_lds[wm + 16 * i + mr];
+          const int off = r * PITCH + (((2 * j + (q >> 1)) ^ (r & (CPR - 1))) << 4) + 8 * (q & 1);
+          float zv[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) zv[e] = __builtin_fmaf((float)acc[i][j][e] * sam, sbv[e], bv[e]);
+          if constexpr (KEEP) {
+            const __bf16 hz[4] = {(__bf16)zv[0], (__bf16)zv[1], (__bf16)zv[2], (__bf16)zv[3]};
+            *reinterpret_cast<uint2*>(zbuf + off) = __builtin_bit_cast(uint2, hz);
+          }
+          uint2 rv = make_uint2(0, 0);
+          if constexpr (RES) rv = *reinterpret_cast<const uint2*>(ybuf + off);
+          const float rf[4] = {lo_bf16(rv.x), hi_bf16(rv.x), lo_bf16(rv.y), hi_bf16(rv.y)};
+          __bf16 hy[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = activation<ACT>(zv[e]);
+            hy[e] = (__bf16)(RES ? y + rf[e] : y);
+          }
+          *reinterpret_cast<uint2*>(ybuf + off) = __builtin_bit_cast(uint2, hy);
+        }
+      }
+      // the region is this wave's own, and its LDS operations stay in order
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      rows_out<ROWS, WN, VEC>(ybuf, C, ldc, mw + h * ROWS, nw, M, N, lane);
+      if constexpr (KEEP) rows_out<ROWS, WN, VEC>(zbuf, reinterpret_cast<__bf16*>(z), ld_z, mw + h * ROWS, nw, M, N, lane);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
   }
 
   template <int BM, int BN, int TM, int TN, bool VEC>
-  __device__ __forceinline__ void store(v4i (&acc)[TM][TN], int64_t m0, int64_t n0, int wm, int wn, int64_t M, int64_t N,
+  __device__ __forceinline__ void store(const v4i (&acc)[TM][TN], int64_t m0, int64_t n0, int wm, int wn, int64_t M, int64_t N,
                                         const float* s_lds, int8_t* stage, __bf16* __restrict__ C, int64_t ldc, int lane,
                                         int wave) const {
 #define I8MP_RUN(A)                                                                                                    \
-  if (residual) run<BM, BN, TM, TN, VEC, A, true>(acc, m0, n0, wm, wn, M, N, s_lds, stage, C, ldc, lane, wave);        \
-  else run<BM, BN, TM, TN, VEC, A, false>(acc, m0, n0, wm, wn, M, N, s_lds, stage, C, ldc, lane, wave);                \
+  if (residual) {                                                                                                      \
+    if (z) run<BM, BN, TM, TN, VEC, A, true, true>(acc, m0, n0, wm, wn, M, N, s_lds, stage, C, ldc, lane, wave);       \
+    else run<BM, BN, TM, TN, VEC, A, true, false>(acc, m0, n0, wm, wn, M, N, s_lds, stage, C, ldc, lane, wave);        \
+  } else {                                                                                                             \
+    if (z) run<BM, BN, TM, TN, VEC, A, false, true>(acc, m0, n0, wm, wn, M, N, s_lds, stage, C, ldc, lane, wave);      \
+    else run<BM, BN, TM, TN, VEC, A, false, false>(acc, m0, n0, wm, wn, M, N, s_lds, stage, C, ldc, lane, wave);       \
+  }                                                                                                                    \
   break
     switch (act) {
       case kActRelu: I8MP_RUN(kActRelu);

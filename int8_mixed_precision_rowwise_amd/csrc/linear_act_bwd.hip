@@ -6,8 +6,9 @@
 // Both quantizations need maxima over the whole of a row and a column, so two
 // passes are the least: the first reads dY and Z, writes dZ and leaves the maxima
 // of every row's segment of 512 columns, the column maxima and the column sums of
-// every band of rows; the second reads dZ once for both sets of codes.  8 (then
-// 4) bytes an element with few operations: both are bound by memory.  A
+// every band of rows; a short launch joins the bands; the second pass reads dZ once
+// for both sets of codes.  6 and 4 bytes an element: both passes are bound by
+// memory (GELU's derivative, some 40 operations, comes near).  A
 // block is 8 waves; a lane owns 8 adjacent columns, a wave a 512-column segment of
 // a row, so a row's maximum is one wave reduction and the columns' sums and maxima
 // stay in the lane's registers over its rows.  Sums are joined in a fixed order:
@@ -21,7 +22,7 @@ namespace i8mp {
 namespace {
 
 constexpr int kTile = 512, kWaves = 8, kBwdThreads = 64 * kWaves;
-constexpr int kMaxBands = 32;  // bands of rows in the first pass
+constexpr int kMaxBands = 256, kBandRows = 32;  // bands of rows in the first pass, at most, of so many rows at least
 constexpr int kMaxBlockRows = 512;  // rows of a block of the second
 
 __device__ __forceinline__ us2 max_us2(us2 a, uint32_t w) { return __builtin_elementwise_max(a, as_us2(w)); }
@@ -102,11 +103,35 @@ __global__ __launch_bounds__(kBwdThreads) void act_grad_stats(ActBwdArgs a) {
   a.band_sum[((int64_t)blockIdx.y * a.tiles + blockIdx.x) * kTile + (t & 63) * 8 + (t >> 6)] = s;
 }
 
-// Second pass: blocks of rows (up to M padded) by column tiles, the tiles of a row adjacent.  Columns
-// N .. np of the row codes and rows M .. mp of the column codes become zero.
+// Column maxima (bf16 bits) and dbias of all the bands: 64
+// columns a block, its 8 waves over the bands.
+__global__ __launch_bounds__(kBwdThreads) void act_grad_join(ActBwdArgs a) {
+  __shared__ uint32_t red_max[kWaves][64];
+  __shared__ float red_sum[kWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane, pitch = (int64_t)a.tiles * kTile;  // pitch is a multiple of 64
+  uint32_t m = 0;
+  float s = 0;
+#pragma unroll 8
+  for (int b = wave; b < a.bands; b += kWaves) {
+    m = max(m, (uint32_t)a.band_max[b * pitch + c]);
+    s += a.band_sum[b * pitch + c];
+  }
+  red_max[wave][lane] = m, red_sum[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = max(m, red_max[w][lane]), s += red_sum[w][lane];
+    a.col_max[c] = (uint16_t)m;
+    if (a.dbias && c < a.N) a.dbias[c] = s;
+  }
+}
+
+// Second pass: blocks of rows (up to M padded) by column tiles, the tiles of a
+// row adjacent.  Columns N .. np of the row codes and rows M .. mp of the column
+// codes become zero.
 template <bool SR, bool ALIGNED4>
 __global__ __launch_bounds__(kBwdThreads) void act_grad_quant(ActBwdArgs a) {
-  __shared__ uint4 red[kWaves][64];
   __shared__ uint32_t row_max[kMaxBlockRows];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tile = (int)(blockIdx.x % a.tiles);
@@ -116,19 +141,15 @@ __global__ __launch_bounds__(kBwdThreads) void act_grad_quant(ActBwdArgs a) {
   const int64_t r_end = min(a.mp, r_begin + a.rows_per_block);
   const int nvalid = (int)max((int64_t)0, min((int64_t)8, a.N - c0));
   const int64_t cl = nvalid > 0 ? c0 : 0;
-  us2 cm[4] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}};
-  for (int b = wave; b < a.bands; b += kWaves)
-    max_columns(cm, *reinterpret_cast<const uint4*>(a.band_max + (int64_t)b * a.tiles * kTile + c0));
-  red[wave][lane] = pack_columns(cm);
   if (a.row_codes && threadIdx.x < a.rows_per_block && r_begin + threadIdx.x < a.M) {
     const uint16_t* seg = a.segmax + (r_begin + threadIdx.x) * a.tiles;
     uint32_t m = 0;
     for (int s = 0; s < a.tiles; ++s) m = max(m, (uint32_t)seg[s]);
     row_max[threadIdx.x] = m;
   }
+  const uint4 cb = *reinterpret_cast<const uint4*>(a.col_max + c0);
+  const us2 cm[4] = {as_us2(cb.x), as_us2(cb.y), as_us2(cb.z), as_us2(cb.w)};
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) max_columns(cm, red[w][lane]);
   GroupScale g[8];
   bool mine = true;
 #pragma unroll
@@ -138,20 +159,12 @@ __global__ __launch_bounds__(kBwdThreads) void act_grad_quant(ActBwdArgs a) {
     mine = mine && (j >= nvalid || g[j].mode == 1);
   }
   const bool all_fma = __all(mine);
-  if (block == 0) {
-    if (wave == 0 && a.col_codes) {
+  if (block == 0 && wave == 0 && a.col_codes) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < nvalid) a.col_scale[c0 + j] = g[j].s;
-    }
-    const int64_t c = (int64_t)tile * kTile + threadIdx.x;
-    if (a.dbias && c < a.N) {
-      float s = 0;
-      for (int b = 0; b < a.bands; ++b) s += a.band_sum[(int64_t)b * a.tiles * kTile + c];
-      a.dbias[c] = s;
-    }
+    for (int j = 0; j < 8; ++j)
+      if (j < nvalid) a.col_scale[c0 + j] = g[j].s;
   }
-  if (c0 >= a.np || (!a.row_codes && !a.col_codes)) return;
+  if (c0 >= a.np) return;
   constexpr int U = 4;
   for (int64_t r0 = r_begin + wave; r0 < r_end; r0 += U * kWaves) {
     uint4 v[U];
@@ -190,11 +203,11 @@ void act_bwd_plan(ActBwdArgs& a) {
   a.np = (a.N + 15) / 16 * 16;
   a.mp = (a.M + 15) / 16 * 16;
   a.tiles = (int)std::max<int64_t>(1, (a.np + kTile - 1) / kTile);
-  const int64_t bands = std::min<int64_t>(kMaxBands, (a.M + 63) / 64);
-  a.rows_per_band = bands > 0 ? (a.M + bands - 1) / bands : 1;
-  a.bands = bands > 0 ? (int)((a.M + a.rows_per_band - 1) / a.rows_per_band) : 0;
-  // about four blocks a CU of at least 32 rows (the scales cost a block
-  // 32 KiB of band maxima at the most)
+  // about eight blocks a CU, in whole turns of a block's waves over the rows
+  // (measured at 8192 x 5632, GELU: see act_grad_stats)
+  const int64_t want = std::min<int64_t>(kMaxBands, std::max<int64_t>(1, 2048 / a.tiles));
+  a.rows_per_band = std::max<int64_t>(1, ((a.M + want - 1) / want + kBandRows - 1) / kBandRows) * kBandRows;
+  a.bands = (int)((a.M + a.rows_per_band - 1) / a.rows_per_band);
   const int64_t blocks = std::max<int64_t>(1, 1024 / a.tiles);
   a.rows_per_block = std::max<int64_t>(32, (a.mp + blocks - 1) / blocks);
   a.rows_per_block = std::min<int64_t>(a.rows_per_block, kMaxBlockRows);
@@ -202,6 +215,7 @@ void act_bwd_plan(ActBwdArgs& a) {
 
 size_t act_bwd_segmax_bytes(const ActBwdArgs& a) { return (size_t)a.M * a.tiles * 2; }
 size_t act_bwd_band_elems(const ActBwdArgs& a) { return (size_t)std::max(1, a.bands) * a.tiles * kTile; }
+size_t act_bwd_columns(const ActBwdArgs& a) { return (size_t)a.tiles * kTile; }
 
 hipError_t launch_act_bwd(const ActBwdArgs& a, int act, int round, hipStream_t stream) {
   if (a.bands > 0) {
@@ -216,6 +230,9 @@ hipError_t launch_act_bwd(const ActBwdArgs& a, int act, int round, hipStream_t s
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  act_grad_join<<<(unsigned)(a.tiles * kTile / 64), kBwdThreads, 0, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || (!a.row_codes && !a.col_codes)) return e;
   const dim3 grid((unsigned)(a.tiles * std::max<int64_t>(1, (a.mp + a.rows_per_block - 1) / a.rows_per_block)));
   if (round == 0) act_grad_quant<false, true><<<grid, kBwdThreads, 0, stream>>>(a);
   else if (a.N % 4 == 0) act_grad_quant<true, true><<<grid, kBwdThreads, 0, stream>>>(a);

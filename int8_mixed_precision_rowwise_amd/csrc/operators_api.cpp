@@ -150,7 +150,7 @@ struct ActBwdWs {
   uint16_t* dz;
   int8_t *q_row, *q_col, *qw, *qx;
   float *s_row, *s_col, *sw, *sx, *band_sum;
-  uint16_t *segmax, *band_max;
+  uint16_t *segmax, *band_max, *col_max;
   void *col, *split;
 };
 size_t carve_act_bwd(void* ws, int64_t M, int64_t N, int64_t K, ActBwdWs* out) {
@@ -172,6 +172,7 @@ size_t carve_act_bwd(void* ws, int64_t M, int64_t N, int64_t K, ActBwdWs* out) {
   w.segmax = static_cast<uint16_t*>(c.take(i8mp::act_bwd_segmax_bytes(a)));
   w.band_max = static_cast<uint16_t*>(c.take(i8mp::act_bwd_band_elems(a) * 2));
   w.band_sum = static_cast<float*>(c.take(i8mp::act_bwd_band_elems(a) * 4));
+  w.col_max = static_cast<uint16_t*>(c.take(i8mp::act_bwd_columns(a) * 2));
   w.col = c.take(std::max(i8mp::colwise_workspace_bytes(N, K), i8mp::colwise_workspace_bytes(M, K)));
   const size_t split = std::max(i8mp::gemm_split_workspace_bytes(I8MP_NN, M, K, a.np, a.np, kp),
                                 i8mp::gemm_split_workspace_bytes(I8MP_TN, N, K, a.mp, a.np, kp));
@@ -451,7 +452,7 @@ i8mp_status i8mp_linear_act_bwd(const i8mp_linear_act_grad* p, const i8mp_linear
     a.row_codes = want_dx ? w.q_row : nullptr, a.row_scale = w.s_row;
     a.col_codes = want_dw ? w.q_col : nullptr, a.col_scale = w.s_col;
     a.dbias = want_db ? p->dbias : nullptr;
-    a.segmax = w.segmax, a.band_max = w.band_max, a.band_sum = w.band_sum;
+    a.segmax = w.segmax, a.band_max = w.band_max, a.band_sum = w.band_sum, a.col_max = w.col_max;
     a.seed = seed, a.row_offset = pass_offset(off, 2), a.col_offset = pass_offset(off, 4);
     e = i8mp::launch_act_bwd(a, p->activation, r, s);
   } else if (want_dx) {  // no columns: scales of zero

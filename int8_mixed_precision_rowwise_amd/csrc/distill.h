@@ -16,13 +16,11 @@
 // A step has to read every logit and write every gradient once, and nothing
 // else of size: it is bound by memory as long as a row is read once.  So one
 // workgroup holds a whole row in registers between the sums and the gradient
-// (a row of 131064 16-bit logits is half a CU's registers).  The sums are
-// taken while the row arrives, each thread rescaling its own to the maximum it
-// has seen so far; the kept entries are left out of them (their elements are
-// set to -inf in the registers) and are evaluated one per thread in 64 bits,
-// which keeps q_rest and mass q_j - p_j free of cancellation.  A table in LDS
-// from each 16-byte chunk of the row to the kept entries inside it tells a
-// thread which of its elements they are.
+// (a row of 131064 16-bit logits is half a CU's registers).  The sums are taken
+// while the row arrives, each thread rescaling its own to the maximum it has seen
+// so far; the kept entries are left out of them (a byte a chunk in LDS tells which
+// elements they are) and are evaluated one per thread in 64 bits, which keeps
+// q_rest and mass q_j - p_j free of cancellation.
 //
 // Rows too long for that, and calls with too few rows to fill the chip, take
 // two launches over (segment, row): partial sums, then the gradient with each
@@ -39,10 +37,14 @@
 
 #include "internal.h"
 
+#include <algorithm>
+#include <utility>
+
 namespace i8mp {
 namespace distill {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 
 constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
 
@@ -80,6 +82,8 @@ template <>
 struct Elem<__bf16> {
   static constexpr int E = 8;
   static constexpr uint32_t kNegInf = 0xFF80u;
+  static __device__ __forceinline__ uint32_t bits(const __bf16* p) { return *reinterpret_cast<const uint16_t*>(p); }
+  static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
   static __device__ __forceinline__ float get(const v4i& v, int e) {
     const uint32_t w = (uint32_t)v[e >> 1];
     return __uint_as_float((e & 1) ? (w & 0xFFFF0000u) : (w << 16));
@@ -89,6 +93,8 @@ template <>
 struct Elem<_Float16> {
   static constexpr int E = 8;
   static constexpr uint32_t kNegInf = 0xFC00u;
+  static __device__ __forceinline__ uint32_t bits(const _Float16* p) { return *reinterpret_cast<const uint16_t*>(p); }
+  static __device__ __forceinline__ float value(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (unsigned short)b); }
   static __device__ __forceinline__ float get(const v4i& v, int e) {
     const uint32_t w = (uint32_t)v[e >> 1];
     return (float)__builtin_bit_cast(_Float16, (unsigned short)((e & 1) ? (w >> 16) : (w & 0xFFFFu)));
@@ -98,6 +104,8 @@ template <>
 struct Elem<float> {
   static constexpr int E = 4;
   static constexpr uint32_t kNegInf = 0xFF800000u;
+  static __device__ __forceinline__ uint32_t bits(const float* p) { return *reinterpret_cast<const uint32_t*>(p); }
+  static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b); }
   static __device__ __forceinline__ float get(const v4i& v, int e) { return __uint_as_float((uint32_t)v[e]); }
 };
 
@@ -153,6 +161,23 @@ struct Row {
     v4i v = chunks[c];
     if (c == 0 || c == nchunks - 1) drop<T>(v, outside(c));
     return v;
+  }
+};
+
+// The chunks of a row held in registers, through a buffer descriptor of just
+// that row: chunks past its end are read as zeros and their writes are dropped,
+// with no branch around the access.  (A branch that may skip a load makes the
+// compiler wait for every access in flight where it needs only an older one.)
+struct RowBuffer {
+  __amdgpu_buffer_rsrc_t rsrc;
+  __device__ __forceinline__ RowBuffer(const void* p, int chunks)
+      : rsrc(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, chunks * 16, 0x00020000)) {}
+  // chunk `first` (the same in every lane) + t
+  __device__ __forceinline__ v4i load(int first, int t) const {
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc, t * 16, first * 16, 0));
+  }
+  __device__ __forceinline__ void store(int first, int t, v4i v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), rsrc, t * 16, first * 16, 2);  // non-temporal
   }
 };
 
@@ -250,6 +275,34 @@ __device__ __forceinline__ int label_at(const DistillArgs& a, int64_t row) {
   return i != a.ignore && i >= 0 && i < a.V ? (int)i : -1;
 }
 
+// The same for the row kernels, in two steps: the loads, of which none waits for
+// another, and what they give.
+struct RawIndex {
+  uint32_t lo, hi;
+  __device__ __forceinline__ void load(const void* p, int64_t at, bool wide) {
+    const uint32_t* w = static_cast<const uint32_t*>(p);
+    lo = w[wide ? 2 * at : at];
+    hi = w[wide ? 2 * at + 1 : at];
+  }
+  // the class, or -1
+  __device__ __forceinline__ int index(const DistillArgs& a, bool wide) const {
+    return lo < (uint32_t)a.V && (!wide || hi == 0) ? (int)lo : -1;
+  }
+  __device__ __forceinline__ int64_t value(bool wide) const {
+    return wide ? (int64_t)((uint64_t)hi << 32 | lo) : (int64_t)(int32_t)lo;
+  }
+};
+__device__ __forceinline__ uint32_t teacher_bits(const DistillArgs& a, int64_t at) {
+  return a.t_dtype == I8MP_FP32 ? static_cast<const uint32_t*>(a.teacher)[at] : (uint32_t) static_cast<const uint16_t*>(a.teacher)[at];
+}
+__device__ __forceinline__ float teacher_value(const DistillArgs& a, uint32_t bits) {
+  switch (a.t_dtype) {
+    case I8MP_BF16: return __uint_as_float(bits << 16);
+    case I8MP_FP16: return (float)__builtin_bit_cast(_Float16, (unsigned short)bits);
+    default: return __uint_as_float(bits);
+  }
+}
+
 // What the joined sums of a row give: the loss and the statistics.
 // sums over kept entries: W = sum w_j, A = sum w_j (ln w_j - ln e_j), e and e1;
 // w_j = exp(t_j / tau - zref), kept: how many there are.
@@ -330,56 +383,72 @@ __device__ __forceinline__ float outside_grad(const Expo<T, MODE>& ex, const Fac
   return __builtin_fmaf(e1, f.out1, e * f.out);
 }
 
-// Entry slots of one row in LDS: the chain to the chunk's next entry with the
-// element inside its chunk, then x_j, later e_j, e1_j and p_j.
-template <int KM>
-struct Slots {
-  int link[KM + 1];
-  float x[KM + 1], x1[KM + 1], p[KM + 1];  // the label's slot is number k; its p: 1 + the kept entry of its class, or 0
-};
-template <typename S>
-__device__ __forceinline__ void insert(int* first, S& s, int chunk, int elem, int j) {
-  s.link[j] = atomicExch(first + chunk, j + 1) << 3 | elem;
+// A byte for each chunk in LDS: the elements that are kept entries.
+__device__ __forceinline__ void mark(uint32_t* table, int chunk, int elem) {
+  atomicOr(table + (chunk >> 2), 1u << (8 * (chunk & 3) + elem));
+}
+__device__ __forceinline__ uint32_t marked(const uint32_t* table, int chunk) {
+  return reinterpret_cast<const uint8_t*>(table)[chunk];
 }
 
-// Gradient of one chunk, kept entries and the label put in from its chain.
-template <typename T, int MODE, typename S>
-__device__ __forceinline__ void grad_chunk(const Row<T>& row, const DistillArgs& a, const Expo<T, MODE>& ex, const Factors& f,
-                                           const S& s, v4i v, int chain, int c, T* __restrict__ d) {
+template <typename T, int MODE>
+__device__ __forceinline__ v4i grad_chunk(const Expo<T, MODE>& ex, const Factors& f, v4i v) {
   constexpr int E = Elem<T>::E;
-  float y[E];
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef T t2 __attribute__((ext_vector_type(2)));
+  struct __attribute__((aligned(16))) Out { t2 p[E / 2]; } o;
 #pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = outside_grad<T, MODE>(ex, f, Elem<T>::get(v, e));
-  if (chain) {
-    int lab = -1;
-    for (int j = chain; j;) {
-      const int link = s.link[j - 1], at = link & 7;
-      if (j - 1 == a.k) {
-        lab = at;
-      } else {
-        float value = __builtin_fmaf(f.kept, s.x[j - 1], -(f.p * s.p[j - 1]));
-        if (f.label != 0) value += __builtin_fmaf(f.c1, s.x1[j - 1], s.p[a.k] == (float)j ? -f.label : 0.0f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = at == e ? value : y[e];
-      }
-      j = link >> 3;
-    }
-    if (lab >= 0 && s.p[a.k] == 0.0f) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = lab == e ? y[e] - f.label : y[e];
-    }
+  for (int e = 0; e < E; e += 2) {  // pairs: one conversion instruction for both
+    const f2 y = {outside_grad<T, MODE>(ex, f, Elem<T>::get(v, e)), outside_grad<T, MODE>(ex, f, Elem<T>::get(v, e + 1))};
+    o.p[e / 2] = __builtin_convertvector(y, t2);
   }
-  T o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = (T)y[e];
+  return __builtin_bit_cast(v4i, o);
+}
+// A kept entry's gradient; x, x1, w: its exp((x - m) / tau), exp(x - m) and w_j.
+__device__ __forceinline__ float kept_grad(const Factors& f, float e, float e1, float w, bool is_label) {
+  float value = __builtin_fmaf(f.kept, e, -(f.p * w));
+  if (f.label != 0) value += __builtin_fmaf(f.c1, e1, is_label ? -f.label : 0.0f);
+  return value;
+}
+
+// The elements of chunk c that lie in the row, one by one.
+template <typename T>
+__device__ __forceinline__ void store_elements(const Row<T>& row, v4i v, int c, T* __restrict__ d) {
+  constexpr int E = Elem<T>::E, BITS = 8 * sizeof(T);
   T* at = d + (int64_t)c * E - row.shift;
-  const uint32_t skip = (c == 0 || c == row.nchunks - 1) ? row.outside(c) : 0;
-  if (!skip && a.d_aligned) {
-    __builtin_nontemporal_store(__builtin_bit_cast(v4i, o), reinterpret_cast<v4i*>(at));
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (!(skip >> e & 1)) at[e] = o[e];
+  const uint32_t skip = row.outside(c);
+#pragma unroll 1
+  for (int e = 0; e < E; ++e) {  // rolled: it stands behind every chunk's store and hardly ever runs
+    if (!(skip >> e & 1)) {
+      if constexpr (E == 4) at[e] = __uint_as_float((uint32_t)v[0]);
+      else at[e] = __builtin_bit_cast(T, (unsigned short)v[0]);
+    }
+    v[0] = (int)__builtin_amdgcn_alignbit((uint32_t)v[1], (uint32_t)v[0], BITS & 31);
+    v[1] = (int)__builtin_amdgcn_alignbit((uint32_t)v[2], (uint32_t)v[1], BITS & 31);
+    v[2] = (int)__builtin_amdgcn_alignbit((uint32_t)v[3], (uint32_t)v[2], BITS & 31);
+    v[3] = (int)((uint32_t)v[3] >> (BITS & 31));
+    if constexpr (E == 4) v = (v4i){v[1], v[2], v[3], 0};
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_chunk(const Row<T>& row, const DistillArgs& a, v4i v, int c, T* __restrict__ d) {
+  if (a.d_aligned && c != 0 && c != row.nchunks - 1)
+    __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(d + (int64_t)c * Elem<T>::E - row.shift));
+  else
+    store_elements<T>(row, v, c, d);
+}
+// Through the gradient row's buffer (which starts at the chunk that holds its
+// first element) where both rows start at the same place in a chunk.
+template <typename T>
+__device__ __forceinline__ void store_chunk(const Row<T>& row, const RowBuffer& out, const DistillArgs& a, v4i v, int first,
+                                            int t, T* __restrict__ d) {
+  const int c = first + t;
+  const bool edge = c == 0 || c == row.nchunks - 1;
+  if (a.d_aligned) {
+    out.store(first, edge ? row.nchunks : t, v);
+    if (edge) store_elements<T>(row, v, c, d);
+  } else if (c < row.nchunks) {
+    store_elements<T>(row, v, c, d);
   }
 }
 
@@ -396,15 +465,14 @@ struct Running {
 #pragma unroll
     for (int e = 0; e < (MODE ? S : 1); ++e) s1[e] = 0;
   }
-  // floor: a maximum of elements that v no longer holds (kept entries)
   template <int N>
-  __device__ __forceinline__ void add(const v4i (&v)[N], float floor, Expo<T, MODE>& ex, const DistillArgs& a) {
-    float m = fmaxf(max, floor);
+  __device__ __forceinline__ void add(const v4i (&v)[N], Expo<T, MODE>& ex) {
+    float m = max;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int e = 0; e < E; ++e) m = fmaxf(m, Elem<T>::get(v[i], e));
-    rescale(m, ex, a);
+    rescale(m, ex);
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -416,7 +484,7 @@ struct Running {
         if constexpr (MODE == 2) s1[e % S] += ex.e1(x, y);
       }
   }
-  __device__ __forceinline__ void rescale(float m, Expo<T, MODE>& ex, const DistillArgs& a) {
+  __device__ __forceinline__ void rescale(float m, Expo<T, MODE>& ex) {
     const float r = ex.r;
     ex.at(m);
     float f = ex.e(r - ex.r), f1 = 1;
@@ -437,196 +505,202 @@ struct Running {
   }
 };
 
-// Elements of v that its chain names: their values go to their slots, kept
-// ones are dropped from v; returns the largest dropped value.
-template <typename T, typename S>
-__device__ __forceinline__ float take_out(v4i& v, int chain, S& s, int k) {
-  float floor = -__builtin_inff();
-  uint32_t mask = 0;
-  for (int j = chain; j;) {
-    const int link = s.link[j - 1];
-    const float x = pick<T>(v, link & 7);
-    s.x[j - 1] = x;
-    if (j - 1 < k) {
-      mask |= 1u << (link & 7);
-      floor = fmaxf(floor, x);
-    }
-    j = link >> 3;
-  }
-  drop<T>(v, mask);
-  return floor;
-}
-
 // ---- one workgroup a row, the row in registers -----------------------------
+//
+// Kept entries are one (or a few) per thread, which holds their logits and writes
+// their gradient over what the row's sweep has put there, behind a barrier.
 
-template <int NT, int KM>
+template <int NT>
 struct RowLds {
-  Slots<KM> slots;
   double sums[NT / 64][6];
-  float wmax[NT / 64];
-  int kept[NT / 64];
-  int label_slot;  // 1 + the kept entry that is the label's class, or 0
-  int row_kept;
-  double zref;
-  RowStats st;
   Factors f;
+  float wmax[NT / 64], tmax[NT / 64];
+  int kept[NT / 64];
+  int label_kept;  // whether the label is a kept entry
 };
 
-constexpr int row_waves(int nt, int nv) { return nv <= 8 ? (nt == 1024 ? 8 : 6) : 4; }  // waves a SIMD
+// f(0), f(1), ... with the index a constant: a row's chunks are registers, and a
+// loop too long for the compiler to unroll would put them into memory.
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, const F& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(const F& f) {
+  each_of(std::make_integer_sequence<int, N>{}, f);
+}
 
-template <typename T, int NT, int NV, int KM, int MODE>
-__global__ __launch_bounds__(NT, row_waves(NT, NV)) void distill_rows(DistillArgs a) {
-  constexpr int W = NT / 64, E = Elem<T>::E, GROUP = 2;
-  constexpr int KPT = (KM + NT - 1) / NT;
-  __shared__ __attribute__((aligned(16))) int first[NT * NV];
-  __shared__ RowLds<NT, KM> l;
+// Sums over chunks g and g + 1 of a thread, kept entries left out (they become -inf).
+template <typename T, int MODE, int NT, int g, int N>
+__device__ __forceinline__ void stats_group(v4i (&v)[N], const Row<T>& x, const uint32_t* table, Running<T, MODE>& run,
+                                            Expo<T, MODE>& ex, int t) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = (g + i) * NT + t;
+    if ((g + i + 1) * NT > x.nchunks && c >= x.nchunks) v[g + i] = all_neg_inf(sizeof(T), Elem<T>::kNegInf);
+    if (c < x.nchunks) {
+      uint32_t mask = marked(table, c);
+      if (c == 0 || c == x.nchunks - 1) mask |= x.outside(c);
+      if (mask) drop<T>(v[g + i], mask);
+    }
+  }
+  const v4i u[2] = {v[g], v[g + 1]};
+  run.add(u, ex);
+  // The sums are wanted now: left alone, the compiler takes them where they are
+  // used, behind the barrier, and holds every term's inputs until then.
+  asm volatile("" : "+v"(run.s[0]), "+v"(run.s[1]), "+v"(run.s[2]), "+v"(run.s[3]));
+  if constexpr (MODE != 0) asm volatile("" : "+v"(run.s1[0]), "+v"(run.s1[1]), "+v"(run.s1[2]), "+v"(run.s1[3]));
+}
+
+// Waves a SIMD: what the row, 4 registers a chunk, leaves room for.
+constexpr int row_waves(int nv) { return nv <= 8 ? 5 : nv <= 16 ? 4 : nv <= 24 ? 3 : 2; }
+
+template <typename T, int NT, int NV, int KPT, int MODE>
+__global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a) {
+  constexpr int W = NT / 64, E = Elem<T>::E;
+  __shared__ uint32_t table[NT * NV / 4];
+  __shared__ RowLds<NT> l;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int k = a.k;
   const int64_t row = blockIdx.x;
-  const int V = (int)a.V, k = a.k;
-  const Row<T> x(a.logits, row, a.ld, V);
-  const int label = label_at(a, row);
-
-  // kept entries first: they are needed before the row has arrived
+  const T* xr = static_cast<const T*>(a.logits) + row * a.ld;
+  const Row<T> x(a.logits, row, a.ld, (int)a.V);
+  // entries and label first: they are needed before the row has arrived
+  RawIndex raw[KPT], raw_label{};
+  uint32_t raw_t[KPT];
+  if (k > 0) {
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      const int j = min(t + i * NT, k - 1);
+      raw[i].load(a.idx, row * a.i_ld + j, a.idx64);
+      raw_t[i] = teacher_bits(a, row * a.t_ld + j);
+    }
+  }
+  if (a.labels) raw_label.load(a.labels, row, a.lab64);
+  const float lse = a.lse ? a.lse[row] : 0.0f;
+  const RowBuffer in(x.chunks, x.nchunks);
+  v4i v[NV];
+  each<NV>([&](auto i) __attribute__((always_inline)) {
+    v[i] = in.load(i * NT, t);
+    __builtin_amdgcn_sched_barrier(0);  // in the order in which they are waited for
+  });
+  const int label = a.labels && raw_label.value(a.lab64) != a.ignore ? raw_label.index(a, a.lab64) : -1;
   int id[KPT];
   float tv[KPT];
-#pragma unroll
-  for (int i = 0; i < KPT; ++i) {
-    const int j = t + i * NT;
-    id[i] = j < k ? kept_at(a, row, j) : -1;
-    tv[i] = id[i] >= 0 ? teacher_at(a, row, j) : 0.0f;
-  }
-  v4i v[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = i * NT + t;
-    v[i] = c < x.nchunks ? x.chunks[c] : all_neg_inf(sizeof(T), Elem<T>::kNegInf);
-  }
-  for (int c = t; c < x.nchunks; c += NT) first[c] = 0;
-  if (t == 0) l.label_slot = 0;
+  uint32_t xraw[KPT];  // bits, a value only behind the row's sums: at once, it would wait for all of the row
   float tmax = -__builtin_inff();
   int kept = 0;
 #pragma unroll
+  for (int i = 0; i < KPT; ++i) {
+    id[i] = t + i * NT < k ? raw[i].index(a, a.idx64) : -1;
+    tv[i] = t + i * NT < k ? teacher_value(a, raw_t[i]) : 0.0f;
+  }
+  for (int c = t; c < NT * NV / 4; c += NT) table[c] = 0;
+  if (t == 0) l.label_kept = 0;
+#pragma unroll
   for (int i = 0; i < KPT; ++i)
     if (id[i] >= 0) tmax = fmaxf(tmax, tv[i]), ++kept;
-  if (wave * 64 < k) {
-    tmax = wave_max(tmax);
-    kept = wave_sum(kept);
-  }
-  if (lane == 0) l.wmax[wave] = tmax, l.kept[wave] = kept;
+  if (wave * 64 < k) tmax = wave_max(tmax), kept = wave_sum(kept);
+  if (lane == 0) l.tmax[wave] = tmax, l.kept[wave] = kept;
   lds_sync();
 #pragma unroll
   for (int i = 0; i < KPT; ++i) {
-    const int j = t + i * NT;
-    if (j >= k) continue;
-    if (id[i] >= 0) {
-      const int at = id[i] + x.shift;
-      l.slots.p[j] = tv[i];
-      insert(first, l.slots, at / E, at % E, j);
-      if (id[i] == label) l.label_slot = j + 1;
-    } else {
-      l.slots.link[j] = -1;
-    }
+    xraw[i] = Elem<T>::kNegInf;
+    if (id[i] < 0) continue;
+    const int at = id[i] + x.shift;
+    mark(table, at / E, at % E);
+    xraw[i] = Elem<T>::bits(xr + id[i]);
+    if (id[i] == label) l.label_kept = 1;
   }
-  if (t == 0) {
-    if (label >= 0) insert(first, l.slots, (label + x.shift) / E, (label + x.shift) % E, k);
-    float tm = l.wmax[0];
-    int n = l.kept[0];
+  const uint32_t lab_raw = Elem<T>::bits(xr + (label >= 0 ? label : 0));
+  tmax = l.tmax[0], kept = l.kept[0];
 #pragma unroll
-    for (int w = 1; w < W; ++w) tm = fmaxf(tm, l.wmax[w]), n += l.kept[w];
-    l.zref = a.lse ? (double)a.lse[row] : (double)tm * a.itau;
-    l.row_kept = n;
-  }
+  for (int w = 1; w < W; ++w) tmax = fmaxf(tmax, l.tmax[w]), kept += l.kept[w];
+  const double zref = a.lse ? (double)lse : (double)tmax * a.itau;
   lds_sync();
 
   Expo<T, MODE> ex(a);
   Running<T, MODE> run;
+  each<NV / 2>([&](auto g) __attribute__((always_inline)) {
+    stats_group<T, MODE, NT, 2 * g>(v, x, table, run, ex, t);
+    __builtin_amdgcn_sched_barrier(0);  // mixed, several chunks' values would not fit the registers
+  });
+  const float xlab = Elem<T>::value(lab_raw);
+  float xj[KPT];
+  float m = run.max;
 #pragma unroll
-  for (int g = 0; g < NV; g += GROUP) {
-    if (g * NT >= x.nchunks) break;  // the whole workgroup
-    float floor = -__builtin_inff();
-    v4i u[GROUP];
-#pragma unroll
-    for (int i = 0; i < GROUP; ++i) {
-      const int c = (g + i) * NT + t;
-      if (c < x.nchunks) {
-        if (c == 0 || c == x.nchunks - 1) drop<T>(v[g + i], x.outside(c));
-        const int chain = first[c];
-        if (chain) floor = fmaxf(floor, take_out<T>(v[g + i], chain, l.slots, k));
-      }
-      u[i] = v[g + i];
-    }
-    run.add(u, floor, ex, a);
-  }
-  const float wm = wave_max(run.max);
-  if (lane == 0) l.wmax[wave] = wm;
+  for (int i = 0; i < KPT; ++i) m = fmaxf(m, xj[i] = Elem<T>::value(xraw[i]));
+  m = wave_max(m);
+  if (lane == 0) l.wmax[wave] = m;
   lds_sync();
-  float m = l.wmax[0];
+  m = l.wmax[0];
 #pragma unroll
   for (int w = 1; w < W; ++w) m = fmaxf(m, l.wmax[w]);
-  run.rescale(uniform(m), ex, a);
+  run.rescale(uniform(m), ex);
   ex.r = uniform(ex.r);
-
-  // sums of this wave; the kept entries in 64 bits
   const float ws = wave_sum(run.sum()), ws1 = MODE ? wave_sum(run.sum1()) : 0;
-  if (wave * 64 < k) {
-    double q[4] = {0, 0, 0, 0};
-    const double zref = l.zref;
-#pragma unroll 1
-    for (int j = t; j < k; j += NT) {
-      if (l.slots.link[j] < 0) continue;
-      const double lw = (double)l.slots.p[j] * a.itau - zref, w = exp2_d(lw * kLog2e);
-      const double xj = (double)l.slots.x[j] - (double)ex.r, y = ex.log2e(xj, a), e = exp2_d(y);
-      const double e1 = MODE == 0 ? e : MODE == 1 ? e * e : exp2_d(ex.log2e1(xj, a));
+  float e0[KPT], e1[KPT], w0[KPT];
+  double q[4] = {0, 0, 0, 0};
+  if (wave * 64 < k) {  // kept entries in 64 bits
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      if (id[i] < 0) continue;
+      const double lw = (double)tv[i] * a.itau - zref, w = exp2_d(lw * kLog2e);
+      const double y = (double)xj[i] - (double)ex.r, ye = ex.log2e(y, a), e = exp2_d(ye);
+      const double f1 = MODE == 0 ? e : MODE == 1 ? e * e : exp2_d(ex.log2e1(y, a));
       q[0] += w;
-      if (!(w == 0)) q[1] += w * (lw - y * kLn2);
+      if (!(w == 0)) q[1] += w * (lw - ye * kLn2);
       q[2] += e;
-      q[3] += e1;
-      l.slots.x[j] = (float)e;
-      l.slots.x1[j] = (float)e1;
-      l.slots.p[j] = (float)w;
+      q[3] += f1;
+      e0[i] = (float)e, e1[i] = (float)f1, w0[i] = (float)w;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const double b = wave_sum(q[i]);
-      if (lane == 0) l.sums[wave][2 + i] = b;
-    }
-  } else if (lane == 0) {
-#pragma unroll
-    for (int i = 2; i < 6; ++i) l.sums[wave][i] = 0;
+    for (int i = 0; i < 4; ++i) q[i] = wave_sum(q[i]);
   }
-  if (lane == 0) l.sums[wave][0] = (double)ws, l.sums[wave][1] = (double)ws1;
+  if (lane == 0) {
+    l.sums[wave][0] = (double)ws, l.sums[wave][1] = (double)ws1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l.sums[wave][2 + i] = q[i];
+  }
   lds_sync();
+  Joined s;
   if (wave == 0) {
+    double b[6];
 #pragma unroll
     for (int i = 0; i < 6; ++i) {
-      double b = lane < W ? l.sums[lane][i] : 0.0;
+      b[i] = lane < W ? l.sums[lane][i] : 0.0;
 #pragma unroll
-      for (int off = 1; off < W; off <<= 1) b += __shfl_xor(b, off);
-      if (lane == 0) l.sums[0][i] = b;
+      for (int off = 1; off < W; off <<= 1) b[i] += __shfl_xor(b[i], off);
     }
+    s = {b[0], b[1], b[2], b[3], b[4], b[5], zref, kept};
     if (lane == 0) {
-      const Joined s = {l.sums[0][0], l.sums[0][1], l.sums[0][2], l.sums[0][3], l.sums[0][4], l.sums[0][5], l.zref, l.row_kept};
-      l.st = join(a, s, (double)ex.r, MODE);
-      // the slots hold w_j = exp(t_j / tau - zref)
-      if (a.d) l.f = factors(a, l.st, s.kept == 0 ? 0 : a.lse ? 1 : 1 / s.W, row, label >= 0, MODE);
-      l.slots.p[k] = (float)l.label_slot;
+#pragma unroll
+      for (int i = 0; i < 6; ++i) l.sums[0][i] = b[i];
+      if (a.d) l.f = factors(a, join(a, s, (double)ex.r, MODE), kept == 0 ? 0 : a.lse ? 1 : 1 / s.W, row, label >= 0, MODE);
     }
   }
   lds_sync();
   if (a.d) {
     const Factors f = uniform(l.f);
     T* d = static_cast<T*>(a.d) + row * a.d_ld;
+    const RowBuffer out(a.d_aligned ? d - x.shift : d, x.nchunks);
+    each<NV>([&](auto i) __attribute__((always_inline)) {
+      // unpacked again: the values that the sums had unpacked are not to be kept for this
+      asm volatile("" : "+v"(v[i]));
+      if (i * NT < x.nchunks) store_chunk<T>(x, out, a, grad_chunk<T, MODE>(ex, f, v[i]), i * NT, t, d);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    __syncthreads();  // the sweep's stores are complete
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = i * NT + t;
-      if (c < x.nchunks) grad_chunk<T, MODE>(x, a, ex, f, l.slots, v[i], first[c], c, d);
-    }
+    for (int i = 0; i < KPT; ++i)
+      if (id[i] >= 0) d[id[i]] = (T)kept_grad(f, e0[i], e1[i], w0[i], id[i] == label);
+    if (t == 0 && label >= 0 && !l.label_kept) d[label] = (T)(outside_grad<T, MODE>(ex, f, xlab) - f.label);
   }
   if (t == 0) {
-    const Joined s = {l.sums[0][0], l.sums[0][1], l.sums[0][2], l.sums[0][3], l.sums[0][4], l.sums[0][5], l.zref, l.row_kept};
-    RowStats st = l.st;
+    s = {l.sums[0][0], l.sums[0][1], l.sums[0][2], l.sums[0][3], l.sums[0][4], l.sums[0][5], zref, kept};
+    RowStats st = join(a, s, (double)ex.r, MODE);
     st.z = teacher_norm(a, s);
-    if (a.loss) a.loss[row] = row_loss(a, s, st, label >= 0 ? ex.log2e1((double)l.slots.x[k] - (double)ex.r, a) : 0, label >= 0);
+    if (a.loss) a.loss[row] = row_loss(a, s, st, label >= 0 ? ex.log2e1((double)xlab - (double)ex.r, a) : 0, label >= 0);
     if (a.stats) static_cast<RowStats*>(a.stats)[row] = st;
   }
 }
@@ -634,32 +708,28 @@ __global__ __launch_bounds__(NT, row_waves(NT, NV)) void distill_rows(DistillArg
 // ---- segments of rows ------------------------------------------------------
 
 constexpr int kSegThreads = 512;
-constexpr int kSegChunks = 4096;  // at most, so that the table of a segment takes 16 KiB
+constexpr int kSegChunks = 4096;  // at most: a byte of the table each
 
 struct SegLds {
-  int first[kSegChunks];
-  Slots<kDistillMaxKept> slots;
+  uint32_t table[kSegChunks / 4];
   double sums[kSegThreads / 64][6];
   float wmax[kSegThreads / 64];
   int kept[kSegThreads / 64];
-  int label_slot;
+  int label_kept;
 };
 
-// Kept entries (and the label) of chunks [c0, c1) go into the table.
+// Kept entries in chunks [c0, c1) go into the table.
 template <typename T>
-__device__ __forceinline__ void seg_table(SegLds& l, const DistillArgs& a, const Row<T>& x, int64_t row, int label, int c0,
-                                          int c1) {
+__device__ __forceinline__ void seg_table(SegLds& l, const DistillArgs& a, const Row<T>& x, int64_t row, int c0, int c1) {
   constexpr int E = Elem<T>::E;
   const int t = threadIdx.x;
-  for (int c = t; c < c1 - c0; c += kSegThreads) l.first[c] = 0;
-  if (t == 0) l.label_slot = 0;
+  for (int c = t; 4 * c < c1 - c0; c += kSegThreads) l.table[c] = 0;
   __syncthreads();
-  for (int j = t; j <= a.k; j += kSegThreads) {
-    const int id = j < a.k ? kept_at(a, row, j) : label;
+  for (int j = t; j < a.k; j += kSegThreads) {
+    const int id = kept_at(a, row, j);
     if (id < 0) continue;
-    if (j < a.k && id == label) l.label_slot = j + 1;
     const int at = id + x.shift, c = at / E;
-    if (c >= c0 && c < c1) insert(l.first, l.slots, c - c0, at % E, j);
+    if (c >= c0 && c < c1) mark(l.table, c - c0, at % E);
   }
   __syncthreads();
 }
@@ -673,12 +743,11 @@ __global__ __launch_bounds__(kSegThreads) void distill_partial(DistillArgs a) {
   const int64_t row = blockIdx.x / a.segs;
   const Row<T> x(a.logits, row, a.ld, (int)a.V);
   const int c0 = seg * a.seg_chunks, c1 = min(x.nchunks, c0 + a.seg_chunks);
-  seg_table<T>(l, a, x, row, -1, c0, c1);
+  seg_table<T>(l, a, x, row, c0, c1);
   Expo<T, MODE> ex(a);
   Running<T, MODE> run;
   for (int g = c0 + t; g < c1; g += GROUP * kSegThreads) {
     v4i v[GROUP];
-    float floor = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < GROUP; ++i) {
       const int c = g + i * kSegThreads;
@@ -687,10 +756,10 @@ __global__ __launch_bounds__(kSegThreads) void distill_partial(DistillArgs a) {
 #pragma unroll
     for (int i = 0; i < GROUP; ++i) {
       const int c = g + i * kSegThreads;
-      const int chain = c < c1 ? l.first[c - c0] : 0;
-      if (chain) floor = fmaxf(floor, take_out<T>(v[i], chain, l.slots, a.k));
+      const uint32_t mask = c < c1 ? marked(l.table, c - c0) : 0;
+      if (mask) drop<T>(v[i], mask);
     }
-    run.add(v, floor, ex, a);
+    run.add(v, ex);
   }
   const float wm = wave_max(run.max);
   if (lane == 0) l.wmax[wave] = wm;
@@ -698,7 +767,7 @@ __global__ __launch_bounds__(kSegThreads) void distill_partial(DistillArgs a) {
   float m = l.wmax[0];
 #pragma unroll
   for (int w = 1; w < W; ++w) m = fmaxf(m, l.wmax[w]);
-  run.rescale(m, ex, a);
+  run.rescale(m, ex);
   const float s = wave_sum(run.sum()), s1 = MODE ? wave_sum(run.sum1()) : 0;
   if (lane == 0) l.sums[wave][0] = s, l.sums[wave][1] = s1;
   __syncthreads();
@@ -722,7 +791,8 @@ __device__ __forceinline__ RowStats seg_join(SegLds& l, const DistillArgs& a, in
   float tmax = -__builtin_inff(), m = -__builtin_inff();
   int kept = 0;
   for (int j = t; j < a.k; j += kSegThreads)
-    if (kept_at(a, row, j) >= 0) tmax = fmaxf(tmax, teacher_at(a, row, j)), ++kept;
+    if (const int id = kept_at(a, row, j); id >= 0)
+      tmax = fmaxf(tmax, teacher_at(a, row, j)), m = fmaxf(m, (float)x[id]), ++kept;
   for (int i = t; i < a.segs; i += kSegThreads) m = fmaxf(m, part[i].max);
   tmax = wave_max(tmax), m = wave_max(m), kept = wave_sum(kept);
   if (lane == 0) l.wmax[wave] = tmax, l.sums[wave][0] = m, l.kept[wave] = kept;
@@ -802,21 +872,7 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad(DistillArgs a) {
   } else {
     st = seg_join<T, MODE>(l, a, row, label, seg == 0, ex);
   }
-  seg_table<T>(l, a, x, row, label, c0, c1);
   const Factors f = uniform(factors(a, st, 1, row, label >= 0, MODE));
-  const T* xr = static_cast<const T*>(a.logits) + row * a.ld;
-  for (int j = t; j < a.k; j += kSegThreads) {
-    const int id = kept_at(a, row, j);
-    if (id < 0) continue;
-    const int c = (id + x.shift) / Elem<T>::E;
-    if (c < c0 || c >= c1) continue;
-    const double xj = (double)(float)xr[id] - (double)ex.r;
-    l.slots.x[j] = (float)exp2_d(ex.log2e(xj, a));
-    l.slots.x1[j] = MODE == 0 ? l.slots.x[j] : (float)exp2_d(ex.log2e1(xj, a));
-    l.slots.p[j] = (float)exp2_d(((double)teacher_at(a, row, j) * a.itau - st.z) * kLog2e);
-  }
-  if (t == 0) l.slots.p[a.k] = (float)l.label_slot;
-  __syncthreads();
   T* d = static_cast<T*>(a.d) + row * a.d_ld;
   for (int g = c0 + t; g < c1; g += GROUP * kSegThreads) {
     v4i v[GROUP];
@@ -828,9 +884,25 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad(DistillArgs a) {
 #pragma unroll
     for (int i = 0; i < GROUP; ++i) {
       const int c = g + i * kSegThreads;
-      if (c < c1) grad_chunk<T, MODE>(x, a, ex, f, l.slots, v[i], l.first[c - c0], c, d);
+      if (c < c1) store_chunk<T>(x, a, grad_chunk<T, MODE>(ex, f, v[i]), c, d);
     }
   }
+  // kept entries and the label over what the sweep has put there
+  const T* xr = static_cast<const T*>(a.logits) + row * a.ld;
+  const auto here = [&](int id) { const int c = (id + x.shift) / Elem<T>::E; return c >= c0 && c < c1; };
+  if (t == 0) l.label_kept = 0;
+  __syncthreads();
+  for (int j = t; j < a.k; j += kSegThreads) {
+    const int id = kept_at(a, row, j);
+    if (id < 0 || !here(id)) continue;
+    const double y = (double)(float)xr[id] - (double)ex.r;
+    const float e = (float)exp2_d(ex.log2e(y, a)), e1 = MODE == 0 ? e : (float)exp2_d(ex.log2e1(y, a));
+    const float w = (float)exp2_d(((double)teacher_at(a, row, j) * a.itau - st.z) * kLog2e);
+    if (id == label) l.label_kept = 1;
+    d[id] = (T)kept_grad(f, e, e1, w, id == label);
+  }
+  __syncthreads();
+  if (t == 0 && label >= 0 && !l.label_kept && here(label)) d[label] = (T)(outside_grad<T, MODE>(ex, f, (float)xr[label]) - f.label);
 }
 
 // ---- launches ---------------------------------------------------------------
@@ -838,11 +910,16 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad(DistillArgs a) {
 template <typename T, int MODE>
 hipError_t launch_mode(const DistillArgs& a, hipStream_t stream) {
   switch (a.plan) {
-    case kRows64x8: distill_rows<T, 64, 8, 256, MODE><<<(unsigned)a.T, 64, 0, stream>>>(a); break;
-    case kRows256x8: distill_rows<T, 256, 8, 256, MODE><<<(unsigned)a.T, 256, 0, stream>>>(a); break;
-    case kRows512x8: distill_rows<T, 512, 8, kDistillMaxKept, MODE><<<(unsigned)a.T, 512, 0, stream>>>(a); break;
-    case kRows1024x8: distill_rows<T, 1024, 8, kDistillMaxKept, MODE><<<(unsigned)a.T, 1024, 0, stream>>>(a); break;
-    case kRows1024x16: distill_rows<T, 1024, 16, kDistillMaxKept, MODE><<<(unsigned)a.T, 1024, 0, stream>>>(a); break;
+    case kRows64x2: distill_rows<T, 64, 2, 2, MODE><<<(unsigned)a.T, 64, 0, stream>>>(a); break;
+    case kRows64x4: distill_rows<T, 64, 4, 2, MODE><<<(unsigned)a.T, 64, 0, stream>>>(a); break;
+    case kRows64x8: distill_rows<T, 64, 8, 2, MODE><<<(unsigned)a.T, 64, 0, stream>>>(a); break;
+    case kRows256x4: distill_rows<T, 256, 4, 2, MODE><<<(unsigned)a.T, 256, 0, stream>>>(a); break;
+    case kRows256x8: distill_rows<T, 256, 8, 2, MODE><<<(unsigned)a.T, 256, 0, stream>>>(a); break;
+    case kRows512x8: distill_rows<T, 512, 8, 2, MODE><<<(unsigned)a.T, 512, 0, stream>>>(a); break;
+    case kRows512x12: distill_rows<T, 512, 12, 2, MODE><<<(unsigned)a.T, 512, 0, stream>>>(a); break;
+    case kRows512x16: distill_rows<T, 512, 16, 2, MODE><<<(unsigned)a.T, 512, 0, stream>>>(a); break;
+    case kRows512x24: distill_rows<T, 512, 24, 2, MODE><<<(unsigned)a.T, 512, 0, stream>>>(a); break;
+    case kRows512x32: distill_rows<T, 512, 32, 2, MODE><<<(unsigned)a.T, 512, 0, stream>>>(a); break;
     default: {
       const dim3 grid((unsigned)(a.T * a.segs));
       if (a.given) {

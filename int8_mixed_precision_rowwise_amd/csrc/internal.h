@@ -235,7 +235,9 @@ hipError_t launch_act_bwd(const ActBwdArgs& a, int act, int round, hipStream_t s
 constexpr int kDistillMaxKept = I8MP_DISTILL_MAX_KEPT;
 // A row in one workgroup's registers (threads x 16-byte chunks a thread), or
 // segments of rows in two launches.
-enum DistillPlan { kRows64x8, kRows256x8, kRows512x8, kRows1024x8, kRows1024x16, kSegments };
+enum DistillPlan {
+  kRows64x2, kRows64x4, kRows64x8, kRows256x4, kRows256x8, kRows512x8, kRows512x12, kRows512x16, kRows512x24, kRows512x32, kSegments
+};
 struct DistillArgs {
   const void *logits, *teacher, *idx, *labels;
   const float *lse, *grad;

@@ -19,7 +19,7 @@ constexpr int64_t kDistillSegMin = 512, kDistillSegMax = 4096;  // chunks of 16 
 static void distill_segments(int64_t T, int64_t chunks, int* segs, int* seg_chunks) {
   const int64_t want = (kDistillFill + T - 1) / T;
   int64_t per = (chunks + want - 1) / want;
-  per = std::min(std::max(per, kDistillSegMin), kDistillSegMax);
+  per = std::min(std::max((per + 1) / 2 * 2, kDistillSegMin), kDistillSegMax);  // even
   *segs = (int)((chunks + per - 1) / per);
   *seg_chunks = (int)per;
 }
@@ -32,11 +32,13 @@ static int64_t distill_chunks(int64_t V, int elem) { return (V * elem + 15 + ele
 static int distill_shape(int64_t T, int64_t V, int k, int elem) {
   const int64_t chunks = distill_chunks(V, elem);
   if (chunks > 16384 || (T < 128 && chunks > 4 * kDistillSegMin)) return kSegments;
-  if (k <= 256) {
-    if (chunks <= 512) return kRows64x8;
-    if (chunks <= 2048) return kRows256x8;
-  }
-  return chunks <= 4096 ? kRows512x8 : chunks <= 8192 ? kRows1024x8 : kRows1024x16;
+  // the least room that holds the row, with two kept entries a thread
+  static const struct { int plan, threads, chunks; } kPlans[] = {
+      {kRows64x2, 64, 2}, {kRows64x4, 64, 4}, {kRows64x8, 64, 8}, {kRows256x4, 256, 4}, {kRows256x8, 256, 8},
+      {kRows512x8, 512, 8}, {kRows512x12, 512, 12}, {kRows512x16, 512, 16}, {kRows512x24, 512, 24}, {kRows512x32, 512, 32}};
+  for (const auto& p : kPlans)
+    if (chunks <= p.threads * p.chunks && k <= 2 * p.threads) return p.plan;
+  return kSegments;
 }
 
 void distill_plan(DistillArgs& a, int elem) {

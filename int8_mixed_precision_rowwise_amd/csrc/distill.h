@@ -27,12 +27,13 @@
 // workgroup joining its row's partial sums itself.  The gradient alone (the
 // backward of an earlier forward) is the second of them with the sums given.
 //
-// Exponentials are 2^(c (x - m)) with m the row's maximum and c = log2(e) / tau
-// rounded to fp32, the same c in the 64-bit part, so that its rounding only
-// scales the temperature by 2^-24.  (c x - c m in one fused operation would
-// save one of about ten per element, but the rounding of c m then decides the
-// result where a whole row is masked with the type's lowest value.)  fp32 logits
-// carry the product's low part too.
+// Exponentials are 2^(c x - R), one fused operation, with c = log2(e) / tau and R =
+// c m (m the row's maximum) both rounded to fp32.  The same c and R stand in the
+// 64-bit part: the rounding of c only scales the temperature by 2^-24, and that of R
+// all of a row's exponentials by one factor, which cancels.  Beyond |R| = 2^22 (a
+// row masked with the type's lowest value) that factor would be far from 1: such a
+// row is summed and swept once more from memory as 2^(c (x - m)).  fp32 logits take
+// x - m first and carry the product's low part.
 #pragma once
 
 #include "internal.h"
@@ -51,8 +52,8 @@ constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
 // What a row's gradient needs besides its logits and kept entries.
 struct RowStats {
   double ref;      // the maximum m of the logits (0 if all are -inf)
-  double total;    // sum of exp((x - m) / tau)
-  double total1;   // sum of exp(x - m)
+  double total;    // sum of the exponentials (2^(c x - R), see Expo)
+  double total1;   // the same at temperature 1
   double outside;  // mass - p_rest / q_rest
   double mass;
   double z;        // p_j = exp(t_j / tau - z)
@@ -112,24 +113,17 @@ struct Elem<float> {
 // Elements whose bit is set in mask become -inf.
 template <typename T>
 __device__ __forceinline__ void drop(v4i& v, uint32_t mask) {
-  constexpr int E = Elem<T>::E;
   constexpr uint32_t inf = Elem<T>::kNegInf;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (!(mask >> e & 1)) continue;
-    if constexpr (E == 4)
-      v[e] = (int)inf;
-    else
-      v[e >> 1] = (e & 1) ? (int)(((uint32_t)v[e >> 1] & 0xFFFFu) | (inf << 16)) : (int)(((uint32_t)v[e >> 1] & 0xFFFF0000u) | inf);
+  for (int w = 0; w < 4; ++w) {
+    if constexpr (Elem<T>::E == 4) {
+      v[w] = mask >> w & 1 ? (int)inf : v[w];
+    } else {
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_sbfe((int)mask, 2 * w, 1), hi = (uint32_t)__builtin_amdgcn_sbfe((int)mask, 2 * w + 1, 1);
+      const uint32_t m = (lo & 0xFFFFu) | (hi << 16);
+      v[w] = (int)(((uint32_t)v[w] & ~m) | ((inf | inf << 16) & m));
+    }
   }
-}
-
-template <typename T>
-__device__ __forceinline__ float pick(const v4i& v, int e) {
-  float x = Elem<T>::get(v, 0);
-#pragma unroll
-  for (int i = 1; i < Elem<T>::E; ++i) x = e == i ? Elem<T>::get(v, i) : x;
-  return x;
 }
 
 // A row as 16-byte chunks of memory: chunk c holds elements c E - shift ...;
@@ -191,10 +185,28 @@ __device__ __forceinline__ v4i all_neg_inf(int elem_bytes, uint32_t inf) {
 template <typename T, int MODE>
 struct Expo {
   static constexpr bool kPrecise = sizeof(T) == 4;
+  static constexpr float kFar = 0x1p22f;
   float c, c_lo, c1, c1_lo;  // log2(e) / tau and log2(e), with their low parts
-  float r;                   // the reference m
-  __device__ __forceinline__ Expo(const DistillArgs& a) : c(a.c), c_lo(a.c_lo), c1(a.c1), c1_lo(a.c1_lo), r(0) {}
-  __device__ __forceinline__ void at(float max) { r = max == -__builtin_inff() ? 0.0f : max; }  // all -inf: every exponential is 0
+  float m, r, r1;            // the reference's maximum, R, and R at temperature 1
+  __device__ __forceinline__ Expo(const DistillArgs& a) : c(a.c), c_lo(a.c_lo), c1(a.c1), c1_lo(a.c1_lo), m(0), r(0), r1(0) {}
+  // A maximum so far.  The bound keeps R finite where everything is -inf or close to
+  // the type's lowest value: exponentials there are 0.
+  __device__ __forceinline__ void at(float max) {
+    if constexpr (kPrecise) {
+      m = max == -__builtin_inff() ? 0.0f : max;
+    } else {
+      r = fmaxf(c * max, -kFar);
+      if constexpr (MODE == 2) r1 = fmaxf(c1 * max, -kFar);
+    }
+  }
+  // A row's maximum.
+  __device__ __forceinline__ void at_row(float max) {
+    at(max);
+    m = max == -__builtin_inff() ? 0.0f : max;
+  }
+  __device__ __forceinline__ bool far() const {
+    return !kPrecise && (__builtin_fabsf(c * m) >= kFar || (MODE == 2 && __builtin_fabsf(c1 * m) >= kFar));
+  }
   __device__ __forceinline__ static float precise(float y, float c, float c_lo) {
     const float h = y * c;
     const float l = __builtin_fmaf(y, c_lo, __builtin_fmaf(y, c, -h));
@@ -202,22 +214,27 @@ struct Expo {
     // y = -inf: h is -inf and l a NaN
     return h < -150.0f ? 0.0f : __builtin_fmaf(e, l * (float)kLn2, e);
   }
-  // exp(y / tau) and, given that, exp(y), for y = x - m
-  __device__ __forceinline__ float e(float y) const {
-    if constexpr (kPrecise) return precise(y, c, c_lo);
-    else return exp2_fast(y * c);
+  // exp(x / tau) and, given that, exp(x), relative to the reference
+  __device__ __forceinline__ float e(float x) const {
+    if constexpr (kPrecise) return precise(x - m, c, c_lo);
+    else return exp2_fast(__builtin_fmaf(x, c, -r));
   }
-  __device__ __forceinline__ float e1(float y, float e) const {
+  __device__ __forceinline__ float e1(float x, float e) const {
     if constexpr (MODE == 1) return e * e;
-    if constexpr (kPrecise) return precise(y, c1, c1_lo);
-    else return exp2_fast(y * c1);
+    if constexpr (kPrecise) return precise(x - m, c1, c1_lo);
+    else return exp2_fast(__builtin_fmaf(x, c1, -r1));
   }
+  // the same for a row far out
+  __device__ __forceinline__ float far_e(float x) const { return exp2_fast((x - m) * c); }
+  __device__ __forceinline__ float far_e1(float x, float e) const { return MODE == 1 ? e * e : exp2_fast((x - m) * c1); }
   // log2 of the same exponentials in 64 bits
-  __device__ __forceinline__ double log2e(double y, const DistillArgs& a) const { return y * (kPrecise ? a.cd : (double)c); }
-  __device__ __forceinline__ double log2e1(double y, const DistillArgs& a) const {
-    if constexpr (MODE == 0) return log2e(y, a);
-    if constexpr (MODE == 1) return 2 * log2e(y, a);
-    return y * (kPrecise ? kLog2e : (double)c1);
+  __device__ __forceinline__ double log2e(double x, const DistillArgs& a) const {
+    return kPrecise || far() ? (x - (double)m) * a.cd : x * (double)c - (double)r;
+  }
+  __device__ __forceinline__ double log2e1(double x, const DistillArgs& a) const {
+    if constexpr (MODE == 0) return log2e(x, a);
+    if constexpr (MODE == 1) return 2 * log2e(x, a);
+    return kPrecise || far() ? (x - (double)m) * kLog2e : x * (double)c1 - (double)r1;
   }
 };
 
@@ -377,10 +394,16 @@ __device__ __forceinline__ Factors uniform(const Factors& f) {
 
 template <typename T, int MODE>
 __device__ __forceinline__ float outside_grad(const Expo<T, MODE>& ex, const Factors& f, float x) {
-  const float e = ex.e(x - ex.r);
+  const float e = ex.e(x);
   if constexpr (MODE == 0) return e * f.out;
-  const float e1 = ex.e1(x - ex.r, e);
-  return __builtin_fmaf(e1, f.out1, e * f.out);
+  if constexpr (MODE == 1) return e * __builtin_fmaf(e, f.out1, f.out);
+  return __builtin_fmaf(ex.e1(x, e), f.out1, e * f.out);
+}
+template <typename T, int MODE>
+__device__ __forceinline__ float far_outside_grad(const Expo<T, MODE>& ex, const Factors& f, float x) {
+  const float e = ex.far_e(x);
+  if constexpr (MODE == 0) return e * f.out;
+  return __builtin_fmaf(ex.far_e1(x, e), f.out1, e * f.out);
 }
 
 // A byte for each chunk in LDS: the elements that are kept entries.
@@ -391,7 +414,7 @@ __device__ __forceinline__ uint32_t marked(const uint32_t* table, int chunk) {
   return reinterpret_cast<const uint8_t*>(table)[chunk];
 }
 
-template <typename T, int MODE>
+template <typename T, int MODE, bool FAR = false>
 __device__ __forceinline__ v4i grad_chunk(const Expo<T, MODE>& ex, const Factors& f, v4i v) {
   constexpr int E = Elem<T>::E;
   typedef float f2 __attribute__((ext_vector_type(2)));
@@ -399,10 +422,18 @@ __device__ __forceinline__ v4i grad_chunk(const Expo<T, MODE>& ex, const Factors
   struct __attribute__((aligned(16))) Out { t2 p[E / 2]; } o;
 #pragma unroll
   for (int e = 0; e < E; e += 2) {  // pairs: one conversion instruction for both
-    const f2 y = {outside_grad<T, MODE>(ex, f, Elem<T>::get(v, e)), outside_grad<T, MODE>(ex, f, Elem<T>::get(v, e + 1))};
+    const float x0 = Elem<T>::get(v, e), x1 = Elem<T>::get(v, e + 1);
+    f2 y;
+    if constexpr (FAR) y = {far_outside_grad<T, MODE>(ex, f, x0), far_outside_grad<T, MODE>(ex, f, x1)};
+    else y = {outside_grad<T, MODE>(ex, f, x0), outside_grad<T, MODE>(ex, f, x1)};
     o.p[e / 2] = __builtin_convertvector(y, t2);
   }
   return __builtin_bit_cast(v4i, o);
+}
+// The gradient at a label that is no kept entry.
+template <typename T, int MODE>
+__device__ __forceinline__ float label_grad(const Expo<T, MODE>& ex, const Factors& f, float x) {
+  return (ex.far() ? far_outside_grad<T, MODE>(ex, f, x) : outside_grad<T, MODE>(ex, f, x)) - f.label;
 }
 // A kept entry's gradient; x, x1, w: its exp((x - m) / tau), exp(x - m) and w_j.
 __device__ __forceinline__ float kept_grad(const Factors& f, float e, float e1, float w, bool is_label) {
@@ -477,7 +508,7 @@ struct Running {
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float x = Elem<T>::get(v[i], e) - ex.r;
+        const float x = Elem<T>::get(v[i], e);
         const float y = ex.e(x);
         s[e % S] += y;
         if constexpr (MODE == 1) s1[e % S] = __builtin_fmaf(y, y, s1[e % S]);
@@ -485,10 +516,17 @@ struct Running {
       }
   }
   __device__ __forceinline__ void rescale(float m, Expo<T, MODE>& ex) {
-    const float r = ex.r;
+    const Expo<T, MODE> was = ex;
     ex.at(m);
-    float f = ex.e(r - ex.r), f1 = 1;
-    if constexpr (MODE != 0) f1 = ex.e1(r - ex.r, f);
+    float f, f1 = 1;
+    if constexpr (Expo<T, MODE>::kPrecise) {
+      f = ex.e(was.m);
+      if constexpr (MODE != 0) f1 = ex.e1(was.m, f);
+    } else {  // between the rounded references, which the terms so far were formed with
+      f = exp2_fast(was.r - ex.r);
+      if constexpr (MODE == 1) f1 = f * f;
+      if constexpr (MODE == 2) f1 = exp2_fast(was.r1 - ex.r1);
+    }
     if (max == -__builtin_inff()) f = f1 = 1;  // nothing summed yet
     max = m;
 #pragma unroll
@@ -530,21 +568,18 @@ __device__ __forceinline__ void each(const F& f) {
   each_of(std::make_integer_sequence<int, N>{}, f);
 }
 
-// Sums over chunks g and g + 1 of a thread, kept entries left out (they become -inf).
-template <typename T, int MODE, int NT, int g, int N>
-__device__ __forceinline__ void stats_group(v4i (&v)[N], const Row<T>& x, const uint32_t* table, Running<T, MODE>& run,
-                                            Expo<T, MODE>& ex, int t) {
+// Sums over chunks g .. g + G - 1 of a thread; the elements that the masks name
+// (kept entries, and what lies outside the row) become -inf.
+template <typename T, int MODE, int g, int G, int N>
+__device__ __forceinline__ void stats_group(v4i (&v)[N], const uint32_t (&masks)[N / 4 + (N < 4)], Running<T, MODE>& run,
+                                            Expo<T, MODE>& ex) {
+  v4i u[G];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int c = (g + i) * NT + t;
-    if ((g + i + 1) * NT > x.nchunks && c >= x.nchunks) v[g + i] = all_neg_inf(sizeof(T), Elem<T>::kNegInf);
-    if (c < x.nchunks) {
-      uint32_t mask = marked(table, c);
-      if (c == 0 || c == x.nchunks - 1) mask |= x.outside(c);
-      if (mask) drop<T>(v[g + i], mask);
-    }
+  for (int i = 0; i < G; ++i) {
+    const uint32_t mask = masks[(g + i) / 4] >> (8 * ((g + i) % 4)) & 0xFFu;
+    if (mask) drop<T>(v[g + i], mask);
+    u[i] = v[g + i];
   }
-  const v4i u[2] = {v[g], v[g + 1]};
   run.add(u, ex);
   // The sums are wanted now: left alone, the compiler takes them where they are
   // used, behind the barrier, and holds every term's inputs until then.
@@ -552,13 +587,34 @@ __device__ __forceinline__ void stats_group(v4i (&v)[N], const Row<T>& x, const 
   if constexpr (MODE != 0) asm volatile("" : "+v"(run.s1[0]), "+v"(run.s1[1]), "+v"(run.s1[2]), "+v"(run.s1[3]));
 }
 
-// Waves a SIMD: what the row, 4 registers a chunk, leaves room for.
-constexpr int row_waves(int nv) { return nv <= 8 ? 5 : nv <= 16 ? 4 : nv <= 24 ? 3 : 2; }
+// A row far out, from memory: this thread's part of its sums, over the chunks first,
+// first + step, ... below end, without the elements that skip(chunk) names.
+template <typename T, int MODE, typename F>
+__device__ __forceinline__ void far_sums(const Row<T>& x, const Expo<T, MODE>& ex, int first, int end, int step, const F& skip,
+                                         float& sum, float& sum1) {
+#pragma unroll 1
+  for (int c = first; c < end; c += step) {
+    v4i v = x.load(c);
+    drop<T>(v, skip(c));
+#pragma unroll
+    for (int e = 0; e < Elem<T>::E; ++e) {
+      const float xe = Elem<T>::get(v, e), y = ex.far_e(xe);
+      sum += y;
+      if (MODE) sum1 += ex.far_e1(xe, y);
+    }
+  }
+}
+
+// Waves a SIMD: what the row, 4 registers a chunk, leaves room for (two of a
+// workgroup of 512 stand on each).
+constexpr int row_waves(int nv) { return nv <= 4 ? 5 : nv <= 16 ? 4 : 2; }
 
 template <typename T, int NT, int NV, int KPT, int MODE>
 __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a) {
   constexpr int W = NT / 64, E = Elem<T>::E;
-  __shared__ uint32_t table[NT * NV / 4];
+  constexpr int WORDS = NV / 4 + (NV < 4), G = NV >= 24 ? 4 : 2;
+  // a byte a chunk, each thread's chunks (t, t + NT, ...) together
+  __shared__ __attribute__((aligned(16))) uint32_t table[NT * WORDS];
   __shared__ RowLds<NT> l;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int k = a.k;
@@ -595,7 +651,17 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
     id[i] = t + i * NT < k ? raw[i].index(a, a.idx64) : -1;
     tv[i] = t + i * NT < k ? teacher_value(a, raw_t[i]) : 0.0f;
   }
-  for (int c = t; c < NT * NV / 4; c += NT) table[c] = 0;
+  // what lies outside the row: chunks behind it, and parts of the first and last
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) {
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 4 * w; i < 4 * w + 4 && i < NV; ++i) {
+      const int c = i * NT + t;
+      if (c == 0 || c >= x.nchunks - 1) word |= (c < x.nchunks ? x.outside(c) & 0xFFu : 0xFFu) << (8 * (i % 4));
+    }
+    table[t * WORDS + w] = word;
+  }
   if (t == 0) l.label_kept = 0;
 #pragma unroll
   for (int i = 0; i < KPT; ++i)
@@ -608,7 +674,8 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
     xraw[i] = Elem<T>::kNegInf;
     if (id[i] < 0) continue;
     const int at = id[i] + x.shift;
-    mark(table, at / E, at % E);
+    const int c = at / E, i_of = c / NT;
+    atomicOr(table + (c % NT) * WORDS + i_of / 4, 1u << (8 * (i_of % 4) + at % E));
     xraw[i] = Elem<T>::bits(xr + id[i]);
     if (id[i] == label) l.label_kept = 1;
   }
@@ -621,8 +688,14 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
 
   Expo<T, MODE> ex(a);
   Running<T, MODE> run;
-  each<NV / 2>([&](auto g) __attribute__((always_inline)) {
-    stats_group<T, MODE, NT, 2 * g>(v, x, table, run, ex, t);
+  uint32_t masks[WORDS];
+  if constexpr (NV >= 24) {  // all at once, where there are few waves to wait behind
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) masks[w] = table[t * WORDS + w];
+  }
+  each<NV / G>([&](auto g) __attribute__((always_inline)) {
+    if constexpr (NV < 24 && G * g % 4 == 0) masks[G * g / 4] = table[t * WORDS + G * g / 4];
+    stats_group<T, MODE, G * g, G>(v, masks, run, ex);
     __builtin_amdgcn_sched_barrier(0);  // mixed, several chunks' values would not fit the registers
   });
   const float xlab = Elem<T>::value(lab_raw);
@@ -637,8 +710,15 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
 #pragma unroll
   for (int w = 1; w < W; ++w) m = fmaxf(m, l.wmax[w]);
   run.rescale(uniform(m), ex);
-  ex.r = uniform(ex.r);
-  const float ws = wave_sum(run.sum()), ws1 = MODE ? wave_sum(run.sum1()) : 0;
+  ex.at_row(uniform(m));
+  ex.r = uniform(ex.r), ex.r1 = uniform(ex.r1);
+  float ws = run.sum(), ws1 = run.sum1();
+  const auto marked_here = [&](int c) {
+    const int i = c / NT;
+    return table[(c % NT) * WORDS + i / 4] >> (8 * (i % 4)) & 0xFFu;
+  };
+  if (ex.far()) ws = ws1 = 0, far_sums<T, MODE>(x, ex, t, x.nchunks, NT, marked_here, ws, ws1);
+  ws = wave_sum(ws), ws1 = MODE ? wave_sum(ws1) : 0;
   float e0[KPT], e1[KPT], w0[KPT];
   double q[4] = {0, 0, 0, 0};
   if (wave * 64 < k) {  // kept entries in 64 bits
@@ -646,7 +726,7 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
     for (int i = 0; i < KPT; ++i) {
       if (id[i] < 0) continue;
       const double lw = (double)tv[i] * a.itau - zref, w = exp2_d(lw * kLog2e);
-      const double y = (double)xj[i] - (double)ex.r, ye = ex.log2e(y, a), e = exp2_d(ye);
+      const double y = (double)xj[i], ye = ex.log2e(y, a), e = exp2_d(ye);
       const double f1 = MODE == 0 ? e : MODE == 1 ? e * e : exp2_d(ex.log2e1(y, a));
       q[0] += w;
       if (!(w == 0)) q[1] += w * (lw - ye * kLn2);
@@ -676,7 +756,7 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < 6; ++i) l.sums[0][i] = b[i];
-      if (a.d) l.f = factors(a, join(a, s, (double)ex.r, MODE), kept == 0 ? 0 : a.lse ? 1 : 1 / s.W, row, label >= 0, MODE);
+      if (a.d) l.f = factors(a, join(a, s, (double)ex.m, MODE), kept == 0 ? 0 : a.lse ? 1 : 1 / s.W, row, label >= 0, MODE);
     }
   }
   lds_sync();
@@ -684,23 +764,28 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
     const Factors f = uniform(l.f);
     T* d = static_cast<T*>(a.d) + row * a.d_ld;
     const RowBuffer out(a.d_aligned ? d - x.shift : d, x.nchunks);
-    each<NV>([&](auto i) __attribute__((always_inline)) {
-      // unpacked again: the values that the sums had unpacked are not to be kept for this
-      asm volatile("" : "+v"(v[i]));
-      if (i * NT < x.nchunks) store_chunk<T>(x, out, a, grad_chunk<T, MODE>(ex, f, v[i]), i * NT, t, d);
-      __builtin_amdgcn_sched_barrier(0);
-    });
+    if (ex.far()) {
+#pragma unroll 1
+      for (int c = t; c < x.nchunks; c += NT) store_chunk<T>(x, a, grad_chunk<T, MODE, true>(ex, f, x.load(c)), c, d);
+    } else {
+      each<NV>([&](auto i) __attribute__((always_inline)) {
+        // unpacked again: the values that the sums had unpacked are not to be kept for this
+        asm volatile("" : "+v"(v[i]));
+        if (i * NT < x.nchunks) store_chunk<T>(x, out, a, grad_chunk<T, MODE>(ex, f, v[i]), i * NT, t, d);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    }
     __syncthreads();  // the sweep's stores are complete
 #pragma unroll
     for (int i = 0; i < KPT; ++i)
       if (id[i] >= 0) d[id[i]] = (T)kept_grad(f, e0[i], e1[i], w0[i], id[i] == label);
-    if (t == 0 && label >= 0 && !l.label_kept) d[label] = (T)(outside_grad<T, MODE>(ex, f, xlab) - f.label);
+    if (t == 0 && label >= 0 && !l.label_kept) d[label] = (T)(label_grad<T, MODE>(ex, f, xlab));
   }
   if (t == 0) {
     s = {l.sums[0][0], l.sums[0][1], l.sums[0][2], l.sums[0][3], l.sums[0][4], l.sums[0][5], zref, kept};
-    RowStats st = join(a, s, (double)ex.r, MODE);
+    RowStats st = join(a, s, (double)ex.m, MODE);
     st.z = teacher_norm(a, s);
-    if (a.loss) a.loss[row] = row_loss(a, s, st, label >= 0 ? ex.log2e1((double)xlab - (double)ex.r, a) : 0, label >= 0);
+    if (a.loss) a.loss[row] = row_loss(a, s, st, label >= 0 ? ex.log2e1((double)xlab, a) : 0, label >= 0);
     if (a.stats) static_cast<RowStats*>(a.stats)[row] = st;
   }
 }
@@ -767,7 +852,7 @@ __global__ __launch_bounds__(kSegThreads) void distill_partial(DistillArgs a) {
   float m = l.wmax[0];
 #pragma unroll
   for (int w = 1; w < W; ++w) m = fmaxf(m, l.wmax[w]);
-  run.rescale(m, ex);
+  run.rescale(m, ex);  // a row far out: these sums are not used
   const float s = wave_sum(run.sum()), s1 = MODE ? wave_sum(run.sum1()) : 0;
   if (lane == 0) l.sums[wave][0] = s, l.sums[wave][1] = s1;
   __syncthreads();
@@ -801,21 +886,38 @@ __device__ __forceinline__ RowStats seg_join(SegLds& l, const DistillArgs& a, in
 #pragma unroll
   for (int w = 0; w < W; ++w) tmax = fmaxf(tmax, l.wmax[w]), m = fmaxf(m, (float)l.sums[w][0]), kept += l.kept[w];
   __syncthreads();
-  ex.at(m);
+  ex.at_row(m);
   double q[6] = {0, 0, 0, 0, 0, 0};
-  for (int i = t; i < a.segs; i += kSegThreads) {
-    const Partial p = part[i];
-    Expo<T, MODE> own(a);
-    own.at(p.max);
-    const double to = (double)own.r - (double)ex.r, y = ex.log2e(to, a), y1 = ex.log2e1(to, a);
-    q[0] += p.sum == 0 ? 0 : (double)p.sum * exp2_d(y);
-    if (MODE) q[1] += p.sum1 == 0 ? 0 : (double)p.sum1 * exp2_d(y1);
+  if (ex.far()) {
+    const Row<T> r(a.logits, row, a.ld, (int)a.V);
+    float s = 0, s1 = 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < r.nchunks; c0 += kSegChunks) {
+      const int c1 = min(r.nchunks, c0 + kSegChunks);
+      seg_table<T>(l, a, r, row, c0, c1);
+      far_sums<T, MODE>(r, ex, c0 + t, c1, kSegThreads, [&](int c) { return marked(l.table, c - c0); }, s, s1);
+      __syncthreads();
+    }
+    q[0] = s, q[1] = s1;
+  } else {
+    for (int i = t; i < a.segs; i += kSegThreads) {
+      const Partial p = part[i];
+      Expo<T, MODE> own(a);
+      own.at(p.max);
+      // between the two references
+      constexpr bool precise = Expo<T, MODE>::kPrecise;
+      const double dm = (double)own.m - (double)ex.m;
+      const double y = precise ? dm * a.cd : (double)own.r - (double)ex.r;
+      const double y1 = MODE == 1 ? 2 * y : precise ? dm * kLog2e : (double)own.r1 - (double)ex.r1;
+      q[0] += p.sum == 0 ? 0 : (double)p.sum * exp2_d(y);
+      if (MODE) q[1] += p.sum1 == 0 ? 0 : (double)p.sum1 * exp2_d(y1);
+    }
   }
   const double itau = a.itau, zref = a.lse ? (double)a.lse[row] : (double)tmax * itau;
   for (int j = t; j < a.k; j += kSegThreads) {
     const int id = kept_at(a, row, j);
     if (id < 0) continue;
-    const double lw = (double)teacher_at(a, row, j) * itau - zref, w = exp2_d(lw * kLog2e), xj = (double)(float)x[id] - (double)ex.r;
+    const double lw = (double)teacher_at(a, row, j) * itau - zref, w = exp2_d(lw * kLog2e), xj = (double)(float)x[id];
     const double y = ex.log2e(xj, a), e = exp2_d(y);
     q[2] += w;
     if (!(w == 0)) q[3] += w * (lw - y * kLn2);
@@ -836,10 +938,10 @@ __device__ __forceinline__ RowStats seg_join(SegLds& l, const DistillArgs& a, in
   }
   __syncthreads();
   const Joined s = {q[0], q[1], q[2], q[3], q[4], q[5], zref, kept};
-  RowStats st = join(a, s, (double)ex.r, MODE);
+  RowStats st = join(a, s, (double)ex.m, MODE);
   st.z = teacher_norm(a, s);
   if (write && t == 0) {
-    if (a.loss) a.loss[row] = row_loss(a, s, st, label >= 0 ? ex.log2e1((double)(float)x[label] - (double)ex.r, a) : 0, label >= 0);
+    if (a.loss) a.loss[row] = row_loss(a, s, st, label >= 0 ? ex.log2e1((double)(float)x[label], a) : 0, label >= 0);
     if (a.stats) static_cast<RowStats*>(a.stats)[row] = st;
   }
   return st;
@@ -868,7 +970,7 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad(DistillArgs a) {
   RowStats st;
   if constexpr (GIVEN) {
     st = static_cast<const RowStats*>(a.stats)[row];
-    ex.r = (float)st.ref;
+    ex.at_row((float)st.ref);
   } else {
     st = seg_join<T, MODE>(l, a, row, label, seg == 0, ex);
   }
@@ -884,7 +986,9 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad(DistillArgs a) {
 #pragma unroll
     for (int i = 0; i < GROUP; ++i) {
       const int c = g + i * kSegThreads;
-      if (c < c1) store_chunk<T>(x, a, grad_chunk<T, MODE>(ex, f, v[i]), c, d);
+      if (c >= c1) continue;
+      if (ex.far()) store_chunk<T>(x, a, grad_chunk<T, MODE, true>(ex, f, v[i]), c, d);
+      else store_chunk<T>(x, a, grad_chunk<T, MODE>(ex, f, v[i]), c, d);
     }
   }
   // kept entries and the label over what the sweep has put there
@@ -895,14 +999,14 @@ __global__ __launch_bounds__(kSegThreads) void distill_grad(DistillArgs a) {
   for (int j = t; j < a.k; j += kSegThreads) {
     const int id = kept_at(a, row, j);
     if (id < 0 || !here(id)) continue;
-    const double y = (double)(float)xr[id] - (double)ex.r;
+    const double y = (double)(float)xr[id];
     const float e = (float)exp2_d(ex.log2e(y, a)), e1 = MODE == 0 ? e : (float)exp2_d(ex.log2e1(y, a));
     const float w = (float)exp2_d(((double)teacher_at(a, row, j) * a.itau - st.z) * kLog2e);
     if (id == label) l.label_kept = 1;
     d[id] = (T)kept_grad(f, e, e1, w, id == label);
   }
   __syncthreads();
-  if (t == 0 && label >= 0 && !l.label_kept && here(label)) d[label] = (T)(outside_grad<T, MODE>(ex, f, (float)xr[label]) - f.label);
+  if (t == 0 && label >= 0 && !l.label_kept && here(label)) d[label] = (T)(label_grad<T, MODE>(ex, f, (float)xr[label]));
 }
 
 // ---- launches ---------------------------------------------------------------

@@ -194,3 +194,47 @@ def test_captured_and_on_another_stream(T, V):
         l2, stats = i8.distill_loss(x2, t, idx, **kw)
         d2 = i8.distill_loss_bwd(x2, t, idx, stats, grad, **kw)
         assert torch.equal(loss, want[0]) and torch.equal(d, want[1]) and torch.equal(leaf_grad, d2)
+
+
+# each size of row that a workgroup holds, full to the last chunks
+@pytest.mark.parametrize("dtype", [bf, fp, f32])
+@pytest.mark.parametrize("T,V,k", [(5, 1003, 20), (5, 2033, 40), (5, 4079, 128), (5, 8171, 300), (5, 16360, 64),
+                                   (129, 32747, 9), (129, 49131, 64), (129, 65521, 640), (129, 98281, 64), (129, 131049, 64)])
+def test_every_size_of_row(T, V, k, dtype):
+    rows = torch.tensor([0, 1, 2, 3, 4, T - 1])
+    for tau, ce in ((1.0, 0.0), (2.0, 0.5), (1.5, 0.25)):
+        x, t, idx, lse, labels, grad = inputs(T, V, k, dtype, V, tau, True)
+        labels = labels if ce else None
+        kw = dict(temperature=tau, teacher_lse=lse, labels=labels, ce_weight=ce)
+        loss, d = i8.distill_loss_and_grad(x, t, idx, grad, **kw)
+        check(x, t, idx, tau, lse, labels, ce, grad, loss, d, rows)
+
+
+@pytest.mark.parametrize("tau,ce", [(1.0, 0.0), (2.0, 0.5), (1.5, 0.25)])
+@pytest.mark.parametrize("T,V", [(9, 700), (130, 33001), (9, 40001)])
+@pytest.mark.parametrize("dtype", [bf, f32])
+def test_logits_far_from_zero(dtype, T, V, tau, ce):
+    """Rows that lie at 2^20 ... 2^60 and at the type's lowest value: nearly every
+    exponential is 0 or that of the maximum.  log2(e) / temperature is rounded once
+    (2^-24 of a loss) and the loss once; the rest as above."""
+    x, t, idx, lse, labels, grad = inputs(T, V, 16, dtype, 8, tau)
+    labels = labels if ce else None
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for r, at in enumerate((2.0 ** 20, -2.0 ** 20, 2.0 ** 22, -2.0 ** 23, 2.0 ** 25, -2.0 ** 60, 2.0 ** 60)):
+        x[r] = (at * (1 + torch.randint(0, 3, (V,), generator=g, device="cuda") / 64)).to(dtype)
+    x[7] = torch.finfo(dtype).min
+    x[8, 5:] = torch.finfo(dtype).min
+    rows = torch.arange(9)
+    pick = lambda v: None if v is None else v[:9]  # noqa: E731
+    want, dw, scale = ref.distill(pick(x), pick(t), pick(idx), tau, None, pick(labels), ce, -100, pick(grad))
+    kw = dict(temperature=tau, labels=labels, ce_weight=ce)
+    loss, d = i8.distill_loss_and_grad(x, t, idx, grad, **kw)
+    loss2, stats = i8.distill_loss(x, t, idx, **kw)
+    d2 = i8.distill_loss_bwd(x, t, idx, stats, grad, **kw)
+    for lo, gd in ((loss, d), (loss2, d2)):
+        tol = (tau * tau + ce) * 2 * REL + 2.0 ** -23 * want.abs()
+        got = lo[rows].cpu()
+        assert bool(((got == want.float()) | ((got.double() - want).abs() <= tol)).all())  # equal: beyond fp32's range
+        tol = scale * REL
+        tol = tol + ref.half_step(dtype) * (dw.abs() + tol) + TINY[dtype]
+        assert bool(((gd[rows].cpu().double() - dw).abs() <= tol).all())

@@ -17,13 +17,28 @@
 // is bound by memory (by the launch, for one token per sequence).  The cosines
 // and sines of a token serve all its heads: a workgroup takes a few whole
 // tokens (or part of one token's heads), computes their table into LDS, then
-// streams the heads with the widest access that the pairs' layout allows.
+// streams the heads with the widest access that the pairs' layout allows.  A
+// token's place in each tensor stands in LDS too: with the division and the wide
+// products in the streaming loop those were what bounded it (16 x 2048 tokens of 36
+// bf16 heads of 64: 95 us, now 55 us for 302 MB, 5.5 TB/s; the backward of 2 x 4001
+// tokens of 40 heads of 128, half of each rotated: 38 us, now 29 us for 164 MB, which
+// partly stay in the last level).  One token of 64 sequences takes 3.7 us.
 #include "internal.h"
+
+#include <type_traits>
 
 namespace i8mp {
 namespace {
 
 constexpr int kRotThreads = 256;
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+
+// Outputs of more bytes than this are written past the caches: with the inputs they
+// would not stay in the last level of 256 MiB anyway.  Rotating, then reading the
+// result (2560 elements a token, 36 heads of 64): 72 MiB out 32 us through the
+// caches and 36 past them, 144 MiB out 73 and 68.
+constexpr int64_t kPast = 96 << 20;
 
 struct RotKernelArgs {
   RotaryTensor t[2];  // q, k
@@ -64,9 +79,12 @@ __device__ __forceinline__ float2 cos_sin(double angle) {
   return make_float2(quarter == 1 || quarter == 2 ? -cc : cc, quarter >= 2 ? -ss : ss);
 }
 
-// V elements of type T, read and written in one access (WIDE) or one by one.
-template <typename T, int V, bool WIDE>
+// V elements of type T, read and written in one access (WIDE) or one by one; PAST:
+// written past the caches.
+template <typename T, int V, bool WIDE, bool PAST>
 struct Pack {
+  template <int BYTES>
+  using Word = std::conditional_t<BYTES == 16, v4i, std::conditional_t<BYTES == 8, v2i, int>>;
   struct __attribute__((aligned(WIDE ? sizeof(T) * V : sizeof(T)))) Mem { T v[V]; };
   static __device__ __forceinline__ void load(const T* p, T (&x)[V]) {
     const Mem m = *reinterpret_cast<const Mem*>(p);
@@ -77,28 +95,42 @@ struct Pack {
     Mem m;
 #pragma unroll
     for (int j = 0; j < V; ++j) m.v[j] = x[j];
-    *reinterpret_cast<Mem*>(p) = m;
+    if constexpr (PAST && WIDE && sizeof(Mem) >= 4)
+      __builtin_nontemporal_store(__builtin_bit_cast(Word<sizeof(Mem)>, m), reinterpret_cast<Word<sizeof(Mem)>*>(p));
+    else
+      *reinterpret_cast<Mem*>(p) = m;
   }
 };
 
 // Every element is read before its pair's outputs are written, by the same
 // thread, so the outputs may be the inputs themselves.
-template <typename T, int V, bool WIDE, bool HALF>
+template <typename T, int V, bool WIDE, bool HALF, bool PAST>
 __global__ __launch_bounds__(kRotThreads) void rotary_kernel(RotKernelArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float2 table[];  // [tokens][rot / 2]: cosine, sine
-  typedef Pack<T, V, WIDE> P;
+  // a token's first elements in q, k and their outputs; [tokens][rot / 2]: cosine, sine
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  int64_t(*at0)[4] = reinterpret_cast<int64_t(*)[4]>(lds);
+  float2* table = reinterpret_cast<float2*>(lds + a.tpw * sizeof(*at0));
+  typedef Pack<T, V, WIDE, PAST> P;
   const int t = threadIdx.x;
   const int half = a.rot / 2;
   const int64_t token0 = (int64_t)blockIdx.x * a.tpw;
   const int tokens = (int)min((int64_t)a.tpw, a.tokens - token0);
   for (int i = t; i < tokens * half; i += kRotThreads) {
     const int tb = i / half, pair = i - tb * half;
-    const int64_t token = token0 + tb, b = token / a.S, s = token - b * a.S;
+    const int64_t token = token0 + tb;
+    const int64_t b = a.tokens >> 31 ? token / a.S : (int64_t)((uint32_t)token / (uint32_t)a.S), s = token - b * a.S;
     const int64_t at = b * a.pos_b + s * a.pos_s;
     const int64_t p = a.pos32 ? (int64_t) static_cast<const int32_t*>(a.pos)[at] : static_cast<const int64_t*>(a.pos)[at];
     float2 cs = cos_sin((double)p * a.freqs[pair]);
     cs.y *= a.sign;
     table[i] = cs;
+    if (pair == 0) {  // once a token: the streaming loop multiplies and divides nothing wide
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        at0[tb][w] = b * a.t[w].x_b + s * a.t[w].x_s;
+        at0[tb][2 + w] = b * a.t[w].y_b + s * a.t[w].y_s;
+      }
+    }
   }
   __syncthreads();
   const int heads = a.t[0].heads + a.t[1].heads;
@@ -108,12 +140,11 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(RotKernelArgs a) {
   int tb = row / rows;
   row -= tb * rows;
   while (tb < tokens) {
-    const int64_t token = token0 + tb, b = token / a.S, s = token - b * a.S;
     const int which = row0 + row >= a.t[0].heads;
     const int h = row0 + row - (which ? a.t[0].heads : 0);
     const RotaryTensor& r = a.t[which];
-    const T* x = static_cast<const T*>(r.x) + b * r.x_b + s * r.x_s + h * r.x_h;
-    T* y = static_cast<T*>(r.y) + b * r.y_b + s * r.y_s + h * r.y_h;
+    const T* x = static_cast<const T*>(r.x) + at0[tb][which] + h * r.x_h;
+    T* y = static_cast<T*>(r.y) + at0[tb][2 + which] + h * r.y_h;
     const float2* cs = table + tb * half;
     if (slot >= a.rot_slots) {  // past the rotated part: copied
       const int e = a.rot + (slot - a.rot_slots) * V;
@@ -154,12 +185,12 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(RotKernelArgs a) {
   }
 }
 
-template <typename T, int V, bool WIDE>
+template <typename T, int V, bool WIDE, bool PAST>
 void launch_pairs(const RotKernelArgs& a, bool half, dim3 grid, size_t lds, hipStream_t stream) {
   if (half)
-    rotary_kernel<T, V, WIDE, true><<<grid, kRotThreads, lds, stream>>>(a);
+    rotary_kernel<T, V, WIDE, true, PAST><<<grid, kRotThreads, lds, stream>>>(a);
   else if constexpr (V >= 2)
-    rotary_kernel<T, V, WIDE, false><<<grid, kRotThreads, lds, stream>>>(a);
+    rotary_kernel<T, V, WIDE, false, PAST><<<grid, kRotThreads, lds, stream>>>(a);
 }
 
 template <typename T>
@@ -192,14 +223,17 @@ hipError_t launch_typed(RotKernelArgs a, bool half, hipStream_t stream) {
   a.drow = kRotThreads / a.slots;
   a.dslot = kRotThreads - a.drow * a.slots;
   const dim3 grid((unsigned)((a.tokens + a.tpw - 1) / a.tpw), (unsigned)((heads + a.rows_per_y - 1) / a.rows_per_y));
-  const size_t lds = (size_t)a.tpw * (a.rot / 2) * sizeof(float2);
+  const size_t lds = (size_t)a.tpw * (a.rot / 2 * sizeof(float2) + 32);
+  const bool past = kPast < (int64_t)sizeof(T) * a.tokens * heads * a.D;
   if constexpr (kWidest >= 8) {
-    if (v == 8) launch_pairs<T, 8, true>(a, half, grid, lds, stream);
+    if (v == 8 && past) launch_pairs<T, 8, true, true>(a, half, grid, lds, stream);
+    if (v == 8 && !past) launch_pairs<T, 8, true, false>(a, half, grid, lds, stream);
   }
-  if (v == 4) launch_pairs<T, 4, true>(a, half, grid, lds, stream);
-  if (v == 2 && wide) launch_pairs<T, 2, true>(a, half, grid, lds, stream);
-  if (v == 2 && !wide) launch_pairs<T, 2, false>(a, half, grid, lds, stream);
-  if (v == 1) launch_pairs<T, 1, true>(a, half, grid, lds, stream);
+  if (v == 4 && past) launch_pairs<T, 4, true, true>(a, half, grid, lds, stream);
+  if (v == 4 && !past) launch_pairs<T, 4, true, false>(a, half, grid, lds, stream);
+  if (v == 2 && wide) launch_pairs<T, 2, true, false>(a, half, grid, lds, stream);
+  if (v == 2 && !wide) launch_pairs<T, 2, false, false>(a, half, grid, lds, stream);
+  if (v == 1) launch_pairs<T, 1, true, false>(a, half, grid, lds, stream);
   return hipGetLastError();
 }
 

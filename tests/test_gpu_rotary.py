@@ -156,3 +156,19 @@ def test_other_stream_and_graph():
         torch.cuda.synchronize()
         assert torch.equal(out, i8.rotary(q, None, pos, freqs)[0])
         check(out, q, pos, freqs, "half")
+
+
+@pytest.mark.parametrize("pairs", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype,step", [(torch.bfloat16, 40), (torch.float16, 36), (torch.float32, 40)])
+def test_large_calls_give_what_their_parts_give(dtype, step, pairs):
+    S, D = 8200, 128 if dtype != torch.float32 else 64
+    store = torch.randn(2, S, step, D, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(dtype)
+    q, k = store[:, :, :32], store[:, :, 32:36]
+    pos = torch.arange(S, device="cuda").expand(2, S)
+    freqs = i8.rotary_frequencies(D // 2).cuda()  # the other half is copied
+    a, b = i8.rotary(q, k, pos, freqs, pairs=pairs)
+    for at in range(0, S, 2050):
+        p, r = i8.rotary(q[:, at:at + 2050], k[:, at:at + 2050], pos[:, at:at + 2050], freqs, pairs=pairs)
+        assert torch.equal(a[:, at:at + 2050], p) and torch.equal(b[:, at:at + 2050], r)
+    i8.rotary(q, k, pos, freqs, pairs=pairs, out_q=q, out_k=k)  # in place
+    assert torch.equal(a, q) and torch.equal(b, k)

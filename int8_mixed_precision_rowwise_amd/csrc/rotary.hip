@@ -102,6 +102,15 @@ struct Pack {
   }
 };
 
+// An fp32 value in T.  Left alone, the compiler gives some fp16 outputs a fused
+// instruction that rounds once where the others round to fp32 first, and which ones
+// differs between this kernel's forms: a call's bits would depend on its size.
+template <typename T>
+__device__ __forceinline__ T rounded(float x) {
+  if constexpr (std::is_same_v<T, _Float16>) asm("" : "+v"(x));
+  return (T)x;
+}
+
 // Every element is read before its pair's outputs are written, by the same
 // thread, so the outputs may be the inputs themselves.
 template <typename T, int V, bool WIDE, bool HALF, bool PAST>
@@ -160,8 +169,8 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(RotKernelArgs a) {
       for (int j = 0; j < V; ++j) {
         const float2 k = cs[e + j];
         const float p = (float)u[j], q = (float)v[j];
-        u[j] = (T)__builtin_fmaf(p, k.x, -(q * k.y));
-        v[j] = (T)__builtin_fmaf(p, k.y, q * k.x);
+        u[j] = rounded<T>(__builtin_fmaf(p, k.x, -(q * k.y)));
+        v[j] = rounded<T>(__builtin_fmaf(p, k.y, q * k.x));
       }
       P::store(y + e, u);
       P::store(y + e + half, v);
@@ -173,8 +182,8 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(RotKernelArgs a) {
       for (int j = 0; j + 1 < V; j += 2) {
         const float2 k = cs[(e + j) / 2];
         const float p = (float)v[j], q = (float)v[j + 1];
-        v[j] = (T)__builtin_fmaf(p, k.x, -(q * k.y));
-        v[j + 1] = (T)__builtin_fmaf(p, k.y, q * k.x);
+        v[j] = rounded<T>(__builtin_fmaf(p, k.x, -(q * k.y)));
+        v[j + 1] = rounded<T>(__builtin_fmaf(p, k.y, q * k.x));
       }
       P::store(y + e, v);
     }

@@ -209,6 +209,10 @@ hipError_t launch_gemm_partials(int64_t M, int64_t N, int64_t K, const int8_t* A
 constexpr int64_t kSkinnyRows = 64;
 hipError_t launch_skinny(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* sa, const int8_t* B,
                          int64_t ldb, const float* sb, uint16_t* C, int64_t ldc, const Epilogue& e, hipStream_t stream);
+// The same from X itself, where its rows are few and short enough.
+bool skinny_takes_x(int64_t M, int64_t K);
+hipError_t launch_skinny_raw(int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t ldx, const int8_t* B, int64_t ldb,
+                             const float* sb, uint16_t* C, int64_t ldc, const Epilogue& e, hipStream_t stream);
 
 // dZ = dY act'(Z) of a backward, its codes along rows and down columns (either
 // may be null) with their scales, and the column sums of the unrounded values.

@@ -394,6 +394,9 @@ i8mp_status i8mp_linear_wq_fwd(const i8mp_linear_act* p, const int8_t* Wq, int64
   ActFwdWs w;
   carve_act_fwd(ws, M, N, K, false, &w);
   const hipStream_t s = as_stream(stream);
+  if (i8mp::skinny_takes_x(M, K))
+    return hip_status(i8mp::launch_skinny_raw(M, N, K, static_cast<const uint16_t*>(p->X), p->ldx, Wq, ldwq, w_scale,
+                                              p->Y, p->ldy, epilogue_of(p), s));
   // without a contraction the codes of X are the padding's zeros, and W's may be anything readable
   if (K == 0) Wq = w.qx, ldwq = 0;
   hipError_t e = i8mp::launch_quantize_rowwise(p->X, M, K, p->ldx, w.qx, padded_k(K), w.sx, I8MP_RNE, 0, 0, s);

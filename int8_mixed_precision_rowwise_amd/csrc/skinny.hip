@@ -9,9 +9,12 @@
 // go from memory straight into the matrix instruction's registers: lane l holds
 // 16 codes of row l % 16 at step offset 16 (l / 16), which is what
 // v_mfma_i32_16x16x64_i8 wants of an operand.  The waves' int32 sums are joined in
-// LDS (exact in any order).
+// LDS (exact in any order).  One token against 14336 x 4096 codes: 15.9 us with the
+// token's quantization (3.7 TB/s; the launch, the first weights' way and the join are 4
+// of them), 64 tokens 34 us, where X's codes cost as many cache reads as the weights.
 #include "activation.h"
 #include "internal.h"
+#include "quant_device.h"
 
 #include <algorithm>
 
@@ -21,6 +24,12 @@ namespace {
 typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr int kSkWaves = 8, kSkThreads = 64 * kSkWaves;
+// Chunks of X, 8 values each, that a thread quantizes at most.  Every workgroup
+// does this work again, so it has to stay small against reading the weights.
+// Both sides, kernels' time with 14336 x 4096 codes: one row (a chunk a thread) 15.9 us,
+// with a launch of its own for the quantization 20; 4 rows (4 chunks) 20.7 and 21;
+// 8 rows (8 chunks) 24.3 and 21.4.  5003 x 2040: 13 rows (8 chunks) 13.7 and 11.1.
+constexpr int kSkChunks = 4;
 
 struct SkinnyArgs {
   const int8_t *A, *B;  // codes of X [M x K] and W [N x K]
@@ -49,6 +58,30 @@ __device__ __forceinline__ float activate(int act, float z) {
     case kActGeluTanh: return activation<kActGeluTanh>(z);
     case kActSilu: return activation<kActSilu>(z);
     default: return z;
+  }
+}
+
+// The waves' sums joined and finished; sa: scales of the rows of X.
+template <int MT, int CT>
+__device__ __forceinline__ void write_outputs(const SkinnyArgs& a, const v4i (*red)[MT * CT][64], const float* sa, int64_t n0) {
+  // one group of 4 adjacent outputs per thread and turn
+  for (int o = threadIdx.x; o < MT * CT * 64; o += kSkThreads) {
+    const int tile = o >> 6, l = o & 63;
+    v4i s = red[0][tile][l];
+#pragma unroll
+    for (int w = 1; w < kSkWaves; ++w) s += red[w][tile][l];
+    const int64_t m = 16 * (tile / CT) + (l & 15), n = n0 + 16 * (tile % CT) + 4 * (l >> 4);
+    if (m >= a.M) continue;
+    const float sam = sa[m];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (n + e >= a.N) break;
+      const float z = __builtin_fmaf((float)s[e] * sam, a.sb[n + e], a.epi.bias ? bf16_at(a.epi.bias, n + e) : 0.0f);
+      float y = activate(a.epi.act, z);
+      if (a.epi.residual) y += bf16_at(a.epi.residual, m * a.epi.ld_residual + n + e);
+      reinterpret_cast<__bf16*>(a.C)[m * a.ldc + n + e] = (__bf16)y;
+      if (a.epi.z) reinterpret_cast<__bf16*>(a.epi.z)[m * a.epi.ld_z + n + e] = (__bf16)z;
+    }
   }
 }
 
@@ -98,31 +131,113 @@ __global__ __launch_bounds__(kSkThreads) void skinny_gemm(SkinnyArgs a) {
 #pragma unroll
     for (int j = 0; j < CT; ++j) red[wave][i * CT + j][lane] = acc[i][j];
   __syncthreads();
-  // one group of 4 adjacent outputs per thread and turn
-  for (int o = threadIdx.x; o < MT * CT * 64; o += kSkThreads) {
-    const int tile = o >> 6, l = o & 63;
-    v4i s = red[0][tile][l];
-#pragma unroll
-    for (int w = 1; w < kSkWaves; ++w) s += red[w][tile][l];
-    const int64_t m = 16 * (tile / CT) + (l & 15), n = n0 + 16 * (tile % CT) + 4 * (l >> 4);
-    if (m >= a.M) continue;
-    const float sam = a.sa[m];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (n + e >= a.N) break;
-      const float z = __builtin_fmaf((float)s[e] * sam, a.sb[n + e], a.epi.bias ? bf16_at(a.epi.bias, n + e) : 0.0f);
-      float y = activate(a.epi.act, z);
-      if (a.epi.residual) y += bf16_at(a.epi.residual, m * a.epi.ld_residual + n + e);
-      reinterpret_cast<__bf16*>(a.C)[m * a.ldc + n + e] = (__bf16)y;
-      if (a.epi.z) reinterpret_cast<__bf16*>(a.epi.z)[m * a.epi.ld_z + n + e] = (__bf16)z;
-    }
-  }
+  write_outputs<MT, CT>(a, red, a.sa, n0);
 }
 
-template <int MT, int CT>
-void launch_skinny_tiles(const SkinnyArgs& a, hipStream_t stream) {
-  skinny_gemm<MT, CT><<<(unsigned)((a.N + 16 * CT - 1) / (16 * CT)), kSkThreads, 0, stream>>>(a);
+// The same from X itself, for up to 16 short rows: every workgroup quantizes them
+// (as quantize_rowwise does) into LDS while its first weights are on the way.
+// Of the 8 waves, kSkWaves / G rows' worth of G waves each share a row.
+template <int Q>
+__global__ __launch_bounds__(kSkThreads) void skinny_raw(SkinnyArgs a, const uint16_t* __restrict__ x, int64_t ldx, int G, int C,
+                                                         int stride) {
+  constexpr int U = 8;  // steps in flight per wave
+  __shared__ __attribute__((aligned(16))) v4i red[kSkWaves][1][64];
+  __shared__ uint32_t amax[16];
+  __shared__ float sx[16];
+  extern __shared__ __attribute__((aligned(16))) int8_t codes[];  // [M][stride]
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int li = lane & 15, q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int K = (int)a.K, M = (int)a.M;
+  // chunk i of a thread: of row row0 + (i / C) rows, 8 values from column 8 (col + (i % C) 64 G)
+  const int rows = kSkWaves / G, row0 = wave / G, col = (wave % G) * 64 + lane;
+  uint4 v[Q];
+#pragma unroll
+  for (int i = 0, r = row0, c = col, n = 0; i < Q; ++i) {
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r < M && 8 * c < K) v[i] = *reinterpret_cast<const uint4*>(x + r * ldx + 8 * c);
+    c += 64 * G;
+    if (++n == C) n = 0, c = col, r += rows;
+  }
+  const int8_t* pb = a.B + min(n0 + li, a.N - 1) * a.ldb;  // rows past the last one repeat it: their outputs are not stored
+  v4i fb[U];
+  // steps past the row's end read its last codes again, against zeros of X: no branch around a load
+  const int last = (K - 1) & ~15;
+  const auto load = [&](int s0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) fb[u] = *reinterpret_cast<const v4i*>(pb + min(s0 + u * kSkWaves * 64 + 16 * q, last));
+  };
+  load(wave * 64);
+  if (t < 16) amax[t] = 0;
+  __syncthreads();
+  us2 m2 = {0, 0};
+#pragma unroll
+  for (int i = 0, r = row0, c = col, n = 0; i < Q; ++i) {
+    if (8 * c + 8 > K) v[i] = keep_first(v[i], max(0, K - 8 * c));
+    m2 = absmax_bits(m2, v[i]);
+    c += 64 * G;
+    if (++n == C || i == Q - 1) {
+      const uint32_t m = wave_max_u32<true>(max((uint32_t)m2.x, (uint32_t)m2.y));
+      if (lane == 0 && r < M) atomicMax(amax + r, m);
+      m2 = (us2){0, 0};
+      n = 0, c = col, r += rows;
+    }
+  }
+  __syncthreads();
+  if (t < M) sx[t] = make_scale(amax[t]).s;
+#pragma unroll
+  for (int i = 0, r = row0, c = col, n = 0; i < Q; ++i) {
+    if (r < M && 8 * c < stride) {
+      const GroupScale g = make_scale(__builtin_amdgcn_readfirstlane(amax[r]));
+      const uint2 w = g.mode == 1 ? quantize_chunk<false, true, false, 1>(v[i], &g, 0, 0, 0)
+                                  : quantize_chunk<false, true, false, -1>(v[i], &g, 0, 0, 0);
+      *reinterpret_cast<uint2*>(codes + r * stride + 8 * c) = w;
+    }
+    c += 64 * G;
+    if (++n == C) n = 0, c = col, r += rows;
+  }
+  __syncthreads();
+  const int8_t* pa = codes + min(li, M - 1) * stride;
+  v4i acc = {0, 0, 0, 0};
+  const auto add = [&](const v4i(&w)[U], int s0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = s0 + u * kSkWaves * 64 + 16 * q;
+      v4i fa = *reinterpret_cast<const v4i*>(pa + min(k, last));
+      if (k + 16 > K) fa = first_bytes(fa, K - k);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u], fa, acc, 0, 0, 0);
+    }
+  };
+  int s0 = wave * 64;
+  for (; s0 + U * kSkWaves * 64 < K; s0 += U * kSkWaves * 64) {
+    v4i w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = fb[u];
+    load(s0 + U * kSkWaves * 64);
+    add(w, s0);
+  }
+  add(fb, s0);
+  red[wave][0][lane] = acc;
+  __syncthreads();
+  write_outputs<1, 1>(a, red, sx, n0);
 }
+
+// One tile of columns a workgroup while each CU gets at most one workgroup; beyond
+// that two, which halve the reads of X's codes (every workgroup takes them from the
+// cache).  Both sides, two tiles and one: 13 rows against 14336 x 4096 21.7 us and
+// 24.2, 17 rows 23.8 and 27.2, 64 rows against 5003 x 2040 13.8 and 17.6; but 13
+// against 4096 x 14336 33 and 26, 64 56 and 48.
+template <int MT>
+void launch_skinny_tiles(const SkinnyArgs& a, hipStream_t stream) {
+  if (a.N > 16 * 256)
+    skinny_gemm<MT, 2><<<(unsigned)((a.N + 31) / 32), kSkThreads, 0, stream>>>(a);
+  else
+    skinny_gemm<MT, 1><<<(unsigned)((a.N + 15) / 16), kSkThreads, 0, stream>>>(a);
+}
+
+// G waves a row of X, and chunks of it a thread.
+int skinny_group(int64_t M) { return M <= 1 ? 8 : M <= 2 ? 4 : M <= 4 ? 2 : 1; }
+int skinny_chunks(int64_t M, int64_t K) { return (int)((K + 511) / 512 + skinny_group(M) - 1) / skinny_group(M); }
 
 }  // namespace
 
@@ -131,11 +246,30 @@ hipError_t launch_skinny(int64_t M, int64_t N, int64_t K, const int8_t* A, int64
   if (M == 0 || N == 0) return hipSuccess;
   const SkinnyArgs a{A, B, sa, sb, C, M, N, K, lda, ldb, ldc, e};
   switch ((M + 15) / 16) {
-    case 1: launch_skinny_tiles<1, 1>(a, stream); break;
-    case 2: launch_skinny_tiles<2, 1>(a, stream); break;
-    case 3: launch_skinny_tiles<3, 2>(a, stream); break;
-    default: launch_skinny_tiles<4, 2>(a, stream);
+    case 1: launch_skinny_tiles<1>(a, stream); break;
+    case 2: launch_skinny_tiles<2>(a, stream); break;
+    case 3: launch_skinny_tiles<3>(a, stream); break;
+    default: launch_skinny_tiles<4>(a, stream);
   }
+  return hipGetLastError();
+}
+
+// M rows in turns of kSkWaves / G, each of `chunks` chunks a thread: as many as registers hold.
+bool skinny_takes_x(int64_t M, int64_t K) {
+  if (M < 1 || M > 16 || K < 1) return false;
+  const int turns = (int)(M * skinny_group(M) + kSkWaves - 1) / kSkWaves;
+  return skinny_chunks(M, K) <= kSkChunks / turns;
+}
+
+hipError_t launch_skinny_raw(int64_t M, int64_t N, int64_t K, const uint16_t* X, int64_t ldx, const int8_t* B, int64_t ldb,
+                             const float* sb, uint16_t* C, int64_t ldc, const Epilogue& e, hipStream_t stream) {
+  const SkinnyArgs a{nullptr, B, nullptr, sb, C, M, N, K, 0, ldb, ldc, e};
+  const int G = skinny_group(M), per = skinny_chunks(M, K), turns = (int)(M * G + kSkWaves - 1) / kSkWaves;
+  const int stride = (int)((K + 15) / 16 * 16 + 16);  // 16 more: rows start in different banks
+  const dim3 grid((unsigned)((N + 15) / 16));
+  const size_t lds = (size_t)M * stride;
+  if (per * turns <= 2) skinny_raw<2><<<grid, kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride);
+  else skinny_raw<kSkChunks><<<grid, kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride);
   return hipGetLastError();
 }
 

@@ -237,3 +237,29 @@ def test_captured_and_on_another_stream(M):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(got, step()))
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9, 16, 17])
+@pytest.mark.parametrize("N,K", [(50, 8), (33, 40), (4100, 264), (70, 1001), (40, 2040), (130, 4104), (24, 16384)])
+def test_few_tokens_have_the_codes_of_the_quantize_pass(M, N, K):
+    """Bits equal to those from codes that quantize_rowwise wrote, whichever kernel forms
+    them; rows of zeros, of tiny and of huge values, and strided rows among them."""
+    g = torch.Generator(device="cuda").manual_seed(M * K)
+    store = torch.randn(M, (K + 15) // 8 * 8, generator=g, device="cuda").bfloat16()
+    X = store[:, :K]
+    X[0] *= 3
+    if M > 1:
+        X[1] = 0
+    if M > 2:
+        X[2] *= 2.0 ** -118
+    if M > 3:
+        X[3, K // 2] = 2.0 ** 100
+    W = torch.randn(N, (K + 7) // 8 * 8, generator=g, device="cuda").bfloat16()[:, :K]
+    bias = torch.randn(N, generator=g, device="cuda").bfloat16()
+    Wq, ws = i8.quantize_rowwise(W)
+    want = i8.linear_act_fwd(X, W, bias=bias, activation="gelu")
+    got = i8.linear_wq_fwd(X, Wq, ws, bias=bias, activation="gelu")
+    assert torch.equal(got, want)
+    X[0, K - 1] = float("nan")
+    got = i8.linear_wq_fwd(X, Wq, ws, bias=bias)
+    assert torch.equal(got[1:], i8.linear_act_fwd(X, W, bias=bias)[1:]) and bool(got[0].isnan().all())

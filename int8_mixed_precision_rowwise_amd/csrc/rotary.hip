@@ -35,10 +35,10 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v2i __attribute__((ext_vector_type(2)));
 
 // Outputs of more bytes than this are written past the caches: with the inputs they
-// would not stay in the last level of 256 MiB anyway.  Rotating, then reading the
-// result (2560 elements a token, 36 heads of 64): 72 MiB out 32 us through the
-// caches and 36 past them, 144 MiB out 73 and 68.
-constexpr int64_t kPast = 96 << 20;
+// would not stay in the last level of 256 MiB anyway.  82 MB out from inputs that are
+// not in the caches: 34 us past them and 41 through them; 75 MB from inputs that
+// are, then read again: 36 and 32; 151 MB: 68 and 73.
+constexpr int64_t kPast = 64 << 20;
 
 struct RotKernelArgs {
   RotaryTensor t[2];  // q, k

@@ -26,10 +26,17 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 constexpr int kSkWaves = 8, kSkThreads = 64 * kSkWaves;
 // Chunks of X, 8 values each, that a thread quantizes at most.  Every workgroup
 // does this work again, so it has to stay small against reading the weights.
-// Both sides, kernels' time with 14336 x 4096 codes: one row (a chunk a thread) 15.9 us,
-// with a launch of its own for the quantization 20; 4 rows (4 chunks) 20.7 and 21;
-// 8 rows (8 chunks) 24.3 and 21.4.  5003 x 2040: 13 rows (8 chunks) 13.7 and 11.1.
-constexpr int kSkChunks = 4;
+// Both sides, all the call's kernels (a separate quantization is one more): one row against
+// 14336 x 4096 codes (a chunk a thread) 16 us and 20, 8 rows (8 chunks) 19.5 and 20.7;
+// 4 rows against 5003 x 2040 (2) 6.4 us and 8.8, 13 rows (8) 9.8 and 9.9.
+constexpr int kSkChunks = 8;
+
+// One tile of columns a workgroup while each CU gets at most one workgroup; beyond
+// that two, which halve the reads of X's codes (every workgroup takes them from the
+// cache).  Both sides, two tiles and one: 13 rows against 14336 x 4096 21.7 us and
+// 24.2, 17 rows 23.8 and 27.2, 64 rows against 5003 x 2040 13.8 and 17.6; but 13
+// against 4096 x 14336 33 and 26, 64 56 and 48.
+constexpr int64_t kSkWideN = 16 * 256;
 
 struct SkinnyArgs {
   const int8_t *A, *B;  // codes of X [M x K] and W [N x K]
@@ -137,17 +144,17 @@ __global__ __launch_bounds__(kSkThreads) void skinny_gemm(SkinnyArgs a) {
 // The same from X itself, for up to 16 short rows: every workgroup quantizes them
 // (as quantize_rowwise does) into LDS while its first weights are on the way.
 // Of the 8 waves, kSkWaves / G rows' worth of G waves each share a row.
-template <int Q>
+template <int Q, int CT>
 __global__ __launch_bounds__(kSkThreads) void skinny_raw(SkinnyArgs a, const uint16_t* __restrict__ x, int64_t ldx, int G, int C,
                                                          int stride) {
-  constexpr int U = 8;  // steps in flight per wave
-  __shared__ __attribute__((aligned(16))) v4i red[kSkWaves][1][64];
+  constexpr int U = 8 / CT;  // steps in flight per wave
+  __shared__ __attribute__((aligned(16))) v4i red[kSkWaves][CT][64];
   __shared__ uint32_t amax[16];
   __shared__ float sx[16];
   extern __shared__ __attribute__((aligned(16))) int8_t codes[];  // [M][stride]
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int li = lane & 15, q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n0 = (int64_t)blockIdx.x * 16 * CT;
   const int K = (int)a.K, M = (int)a.M;
   // chunk i of a thread: of row row0 + (i / C) rows, 8 values from column 8 (col + (i % C) 64 G)
   const int rows = kSkWaves / G, row0 = wave / G, col = (wave % G) * 64 + lane;
@@ -159,13 +166,17 @@ __global__ __launch_bounds__(kSkThreads) void skinny_raw(SkinnyArgs a, const uin
     c += 64 * G;
     if (++n == C) n = 0, c = col, r += rows;
   }
-  const int8_t* pb = a.B + min(n0 + li, a.N - 1) * a.ldb;  // rows past the last one repeat it: their outputs are not stored
-  v4i fb[U];
+  const int8_t* pb[CT];  // rows past the last one repeat it: their outputs are not stored
+#pragma unroll
+  for (int j = 0; j < CT; ++j) pb[j] = a.B + min(n0 + 16 * j + li, a.N - 1) * a.ldb;
+  v4i fb[U][CT];
   // steps past the row's end read its last codes again, against zeros of X: no branch around a load
   const int last = (K - 1) & ~15;
   const auto load = [&](int s0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) fb[u] = *reinterpret_cast<const v4i*>(pb + min(s0 + u * kSkWaves * 64 + 16 * q, last));
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < CT; ++j) fb[u][j] = *reinterpret_cast<const v4i*>(pb[j] + min(s0 + u * kSkWaves * 64 + 16 * q, last));
   };
   load(wave * 64);
   if (t < 16) amax[t] = 0;
@@ -198,38 +209,39 @@ __global__ __launch_bounds__(kSkThreads) void skinny_raw(SkinnyArgs a, const uin
   }
   __syncthreads();
   const int8_t* pa = codes + min(li, M - 1) * stride;
-  v4i acc = {0, 0, 0, 0};
-  const auto add = [&](const v4i(&w)[U], int s0) __attribute__((always_inline)) {
+  v4i acc[CT];
+#pragma unroll
+  for (int j = 0; j < CT; ++j) acc[j] = (v4i){0, 0, 0, 0};
+  const auto add = [&](const v4i(&w)[U][CT], int s0) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = s0 + u * kSkWaves * 64 + 16 * q;
       v4i fa = *reinterpret_cast<const v4i*>(pa + min(k, last));
       if (k + 16 > K) fa = first_bytes(fa, K - k);
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u], fa, acc, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < CT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][j], fa, acc[j], 0, 0, 0);
     }
   };
   int s0 = wave * 64;
   for (; s0 + U * kSkWaves * 64 < K; s0 += U * kSkWaves * 64) {
-    v4i w[U];
+    v4i w[U][CT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = fb[u];
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < CT; ++j) w[u][j] = fb[u][j];
     load(s0 + U * kSkWaves * 64);
     add(w, s0);
   }
   add(fb, s0);
-  red[wave][0][lane] = acc;
+#pragma unroll
+  for (int j = 0; j < CT; ++j) red[wave][j][lane] = acc[j];
   __syncthreads();
-  write_outputs<1, 1>(a, red, sx, n0);
+  write_outputs<1, CT>(a, red, sx, n0);
 }
 
-// One tile of columns a workgroup while each CU gets at most one workgroup; beyond
-// that two, which halve the reads of X's codes (every workgroup takes them from the
-// cache).  Both sides, two tiles and one: 13 rows against 14336 x 4096 21.7 us and
-// 24.2, 17 rows 23.8 and 27.2, 64 rows against 5003 x 2040 13.8 and 17.6; but 13
-// against 4096 x 14336 33 and 26, 64 56 and 48.
 template <int MT>
 void launch_skinny_tiles(const SkinnyArgs& a, hipStream_t stream) {
-  if (a.N > 16 * 256)
+  if (a.N > kSkWideN)
     skinny_gemm<MT, 2><<<(unsigned)((a.N + 31) / 32), kSkThreads, 0, stream>>>(a);
   else
     skinny_gemm<MT, 1><<<(unsigned)((a.N + 15) / 16), kSkThreads, 0, stream>>>(a);
@@ -266,10 +278,16 @@ hipError_t launch_skinny_raw(int64_t M, int64_t N, int64_t K, const uint16_t* X,
   const SkinnyArgs a{nullptr, B, nullptr, sb, C, M, N, K, 0, ldb, ldc, e};
   const int G = skinny_group(M), per = skinny_chunks(M, K), turns = (int)(M * G + kSkWaves - 1) / kSkWaves;
   const int stride = (int)((K + 15) / 16 * 16 + 16);  // 16 more: rows start in different banks
-  const dim3 grid((unsigned)((N + 15) / 16));
   const size_t lds = (size_t)M * stride;
-  if (per * turns <= 2) skinny_raw<2><<<grid, kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride);
-  else skinny_raw<kSkChunks><<<grid, kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride);
+  const int held = per * turns <= 2 ? 2 : per * turns <= 4 ? 4 : kSkChunks;
+  switch (held + (N > kSkWideN)) {
+    case 2: skinny_raw<2, 1><<<(unsigned)((N + 15) / 16), kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride); break;
+    case 3: skinny_raw<2, 2><<<(unsigned)((N + 31) / 32), kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride); break;
+    case 4: skinny_raw<4, 1><<<(unsigned)((N + 15) / 16), kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride); break;
+    case 5: skinny_raw<4, 2><<<(unsigned)((N + 31) / 32), kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride); break;
+    case 8: skinny_raw<8, 1><<<(unsigned)((N + 15) / 16), kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride); break;
+    default: skinny_raw<8, 2><<<(unsigned)((N + 31) / 32), kSkThreads, lds, stream>>>(a, X, ldx, G, per, stride);
+  }
   return hipGetLastError();
 }
 

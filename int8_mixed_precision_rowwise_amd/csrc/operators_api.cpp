@@ -29,9 +29,9 @@ static int64_t distill_chunks(int64_t V, int elem) { return (V * elem + 15 + ele
 
 // A row in one workgroup's registers is read once; segments read it twice but
 // spread few rows over the chip.  Both sides, loss and gradient of bf16 rows (a row a
-// workgroup takes the same time up to 256 rows): 32000 classes 12 us, in segments 13
-// for one row; 64000 classes 16 us, in segments 13 for 16 rows and 17 for 32;
-// 128256 classes 25 us, in segments 17 for 16 rows and 26 for 32.
+// workgroup takes nearly the same time up to 256 rows): 32000 classes 10 us, in
+// segments 13 for one row; 64000 classes 15 us, in segments 13 for 16 rows and 17
+// for 32; 128256 classes 22 us, in segments 16 for 16 rows and 26 for 32.
 static int distill_shape(int64_t T, int64_t V, int k, int elem) {
   const int64_t chunks = distill_chunks(V, elem);
   if (chunks > 16384 || (T < 24 && chunks > 4096)) return kSegments;

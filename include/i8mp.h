@@ -441,7 +441,7 @@ i8mp_status i8mp_linear_act_fwd(const i8mp_linear_act* p, const i8mp_linear_opts
  * The same forward over weights quantized once (serving): Wq int8 [N x K] codes
  * with scales w_scale [N], for instance from i8mp_quantize_rowwise; p->W and
  * p->ldw are not read.  X is quantized to nearest.  Up to 64 rows take a kernel
- * for few tokens.
+ * for few tokens.  Few short rows need no workspace (0 bytes; ws is then not looked at).
  */
 size_t i8mp_linear_wq_workspace_bytes(int64_t M, int64_t N, int64_t K);
 i8mp_status i8mp_linear_wq_fwd(const i8mp_linear_act* p, const int8_t* Wq, int64_t ldwq, const float* w_scale,

@@ -23,7 +23,7 @@
 // q_rest and mass q_j - p_j free of cancellation.
 //
 // Measured: loss and gradient of 4096 x 128256 bf16 logits, temperature 2 with hard
-// labels, 524 - 568 us for 2.1 GB, 3.7 - 4.0 TB/s where a copy of that size reaches 5.1.  Two
+// labels, 513 - 552 us for 2.1 GB, 3.8 - 4.1 TB/s where a copy of that size reaches 5.1.  Two
 // exponentials an element at a quarter of the vector rate and some 13 other operations
 // are about 240 us of every CU's time; a row of this length fills a CU, so they
 // overlap with memory only as far as the CUs are at different places of their rows.  Loss of

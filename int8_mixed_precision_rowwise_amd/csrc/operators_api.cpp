@@ -318,7 +318,7 @@ size_t i8mp_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t 
 }
 
 size_t i8mp_linear_wq_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return linear_dims_ok(M, N, K) ? carve_act_fwd(nullptr, M, N, K, false, nullptr) : 0;
+  return linear_dims_ok(M, N, K) && !i8mp::skinny_takes_x(M, K) ? carve_act_fwd(nullptr, M, N, K, false, nullptr) : 0;
 }
 
 i8mp_status i8mp_linear_act_fwd(const i8mp_linear_act* p, const i8mp_linear_opts* opts, float* colmax_x,
@@ -387,6 +387,12 @@ i8mp_status i8mp_linear_wq_fwd(const i8mp_linear_act* p, const int8_t* Wq, int64
     if (overlap(out[0], r) || overlap(out[1], r)) return I8MP_EINVAL;
   if (overlap(out[0], out[1])) return I8MP_EINVAL;
   if (M == 0 || N == 0) return I8MP_OK;
+  const hipStream_t s = as_stream(stream);
+  if (i8mp::skinny_takes_x(M, K)) {
+    if ((st = device_check()) != I8MP_OK) return st;
+    return hip_status(i8mp::launch_skinny_raw(M, N, K, static_cast<const uint16_t*>(p->X), p->ldx, Wq, ldwq, w_scale,
+                                              p->Y, p->ldy, epilogue_of(p), s));
+  }
   const size_t need = carve_act_fwd(nullptr, M, N, K, false, nullptr);
   if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return I8MP_EWORKSPACE;
   const Range rw = vec_range(ws, (int64_t)need, 1);
@@ -396,10 +402,6 @@ i8mp_status i8mp_linear_wq_fwd(const i8mp_linear_act* p, const int8_t* Wq, int64
   if ((st = device_check()) != I8MP_OK) return st;
   ActFwdWs w;
   carve_act_fwd(ws, M, N, K, false, &w);
-  const hipStream_t s = as_stream(stream);
-  if (i8mp::skinny_takes_x(M, K))
-    return hip_status(i8mp::launch_skinny_raw(M, N, K, static_cast<const uint16_t*>(p->X), p->ldx, Wq, ldwq, w_scale,
-                                              p->Y, p->ldy, epilogue_of(p), s));
   // without a contraction the codes of X are the padding's zeros, and W's may be anything readable
   if (K == 0) Wq = w.qx, ldwq = 0;
   hipError_t e = i8mp::launch_quantize_rowwise(p->X, M, K, p->ldx, w.qx, padded_k(K), w.sx, I8MP_RNE, 0, 0, s);

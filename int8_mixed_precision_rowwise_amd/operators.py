@@ -190,7 +190,8 @@ def linear_wq_fwd(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, bias
     if not isinstance(w_scale, torch.Tensor):
         raise TypeError(f"w_scale: torch.Tensor expected, got {type(w_scale).__name__}")
     p, dev, Y, _ = _act_forward(X, Wq, w_scale, bias, activation, residual, out, workspace)
-    ws, n = _space(workspace, linear_wq_workspace_bytes(p.M, p.N, p.K), dev)
+    need = linear_wq_workspace_bytes(p.M, p.N, p.K)
+    ws, n = _space(workspace, need, dev) if need else (None, 0)  # few short rows take none
     _call(dev, "i8mp_linear_wq_fwd", p, _ptr(Wq), _ld2(Wq), _ptr(w_scale), ws, n)
     return Y
 

@@ -240,7 +240,7 @@ def test_captured_and_on_another_stream(M):
 
 
 @pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9, 16, 17])
-@pytest.mark.parametrize("N,K", [(50, 8), (33, 40), (4100, 264), (70, 1001), (40, 2040), (130, 4104), (24, 16384)])
+@pytest.mark.parametrize("N,K", [(50, 8), (33, 40), (4100, 264), (70, 1001), (40, 2040), (4107, 2040), (130, 4104), (24, 16384)])
 def test_few_tokens_have_the_codes_of_the_quantize_pass(M, N, K):
     """Bits equal to those from codes that quantize_rowwise wrote, whichever kernel forms
     them; rows of zeros, of tiny and of huge values, and strided rows among them."""

@@ -92,10 +92,11 @@ def linear_wq_workspace_bytes(M: int, N: int, K: int) -> int:
     return _pkg.lib.i8mp_linear_wq_workspace_bytes(M, N, K)
 
 
-def _space(workspace, need: int, dev):
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    return workspace.data_ptr(), workspace.numel()
+def _space(workspace, need: int, dev) -> torch.Tensor:
+    """The workspace of a call, which the caller holds until the call has returned: the
+    library lets other threads run while it launches, and a block given back before
+    would be theirs on the same stream."""
+    return torch.empty(max(need, 1), dtype=torch.uint8, device=dev) if workspace is None else workspace
 
 
 def _act_forward(X, W, w_scale, bias, activation, residual, out, workspace, keep_z=False):
@@ -163,8 +164,8 @@ def linear_act_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None =
     residual are added in fp32 and Y is rounded once.  Y's rows start every 16
     bytes unless out is given."""
     p, dev, Y, _ = _act_forward(X, W, None, bias, activation, residual, out, workspace)
-    ws, n = _space(workspace, linear_act_workspace_bytes(p.M, p.N, p.K, False), dev)
-    _call(dev, "i8mp_linear_act_fwd", p, _pkg._opts(rounding, seed, offset), None, None, ws, n)
+    ws = _space(workspace, linear_act_workspace_bytes(p.M, p.N, p.K, False), dev)
+    _call(dev, "i8mp_linear_act_fwd", p, _pkg._opts(rounding, seed, offset), None, None, ws.data_ptr(), ws.numel())
     return Y
 
 
@@ -177,8 +178,8 @@ def linear_act_fwd_train(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | 
     p, dev, Y, Z = _act_forward(X, W, None, bias, activation, residual, out, workspace, keep_z=True)
     cx = torch.empty(p.K, dtype=torch.float32, device=dev)
     cw = torch.empty(p.K, dtype=torch.float32, device=dev)
-    ws, n = _space(workspace, linear_act_workspace_bytes(p.M, p.N, p.K, False), dev)
-    _call(dev, "i8mp_linear_act_fwd", p, _pkg._opts(rounding, seed, offset), _ptr(cx), _ptr(cw), ws, n)
+    ws = _space(workspace, linear_act_workspace_bytes(p.M, p.N, p.K, False), dev)
+    _call(dev, "i8mp_linear_act_fwd", p, _pkg._opts(rounding, seed, offset), _ptr(cx), _ptr(cw), ws.data_ptr(), ws.numel())
     return Y, Z, cx, cw
 
 
@@ -191,8 +192,9 @@ def linear_wq_fwd(X: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, bias
         raise TypeError(f"w_scale: torch.Tensor expected, got {type(w_scale).__name__}")
     p, dev, Y, _ = _act_forward(X, Wq, w_scale, bias, activation, residual, out, workspace)
     need = linear_wq_workspace_bytes(p.M, p.N, p.K)
-    ws, n = _space(workspace, need, dev) if need else (None, 0)  # few short rows take none
-    _call(dev, "i8mp_linear_wq_fwd", p, _ptr(Wq), _ld2(Wq), _ptr(w_scale), ws, n)
+    ws = _space(workspace, need, dev) if need else None  # few short rows take none
+    _call(dev, "i8mp_linear_wq_fwd", p, _ptr(Wq), _ld2(Wq), _ptr(w_scale), None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
     return Y
 
 
@@ -234,8 +236,9 @@ def linear_act_bwd(dY: torch.Tensor, Z: torch.Tensor | None, X: torch.Tensor, W:
     p = _pkg._LinearActGrad(M, N, K, _ptr(dY), _ld2(dY), _ptr(Z), 0 if Z is None else _ld2(Z), _ptr(X), _ld2(X), _ptr(W),
                             _ld2(W), act, _ptr(dX), 0 if dX is None else _ld2(dX), _ptr(dW), 0 if dW is None else _ld2(dW),
                             _ptr(dbias))
-    ws, n = _space(workspace, linear_act_workspace_bytes(M, N, K, True), dev)
-    _call(dev, "i8mp_linear_act_bwd", p, _pkg._opts(rounding, seed, offset), _ptr(colmax_x), _ptr(colmax_w), ws, n)
+    ws = _space(workspace, linear_act_workspace_bytes(M, N, K, True), dev)
+    _call(dev, "i8mp_linear_act_bwd", p, _pkg._opts(rounding, seed, offset), _ptr(colmax_x), _ptr(colmax_w), ws.data_ptr(),
+          ws.numel())
     return dX, dW, dbias
 
 
@@ -467,10 +470,9 @@ def _distill_checks(logits, teacher, idx, temperature, teacher_lse, labels, ce_w
 
 
 def _distill_ws(p, dev, workspace):
+    """The workspace to hold until the call has returned, or None."""
     need = _pkg.lib.i8mp_distill_workspace_bytes(p.T, p.V, p.kept, p.dtype)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    return _space(workspace, need, dev) if need else workspace
 
 
 def _grad_out(logits, out, dev):
@@ -503,8 +505,9 @@ def distill_loss(logits: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor,
     p, dev, T, _ = _distill(logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index, workspace=workspace)
     loss = torch.empty(T, dtype=torch.float32, device=dev)
     stats = torch.empty((T, DISTILL_STATS), dtype=torch.float64, device=dev)
-    ws, n = _distill_ws(p, dev, workspace)
-    _call(dev, "i8mp_distill_fwd", p, loss.data_ptr(), stats.data_ptr(), ws, n)
+    ws = _distill_ws(p, dev, workspace)
+    _call(dev, "i8mp_distill_fwd", p, loss.data_ptr(), stats.data_ptr(), None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
     return loss, stats
 
 
@@ -536,6 +539,7 @@ def distill_loss_and_grad(logits: torch.Tensor, teacher: torch.Tensor, idx: torc
                             workspace, backward=True)
     d = _grad_out(logits, out, dev)
     loss = torch.empty(T, dtype=torch.float32, device=dev)
-    ws, n = _distill_ws(p, dev, workspace)
-    _call(dev, "i8mp_distill_step", p, grad.data_ptr(), grad.stride(0), loss.data_ptr(), d.data_ptr(), _ld2(d), ws, n)
+    ws = _distill_ws(p, dev, workspace)
+    _call(dev, "i8mp_distill_step", p, grad.data_ptr(), grad.stride(0), loss.data_ptr(), d.data_ptr(), _ld2(d),
+          None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return loss, d

@@ -489,7 +489,8 @@ i8mp_status i8mp_linear_act_bwd(const i8mp_linear_act_grad* p, const i8mp_linear
  * or none of the V classes, no second.  The gradient of sum_r grad[r] loss[r] is
  * written in the logits' type, rounded once from fp32.
  * Logits of -inf are classes the student cannot choose; their gradient is that
- * of a probability of zero.  A row holding +inf or NaN gives NaN.
+ * of a probability of zero (also where all the rest are -inf and p_rest is not 0,
+ * which makes the loss +inf).  A row holding +inf or NaN gives NaN.
  *   logits, dlogits: bf16, fp16 or fp32 (dtype), rows of any alignment; only
  *     whole 16-byte chunks that hold part of a row are read, and dlogits is
  *     written inside its rows

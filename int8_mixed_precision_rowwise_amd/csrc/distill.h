@@ -22,6 +22,14 @@
 // elements they are) and are evaluated one per thread in 64 bits, which keeps
 // q_rest and mass q_j - p_j free of cancellation.
 //
+// The other entries' sums are relative to the maximum of those entries, mo, and only
+// joined in 64 bits with the kept ones, which are relative to the row's maximum m:
+// where the kept logits stand 88 tau and more above the rest, fp32 sums relative to m
+// would be 0 and p_rest / q_rest infinite.  With e' = exp((x - mo) / tau), S' their
+// sum and S = S' exp((mo - m) / tau) + the kept entries' sum, the gradient outside is
+//   g tau e'_i [mass exp((mo - m) / tau) / S - p_rest / S'],
+// every factor of which is in range.  Rest entries that are all -inf have e' = 0.
+//
 // Measured: loss and gradient of 4096 x 128256 bf16 logits, temperature 2 with hard
 // labels, 513 - 552 us for 2.1 GB, 3.8 - 4.1 TB/s where a copy of that size reaches 5.1.  Two
 // exponentials an element at a quarter of the vector rate and some 13 other operations
@@ -37,12 +45,12 @@
 // backward of an earlier forward) is the second of them with the sums given.
 //
 // Exponentials are 2^(c x - R), one fused operation, with c = log2(e) / tau and R =
-// c m (m the row's maximum) both rounded to fp32.  The same c and R stand in the
-// 64-bit part: the rounding of c only scales the temperature by 2^-24, and that of R
-// all of a row's exponentials by one factor, which cancels.  Beyond |R| = 2^22 (a
-// row masked with the type's lowest value) that factor would be far from 1: such a
-// row is summed and swept once more from memory as 2^(c (x - m)).  fp32 logits take
-// x - m first and carry the product's low part.
+// c mo (c m for the kept entries) rounded to fp32.  The same c and R stand in the
+// 64-bit part: the rounding of c only scales the temperature by 2^-24, and that of
+// each R cancels, as the two are joined by their exact difference.  Beyond |R| = 2^22 (a
+// row masked with the type's lowest value) the rounding of R is no longer small
+// against its terms: such a row is summed and swept once more from memory as
+// 2^(c (x - mo)).  fp32 logits take x - mo first and carry the product's low part.
 #pragma once
 
 #include "internal.h"
@@ -61,12 +69,13 @@ constexpr double kLog2e = 1.4426950408889634074, kLn2 = 0.69314718055994530942;
 // What a row's gradient needs besides its logits and kept entries.
 struct RowStats {
   double ref;      // the maximum m of the logits (0 if all are -inf)
-  double total;    // sum of the exponentials (2^(c x - R), see Expo)
-  double total1;   // the same at temperature 1
-  double outside;  // mass - p_rest / q_rest
-  double mass;
+  double ref_out;  // the maximum mo of those not kept (0 if all are -inf)
+  double kept;     // mass / S, S the sum of the exponentials (2^(c x - R), see Expo) relative to m
+  double kept1;    // 1 / S at temperature 1
+  double outside;  // mass exp((mo - m) / tau) / S - p_rest / (sum outside, relative to mo)
+  double outside1; // exp(mo - m) / S at temperature 1
   double z;        // p_j = exp(t_j / tau - z)
-  double spare[2];
+  double spare;
 };
 static_assert(sizeof(RowStats) == 8 * I8MP_DISTILL_STATS, "one row of the caller's statistics");
 
@@ -84,6 +93,8 @@ __device__ __forceinline__ void lds_sync() {
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
 
 // The row's element type: 16-byte chunks of E elements.
 template <typename T>
@@ -189,15 +200,19 @@ __device__ __forceinline__ v4i all_neg_inf(int elem_bytes, uint32_t inf) {
   return (v4i){w, w, w, w};
 }
 
-// Exponentials of a row relative to one reference.  MODE 0: one temperature
+// Exponentials of a row: in its sweeps relative to the entries that are not kept,
+// of kept entries in 64 bits relative to the whole row.  MODE 0: one temperature
 // (no hard labels, or tau = 1); 1: tau = 2, exp(x) as the square; 2: two.
 template <typename T, int MODE>
 struct Expo {
   static constexpr bool kPrecise = sizeof(T) == 4;
   static constexpr float kFar = 0x1p22f;
   float c, c_lo, c1, c1_lo;  // log2(e) / tau and log2(e), with their low parts
-  float m, r, r1;            // the reference's maximum, R, and R at temperature 1
-  __device__ __forceinline__ Expo(const DistillArgs& a) : c(a.c), c_lo(a.c_lo), c1(a.c1), c1_lo(a.c1_lo), m(0), r(0), r1(0) {}
+  float m, r, r1;            // the sweep's maximum, R, and R at temperature 1
+  float mk, rk, rk1;         // the same of the row
+  bool rest;                 // the entries not kept are a class
+  __device__ __forceinline__ Expo(const DistillArgs& a)
+      : c(a.c), c_lo(a.c_lo), c1(a.c1), c1_lo(a.c1_lo), m(0), r(0), r1(0), mk(0), rk(0), rk1(0), rest(a.lse != nullptr) {}
   // A maximum so far.  The bound keeps R finite where everything is -inf or close to
   // the type's lowest value: exponentials there are 0.
   __device__ __forceinline__ void at(float max) {
@@ -208,13 +223,22 @@ struct Expo {
       if constexpr (MODE == 2) r1 = fmaxf(c1 * max, -kFar);
     }
   }
-  // A row's maximum.
-  __device__ __forceinline__ void at_row(float max) {
-    at(max);
-    m = max == -__builtin_inff() ? 0.0f : max;
+  // The maxima of a row's entries that are not kept, and of all.
+  __device__ __forceinline__ void at_row(float out, float all) {
+    at(out);
+    m = out == -__builtin_inff() ? 0.0f : out;
+    mk = all == -__builtin_inff() ? 0.0f : all;
+    rk = fmaxf(c * mk, -kFar);
+    if constexpr (MODE == 2) rk1 = fmaxf(c1 * mk, -kFar);
   }
+  // One value for all lanes: scalar registers.
+  __device__ __forceinline__ void uniform_all() {
+    m = uniform(m), r = uniform(r), r1 = uniform(r1), mk = uniform(mk), rk = uniform(rk), rk1 = uniform(rk1);
+  }
+  // Where the entries not kept are no class of their own, a maximum of theirs below the
+  // bound does not matter: next to the row's they are then 0.
   __device__ __forceinline__ bool far() const {
-    return !kPrecise && (__builtin_fabsf(c * m) >= kFar || (MODE == 2 && __builtin_fabsf(c1 * m) >= kFar));
+    return !kPrecise && (__builtin_fabsf(c * mk) >= kFar || (MODE == 2 && __builtin_fabsf(c1 * mk) >= kFar) || (rest && c * m <= -kFar));
   }
   __device__ __forceinline__ static float precise(float y, float c, float c_lo) {
     const float h = y * c;
@@ -236,14 +260,23 @@ struct Expo {
   // the same for a row far out
   __device__ __forceinline__ float far_e(float x) const { return exp2_fast((x - m) * c); }
   __device__ __forceinline__ float far_e1(float x, float e) const { return MODE == 1 ? e * e : exp2_fast((x - m) * c1); }
-  // log2 of the same exponentials in 64 bits
+  // log2 of the same exponentials relative to the whole row, in 64 bits
   __device__ __forceinline__ double log2e(double x, const DistillArgs& a) const {
-    return kPrecise || far() ? (x - (double)m) * a.cd : x * (double)c - (double)r;
+    return kPrecise || far() ? (x - (double)mk) * a.cd : x * (double)c - (double)rk;
   }
   __device__ __forceinline__ double log2e1(double x, const DistillArgs& a) const {
     if constexpr (MODE == 0) return log2e(x, a);
     if constexpr (MODE == 1) return 2 * log2e(x, a);
-    return kPrecise || far() ? (x - (double)m) * kLog2e : x * (double)c1 - (double)r1;
+    return kPrecise || far() ? (x - (double)mk) * kLog2e : x * (double)c1 - (double)rk1;
+  }
+  // log2 of what takes the sweep's exponentials there
+  __device__ __forceinline__ double gap(const DistillArgs& a) const {
+    return kPrecise || far() ? ((double)m - (double)mk) * a.cd : (double)r - (double)rk;
+  }
+  __device__ __forceinline__ double gap1(const DistillArgs& a) const {
+    if constexpr (MODE == 0) return gap(a);
+    if constexpr (MODE == 1) return 2 * gap(a);
+    return kPrecise || far() ? ((double)m - (double)mk) * kLog2e : (double)r1 - (double)rk1;
   }
 };
 
@@ -265,8 +298,11 @@ __device__ __forceinline__ double exp2_d(double y) {
   // -inf (where the polynomial is a NaN) and what underflows give 0; beyond the range: infinity
   return y < -1100 ? 0 : y > 1100 ? (double)__builtin_inff() : __builtin_amdgcn_ldexp(p, (int)n);
 }
-
-__device__ __forceinline__ float uniform(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x))); }
+// 2^y within a few 2^-24 where fp32 holds it, 0 below: for y <= 0 whose power only adds to larger numbers.
+__device__ __forceinline__ double exp2_f(double y) {
+  const float h = (float)y, e = exp2_fast(h);
+  return h < -150.0f ? 0.0 : (double)__builtin_fmaf(e, (float)(y - (double)h) * (float)kLn2, e);
+}
 
 template <typename F>
 __device__ __forceinline__ F wave_sum(F v) {
@@ -278,6 +314,15 @@ __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
   return v;
+}
+
+// Both at once: one after the other they would wait twice.
+__device__ __forceinline__ void wave_max2(float& a, float& b) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    const float x = __shfl_xor(a, off), y = __shfl_xor(b, off);
+    a = fmaxf(a, x), b = fmaxf(b, y);
+  }
 }
 
 __device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t row, int j) {
@@ -333,35 +378,43 @@ __device__ __forceinline__ float teacher_value(const DistillArgs& a, uint32_t bi
 // sums over kept entries: W = sum w_j, A = sum w_j (ln w_j - ln e_j), e and e1;
 // w_j = exp(t_j / tau - zref), kept: how many there are.
 struct Joined {
-  double out, out1;  // sums over the entries not kept
+  double out, out1;  // sums over the entries not kept, relative to their maximum
   double W, A, e, e1;
   double zref;
   int kept;
 };
-__device__ __forceinline__ RowStats join(const DistillArgs& a, const Joined& s, double ref, int mode) {
-  RowStats st;
-  st.ref = ref, st.spare[0] = st.spare[1] = 0;
-  st.total = s.out + s.e;
-  st.total1 = mode == 0 ? st.total : s.out1 + s.e1;
-  if (s.kept == 0) {
-    st.outside = st.mass = 0;
-  } else if (a.lse) {
-    const double p_rest = s.W < 1 ? 1 - s.W : s.W >= 1 ? 0 : s.W;  // a NaN stays one
-    st.mass = s.W + p_rest;
-    st.outside = p_rest == 0 ? st.mass : st.mass - p_rest * st.total / s.out;
-  } else {
-    st.mass = st.outside = 1;
+struct Totals {
+  RowStats st;          // but for z
+  double total, total1; // S, at both temperatures
+  double p_rest;
+};
+template <typename T, int MODE>
+__device__ __forceinline__ Totals join(const DistillArgs& a, const Joined& s, const Expo<T, MODE>& ex) {
+  Totals r;
+  // nothing outside: whatever the factors, they meet exponentials of 0
+  const double g = s.out == 0 ? 0 : exp2_f(ex.gap(a)), g1 = MODE == 0 ? g : s.out == 0 ? 0 : exp2_f(ex.gap1(a));
+  r.total = s.out * g + s.e;
+  r.total1 = MODE == 0 ? r.total : s.out1 * g1 + s.e1;
+  r.p_rest = !a.lse || s.W >= 1 || s.kept == 0 ? 0 : 1 - s.W;  // a NaN stays one
+  const double i = 1 / r.total, i1 = MODE == 0 ? i : 1 / r.total1, rest = r.p_rest == 0 || s.out == 0 ? 0 : r.p_rest / s.out;
+  RowStats& st = r.st;
+  st.ref = (double)ex.mk, st.ref_out = (double)ex.m;
+  st.kept1 = i1, st.outside1 = g1 * i1;
+  st.kept = st.outside = st.z = st.spare = 0;
+  if (s.kept != 0) {
+    st.kept = a.lse ? (s.W + r.p_rest) * i : i;
+    st.outside = st.kept * g - rest;
   }
-  st.z = 0;
-  return st;
+  return r;
 }
 // A row's loss and statistics, by the 64 lanes of one wave: its five logarithms at
 // once, a lane each (one after the other they took 2 us behind every row).
-__device__ __forceinline__ void write_row(const DistillArgs& a, int64_t row, const Joined& s, RowStats st, double label_log2e1,
-                                          bool has_label) {
+// gap: log2 of what takes s.out to the row's reference.
+__device__ __forceinline__ void write_row(const DistillArgs& a, int64_t row, const Joined& s, Totals r, double gap,
+                                          double label_log2e1, bool has_label) {
   const int lane = threadIdx.x & 63;
-  const double p_rest = a.lse ? st.mass - s.W : 0;
-  const double of = lane == 0 ? st.total : lane == 1 ? s.W : lane == 2 ? p_rest : lane == 3 ? s.out : st.total1;
+  const double p_rest = r.p_rest;
+  const double of = lane == 0 ? r.total : lane == 1 ? s.W : lane == 2 ? p_rest : lane == 3 ? s.out : r.total1;
   const double ln = log(of);
   const double ln_total = __shfl(ln, 0), ln_w = __shfl(ln, 1), ln_rest = __shfl(ln, 2), ln_out = __shfl(ln, 3), ln_total1 = __shfl(ln, 4);
   if (lane != 0) return;
@@ -369,7 +422,7 @@ __device__ __forceinline__ void write_row(const DistillArgs& a, int64_t row, con
   if (s.kept > 0) {
     if (a.lse) {
       loss = s.A + s.W * ln_total;
-      if (!(p_rest == 0)) loss += p_rest * (ln_rest - ln_out + ln_total);
+      if (!(p_rest == 0)) loss += p_rest * (ln_rest - (ln_out + gap * kLn2) + ln_total);
     } else {
       loss = s.A / s.W - ln_w + ln_total;
     }
@@ -378,8 +431,8 @@ __device__ __forceinline__ void write_row(const DistillArgs& a, int64_t row, con
   if (has_label) loss += (double)a.ce * (ln_total1 - label_log2e1 * kLn2);
   if (a.loss) a.loss[row] = (float)loss;
   if (a.stats) {
-    st.z = s.kept == 0 ? 0 : a.lse ? s.zref : s.zref + ln_w;  // p_j = exp(t_j / tau - z)
-    static_cast<RowStats*>(a.stats)[row] = st;
+    r.st.z = s.kept == 0 ? 0 : a.lse ? s.zref : s.zref + ln_w;  // p_j = exp(t_j / tau - z)
+    static_cast<RowStats*>(a.stats)[row] = r.st;
   }
 }
 
@@ -393,14 +446,14 @@ struct Factors {
 __device__ __forceinline__ Factors factors(const DistillArgs& a, const RowStats& st, double w_scale, int64_t row, bool has_label,
                                            int mode) {
   const double g = (double)a.grad[row * a.grad_s], gt = g * (double)a.tau;
-  const double label = has_label ? g * (double)a.ce : 0, c1 = has_label ? label / st.total1 : 0;
-  const double out = st.outside == 0 && st.mass == 0 ? 0 : gt * st.outside / st.total;
+  const double label = has_label ? g * (double)a.ce : 0, out = gt * st.outside, out1 = has_label ? label * st.outside1 : 0;
   Factors f;
   f.label = (float)label;
-  f.c1 = f.out1 = (float)c1;
-  f.kept = (float)(st.mass == 0 ? 0 : gt * st.mass / st.total);
+  f.c1 = has_label ? (float)(label * st.kept1) : 0.0f;
+  f.out1 = (float)out1;
+  f.kept = (float)(gt * st.kept);
   f.p = (float)(gt * w_scale);
-  f.out = (float)(mode == 0 ? out + c1 : out);
+  f.out = (float)(mode == 0 ? out + out1 : out);
   return f;
 }
 __device__ __forceinline__ Factors uniform(const Factors& f) {
@@ -567,7 +620,7 @@ template <int NT>
 struct RowLds {
   double sums[NT / 64][6];
   Factors f;
-  float wmax[NT / 64], tmax[NT / 64];
+  float wmax[NT / 64], kmax[NT / 64], tmax[NT / 64];
   int kept[NT / 64];
   int label_kept;  // whether the label is a kept entry
 };
@@ -698,7 +751,8 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
   tmax = l.tmax[0], kept = l.kept[0];
 #pragma unroll
   for (int w = 1; w < W; ++w) tmax = fmaxf(tmax, l.tmax[w]), kept += l.kept[w];
-  const double zref = a.lse ? (double)lse : (double)tmax * a.itau;
+  // scalar registers, and zref only where it is used: the row's sums leave no others
+  tmax = uniform(a.lse ? lse : tmax), kept = __builtin_amdgcn_readfirstlane(kept);
   lds_sync();
 
   Expo<T, MODE> ex(a);
@@ -713,20 +767,22 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
     stats_group<T, MODE, G * g, G>(v, masks, run, ex);
     __builtin_amdgcn_sched_barrier(0);  // mixed, several chunks' values would not fit the registers
   });
-  const float xlab = Elem<T>::value(lab_raw);
+  __builtin_amdgcn_sched_barrier(0);  // nothing of what follows takes registers from the sums
+  const float xlab = uniform(Elem<T>::value(lab_raw));
   float xj[KPT];
-  float m = run.max;
+  float m = run.max, mk = -__builtin_inff();  // of the entries not kept, and of the kept
 #pragma unroll
-  for (int i = 0; i < KPT; ++i) m = fmaxf(m, xj[i] = Elem<T>::value(xraw[i]));
-  m = wave_max(m);
-  if (lane == 0) l.wmax[wave] = m;
+  for (int i = 0; i < KPT; ++i) mk = fmaxf(mk, xj[i] = Elem<T>::value(xraw[i]));
+  wave_max2(m, mk);
+  if (lane == 0) l.wmax[wave] = m, l.kmax[wave] = mk;
   lds_sync();
-  m = l.wmax[0];
+  m = l.wmax[0], mk = l.kmax[0];
 #pragma unroll
-  for (int w = 1; w < W; ++w) m = fmaxf(m, l.wmax[w]);
-  run.rescale(uniform(m), ex);
-  ex.at_row(uniform(m));
-  ex.r = uniform(ex.r), ex.r1 = uniform(ex.r1);
+  for (int w = 1; w < W; ++w) m = fmaxf(m, l.wmax[w]), mk = fmaxf(mk, l.kmax[w]);
+  m = uniform(m);
+  run.rescale(m, ex);
+  ex.at_row(m, uniform(fmaxf(m, mk)));
+  ex.uniform_all();
   float ws = run.sum(), ws1 = run.sum1();
   const auto marked_here = [&](int c) {
     const int i = c / NT;
@@ -734,6 +790,7 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
   };
   if (ex.far()) ws = ws1 = 0, far_sums<T, MODE>(x, ex, t, x.nchunks, NT, marked_here, ws, ws1);
   ws = wave_sum(ws), ws1 = MODE ? wave_sum(ws1) : 0;
+  const double zref = a.lse ? (double)tmax : (double)tmax * a.itau;
   float e0[KPT], e1[KPT], w0[KPT];
   double q[4] = {0, 0, 0, 0};
   if (wave * 64 < k) {  // kept entries in 64 bits
@@ -758,20 +815,20 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
     for (int i = 0; i < 4; ++i) l.sums[wave][2 + i] = q[i];
   }
   lds_sync();
-  Joined s;
+  const auto joined = [&]() -> Joined {
+    return {l.sums[0][0], l.sums[0][1], l.sums[0][2], l.sums[0][3], l.sums[0][4], l.sums[0][5], zref, kept};
+  };
   if (wave == 0) {
-    double b[6];
+    if (lane < 6) {  // a sum a lane
+      double b = l.sums[0][lane];
 #pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      b[i] = lane < W ? l.sums[lane][i] : 0.0;
-#pragma unroll
-      for (int off = 1; off < W; off <<= 1) b[i] += __shfl_xor(b[i], off);
+      for (int w = 1; w < W; ++w) b += l.sums[w][lane];
+      l.sums[0][lane] = b;
     }
-    s = {b[0], b[1], b[2], b[3], b[4], b[5], zref, kept};
-    if (lane == 0) {
-#pragma unroll
-      for (int i = 0; i < 6; ++i) l.sums[0][i] = b[i];
-      if (a.d) l.f = factors(a, join(a, s, (double)ex.m, MODE), kept == 0 ? 0 : a.lse ? 1 : 1 / s.W, row, label >= 0, MODE);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a wave's LDS operations stay in order
+    if (lane == 0 && a.d) {
+      const Joined s = joined();
+      l.f = factors(a, join(a, s, ex).st, kept == 0 ? 0 : a.lse ? 1 : 1 / s.W, row, label >= 0, MODE);
     }
   }
   lds_sync();
@@ -792,13 +849,13 @@ __global__ __launch_bounds__(NT, row_waves(NV)) void distill_rows(DistillArgs a)
     }
   }
   if (wave == W - 1) {  // while the sweep's stores arrive
-    s = {l.sums[0][0], l.sums[0][1], l.sums[0][2], l.sums[0][3], l.sums[0][4], l.sums[0][5], zref, kept};
-    write_row(a, row, s, join(a, s, (double)ex.m, MODE), label >= 0 ? ex.log2e1((double)xlab, a) : 0, label >= 0);
+    const Joined s = joined();
+    write_row(a, row, s, join(a, s, ex), ex.gap(a), label >= 0 ? ex.log2e1((double)xlab, a) : 0, label >= 0);
   }
   if (a.d) {
     T* d = static_cast<T*>(a.d) + row * a.d_ld;
     const Factors f = uniform(l.f);
-    __syncthreads();  // the sweep's stores are complete
+    __syncthreads();  // what follows is stored behind the sweep's stores
 #pragma unroll
     for (int i = 0; i < KPT; ++i)
       if (id[i] >= 0) d[id[i]] = (T)kept_grad(f, e0[i], e1[i], w0[i], id[i] == label);
@@ -814,7 +871,7 @@ constexpr int kSegChunks = 4096;  // at most: a byte of the table each
 struct SegLds {
   uint32_t table[kSegChunks / 4];
   double sums[kSegThreads / 64][6];
-  float wmax[kSegThreads / 64];
+  float wmax[kSegThreads / 64], kmax[kSegThreads / 64];
   int kept[kSegThreads / 64];
   int label_kept;
   Joined joined;  // of thread 0, until it writes the loss
@@ -904,19 +961,23 @@ __device__ __forceinline__ Joined seg_join(SegLds& l, const DistillArgs& a, int6
   const Partial* part = static_cast<const Partial*>(a.partial) + row * a.segs;
   const Partial my_part = part[min(t, a.segs - 1)];
   const float lse = a.lse ? a.lse[row] : 0.0f;
-  float tmax = -__builtin_inff(), m = -__builtin_inff();
+  float tmax = -__builtin_inff(), m = -__builtin_inff(), mk = -__builtin_inff();
   int kept = 0;
   for (int j = t; j < a.k; j += kSegThreads)
-    if (const Kept e = j == t ? mine : fetch_kept<T>(a, row, j); e.id >= 0) tmax = fmaxf(tmax, e.t), m = fmaxf(m, e.x), ++kept;
+    if (const Kept e = j == t ? mine : fetch_kept<T>(a, row, j); e.id >= 0) tmax = fmaxf(tmax, e.t), mk = fmaxf(mk, e.x), ++kept;
   for (int i = t; i < a.segs; i += kSegThreads) m = fmaxf(m, i == t ? my_part.max : part[i].max);
-  tmax = wave_max(tmax), m = wave_max(m), kept = wave_sum(kept);
-  if (lane == 0) l.wmax[wave] = tmax, l.sums[wave][0] = m, l.kept[wave] = kept;
+  wave_max2(m, mk);
+  tmax = wave_max(tmax), kept = wave_sum(kept);
+  if (lane == 0) l.wmax[wave] = tmax, l.kmax[wave] = mk, l.sums[wave][0] = m, l.kept[wave] = kept;
   __syncthreads();
-  tmax = m = -__builtin_inff(), kept = 0;
+  tmax = m = mk = -__builtin_inff(), kept = 0;
 #pragma unroll
-  for (int w = 0; w < W; ++w) tmax = fmaxf(tmax, l.wmax[w]), m = fmaxf(m, (float)l.sums[w][0]), kept += l.kept[w];
+  for (int w = 0; w < W; ++w)
+    tmax = fmaxf(tmax, l.wmax[w]), m = fmaxf(m, (float)l.sums[w][0]), mk = fmaxf(mk, l.kmax[w]), kept += l.kept[w];
   __syncthreads();
-  ex.at_row(m);
+  tmax = uniform(tmax), m = uniform(m), kept = __builtin_amdgcn_readfirstlane(kept);
+  ex.at_row(m, uniform(fmaxf(m, mk)));
+  ex.uniform_all();
   double q[6] = {0, 0, 0, 0, 0, 0};
   if (ex.far()) {
     const Row<T> r(a.logits, row, a.ld, (int)a.V);
@@ -980,7 +1041,7 @@ __global__ __launch_bounds__(kSegThreads) void distill_finish(DistillArgs a) {
   if (threadIdx.x >= 64) return;
   const int label = label_at(a, row);
   const T* x = static_cast<const T*>(a.logits) + row * a.ld;
-  write_row(a, row, s, join(a, s, (double)ex.m, MODE), label >= 0 ? ex.log2e1((double)(float)x[label], a) : 0, label >= 0);
+  write_row(a, row, s, join(a, s, ex), ex.gap(a), label >= 0 ? ex.log2e1((double)(float)x[label], a) : 0, label >= 0);
 }
 
 // GIVEN: the row's statistics come from an earlier forward.
@@ -1007,11 +1068,11 @@ __global__ __launch_bounds__(kSegThreads, 4) void distill_grad(DistillArgs a) {
   double w_ref, w_scale;  // p_j = w_scale exp(t_j / tau - w_ref)
   if constexpr (GIVEN) {
     st = static_cast<const RowStats*>(a.stats)[row];
-    ex.at_row((float)st.ref);
+    ex.at_row((float)st.ref_out, (float)st.ref);
     w_ref = st.z, w_scale = 1;
   } else {
     const Joined s = seg_join<T, MODE>(l, a, row, mine, ex);
-    st = join(a, s, (double)ex.m, MODE);
+    st = join(a, s, ex).st;
     if (t == 0) l.joined = s;
     w_ref = s.zref, w_scale = s.kept == 0 ? 0 : a.lse ? 1 : 1 / s.W;
   }
@@ -1035,7 +1096,7 @@ __global__ __launch_bounds__(kSegThreads, 4) void distill_grad(DistillArgs a) {
   __syncthreads();
   if constexpr (!GIVEN) {
     if (t >= kSegThreads - 64 && seg == 0)
-      write_row(a, row, l.joined, join(a, l.joined, (double)ex.m, MODE), label >= 0 ? ex.log2e1((double)(float)xr[label], a) : 0, label >= 0);
+      write_row(a, row, l.joined, join(a, l.joined, ex), ex.gap(a), label >= 0 ? ex.log2e1((double)(float)xr[label], a) : 0, label >= 0);
   }
   for (int j = t; j < a.k; j += kSegThreads) {
     const Kept k = j == t ? mine : fetch_kept<T>(a, row, j);

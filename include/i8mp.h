@@ -433,7 +433,8 @@ typedef struct {
 } i8mp_linear_act;
 /* Bytes of workspace of the forward (backward = 0) or the backward (1). */
 size_t i8mp_linear_act_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t backward);
-/* colmax_x, colmax_w: as in i8mp_linear_fwd_colmax (either may be NULL). */
+/* colmax_x, colmax_w: as in i8mp_linear_fwd_colmax (either may be NULL); written for
+ * empty M or N too, 0 for an operand without rows. */
 i8mp_status i8mp_linear_act_fwd(const i8mp_linear_act* p, const i8mp_linear_opts* opts, float* colmax_x,
                                 float* colmax_w, void* ws, size_t ws_bytes, void* stream);
 

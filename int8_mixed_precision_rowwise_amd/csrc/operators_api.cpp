@@ -338,7 +338,9 @@ i8mp_status i8mp_linear_act_fwd(const i8mp_linear_act* p, const i8mp_linear_opts
     for (int j = 0; j < i; ++j)
       if (overlap(out[i], out[j])) return I8MP_EINVAL;
   }
-  if (M == 0 || N == 0) return I8MP_OK;
+  // without outputs there are still the column maxima: the other operand's, and 0 of the one without rows
+  const bool empty = M == 0 || N == 0;
+  if (empty && (K == 0 || (!colmax_x && !colmax_w))) return I8MP_OK;
   const size_t need = carve_act_fwd(nullptr, M, N, K, true, nullptr);
   if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return I8MP_EWORKSPACE;
   const Range rw = vec_range(ws, (int64_t)need, 1);
@@ -371,7 +373,9 @@ i8mp_status i8mp_linear_act_fwd(const i8mp_linear_act* p, const i8mp_linear_opts
               ? i8mp::launch_quantize_rowwise_colmax(p->W, N, K, p->ldw, w.qw, kp, w.sw, colmax_w, r, opts->seed, ow, w.part_w, s)
               : i8mp::launch_quantize_rowwise(p->W, N, K, p->ldw, w.qw, kp, w.sw, r, opts->seed, ow, s);
   }
-  if (e == hipSuccess) e = act_product(p, w.qx, w.sx, w.qw, kp, w.sw, w.split, side.n ? &side : nullptr, s);
+  if (e == hipSuccess)
+    e = empty ? i8mp::launch_colmax_finalize(side, s)
+              : act_product(p, w.qx, w.sx, w.qw, kp, w.sw, w.split, side.n ? &side : nullptr, s);
   return hip_status(e);
 }
 

@@ -1,0 +1,44 @@
+"""Edges of the linears with an epilogue on the GPU."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+i8 = pytest.importorskip("int8_mixed_precision_rowwise_amd")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+bf = torch.bfloat16
+
+
+def randn(seed, *shape):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(bf)
+
+
+def leave_nan_behind(*sizes):
+    """Blocks full of NaN in the allocator's cache, for the calls' own tensors to be cut from."""
+    held = [torch.full((n,), float("nan"), device="cuda") for n in sizes for _ in range(4)]
+    del held
+
+
+@pytest.mark.parametrize("K", [16, 264, 20000])
+@pytest.mark.parametrize("M,N", [(0, 24), (24, 0), (0, 0)])
+def test_empty_operands_have_column_maxima(M, N, K):
+    X, W, bias = randn(1, M, K), randn(2, N, K), randn(3, N)
+    for rounding in ("rne", "sr"):
+        leave_nan_behind(K, K, 4096, 1 << 16)
+        Y, Z, cx, cw = i8.linear_act_fwd_train(X, W, bias=bias, activation="gelu", rounding=rounding)
+        assert torch.equal(cx, X.abs().amax(0).float() if M else torch.zeros(K, device="cuda"))
+        assert torch.equal(cw, W.abs().amax(0).float() if N else torch.zeros(K, device="cuda"))
+        dX, dW, db = i8.linear_act_bwd(Y, Z, X, W, "gelu", want_dbias=True, colmax_x=cx, colmax_w=cw, rounding=rounding)
+        assert torch.equal(dX, torch.zeros_like(X)) and torch.equal(dW, torch.zeros_like(W)) and torch.equal(db, torch.zeros(N, device="cuda"))
+
+
+def test_empty_batch_through_autograd():
+    from int8_mixed_precision_rowwise_amd import training
+    w, b = randn(2, 24, 40).requires_grad_(), randn(3, 24).requires_grad_()
+    x = randn(1, 0, 40).requires_grad_()
+    leave_nan_behind(40, 4096, 1 << 16)
+    training.linear_act(x, w, b, "silu").sum().backward()
+    assert torch.equal(w.grad, torch.zeros_like(w)) and torch.equal(b.grad, torch.zeros_like(b)) and x.grad.shape == (0, 40)

@@ -262,9 +262,27 @@ hipError_t launch_gemm_epilogue(int64_t M, int64_t N, int64_t K, const int8_t* A
   ActEpilogue epi;
   static_cast<Epilogue&>(epi) = e;
   const SplitPlan p = plan_split<true, true>(M, N, K, lda, ldb);
-  if (p.splits < 2 || !ws)
-    return big_tiles(M, N) >= kBigTileMin ? run_tiles<256>(M, N, K, A, lda, sa, B, ldb, sb, C, ldc, side, epi, stream)
-                                          : run_tiles<128>(M, N, K, A, lda, sa, B, ldb, sb, C, ldc, side, epi, stream);
+  if (p.splits < 2 || !ws) {
+    if (big_tiles(M, N) >= kBigTileMin && pipelined_ok<256, 256, true, true>(M, N, K, lda, ldb))
+      return run_tiles<256>(M, N, K, A, lda, sa, B, ldb, sb, C, ldc, side, epi, stream);
+    if (pipelined_ok<128, 128, true, true>(M, N, K, lda, ldb))
+      return run_tiles<128>(M, N, K, A, lda, sa, B, ldb, sb, C, ldc, side, epi, stream);
+    // rows too far apart for 32-bit offsets in a tile (a view of 16 MiB and more between
+    // weight rows): the few-token kernel, whose addresses are whole, with the same bits
+    if (side) {
+      const hipError_t err = launch_colmax_finalize(*side, stream);
+      if (err != hipSuccess) return err;
+    }
+    for (int64_t m = 0; m < M; m += kSkinnyRows) {
+      Epilogue part = e;
+      if (e.residual) part.residual = e.residual + m * e.ld_residual;
+      if (e.z) part.z = e.z + m * e.ld_z;
+      const hipError_t err = launch_skinny(std::min(M - m, kSkinnyRows), N, K, A + m * lda, lda, sa + m, B, ldb, sb, C + m * ldc, ldc,
+                                           part, stream);
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  }
   const hipError_t err = launch_gemm_partials(M, N, K, A, lda, B, ldb, ws, side, stream);
   if (err != hipSuccess) return err;
   const dim3 grid((unsigned)((N + 1023) / 1024), (unsigned)std::min<int64_t>(M, 65535));

@@ -42,3 +42,18 @@ def test_empty_batch_through_autograd():
     leave_nan_behind(40, 4096, 1 << 16)
     training.linear_act(x, w, b, "silu").sum().backward()
     assert torch.equal(w.grad, torch.zeros_like(w)) and torch.equal(b.grad, torch.zeros_like(b)) and x.grad.shape == (0, 40)
+
+
+@pytest.mark.parametrize("M,N,K,pitch", [(16500, 260, 64, 1 << 24), (16500, 260, 64, 1 << 23), (100, 130, 40, (1 << 25) + 16), (200, 7, 520, 1 << 28)])
+def test_weight_rows_far_apart(M, N, K, pitch):
+    """Views whose rows lie further apart than a tile's 32-bit offsets reach: the bits of dense weights."""
+    X, W, bias, R = randn(1, M, K), randn(2, N, K), randn(3, N), randn(4, M, (N + 7) // 8 * 8)[:, :N]
+    Wq, ws = i8.quantize_rowwise(W)
+    store = torch.empty(N * pitch, dtype=torch.int8, device="cuda")
+    far = store.view(N, pitch)[:, :K]
+    far.copy_(Wq)
+    kw = dict(bias=bias, activation="silu", residual=R)
+    want = i8.linear_wq_fwd(X, Wq, ws, **kw)
+    out = torch.full((M, N + 1), 7.0, dtype=bf, device="cuda")
+    got = i8.linear_wq_fwd(X, far, ws, out=out[:, :N], **kw)
+    assert torch.equal(got, want) and bool((out[:, N] == 7).all())

@@ -404,13 +404,30 @@ class Int8MixedPrecisionActLinear(Int8MixedPrecisionLinear):
     def __init__(self, in_features: int, out_features: int, bias: bool = True, activation: str = "none",
                  config: Optional[Int8MixedPrecisionConfig] = None, seed: int = 0, device=None, dtype=torch.bfloat16):
         super().__init__(in_features, out_features, config, seed, device, dtype)
-        c = self.config
-        if c.fp8 or not (c.output and c.grad_input and c.grad_weight):
-            raise ValueError("linear layers with an epilogue run all three GEMMs in INT8")
-        _ops._activation(activation)
+        self._check(self.config, activation)
         self.activation = activation
         if bias:
             self.bias = torch.nn.Parameter(torch.zeros(out_features, device=device, dtype=dtype))
+
+    @staticmethod
+    def _check(c: Int8MixedPrecisionConfig, activation: str) -> None:
+        if c.fp8 or not (c.output and c.grad_input and c.grad_weight):
+            raise ValueError("linear layers with an epilogue run all three GEMMs in INT8")
+        _ops._activation(activation)
+
+    @classmethod
+    def from_linear(cls, lin: torch.nn.Linear, config: Int8MixedPrecisionConfig, seed: int,
+                    activation: str = "none") -> "Int8MixedPrecisionActLinear":
+        """Wrap an existing linear, with or without a bias, keeping its Parameters (the
+        same objects)."""
+        cls._check(config, activation)
+        new = cls.__new__(cls)
+        torch.nn.Module.__init__(new)
+        new.in_features, new.out_features = lin.in_features, lin.out_features
+        new.weight = lin.weight
+        new.register_parameter("bias", lin.bias)
+        new.config, new.seed, new.step, new.activation = config, seed, 0, activation
+        return new
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
         key, offset = self._key_offset()

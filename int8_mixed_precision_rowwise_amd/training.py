@@ -361,21 +361,27 @@ def _aligned_rows(t: torch.Tensor, cols: int) -> torch.Tensor:
 class LinearActFunction(torch.autograd.Function):
     """y = act(x @ weight.T + bias) + residual with all three GEMMs in INT8
     (operators.linear_act_fwd_train / linear_act_bwd).  Saved for backward: input,
-    weight, the pre-activation and the column maxima of the first two."""
+    weight, the pre-activation and the column maxima of the first two; nothing where
+    only the residual takes a gradient."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, activation, residual, rounding, seed, offset):
         N, K = weight.shape
         x2, w = _aligned_rows(x, K), _aligned_rows(weight, K)
         r2 = None if residual is None else _aligned_rows(residual, N)
-        y, z, cx, cw = _ops.linear_act_fwd_train(x2, w, bias, activation, r2, rounding, seed, offset)
-        ctx.save_for_backward(x2, w, z, cx, cw)
+        if any(ctx.needs_input_grad[:3]):
+            y, z, cx, cw = _ops.linear_act_fwd_train(x2, w, bias, activation, r2, rounding, seed, offset)
+            ctx.save_for_backward(x2, w, z, cx, cw)
+        else:
+            y = _ops.linear_act_fwd(x2, w, bias, activation, r2, rounding, seed, offset)
         ctx.args = activation, rounding, seed, offset
         ctx.shape, ctx.bias_dtype = x.shape, None if bias is None else bias.dtype
         return y.reshape(*x.shape[:-1], N)
 
     @staticmethod
     def backward(ctx, dy):
+        if not any(ctx.needs_input_grad[:3]):
+            return None, None, None, None, dy, None, None, None
         x2, w, z, cx, cw = ctx.saved_tensors
         activation, rounding, seed, offset = ctx.args
         dx, dw, db = _ops.linear_act_bwd(_aligned_rows(dy, w.shape[0]), z, x2, w, activation, rounding, seed, offset,
@@ -392,6 +398,12 @@ def linear_act(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
         raise ValueError(f"shapes {tuple(x.shape)} and {tuple(weight.shape)} do not match")
     if residual is not None and residual.shape != (*x.shape[:-1], weight.shape[0]):
         raise ValueError(f"residual: shape {(*x.shape[:-1], weight.shape[0])} expected, got {tuple(residual.shape)}")
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias, residual))):
+        # no backward to come: neither the pre-activation nor the column maxima are formed
+        N, K = weight.shape
+        y = _ops.linear_act_fwd(_aligned_rows(x, K), _aligned_rows(weight, K), bias, activation,
+                                None if residual is None else _aligned_rows(residual, N), rounding, seed, offset)
+        return y.reshape(*x.shape[:-1], N)
     return LinearActFunction.apply(x, weight, bias, activation, residual, rounding, seed, offset)
 
 

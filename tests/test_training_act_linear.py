@@ -32,3 +32,45 @@ def test_from_linear_refuses_what_the_constructor_refuses():
             T.Int8MixedPrecisionActLinear.from_linear(lin, T.Int8MixedPrecisionConfig(**bad), 0)
     with pytest.raises(ValueError, match="activation must be one of"):
         T.Int8MixedPrecisionActLinear.from_linear(lin, T.Int8MixedPrecisionConfig(), 0, activation="tanh")
+
+
+@pytest.fixture
+def forwards(monkeypatch):
+    """Names of the forwards called, with stand-ins that compute nothing but the shapes."""
+    seen = []
+
+    def plain(x, w, bias, activation, residual, rounding, seed, offset):
+        seen.append("plain")
+        return torch.zeros(x.shape[0], w.shape[0], dtype=bf)
+
+    def train(x, w, *rest):
+        seen.append("train")
+        y = torch.zeros(x.shape[0], w.shape[0], dtype=bf)
+        return y, torch.zeros_like(y), torch.zeros(x.shape[1]), torch.zeros(x.shape[1])
+
+    monkeypatch.setattr(T._ops, "linear_act_fwd", plain)
+    monkeypatch.setattr(T._ops, "linear_act_fwd_train", train)
+    return seen
+
+
+def test_the_pre_activation_is_kept_for_a_backward_only(forwards):
+    x, w, b, r = torch.zeros(2, 3, 8, dtype=bf), torch.zeros(16, 8, dtype=bf), torch.zeros(16, dtype=bf), torch.zeros(2, 3, 16, dtype=bf)
+    assert T.linear_act(x, w, b, "silu", r).shape == (2, 3, 16) and forwards == ["plain"]
+    m = T.Int8MixedPrecisionActLinear(8, 16, activation="silu")
+    with torch.no_grad():
+        assert m(x, r).shape == (2, 3, 16)
+    with torch.inference_mode():
+        m(x)
+    assert forwards == ["plain"] * 3
+    y = m(x)
+    assert y.requires_grad and forwards[3:] == ["train"]
+    for leaf in ("x", "w", "b"):
+        a = dict(x=x, w=w, b=b)
+        a[leaf] = a[leaf].clone().requires_grad_()
+        T.linear_act(a["x"], a["w"], a["b"], "silu", r)
+    assert forwards[4:] == ["train"] * 3
+    res = r.clone().requires_grad_()  # the residual's gradient is the output's own
+    out = T.linear_act(x, w, b, "silu", res)
+    assert forwards[7:] == ["plain"]
+    g = torch.ones(2, 3, 16, dtype=bf)
+    assert torch.equal(torch.autograd.grad(out, res, g)[0], g)

@@ -296,25 +296,26 @@ def swap_linear_modules(model: torch.nn.Module, config: Optional[Int8MixedPrecis
 
 class RotaryFunction(torch.autograd.Function):
     """Positions turned into q and k (operators.rotary); the backward turns the
-    gradients back."""
+    gradients back by the same function, so it has a gradient of its own."""
 
     @staticmethod
-    def forward(ctx, q, k, positions, freqs, pairs):
+    def forward(ctx, q, k, positions, freqs, pairs, inverse=False):
         ctx.save_for_backward(positions, freqs)
-        ctx.pairs = pairs
+        ctx.pairs, ctx.inverse = pairs, inverse
         ctx.set_materialize_grads(False)
-        return _ops.rotary(q, k, positions, freqs, pairs)
+        return _ops.rotary(q, k, positions, freqs, pairs, inverse)
 
     @staticmethod
     def backward(ctx, dq, dk):
         positions, freqs = ctx.saved_tensors
         d = [None if g is None else g if g.dim() == 4 and (g.shape[3] <= 1 or g.stride(3) == 1) else g.contiguous()
              for g in (dq, dk)]
+        back = (positions, freqs, ctx.pairs, not ctx.inverse)
         if d[0] is None:
-            d = [None, None if d[1] is None else _ops.rotary(d[1], None, positions, freqs, ctx.pairs, inverse=True)[0]]
+            d = [None, None if d[1] is None else RotaryFunction.apply(d[1], None, *back)[0]]
         else:
-            d = _ops.rotary(d[0], d[1], positions, freqs, ctx.pairs, inverse=True)
-        return d[0], d[1], None, None, None
+            d = RotaryFunction.apply(d[0], d[1], *back)
+        return d[0], d[1], None, None, None, None
 
 
 def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, freqs: torch.Tensor,
@@ -323,9 +324,31 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, 
     return RotaryFunction.apply(q, k, positions, freqs, pairs)
 
 
+class _Once(torch.autograd.Function):
+    """A gradient without a gradient of its own."""
+
+    @staticmethod
+    def forward(ctx, what, d):
+        ctx.what = what
+        return d.view_as(d)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError(f"{ctx.what} has no second derivative")
+
+
+def _once(what: str, d: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """d, which raises if it is differentiated (in a backward with create_graph, where
+    it would otherwise be taken for a constant)."""
+    if d is None or not torch.is_grad_enabled():
+        return d
+    return _Once.apply(what, d.detach().requires_grad_())
+
+
 class DistillFunction(torch.autograd.Function):
     """Rows' losses against a teacher's kept logits (operators.distill_loss);
-    the backward reads the logits again with the forward's statistics."""
+    the backward reads the logits again with the forward's statistics.  There is no
+    second derivative: asking for one raises."""
 
     @staticmethod
     def forward(ctx, logits, teacher, idx, temperature, teacher_lse, labels, ce_weight, ignore_index):
@@ -339,7 +362,7 @@ class DistillFunction(torch.autograd.Function):
         logits, teacher, idx, lse, labels, stats = ctx.saved_tensors
         temperature, ce, ignore = ctx.args
         d = _ops.distill_loss_bwd(logits, teacher, idx, stats, grad, temperature, lse, labels, ce, ignore)
-        return d, None, None, None, None, None, None, None
+        return _once("distill_loss", d), None, None, None, None, None, None, None
 
 
 def distill_loss(logits: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor, temperature: float = 1.0,
@@ -362,7 +385,8 @@ class LinearActFunction(torch.autograd.Function):
     """y = act(x @ weight.T + bias) + residual with all three GEMMs in INT8
     (operators.linear_act_fwd_train / linear_act_bwd).  Saved for backward: input,
     weight, the pre-activation and the column maxima of the first two; nothing where
-    only the residual takes a gradient."""
+    only the residual takes a gradient.  There is no second derivative: asking for one
+    raises."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, activation, residual, rounding, seed, offset):
@@ -387,7 +411,8 @@ class LinearActFunction(torch.autograd.Function):
         dx, dw, db = _ops.linear_act_bwd(_aligned_rows(dy, w.shape[0]), z, x2, w, activation, rounding, seed, offset,
                                          want_dx=ctx.needs_input_grad[0], want_dw=ctx.needs_input_grad[1],
                                          want_dbias=ctx.needs_input_grad[2], colmax_x=cx, colmax_w=cw)
-        return (None if dx is None else dx.view(ctx.shape), dw, None if db is None else db.to(ctx.bias_dtype), None,
+        dx, dw = _once("linear_act", None if dx is None else dx.view(ctx.shape)), _once("linear_act", dw)
+        return (dx, dw, _once("linear_act", None if db is None else db.to(ctx.bias_dtype)), None,
                 dy if ctx.needs_input_grad[4] else None, None, None, None)
 
 

@@ -74,3 +74,37 @@ def test_the_pre_activation_is_kept_for_a_backward_only(forwards):
     assert forwards[7:] == ["plain"]
     g = torch.ones(2, 3, 16, dtype=bf)
     assert torch.equal(torch.autograd.grad(out, res, g)[0], g)
+
+
+def test_second_derivatives_are_right_or_refused(monkeypatch):
+    """Rotary's is the rotation itself; the others have none and say so."""
+    def turned(q, k, positions, freqs, pairs="half", inverse=False):  # a quarter turn of both halves, on the CPU
+        a, b = q.chunk(2, -1)
+        return (torch.cat((b, -a), -1) if inverse else torch.cat((-b, a), -1)), k
+
+    monkeypatch.setattr(T._ops, "rotary", turned)
+    q = torch.randn(1, 2, 3, 8, dtype=torch.float64, requires_grad=True)
+    g = torch.randn(1, 2, 3, 8, dtype=torch.float64, requires_grad=True)
+    out, _ = T.rotary(q, None, None, None)
+    (dq,) = torch.autograd.grad(out, q, g, create_graph=True)
+    v = torch.randn_like(q)
+    (dg,) = torch.autograd.grad(dq, g, v)
+    assert torch.equal(dq, turned(g, None, None, None, inverse=True)[0]) and torch.equal(dg, turned(v, None, None, None)[0])
+
+    y = torch.zeros(4, 16)
+    monkeypatch.setattr(T._ops, "distill_loss", lambda x, *a: (x.sum(1), torch.zeros(4, 8, dtype=torch.float64)))
+    monkeypatch.setattr(T._ops, "distill_loss_bwd", lambda x, *a: x * 2)
+    x = torch.randn(4, 16, requires_grad=True)
+    (d,) = torch.autograd.grad(T.distill_loss(x, y, y).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="no second derivative"):
+        (d.sum() + x.square().sum()).backward()
+
+    monkeypatch.setattr(T._ops, "linear_act_fwd_train", lambda x, w, *a: (x @ w.t(), x @ w.t(), x[0].float(), x[0].float()))
+    monkeypatch.setattr(T._ops, "linear_act_bwd", lambda dy, z, x, w, *a, **k: (dy @ w, dy.t() @ x, None))
+    x, w = torch.randn(4, 8, dtype=bf, requires_grad=True), torch.randn(16, 8, dtype=bf, requires_grad=True)
+    d = torch.autograd.grad(T.linear_act(x, w).square().sum(), (x, w), create_graph=True)
+    for part in d:
+        with pytest.raises(RuntimeError, match="no second derivative"):
+            (part.sum() + x.square().sum()).backward(retain_graph=True)
+    T.linear_act(x, w).square().sum().backward()  # the first is as it was
+    assert x.grad.grad_fn is None and torch.equal(w.grad, d[1].detach())

@@ -96,21 +96,28 @@ bool heads_distinct(const HeadsView& v, int64_t B, int64_t S, int64_t D) {
   return true;
 }
 
-// Whether two views share no element: disjoint byte ranges, or the same batch
-// and token strides with the two views' heads in separate parts of a token.
+// Whether two views share no element: disjoint byte ranges, or views with the same
+// batch and token strides (of dimensions of one, any) whose heads lie in separate
+// parts of a token, or are rows of one larger view that shares none.
 bool heads_disjoint(const HeadsView& a, const HeadsView& c, int64_t B, int64_t S, int64_t D, int64_t elem) {
   if (!overlap(heads_range(a, B, S, D, elem), heads_range(c, B, S, D, elem))) return true;
-  if (a.s != c.s || a.b != c.b) return false;
+  if ((S > 1 && a.s != c.s) || (B > 1 && a.b != c.b)) return false;
+  const HeadsView& lo = a.p <= c.p ? a : c;
+  const HeadsView& hi = a.p <= c.p ? c : a;
+  if ((hi.p - lo.p) % (uintptr_t)elem) return false;
+  const int64_t off = (int64_t)((hi.p - lo.p) / (uintptr_t)elem);
+  // heads lo.H, lo.H + 1, ... of the larger view, `first` of them before hi's (heads before tokens in memory)
+  const int64_t h = lo.H > 1 ? lo.h : hi.H > 1 ? hi.h : off;
+  if (h > 0 && off % h == 0 && (hi.H == 1 || hi.h == h)) {
+    const int64_t first = off / h;
+    if (first >= lo.H && heads_distinct({lo.p, lo.b, lo.s, h, first + hi.H}, B, S, D)) return true;
+  }
   int64_t period = S > 1 ? a.s : a.b;  // from one token to the next
   if (S > 1 && B > 1) {
     const bool s_inner = a.s <= a.b;
     period = s_inner ? a.s : a.b;
     if (s_inner ? a.b < S * a.s : a.s < B * a.b) return false;
   }
-  const HeadsView& lo = a.p <= c.p ? a : c;
-  const HeadsView& hi = a.p <= c.p ? c : a;
-  if ((hi.p - lo.p) % (uintptr_t)elem) return false;
-  const int64_t off = (int64_t)((hi.p - lo.p) / (uintptr_t)elem);
   const int64_t lo_ext = (lo.H - 1) * lo.h + D, hi_ext = (hi.H - 1) * hi.h + D;
   return off >= lo_ext && (B * S == 1 || off + hi_ext <= period);
 }

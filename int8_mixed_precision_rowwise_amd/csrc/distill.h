@@ -1145,11 +1145,38 @@ hipError_t launch_mode(const DistillArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Rows [row, row + rows) of a call.
+template <typename T>
+DistillArgs rows_of(DistillArgs a, int64_t row, int64_t rows) {
+  const auto at = [&](const void* p, int64_t per_row, int64_t elem) {
+    return p ? static_cast<const char*>(p) + row * per_row * elem : nullptr;
+  };
+  const int64_t index = a.idx64 ? 8 : 4, label = a.lab64 ? 8 : 4;
+  a.logits = at(a.logits, a.ld, sizeof(T));
+  a.teacher = at(a.teacher, a.t_ld, a.t_dtype == I8MP_FP32 ? 4 : 2), a.idx = at(a.idx, a.i_ld, index);
+  a.labels = at(a.labels, 1, label);
+  if (a.lse) a.lse += row;
+  if (a.grad) a.grad += row * a.grad_s;
+  if (a.loss) a.loss += row;
+  a.stats = const_cast<char*>(at(a.stats, 1, sizeof(RowStats)));
+  a.d = const_cast<char*>(at(a.d, a.d_ld, sizeof(T)));
+  a.partial = const_cast<char*>(at(a.partial, a.segs, sizeof(Partial)));
+  a.T = rows;
+  return a;
+}
+
 template <typename T>
 hipError_t launch_typed(const DistillArgs& a, hipStream_t stream) {
-  if (!a.labels || a.tau == 1.0f) return launch_mode<T, 0>(a, stream);
-  if (a.tau == 2.0f) return launch_mode<T, 1>(a, stream);
-  return launch_mode<T, 2>(a, stream);
+  // A launch holds fewer than 2^32 work items; as many rows as that leaves at 512 a segment.
+  const int64_t per = std::max<int64_t>(1, ((int64_t(1) << 32) - 1) / ((int64_t)kSegThreads * a.segs));
+  for (int64_t row = 0; row < a.T; row += per) {
+    const DistillArgs part = rows_of<T>(a, row, std::min(per, a.T - row));
+    const hipError_t e = !part.labels || a.tau == 1.0f ? launch_mode<T, 0>(part, stream)
+                         : a.tau == 2.0f               ? launch_mode<T, 1>(part, stream)
+                                                       : launch_mode<T, 2>(part, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace distill

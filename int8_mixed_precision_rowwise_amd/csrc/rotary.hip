@@ -43,6 +43,7 @@ constexpr int64_t kPast = 64 << 20;
 struct RotKernelArgs {
   RotaryTensor t[2];  // q, k
   int64_t tokens, S;
+  int64_t first;     // token of the launch's first workgroup
   const void* pos;
   int64_t pos_b, pos_s;
   const double* freqs;
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(kRotThreads) void rotary_kernel(RotKernelArgs a) {
   typedef Pack<T, V, WIDE, PAST> P;
   const int t = threadIdx.x;
   const int half = a.rot / 2;
-  const int64_t token0 = (int64_t)blockIdx.x * a.tpw;
+  const int64_t token0 = a.first + (int64_t)blockIdx.x * a.tpw;
   const int tokens = (int)min((int64_t)a.tpw, a.tokens - token0);
   for (int i = t; i < tokens * half; i += kRotThreads) {
     const int tb = i / half, pair = i - tb * half;
@@ -231,19 +232,26 @@ hipError_t launch_typed(RotKernelArgs a, bool half, hipStream_t stream) {
   if (a.tpw == 1 && a.tokens < 1024) a.rows_per_y = (int)max((int64_t)1, min((int64_t)heads, (int64_t)kRotThreads / a.slots));
   a.drow = kRotThreads / a.slots;
   a.dslot = kRotThreads - a.drow * a.slots;
-  const dim3 grid((unsigned)((a.tokens + a.tpw - 1) / a.tpw), (unsigned)((heads + a.rows_per_y - 1) / a.rows_per_y));
   const size_t lds = (size_t)a.tpw * (a.rot / 2 * sizeof(float2) + 32);
   const bool past = kPast < (int64_t)sizeof(T) * a.tokens * heads * a.D;
-  if constexpr (kWidest >= 8) {
-    if (v == 8 && past) launch_pairs<T, 8, true, true>(a, half, grid, lds, stream);
-    if (v == 8 && !past) launch_pairs<T, 8, true, false>(a, half, grid, lds, stream);
+  // a launch holds fewer than 2^32 work items
+  const int64_t step = ((int64_t(1) << 32) / kRotThreads - 1) * a.tpw;
+  for (a.first = 0; a.first < a.tokens; a.first += step) {
+    const dim3 grid((unsigned)((min(step, a.tokens - a.first) + a.tpw - 1) / a.tpw),
+                    (unsigned)((heads + a.rows_per_y - 1) / a.rows_per_y));
+    if constexpr (kWidest >= 8) {
+      if (v == 8 && past) launch_pairs<T, 8, true, true>(a, half, grid, lds, stream);
+      if (v == 8 && !past) launch_pairs<T, 8, true, false>(a, half, grid, lds, stream);
+    }
+    if (v == 4 && past) launch_pairs<T, 4, true, true>(a, half, grid, lds, stream);
+    if (v == 4 && !past) launch_pairs<T, 4, true, false>(a, half, grid, lds, stream);
+    if (v == 2 && wide) launch_pairs<T, 2, true, false>(a, half, grid, lds, stream);
+    if (v == 2 && !wide) launch_pairs<T, 2, false, false>(a, half, grid, lds, stream);
+    if (v == 1) launch_pairs<T, 1, true, false>(a, half, grid, lds, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  if (v == 4 && past) launch_pairs<T, 4, true, true>(a, half, grid, lds, stream);
-  if (v == 4 && !past) launch_pairs<T, 4, true, false>(a, half, grid, lds, stream);
-  if (v == 2 && wide) launch_pairs<T, 2, true, false>(a, half, grid, lds, stream);
-  if (v == 2 && !wide) launch_pairs<T, 2, false, false>(a, half, grid, lds, stream);
-  if (v == 1) launch_pairs<T, 1, true, false>(a, half, grid, lds, stream);
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace

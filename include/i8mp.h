@@ -409,6 +409,7 @@ i8mp_status i8mp_rotary(const i8mp_heads* q, const i8mp_heads* k, int64_t B, int
  * and the sum are fp32, Y and Z (z kept for the backward; NULL: not) are rounded
  * once.  GELU is z Phi(z); GELU_TANH z (1 + tanh(sqrt(2 / pi)(z + 0.044715 z^3))) / 2;
  * SILU z / (1 + exp(-z)).
+ *   N: below 2^28
  *   bias: bf16 [N] or NULL; residual: bf16 [M x N] or NULL
  *   Y, Z: bf16 [M x N], any alignment of elements (rows of 16-byte aligned starts
  *     leave in whole 16-byte stores)

@@ -125,11 +125,12 @@ bool heads_disjoint(const HeadsView& a, const HeadsView& c, int64_t B, int64_t S
 bool act_ok(int32_t act) { return act >= I8MP_ACT_NONE && act <= I8MP_ACT_SILU; }
 uint64_t pass_offset(uint64_t offset, int j) { return offset + ((uint64_t)j << 40); }
 bool opts_ok(const i8mp_linear_opts* o) { return o && (o->round == I8MP_RNE || o->round == I8MP_SR); }
-// Sizes whose buffers' byte counts stay far from overflow.
+// Sizes whose buffers' byte counts stay far from overflow, and whose columns (16 work
+// items each in the few-token kernel, 8 in the backward's join) fit a launch of fewer than 2^32.
 bool linear_dims_ok(int64_t M, int64_t N, int64_t K) {
-  constexpr int64_t kArea = int64_t(1) << 50;
+  constexpr int64_t kArea = int64_t(1) << 50, kMaxColumns = int64_t(1) << 28;
   const int64_t m = M + 16, n = N + 16, k = K + 16;
-  return dims_ok(M, N, K) && m <= kArea / n && m <= kArea / k && n <= kArea / k;
+  return dims_ok(M, N, K) && N < kMaxColumns && m <= kArea / n && m <= kArea / k && n <= kArea / k;
 }
 
 // The contraction a GEMM runs over: padded to whole 16-byte chunks.

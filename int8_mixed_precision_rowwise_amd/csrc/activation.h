@@ -100,7 +100,8 @@ __device__ __forceinline__ float activation_grad(float z) {
     float s, c;
     sigmoid_pair(z * __builtin_fmaf(z2, 2 * kGeluB * kGeluC, 2 * kGeluB), s, c);
     const float du = __builtin_fmaf(z2, 6 * kGeluB * kGeluC, 2 * kGeluB);
-    return __builtin_fmaf(z * du, s * c, s);
+    const float w = s * c;  // 0 from |z| = 11 on; z du is infinite from 10^13 on
+    return __builtin_fmaf(z * (w == 0.0f ? 0.0f : du), w, s);
   }
   if constexpr (ACT == kActSilu) {
     float s, c;

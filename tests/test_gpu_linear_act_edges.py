@@ -57,3 +57,22 @@ def test_weight_rows_far_apart(M, N, K, pitch):
     out = torch.full((M, N + 1), 7.0, dtype=bf, device="cuda")
     got = i8.linear_wq_fwd(X, far, ws, out=out[:, :N], **kw)
     assert torch.equal(got, want) and bool((out[:, N] == 7).all())
+
+
+@pytest.mark.parametrize("act", list(i8.ACTIVATIONS)[1:])
+def test_derivatives_far_out(act):
+    """Finite pre-activations up to the type's largest.  On the right the derivative is 1;
+    on the left at most 64 exp(-64), below 2^-80 (and 0 from 10^4 on): the gradients and
+    the activation itself are those of 1 and 0 within 16 such numbers."""
+    far = torch.tensor([64.0, 1e4, 1.5e13, 1e14, 1e19, 2e19, 1e30, 3.3e38])
+    z = torch.cat((far, -far)).to(bf).cuda()
+    N = z.numel()
+    Z = z.expand(8, N).contiguous()
+    dY = torch.ones(8, N, dtype=bf, device="cuda")
+    X, W = torch.ones(8, 16, dtype=bf, device="cuda"), torch.eye(N, dtype=bf, device="cuda")
+    dX, dW, db = i8.linear_act_bwd(dY, Z, X, W, act, want_dbias=True)
+    one = (z > 0).to(bf)
+    Y = i8.linear_act_fwd(torch.zeros(8, 16, dtype=bf, device="cuda"), W[:, :16].contiguous(), bias=z, activation=act)
+    for got, want in ((db, 8 * one), (dX, one.expand(8, N)), (dW, 8 * one[:, None].expand(N, 16)),
+                      (Y, torch.where(z > 0, z, 0.0).expand(8, N))):
+        assert bool(((got.double() - want.double()).abs() <= 2.0 ** -76).all())

@@ -76,3 +76,25 @@ def test_derivatives_far_out(act):
     for got, want in ((db, 8 * one), (dX, one.expand(8, N)), (dW, 8 * one[:, None].expand(N, 16)),
                       (Y, torch.where(z > 0, z, 0.0).expand(8, N))):
         assert bool(((got.double() - want.double()).abs() <= 2.0 ** -76).all())
+
+
+@pytest.mark.parametrize("act,M,N,K", [("silu", 33, 4107, 2040), ("gelu", 48, 4100, 1001), ("gelu_tanh", 49, 5003, 520),
+                                       ("relu", 64, 4099, 8200), ("none", 64, 4097, 24)])
+def test_many_few_tokens_over_wide_outputs(act, M, N, K):
+    """33 to 64 rows with two column tiles a workgroup: against 64 bits, with kept
+    pre-activations, and the same bits over weights quantized once and where rows of the
+    output start anywhere."""
+    import oracle
+    from tests.gpu_util import tensor_bits
+    from tests.test_gpu_linear_act import check_forward, product, rows
+    X, W = rows(randn(1, M, K)), rows(randn(2, N, K))
+    bias, residual = randn(3, N), rows(randn(4, M, N))
+    p = product(*oracle.quantize_rowwise(tensor_bits(X), oracle.RNE, 0, 0), *oracle.quantize_rowwise(tensor_bits(W), oracle.RNE, 0, 0))
+    kw = dict(bias=bias, activation=act, residual=residual)
+    Y, Z, cx, cw = i8.linear_act_fwd_train(X, W, **kw)
+    check_forward(p, bias, act, residual, Y, Z)
+    assert torch.equal(cx, X.abs().amax(0).float()) and torch.equal(cw, W.abs().amax(0).float())
+    Wq, ws = i8.quantize_rowwise(W)
+    store = torch.full((M, N + 3), 7.0, dtype=bf, device="cuda")
+    got = i8.linear_wq_fwd(X, Wq, ws, out=store[:, :N], **kw)
+    assert torch.equal(got, Y) and bool((store[:, N:] == 7).all())

@@ -301,7 +301,8 @@ i8mp_status i8mp_linear_fwd_colmax(const uint16_t* X, const uint16_t* W, uint16_
   for (Range o : {ry, rx, rwt})
     if (overlap(o, rcx) || overlap(o, rcw)) return I8MP_EINVAL;
   if (overlap(rcx, rcw)) return I8MP_EINVAL;
-  if (M == 0 || N == 0) return I8MP_OK;
+  // without outputs there are still the column maxima: the other operand's, and 0 of the one without rows
+  if ((M == 0 || N == 0) && (K == 0 || (!colmax_x && !colmax_w))) return I8MP_OK;
   const size_t need = carve_fwd(nullptr, M, N, K, nullptr);
   if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return I8MP_EWORKSPACE;
   const Range rw = vec_range(ws, (int64_t)need, 1);
@@ -532,7 +533,8 @@ i8mp_status i8mp_linear_fwd_fp8_colmax(const uint16_t* X, const uint16_t* W, uin
   for (Range o : {ry, rx, rwt})
     if (overlap(o, rcx) || overlap(o, rcw)) return I8MP_EINVAL;
   if (overlap(rcx, rcw)) return I8MP_EINVAL;
-  if (M == 0 || N == 0) return I8MP_OK;
+  // without outputs there are still the column maxima: the other operand's, and 0 of the one without rows
+  if ((M == 0 || N == 0) && (K == 0 || (!colmax_x && !colmax_w))) return I8MP_OK;
   const size_t need = carve_fwd(nullptr, M, N, K, nullptr);
   if (!ws || !aligned(ws, kAlign) || ws_bytes < need) return I8MP_EWORKSPACE;
   const Range rw = vec_range(ws, (int64_t)need, 1);

@@ -37,6 +37,7 @@ run without checkpointing.
 from __future__ import annotations
 
 import dataclasses
+import math
 import threading
 from typing import Callable, Optional
 
@@ -374,7 +375,7 @@ def distill_loss(logits: torch.Tensor, teacher: torch.Tensor, idx: torch.Tensor,
 
 def _aligned_rows(t: torch.Tensor, cols: int) -> torch.Tensor:
     """t as a matrix of `cols` columns whose rows start every 16 bytes."""
-    t = t.reshape(-1, cols)
+    t = t.reshape(math.prod(t.shape[:-1]), cols)  # -1 would be any number of rows without columns
     if t.stride(1) == 1 and t.stride(0) % 8 == 0 and t.stride(0) >= cols and t.data_ptr() % 16 == 0:
         return t
     store = torch.empty((t.shape[0], max(8, (cols + 7) // 8 * 8)), dtype=t.dtype, device=t.device)

@@ -108,3 +108,20 @@ def test_second_derivatives_are_right_or_refused(monkeypatch):
             (part.sum() + x.square().sum()).backward(retain_graph=True)
     T.linear_act(x, w).square().sum().backward()  # the first is as it was
     assert x.grad.grad_fn is None and torch.equal(w.grad, d[1].detach())
+
+
+@pytest.mark.parametrize("lead,N,K", [((3,), 16, 0), ((2, 3), 0, 8), ((2, 0), 16, 8), ((0,), 0, 0), ((), 16, 8)])
+def test_empty_dimensions(forwards, monkeypatch, lead, N, K):
+    """No columns in, none out, no rows, and a single vector: shapes forward and backward."""
+    def bwd(dy, z, x, w, *a, **k):
+        return torch.zeros_like(x), torch.zeros_like(w), torch.zeros(w.shape[0])
+
+    monkeypatch.setattr(T._ops, "linear_act_bwd", bwd)
+    x, w = torch.zeros(*lead, K, dtype=bf, requires_grad=True), torch.zeros(N, K, dtype=bf, requires_grad=True)
+    b, r = torch.zeros(N, dtype=bf, requires_grad=True), torch.zeros(*lead, N, dtype=bf, requires_grad=True)
+    y = T.linear_act(x, w, b, "silu", r)
+    assert y.shape == (*lead, N)
+    grads = torch.autograd.grad(y, (x, w, b, r), torch.ones_like(y))
+    assert [g.shape for g in grads] == [x.shape, w.shape, b.shape, r.shape]
+    with torch.no_grad():
+        assert T.linear_act(x, w, b, "silu", r).shape == (*lead, N)

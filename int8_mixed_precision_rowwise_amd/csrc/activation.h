@@ -1,7 +1,7 @@
 // Activations and their derivatives in fp32, for the epilogues and the
 // backward of the linears.
 //
-// An activation's value is rounded to bf16 (2^-9) at once and sits in a GEMM's
+// An activation's value is rounded to bf16 (half a step is 2^-8 of it at most) at once and sits in a GEMM's
 // epilogue, where every operation shows: it takes the hardware's exponential and
 // reciprocal (1 ulp each) as they are.  A derivative also goes into the bias
 // gradient, which stays fp32, and into a pass that memory bounds: it carries the low

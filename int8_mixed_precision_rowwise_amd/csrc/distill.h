@@ -31,12 +31,13 @@
 // every factor of which is in range.  Rest entries that are all -inf have e' = 0.
 //
 // Measured: loss and gradient of 4096 x 128256 bf16 logits, temperature 2 with hard
-// labels, 513 - 552 us for 2.1 GB, 3.8 - 4.1 TB/s where a copy of that size reaches 5.1.  Two
+// labels, 520 - 525 us in calls one after another for 2.1 GB, 4.0 TB/s where a copy of that
+// size reaches 5.1 (the kernel alone under the profiler 537 - 590, 553 on average).  Two
 // exponentials an element at a quarter of the vector rate and some 13 other operations
 // are about 240 us of every CU's time; a row of this length fills a CU, so they
 // overlap with memory only as far as the CUs are at different places of their rows.  Loss of
-// 2000 x 32000 fp32 52 us (4.9 TB/s); loss, then gradient, of 1021 x 32003 fp16 26 and
-// 27 us; three rows of 128256 in segments 4.7 and 8.3 us, bound by one load waiting
+// 2000 x 32000 fp32 51 us (5.0 TB/s); loss, then gradient, of 1021 x 32003 fp16 26 and
+// 27 us; three rows of 128256 in segments 4.5 and 8.7 us, bound by one load waiting
 // for the other.
 //
 // Rows too long for that, and calls with too few rows to fill the chip, take

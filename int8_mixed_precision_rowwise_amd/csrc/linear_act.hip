@@ -14,10 +14,11 @@
 // operand's codes fills the padding with zeros, and the second's padding may
 // hold anything.
 //
-// Measured, this kernel alone: 8192 x 5632 x 2048 with SiLU and the pre-activation kept
-// 112 - 116 us, 8192 x 2048 x 5632 with the residual 79 - 81 us (1.7 and 2.3 Pop/s; 8192 cubed
-// without an epilogue runs at 2.5, which would be 74 us for either).  The first writes
-// 185 MB behind its products, and one workgroup fills a CU, so nothing overlaps them.
+// Measured, this kernel alone, on several cards: 8192 x 5632 x 2048 with SiLU and the
+// pre-activation kept 112 - 122 us, 8192 x 2048 x 5632 with the residual 79 - 86 us (1.6 and
+// 2.3 Pop/s; 8192 cubed without an epilogue runs at 2.5, which would be 74 us for either).
+// The first writes 185 MB behind its products, and one workgroup of 256 x 256 outputs fills
+// a CU, so nothing overlaps them (smaller tiles, of which two fit, were not measured here).
 #include "activation.h"
 #include "gemm_pipelined.h"
 

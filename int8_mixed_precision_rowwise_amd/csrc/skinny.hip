@@ -9,9 +9,10 @@
 // go from memory straight into the matrix instruction's registers: lane l holds
 // 16 codes of row l % 16 at step offset 16 (l / 16), which is what
 // v_mfma_i32_16x16x64_i8 wants of an operand.  The waves' int32 sums are joined in
-// LDS (exact in any order).  One token against 14336 x 4096 codes: 15.9 us with the
+// LDS (exact in any order).  One token against 14336 x 4096 codes: 15.7 us with the
 // token's quantization (3.7 TB/s; the launch, the first weights' way and the join are 4
-// of them), 64 tokens 34 us, where X's codes cost as many cache reads as the weights.
+// of them), 64 tokens 35 us, where every workgroup reads all of X's codes again: twice the
+// weights' bytes, from the cache.
 #include "activation.h"
 #include "internal.h"
 #include "quant_device.h"
@@ -33,9 +34,14 @@ constexpr int kSkChunks = 8;
 
 // One tile of columns a workgroup while each CU gets at most one workgroup; beyond
 // that two, which halve the reads of X's codes (every workgroup takes them from the
-// cache).  Both sides, two tiles and one: 13 rows against 14336 x 4096 21.7 us and
-// 24.2, 17 rows 23.8 and 27.2, 64 rows against 5003 x 2040 13.8 and 17.6; but 13
-// against 4096 x 14336 33 and 26, 64 56 and 48.
+// cache) and the workgroups that quantize X.  Both sides, two tiles and one, all the
+// call's kernels.  X quantized in the kernel: 1 row against 5003 x 2040 5.8 us and 7.7, 13
+// rows 9.7 and 13.7, 8 rows against 6000 x 4096 12.3 and 13.5, 16 against 8191 x 2048
+// 10.0 and 14.2, 8 against 14336 x 4096 19.8 and 24.8 (only 1 to 4 rows against
+// 8191 x 4096 are better off with one: 10.4 and 9.2, 11.7 and 10.7).  Separately: 13 rows
+// against 14336 x 4096 21.8 and 24.4, 64 rows 35.0 and 49.6, 64 against 5003 x 2040 13.8 and
+// 17.3.  Up to 4096 columns, the other way: 13 against 4096 x 14336 34.5 and 26.7, 64
+// rows 58.2 and 49.8, 1 row against 4096 x 4096 8.0 and 6.4.
 constexpr int64_t kSkWideN = 16 * 256;
 
 struct SkinnyArgs {

@@ -311,11 +311,12 @@ class RotaryFunction(torch.autograd.Function):
         positions, freqs = ctx.saved_tensors
         d = [None if g is None else g if g.dim() == 4 and (g.shape[3] <= 1 or g.stride(3) == 1) else g.contiguous()
              for g in (dq, dk)]
+        turn = RotaryFunction.apply if torch.is_grad_enabled() else _ops.rotary
         back = (positions, freqs, ctx.pairs, not ctx.inverse)
         if d[0] is None:
-            d = [None, None if d[1] is None else RotaryFunction.apply(d[1], None, *back)[0]]
+            d = [None, None if d[1] is None else turn(d[1], None, *back)[0]]
         else:
-            d = RotaryFunction.apply(d[0], d[1], *back)
+            d = turn(d[0], d[1], *back)
         return d[0], d[1], None, None, None, None
 
 

@@ -537,6 +537,123 @@ i8mp_status i8mp_distill_bwd(const i8mp_distill* p, const double* stats, const f
 i8mp_status i8mp_distill_step(const i8mp_distill* p, const float* grad, int64_t grad_s, float* loss,
                               void* dlogits, int64_t d_ld, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- block-scaled FP8 linears and experts ------------------------------- */
+
+/*
+ * Operands are E4M3 codes with one power-of-two scale for each 128 of the
+ * contraction.  With a the largest magnitude of a block, its scale is the least
+ * 2^e, e >= -126, with a <= 448 * 2^e; a code is the nearest E4M3 value (ties to
+ * even) of x / 2^e, and the scale is held as the byte e + 127.  Products are summed
+ * in fp32 by the matrix core, which applies the scales, and rounded to bf16 once.  A
+ * block that holds an infinity or NaN makes the outputs that it takes part in NaN.
+ *
+ * Weights: W bf16 [E][N][K] (matrix e at e * w_stride, rows ldw apart) has one
+ * scale for each 128 x 128 (of N and K), so that the same codes serve Y = X W^T and
+ * dX = dY W.
+ *   codes: [E][N][Kp], Kp = K rounded up to 16, zeros behind K; 16-byte aligned
+ *   exps: [E][ceil(N / 128)][ceil(K / 128)]
+ */
+i8mp_status i8mp_quantize_block_weight(const uint16_t* W, int64_t E, int64_t N, int64_t K, int64_t ldw,
+                                       int64_t w_stride, uint8_t* codes, uint8_t* exps, void* stream);
+
+/*
+ * One linear layer (experts = 0), or one for each of many experts whose rows lie
+ * one expert after another: expert e has rows offsets[e] .. offsets[e + 1] - 1 of
+ * M.  The offsets are read on the GPU: they must not fall and must lie in [0, M];
+ * others give outputs without meaning, but nothing outside the tensors is touched.
+ *   M: rows of Y and dY (and of X, unless rows is given)
+ *   codes, exps: as written by i8mp_quantize_block_weight ([N][Kp] or [E][N][Kp])
+ *   offsets: int32 or int64 (offset_bits) [experts + 1]
+ *   rows: NULL, or int32 [M]: row r is X's row rows[r], of `tokens`; one outside
+ *     them is a row of zeros
+ *   X: bf16 [tokens x K], rows 16-byte aligned
+ *   Sizes: M < 2^28, N and K < 2^23, experts < 2^16.
+ */
+typedef struct {
+  int64_t M, N, K;
+  const uint8_t* codes;
+  const uint8_t* exps;
+  int64_t experts;
+  const void* offsets;
+  int32_t offset_bits;
+  const int32_t* rows;
+  const uint16_t* X;
+  int64_t ldx, tokens;
+} i8mp_block;
+/* Bytes of workspace of the forward (backward = 0) or the backward (1); 0: none is
+ * looked at (few rows, whose kernel quantizes X by itself). */
+size_t i8mp_block_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t experts, int32_t backward);
+/*
+ * Y = X W^T, bf16 [M x N].  clear: rows behind the last expert's (from
+ * offsets[experts] on) are written as zeros; otherwise they are left as they were.
+ */
+i8mp_status i8mp_block_fwd(const i8mp_block* p, uint16_t* Y, int64_t ldy, int32_t clear, void* ws, size_t ws_bytes,
+                           void* stream);
+/*
+ * dX = dY W (bf16 [M x K], one row for each row of dY whether or not `rows` is
+ * given; clear as above) and dW = dY^T X (bf16 [N x K], or [E][N][K]; zeros for an
+ * expert without rows).  dY has its scales along N for dX; dY and X have them down
+ * the rows for dW, blocks of 128 from each expert's first row on.  Either output may
+ * be NULL.  p->codes may be NULL without dX, p->X without dW.
+ *   dY: bf16 [M x N], rows 16-byte aligned
+ */
+i8mp_status i8mp_block_bwd(const i8mp_block* p, const uint16_t* dY, int64_t lddy, uint16_t* dX, int64_t lddx,
+                           uint16_t* dW, int64_t lddw, int32_t clear, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The experts of each token.  Token t takes the k largest of its scores
+ * logits[t][0 .. E - 1] (equal ones: the lower expert first; -inf and NaN are never
+ * taken, so a row of -inf, a padding token, takes none):
+ *   experts[t][j], in falling order of their scores; -1 for none
+ *   weights[t][j]: I8MP_SOFTMAX: exp(x) over the sum of all (normalize = 0) or of the
+ *     taken (1) exponentials; I8MP_SIGMOID: 1 / (1 + exp(-x)), over the sum of the
+ *     taken ones (1; 0 where that is 0) or itself (0).  0 for none.  A score of NaN or +inf
+ *     makes its token's weights NaN.
+ *   offsets[0 .. E]: first row of each expert among the rows sorted by expert and,
+ *     within one, by token; offsets[E] is the number of rows taken
+ *   places[t][j]: the row of token t's j-th expert; -1 for none
+ *   rows[0 .. T k - 1]: the token of each row; -1 behind the last
+ *   logits: bf16, fp16 or fp32; E <= 1024, k <= min(E, 32), T k < 2^31
+ * The same call gives the same bits.
+ */
+typedef enum { I8MP_SOFTMAX = 0, I8MP_SIGMOID = 1 } i8mp_score;
+typedef struct {
+  const void* logits;
+  int64_t T, E, ld;
+  int32_t dtype, k, score, normalize;
+} i8mp_route;
+size_t i8mp_expert_route_workspace_bytes(int64_t T, int64_t E, int32_t k);
+i8mp_status i8mp_expert_route(const i8mp_route* p, float* weights, int32_t* experts, int32_t* places, int32_t* rows,
+                              int32_t* offsets, void* ws, size_t ws_bytes, void* stream);
+/* The gradient of sum(dweights * weights) at the logits, in their type, for the given choice. */
+i8mp_status i8mp_expert_route_bwd(const i8mp_route* p, const int32_t* experts, const float* dweights, void* dlogits,
+                                  int64_t ld, void* stream);
+
+/*
+ * out[t] = residual[t] + sum_j weights[t][j] Y[places[t][j]], summed in fp32 in the
+ * order of j and rounded once.  A place outside [0, R) adds nothing.
+ *   Y [R x N], residual (NULL: none) and out [T x N]: bf16, fp16 or fp32 (dtype);
+ *   places int32 [T x k], weights fp32 [T x k] or NULL (all 1)
+ */
+typedef struct {
+  int64_t T, R, N;
+  int32_t k, dtype;
+  const void* Y;
+  int64_t ldy;
+  const int32_t* places;
+  const float* weights;
+} i8mp_combine;
+i8mp_status i8mp_expert_combine(const i8mp_combine* p, const void* residual, int64_t ldr, void* out, int64_t ldo,
+                                void* stream);
+/*
+ * Its gradients: dY[places[t][j]] = weights[t][j] dout[t] and dweights[t][j] = <dout[t],
+ * Y[places[t][j]]> (fp32; 0 without a place).  Either output may be NULL.  Places other
+ * than the negative ones must be distinct.  rows: NULL, or int32 [R] as above: rows r with
+ * rows[r] < 0 of dY are written as zeros; without it rows that no place names are left.
+ */
+i8mp_status i8mp_expert_combine_bwd(const i8mp_combine* p, const void* dout, int64_t ldd, const int32_t* rows, void* dY,
+                                    int64_t ldg, float* dweights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -30,6 +30,8 @@ __all__ = [
     "rotary", "rotary_frequencies", "distill_loss", "distill_loss_bwd", "distill_loss_and_grad",
     "linear_act_fwd", "linear_act_fwd_train", "linear_act_bwd", "linear_wq_fwd", "linear_act_workspace_bytes",
     "linear_wq_workspace_bytes", "ACTIVATIONS",
+    "quantize_block_weight", "linear_block_fwd", "linear_block_bwd", "block_workspace_bytes", "expert_linear_fwd",
+    "expert_linear_bwd", "Route", "expert_route", "expert_route_bwd", "expert_combine", "expert_combine_bwd",
 ]
 
 RNE, SR = 0, 1
@@ -52,6 +54,9 @@ EXPORTED_SYMBOLS = (
     "i8mp_rotary", "i8mp_distill_workspace_bytes", "i8mp_distill_fwd", "i8mp_distill_bwd", "i8mp_distill_step",
     "i8mp_linear_act_workspace_bytes", "i8mp_linear_act_fwd", "i8mp_linear_wq_workspace_bytes", "i8mp_linear_wq_fwd",
     "i8mp_linear_act_bwd",
+    "i8mp_quantize_block_weight", "i8mp_block_workspace_bytes", "i8mp_block_fwd", "i8mp_block_bwd",
+    "i8mp_expert_route_workspace_bytes", "i8mp_expert_route", "i8mp_expert_route_bwd", "i8mp_expert_combine",
+    "i8mp_expert_combine_bwd",
 )
 
 
@@ -92,6 +97,24 @@ class _LinearActGrad(ctypes.Structure):
                 ("ldx", ctypes.c_int64), ("W", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("activation", ctypes.c_int32),
                 ("dX", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dW", ctypes.c_void_p), ("lddw", ctypes.c_int64),
                 ("dbias", ctypes.c_void_p)]
+
+
+class _Block(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("exps", ctypes.c_void_p), ("experts", ctypes.c_int64), ("offsets", ctypes.c_void_p),
+                ("offset_bits", ctypes.c_int32), ("rows", ctypes.c_void_p), ("X", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("tokens", ctypes.c_int64)]
+
+
+class _Route(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("T", ctypes.c_int64), ("E", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32), ("normalize", ctypes.c_int32)]
+
+
+class _Combine(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("R", ctypes.c_int64), ("N", ctypes.c_int64), ("k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("places", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -140,6 +163,15 @@ def _load() -> ctypes.CDLL:
         "i8mp_distill_workspace_bytes": ([i64, i64, i32, i32], sz),
         "i8mp_distill_fwd": ([ctypes.POINTER(_Distill), p, p, p, sz, p], i32),
         "i8mp_distill_bwd": ([ctypes.POINTER(_Distill), p, p, i64, p, i64, p], i32),
+        "i8mp_quantize_block_weight": ([p, i64, i64, i64, i64, i64, p, p, p], i32),
+        "i8mp_block_workspace_bytes": ([i64, i64, i64, i64, i32], sz),
+        "i8mp_block_fwd": ([ctypes.POINTER(_Block), p, i64, i32, p, sz, p], i32),
+        "i8mp_block_bwd": ([ctypes.POINTER(_Block), p, i64, p, i64, p, i64, i32, p, sz, p], i32),
+        "i8mp_expert_route_workspace_bytes": ([i64, i64, i32], sz),
+        "i8mp_expert_route": ([ctypes.POINTER(_Route), p, p, p, p, p, p, sz, p], i32),
+        "i8mp_expert_route_bwd": ([ctypes.POINTER(_Route), p, p, p, i64, p], i32),
+        "i8mp_expert_combine": ([ctypes.POINTER(_Combine), p, i64, p, i64, p], i32),
+        "i8mp_expert_combine_bwd": ([ctypes.POINTER(_Combine), p, i64, p, p, i64, p, p], i32),
         "i8mp_distill_step": ([ctypes.POINTER(_Distill), p, i64, p, p, i64, p, sz, p], i32),
     }
     for name, (args, res) in sigs.items():
@@ -713,3 +745,6 @@ def linear_bwd_fp8(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, want_dx: 
 from .operators import (ACTIVATIONS, distill_loss, distill_loss_and_grad, distill_loss_bwd,  # noqa: E402
                         linear_act_bwd, linear_act_fwd, linear_act_fwd_train, linear_act_workspace_bytes, linear_wq_fwd,
                         linear_wq_workspace_bytes, rotary, rotary_frequencies)
+from .block_operators import (Route, block_workspace_bytes, expert_combine, expert_combine_bwd,  # noqa: E402
+                              expert_linear_bwd, expert_linear_fwd, expert_route, expert_route_bwd, linear_block_bwd,
+                              linear_block_fwd, quantize_block_weight)

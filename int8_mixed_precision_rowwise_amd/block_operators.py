@@ -1,0 +1,430 @@
+"""Block-scaled FP8 linears, the same for many experts, and the experts' routing.
+
+A linear layer over E4M3 codes with one power-of-two scale for each 128 of the
+contraction (``quantize_block_weight``, ``linear_block_fwd``, ``linear_block_bwd``),
+one for each of many experts over rows sorted by expert (``expert_linear_fwd``,
+``expert_linear_bwd``), and what brings tokens there and back: ``expert_route``,
+``expert_route_bwd``, ``expert_combine``, ``expert_combine_bwd``.  Bound like the
+package's other operators; ``training`` holds their autograd forms.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+import int8_mixed_precision_rowwise_amd as _pkg
+from .operators import _DTYPE, _call, _ld2, _new_rows, _on_gpu, _ptr, _rows, _space
+
+__all__ = ["BLOCK", "SCORES", "quantize_block_weight", "linear_block_fwd", "linear_block_bwd", "block_workspace_bytes",
+           "expert_linear_fwd", "expert_linear_bwd", "Route", "expert_route", "expert_route_bwd", "expert_combine",
+           "expert_combine_bwd"]
+
+BLOCK = 128  # contraction elements that share a scale
+SCORES = ("softmax", "sigmoid")
+_SCORE = {s: i for i, s in enumerate(SCORES)}
+_bf, _u8, _i32 = torch.bfloat16, torch.uint8, torch.int32
+_OFFSETS = {torch.int32: 32, torch.int64: 64}
+
+
+def _blocks(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _pad16(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+def block_workspace_bytes(M: int, N: int, K: int, experts: int, backward: bool) -> int:
+    return _pkg.lib.i8mp_block_workspace_bytes(M, N, K, experts, int(backward))
+
+
+# --------------------------------------------------------------------------- weights
+
+
+def quantize_block_weight(W: torch.Tensor, codes: torch.Tensor | None = None, exponents: torch.Tensor | None = None):
+    """E4M3 codes of bf16 weights [N, K] or [E, N, K] with a power-of-two scale for each
+    128 x 128 of N and K: (codes uint8 [..., N, K rounded up to 16], exponents uint8
+    [..., ceil(N / 128), ceil(K / 128)]).
+
+    A block's scale is the least 2^e (e >= -126) that brings its largest magnitude to
+    at most 448; the exponents hold e + 127 (``exponents.view(torch.float8_e8m0fnu)``
+    are the scales, ``codes.view(torch.float8_e4m3fn)`` the values under them).  The
+    columns behind K are zero.  The same codes serve the forward and the gradient at
+    the input; a training step quantizes a weight once after each update."""
+    _pkg._tensor(W, "W", _bf)
+    if W.dim() not in (2, 3):
+        raise ValueError(f"W: [N, K] or [E, N, K] expected, got {W.dim()}-D")
+    *lead, N, K = W.shape
+    if lead and lead[0] < 1:
+        raise ValueError("W: at least one expert expected")
+    if W.numel() and ((K > 1 and W.stride(-1) != 1) or (N > 1 and W.stride(-2) < K) or (lead and lead[0] > 1 and W.stride(0) < 0)):
+        raise ValueError("W: rows of adjacent elements, no two rows sharing any, expected")
+    want = ((*lead, N, _pad16(K)), (*lead, _blocks(N), _blocks(K)))
+    for t, name, shape in ((codes, "codes", want[0]), (exponents, "exponents", want[1])):
+        if t is not None:
+            _codes(t, name, shape)
+    dev = _pkg._device(W, codes, exponents)
+    codes = torch.empty(want[0], dtype=_u8, device=dev) if codes is None else codes
+    exponents = torch.empty(want[1], dtype=_u8, device=dev) if exponents is None else exponents
+    ld = W.stride(-2) if N > 1 else max(K, 8)
+    E = lead[0] if lead else 1
+    _call(dev, "i8mp_quantize_block_weight", _ptr(W), E, N, K, _pad8(ld) if N <= 1 else ld, W.stride(0) if E > 1 else 0,
+          _ptr(codes), _ptr(exponents))
+    return codes, exponents
+
+
+def _pad8(n: int) -> int:
+    return (n + 7) // 8 * 8
+
+
+def _codes(t, name: str, shape):
+    _pkg._tensor(t, name, _u8)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor expected")
+
+
+# --------------------------------------------------------------------------- linears
+
+
+def _ld_rows(t: torch.Tensor) -> int:
+    """Leading dimension of a matrix read in 16-byte chunks (one row: any)."""
+    return t.stride(0) if t.shape[0] > 1 else _pad8(max(t.shape[1], 1))
+
+
+def _block(X, codes, exps, offsets, rows, K, N, M, dy=None, out=None, out_cols=0, more=(), workspace=None):
+    """Checks of a product: (the C structure, device).  dy: what is read in X's place as rows (backward)."""
+    lead = codes.dim() - 2 if isinstance(codes, torch.Tensor) else 0
+    E = codes.shape[0] if lead == 1 else 0
+    try:
+        sx = X.stride()
+        fine = (X.dtype == _bf and X.dim() == 2 and X.shape[1] == K and K > 0 and M > 0 and N > 0 and sx[1] == 1 and sx[0] >= K
+                and codes.dtype == _u8 and codes.shape[-1] == _pad16(K) and codes.is_contiguous()
+                and exps.dtype == _u8 and exps.shape == (*codes.shape[:lead], _blocks(N), _blocks(K)) and exps.is_contiguous()
+                and (offsets is None) == (lead == 0) and _on_gpu(X, codes, exps, offsets, rows, dy, out, workspace, *more))
+        if offsets is not None:
+            fine = fine and offsets.dtype in _OFFSETS and offsets.shape == (E + 1,) and offsets.is_contiguous()
+        if rows is not None:
+            fine = fine and rows.dtype == _i32 and rows.shape == (M,) and rows.is_contiguous()
+        else:
+            fine = fine and X.shape[0] == M
+        if dy is not None:
+            sd = dy.stride()
+            fine = fine and dy.dtype == _bf and dy.shape == (M, N) and sd[1] == 1 and sd[0] >= N
+        if out is not None:
+            so = out.stride()
+            fine = fine and out.dtype == _bf and out.shape == (M, out_cols) and so[1] == 1 and so[0] >= out_cols
+        if workspace is not None:
+            fine = fine and workspace.dtype == _u8 and workspace.dim() == 1 and workspace.is_contiguous()
+    except (AttributeError, IndexError, TypeError):
+        fine = False
+    if not fine:
+        _block_checks(X, codes, exps, offsets, rows, K, N, M, E, dy, out, out_cols, more, workspace)
+    p = _pkg._Block(M, N, K, _ptr(codes), _ptr(exps), E, None if offsets is None else offsets.data_ptr(),
+                    0 if offsets is None else _OFFSETS[offsets.dtype], None if rows is None else _ptr(rows), _ptr(X), _ld_rows(X),
+                    X.shape[0])
+    return p, X.device
+
+
+def _block_checks(X, codes, exps, offsets, rows, K, N, M, E, dy, out, out_cols, more, workspace):
+    """The same one by one: raises what is wrong with the first that fails."""
+    _pkg._mat(X, "X", _bf)
+    if X.shape[1] != K:
+        raise ValueError(f"X: {K} columns expected, got {tuple(X.shape)}")
+    lead = (E,) if codes.dim() == 3 else ()
+    _codes(codes, "codes", (*lead, N, _pad16(K)))
+    _codes(exps, "exponents", (*lead, _blocks(N), _blocks(K)))
+    if lead:
+        if E < 1:
+            raise ValueError("codes: at least one expert expected")
+        if not isinstance(offsets, torch.Tensor) or offsets.dtype not in _OFFSETS:
+            raise TypeError("offsets: torch.int32 or torch.int64 tensor expected")
+        _pkg._vec(offsets, "offsets", E + 1, offsets.dtype)
+    elif offsets is not None:
+        raise ValueError("offsets given without experts (codes are [N, K])")
+    if rows is not None:
+        _pkg._vec(rows, "rows", M, _i32)
+    elif X.shape[0] != M:
+        raise ValueError(f"X: {M} rows expected, got {tuple(X.shape)}")
+    if dy is not None:
+        _pkg._mat(dy, "dY", _bf, (M, N))
+    if out is not None:
+        _pkg._mat(out, "dX" if dy is not None else "out", _bf, (M, out_cols))
+    if workspace is not None:
+        _pkg._workspace(workspace)
+    _pkg._device(X, codes, exps, offsets, rows, dy, out, workspace, *more)
+
+
+def _shape_of(codes, experts: bool):
+    _pkg._tensor(codes, "codes", _u8)
+    if codes.dim() != (3 if experts else 2):
+        raise ValueError(f"codes: {'[E, N, K]' if experts else '[N, K]'} expected, got {codes.dim()}-D")
+    return codes.shape[-2]
+
+
+def _features(X) -> int:
+    if not isinstance(X, torch.Tensor):
+        raise TypeError(f"X: torch.Tensor expected, got {type(X).__name__}")
+    if X.dim() != 2:
+        raise ValueError(f"X: 2-D tensor expected, got {X.dim()}-D")
+    return X.shape[1]
+
+
+def _forward(X, codes, exps, offsets, rows, out, workspace, experts):
+    N, K = _shape_of(codes, experts), _features(X)
+    M = X.shape[0] if rows is None else _count(rows)
+    p, dev = _block(X, codes, exps, offsets, rows, K, N, M, out=out, out_cols=N, workspace=workspace)
+    Y = _new_rows(M, N, dev) if out is None else out
+    need = block_workspace_bytes(M, N, K, p.experts, False)
+    ws = _space(workspace, need, dev) if need else None
+    _call(dev, "i8mp_block_fwd", p, _ptr(Y), _ld2(Y), int(out is None), None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
+    return Y
+
+
+def _count(rows) -> int:
+    if not isinstance(rows, torch.Tensor):
+        raise TypeError(f"rows: torch.Tensor expected, got {type(rows).__name__}")
+    if rows.dim() != 1:
+        raise ValueError(f"rows: 1-D tensor expected, got {rows.dim()}-D")
+    return rows.shape[0]
+
+
+def linear_block_fwd(X: torch.Tensor, codes: torch.Tensor, exponents: torch.Tensor, out: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = X @ W.T over weight codes from quantize_block_weight: bf16 [M, N].
+
+    X bf16 [M, K] (rows may lie further apart than they are long, 16-byte aligned) is
+    quantized in the call, with a scale for each row and 128 of K.  Products are summed
+    in fp32 and rounded once.  Up to a few tens of rows take one kernel that is bound by
+    reading the codes, and no workspace."""
+    return _forward(X, codes, exponents, None, None, out, workspace, False)
+
+
+def _backward(dY, X, codes, exps, offsets, rows, want_dx, want_dw, dX, dW, workspace, experts):
+    N, K = _shape_of(codes, experts), _features(X)
+    if not isinstance(dY, torch.Tensor):
+        raise TypeError(f"dY: torch.Tensor expected, got {type(dY).__name__}")
+    if dY.dim() != 2:
+        raise ValueError(f"dY: 2-D tensor expected, got {dY.dim()}-D")
+    M = dY.shape[0]
+    shape = (*codes.shape[:-2], N, K)
+    if dW is not None:
+        _pkg._tensor(dW, "dW", _bf)
+        if tuple(dW.shape) != shape:
+            raise ValueError(f"dW: shape {shape} expected, got {tuple(dW.shape)}")
+        if experts and not dW.is_contiguous():
+            raise ValueError("dW: contiguous tensor expected")
+        if not experts:
+            _pkg._mat(dW, "dW", _bf, shape)
+    p, dev = _block(X, codes, exps, offsets, rows, K, N, M, dy=dY, out=dX, out_cols=K, more=(dW,), workspace=workspace)
+    clear = dX is None
+    dX = None if not want_dx else _new_rows(M, K, dev) if dX is None else dX
+    dW = None if not want_dw else torch.empty(shape, dtype=_bf, device=dev) if dW is None else dW
+    ws = _space(workspace, block_workspace_bytes(M, N, K, p.experts, True), dev)
+    _call(dev, "i8mp_block_bwd", p, _ptr(dY), _ld_rows(dY), _ptr(dX), 0 if dX is None else _ld2(dX), _ptr(dW),
+          0 if dW is None else K if experts else _ld2(dW), int(clear), ws.data_ptr(), ws.numel())
+    return dX, dW
+
+
+def linear_block_bwd(dY: torch.Tensor, X: torch.Tensor, codes: torch.Tensor, exponents: torch.Tensor, want_dx: bool = True,
+                     want_dw: bool = True, dX: torch.Tensor | None = None, dW: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None):
+    """Backward of linear_block_fwd: (dX = dY @ W [M, K], dW = dY.T @ X [N, K]), bf16; None for
+    what is not wanted.
+
+    dY is quantized with a scale for each row and 128 of N for dX; dY and X with one for
+    each column and 128 rows for dW.  codes and exponents are the forward's."""
+    return _backward(dY, X, codes, exponents, None, None, want_dx, want_dw, dX, dW, workspace, False)
+
+
+def expert_linear_fwd(X: torch.Tensor, codes: torch.Tensor, exponents: torch.Tensor, offsets: torch.Tensor,
+                      rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """linear_block_fwd for each of many experts over their own rows: bf16 [R, N].
+
+    codes [E, N, K rounded up to 16] and exponents from quantize_block_weight; expert e
+    has rows offsets[e] .. offsets[e + 1] - 1 (int32 or int64 [E + 1] on the GPU, which
+    the host never reads).  rows (int32 [R]): the row of X that each row is, as
+    expert_route gives them; then X holds the tokens and is not copied into the experts'
+    order.  Without it R is X's own number of rows.  Rows behind the last expert's are
+    zero, or, in a given `out`, left as they were."""
+    if offsets is None:
+        raise TypeError("offsets: torch.int32 or torch.int64 tensor expected")
+    return _forward(X, codes, exponents, offsets, rows, out, workspace, True)
+
+
+def expert_linear_bwd(dY: torch.Tensor, X: torch.Tensor, codes: torch.Tensor, exponents: torch.Tensor, offsets: torch.Tensor,
+                      rows: torch.Tensor | None = None, want_dx: bool = True, want_dw: bool = True,
+                      dX: torch.Tensor | None = None, dW: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Backward of expert_linear_fwd: (dX [R, K], dW [E, N, K]), bf16.
+
+    dX has a row for each row of dY; where the rows were read through `rows`,
+    expert_combine adds a token's rows up.  An expert without rows has a gradient of
+    zeros; rows of dX behind the last expert's as in the forward."""
+    if offsets is None:
+        raise TypeError("offsets: torch.int32 or torch.int64 tensor expected")
+    return _backward(dY, X, codes, exponents, offsets, rows, want_dx, want_dw, dX, dW, workspace, True)
+
+
+# --------------------------------------------------------------------------- routing
+
+
+class Route(NamedTuple):
+    """What expert_route gives: the k experts of each token and their weights, [T, k];
+    the row that each has among the rows sorted by expert; the token of each row [T k];
+    the first row of each expert [E + 1]."""
+    weights: torch.Tensor
+    experts: torch.Tensor
+    places: torch.Tensor
+    rows: torch.Tensor
+    offsets: torch.Tensor
+
+
+def _route(logits, k, score, normalize, experts=None, dweights=None, out=None, workspace=None, backward=False):
+    try:
+        T, E = logits.shape
+        sl = logits.stride()
+        fine = (logits.dtype in _DTYPE and 1 <= k <= min(E, 32) and E <= 1024 and sl[1] == 1 and sl[0] >= E and T > 0 and score in _SCORE
+                and _on_gpu(logits, experts, dweights, out, workspace))
+        if backward:
+            fine = fine and (experts.shape == dweights.shape == (T, k) and experts.dtype == _i32 and dweights.dtype == torch.float32
+                             and experts.is_contiguous() and dweights.is_contiguous())
+        if out is not None:
+            so = out.stride()
+            fine = fine and out.shape == (T, E) and out.dtype == logits.dtype and so[1] == 1 and so[0] >= E
+        if workspace is not None:
+            fine = fine and workspace.dtype == _u8 and workspace.dim() == 1 and workspace.is_contiguous()
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _rows(logits, "logits", tuple(_DTYPE))
+        T, E = logits.shape
+        if score not in _SCORE:
+            raise ValueError(f"score must be one of {SCORES}, got {score!r}")
+        if not 1 <= E <= 1024:
+            raise ValueError(f"1 to 1024 experts expected, got {E}")
+        if not (isinstance(k, int) and 1 <= k <= min(E, 32)):
+            raise ValueError(f"k from 1 to {min(E, 32)} expected, got {k}")
+        if backward:
+            _pkg._mat(experts, "experts", _i32, (T, k), dense=True)
+            _pkg._mat(dweights, "dweights", torch.float32, (T, k), dense=True)
+        if out is not None:
+            _pkg._mat(out, "out", logits.dtype, (T, E))
+        if workspace is not None:
+            _pkg._workspace(workspace)
+        _pkg._device(logits, experts, dweights, out, workspace)
+    return _pkg._Route(_ptr(logits), T, E, _ld2(logits), _DTYPE[logits.dtype], k, _SCORE[score], int(bool(normalize))), logits.device
+
+
+def expert_route(logits: torch.Tensor, k: int, score: str = "softmax", normalize: bool = True,
+                 workspace: torch.Tensor | None = None) -> Route:
+    """The k experts with the largest of each token's scores, and the rows sorted by expert.
+
+    logits [T, E], bf16, fp16 or fp32; E <= 1024, k <= 32.  Equal scores: the lower
+    expert first.  A score of -inf is never taken: a padding token's row of them has no
+    experts (-1), weights of 0 and no rows.  score "softmax": weights are the softmax
+    over the taken experts (normalize) or over all; "sigmoid": 1 / (1 + exp(-x)), divided
+    by the taken ones' sum (normalize) or not.  weights are fp32, the others int32;
+    rows behind offsets[E] are -1."""
+    p, dev = _route(logits, k, score, normalize, workspace=workspace)
+    T, E = p.T, p.E
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    ints = torch.empty(3 * T * k + E + 1, dtype=_i32, device=dev)
+    n = T * k
+    experts, places, rows, offsets = ints[:n].view(T, k), ints[n:2 * n].view(T, k), ints[2 * n:3 * n], ints[3 * n:]
+    need = _pkg.lib.i8mp_expert_route_workspace_bytes(T, E, k)
+    ws = _space(workspace, need, dev) if need else None
+    at = ints.data_ptr()
+    _call(dev, "i8mp_expert_route", p, _ptr(weights), at, at + 4 * n, at + 8 * n, at + 12 * n, None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel())
+    return Route(weights, experts, places, rows, offsets)
+
+
+def expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
+                     normalize: bool = True, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of sum(dweights * weights) at the logits [T, E], in their type, the choice
+    of experts (from expert_route, with the same score and normalize) taken as given."""
+    if not isinstance(experts, torch.Tensor):
+        raise TypeError(f"experts: torch.Tensor expected, got {type(experts).__name__}")
+    k = experts.shape[-1] if experts.dim() else 0
+    p, dev = _route(logits, k, score, normalize, experts, dweights, out, backward=True)
+    d = torch.empty((p.T, p.E), dtype=logits.dtype, device=dev) if out is None else out
+    _call(dev, "i8mp_expert_route_bwd", p, _ptr(experts), _ptr(dweights), _ptr(d), _ld2(d))
+    return d
+
+
+def _combine(Y, places, weights, same=(), rows=None):
+    """Checks of a combination; `same`: (tensor, name) of Y's type and [T, N] each, or None."""
+    try:
+        (R, N), (T, k) = Y.shape, places.shape
+        sy = Y.stride()
+        fine = (Y.dtype in _DTYPE and T > 0 and R > 0 and N > 0 and k > 0 and sy[1] == 1 and sy[0] >= N and places.dtype == _i32
+                and places.is_contiguous() and _on_gpu(Y, places, weights, rows, *(t for t, _ in same)))
+        if weights is not None:
+            fine = fine and weights.shape == (T, k) and weights.dtype == torch.float32 and weights.is_contiguous()
+        if rows is not None:
+            fine = fine and rows.shape == (R,) and rows.dtype == _i32 and rows.is_contiguous()
+        for t, _ in same:
+            if t is not None:
+                st = t.stride()
+                fine = fine and t.shape == (T, N) and t.dtype == Y.dtype and st[1] == 1 and st[0] >= N
+    except (AttributeError, IndexError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _rows(Y, "Y", tuple(_DTYPE))
+        R, N = Y.shape
+        _pkg._mat(places, "places", _i32, dense=True)
+        T, k = places.shape
+        if k < 1:
+            raise ValueError("places: at least one for each token expected")
+        if weights is not None:
+            _pkg._mat(weights, "weights", torch.float32, (T, k), dense=True)
+        if rows is not None:
+            _pkg._vec(rows, "rows", R, _i32)
+        for t, name in same:
+            if t is not None:
+                _pkg._mat(t, name, Y.dtype, (T, N))
+        _pkg._device(Y, places, weights, rows, *(t for t, _ in same))
+    p = _pkg._Combine(T, R, N, k, _DTYPE[Y.dtype], _ptr(Y), _ld2(Y), _ptr(places), None if weights is None else _ptr(weights))
+    return p, Y.device
+
+
+def expert_combine(Y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor | None = None,
+                   residual: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[t] = residual[t] + sum_j weights[t, j] Y[places[t, j]]: [T, N] in Y's type.
+
+    Y [R, N] bf16, fp16 or fp32; places int32 [T, k] (outside [0, R): nothing is added);
+    weights fp32 [T, k], or None for 1 each, which is also the gradient at the tokens of
+    rows read through expert_route's `rows`.  Sums are fp32, in the order of j, rounded
+    once.  residual may be `out` itself."""
+    p, dev = _combine(Y, places, weights, ((residual, "residual"), (out, "out")))
+    out = torch.empty((p.T, p.N), dtype=Y.dtype, device=dev) if out is None else out
+    _call(dev, "i8mp_expert_combine", p, _ptr(residual), 0 if residual is None else _ld2(residual), _ptr(out), _ld2(out))
+    return out
+
+
+def expert_combine_bwd(dout: torch.Tensor, Y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor | None = None,
+                       rows: torch.Tensor | None = None, want_dy: bool = True, want_dweights: bool = True,
+                       dY: torch.Tensor | None = None):
+    """Backward of expert_combine: (dY [R, N] in Y's type, dweights fp32 [T, k]), None for what
+    is not wanted (the residual's gradient is dout itself).
+
+    places must be distinct but for those that add nothing.  rows (int32 [R], from
+    expert_route): rows that no token has (a negative entry) are written as zeros; without
+    it a new dY is cleared first, and a given one keeps them."""
+    p, dev = _combine(Y, places, weights, ((dout, "dout"),), rows)
+    if dout is None:
+        raise TypeError("dout: torch.Tensor expected, got NoneType")
+    if dY is not None:
+        _pkg._mat(dY, "dY", Y.dtype, tuple(Y.shape))
+        _pkg._device(Y, dY)
+    if want_dy and dY is None:
+        dY = (torch.zeros if rows is None else torch.empty)((p.R, p.N), dtype=Y.dtype, device=dev)
+    dY = dY if want_dy else None
+    dw = torch.empty((p.T, p.k), dtype=torch.float32, device=dev) if want_dweights else None
+    _call(dev, "i8mp_expert_combine_bwd", p, _ptr(dout), _ld2(dout), None if rows is None else _ptr(rows), _ptr(dY),
+          0 if dY is None else _ld2(dY), _ptr(dw))
+    return dY, dw

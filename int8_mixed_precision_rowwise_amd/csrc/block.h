@@ -1,0 +1,155 @@
+// What the block-scaled FP8 kernels share: where an expert's rows lie, the exponent
+// of a block's scale, and the launchers.
+//
+// Codes are E4M3 with one power-of-two scale for each 128 of the contraction.  A
+// block's exponent is the least e >= -126 with amax <= 448 * 2^e, held as the byte
+// e + 127 (E8M0), which the matrix instruction applies by itself while it
+// multiplies: no scale costs a vector operation in the product, and x / 2^e is exact,
+// so a code is rounded once.  A block that holds an infinity or NaN has the byte 255,
+// the NaN of that format, and codes that are NaN.
+#pragma once
+
+#include "internal.h"
+
+namespace i8mp {
+
+constexpr int kBlock = 128;
+
+// Rows of experts one after another: expert e has rows off[e] .. off[e + 1] - 1 of
+// `rows` (offsets in device memory, 32 or 64 bits).  No offsets: one expert with all rows.
+struct Ragged {
+  const void* off;
+  int bits;
+  int64_t E, rows;
+};
+
+// Room that holds `rows` rows of E experts with each expert's first row at a multiple of
+// `unit` (expert e's at unit * (off[e] / unit + e), which needs no sum over the experts
+// before it), in units.
+inline int64_t ragged_units(int64_t rows, int64_t E, int64_t unit) { return rows / unit + E; }
+
+#ifdef __HIPCC__
+namespace {
+
+__device__ __forceinline__ int64_t offset_at(const Ragged& r, int64_t e) {
+  const int64_t v = r.bits == 64 ? static_cast<const int64_t*>(r.off)[e] : (int64_t) static_cast<const int32_t*>(r.off)[e];
+  return min(max(v, (int64_t)0), r.rows);  // whatever the offsets hold, rows stay within the tensors
+}
+
+// Block `s` of the room in units of UNIT rows: the expert it belongs to (e), its first row
+// within that expert (local), and the expert's first row and number of rows.  false: none.
+struct Place {
+  int64_t e, local, first, count;
+};
+
+template <int UNIT>
+__device__ __forceinline__ bool locate(const Ragged& r, int64_t s, Place& p) {
+  if (!r.off) {
+    p.e = 0, p.first = 0, p.count = r.rows, p.local = s * UNIT;
+    return p.local < p.count;
+  }
+  // the last expert whose first unit is at most s; a wave looks at 64 experts at a time
+  const int lane = threadIdx.x & 63;
+  int64_t below = 0;
+  for (int64_t e0 = 0; e0 < r.E; e0 += 64) {
+    const int64_t e = e0 + lane;
+    const bool in = e < r.E && offset_at(r, e) / UNIT + e <= s;
+    const uint64_t m = __ballot(in);
+    below += __popcll(m);
+    if (m != ~uint64_t(0)) break;
+  }
+  if (below == 0) return false;
+  p.e = below - 1;
+  p.first = offset_at(r, p.e);
+  p.count = offset_at(r, p.e + 1) - p.first;
+  p.local = (s - (p.first / UNIT + p.e)) * UNIT;
+  return p.local >= 0 && p.local < p.count;
+}
+
+// First unit of an expert in that room.
+template <int UNIT>
+__device__ __forceinline__ int64_t unit_of(const Place& p) {
+  return p.first / UNIT + p.e;
+}
+
+// The exponent's byte of a block whose largest magnitude has the bf16 bits b:
+// 448 = 1.75 * 2^8, so e is b's exponent less 8, and one more where its fraction is over 0.75.
+__device__ __forceinline__ uint32_t exponent_byte(uint32_t b) {
+  const int byte = max((int)((b + 0x1F) >> 7) - 8, 1);
+  return b >= 0x7F80u ? 255u : (uint32_t)byte;
+}
+
+// 2^-e; NaN for the byte 255.
+__device__ __forceinline__ float inverse_scale(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7FC00000u : (254u - byte) << 23);
+}
+
+}  // namespace
+#endif
+
+// Codes of a bf16 matrix x [rows of rag][cols], read through `index` (row r is x's row
+// index[r], of n_src; a negative index or one past the end is a row of zeros) unless NULL.
+// Along the rows: codes at rows 16 * unit_of<16> + local of q_row, exponents s_row[block][that
+// row].  Down the rows, blocks starting at the expert's first row: codes at the rows
+// themselves of q_col, exponents s_col[unit_of<128> + block][column].  Pitch of codes: ldq
+// = cols rounded up to 16, zeros behind cols.
+struct BlockQuant {
+  const uint16_t* x;
+  int64_t ldx, cols, n_src;
+  const int32_t* index;
+  Ragged rag;
+  uint8_t *q_row, *s_row, *q_col, *s_col;
+  int64_t ldq, ld_srow, ld_scol;
+};
+
+// Exponents of weight blocks [E][ceil(N / 128)][ceil(K / 128)] spread to one byte for each
+// row (along = 0: planes [E][K blocks][ld], byte n) or column (along = 1: [E][N blocks][ld],
+// byte k) of the weight, as the products read them; ld a multiple of 16.
+struct SpreadJob {
+  const uint8_t* exps;
+  int64_t E, nb, kb, ld;
+  int along;
+  uint8_t* planes;
+  __host__ __device__ int64_t groups() const { return planes ? E * (along ? nb : kb) * (ld / 16) : 0; }
+};
+
+// rows / cols codes of `a`, column codes of `b` (NULL: none) and the spread exponents, in one launch.
+hipError_t launch_block_quant(const BlockQuant& a, const BlockQuant* b, const SpreadJob& spread, hipStream_t stream);
+
+hipError_t launch_block_quant_weight(const uint16_t* w, int64_t E, int64_t N, int64_t K, int64_t ldw, int64_t w_stride,
+                                     uint8_t* codes, uint8_t* exps, hipStream_t stream);
+
+// The products.  FORWARD: C[r][n] = sum_k A[r][k] B[e][n][k]; INPUT: C[r][k] = sum_n A[r][n]
+// B[e][n][k]; WEIGHT: C[e][n][k] = sum_r A[r][n] B[r][k] over the expert's rows.
+enum BlockProduct { kBlockForward = 0, kBlockInput = 1, kBlockWeight = 2 };
+struct BlockGemm {
+  int64_t rows_out;      // C's rows (WEIGHT: N); others: rag's
+  int64_t cols_out;      // C's columns
+  int64_t contraction;   // FORWARD: K, INPUT: N; WEIGHT: the expert's rows
+  const uint8_t *A, *sA; // codes and exponent planes
+  int64_t lda, ldsa;
+  const uint8_t *B, *sB;
+  int64_t ldb, ldsb, b_stride, sb_stride;  // strides between experts (FORWARD, INPUT)
+  uint16_t* C;
+  int64_t ldc, c_stride;
+  Ragged rag;
+  int clear;  // rows behind the last expert are written as zeros
+};
+hipError_t launch_block_gemm(BlockProduct what, const BlockGemm& g, hipStream_t stream);
+
+// Few rows an expert against weight codes: bound by reading them, X quantized in the kernel.
+struct BlockFew {
+  const uint16_t* x;
+  int64_t ldx, n_src;
+  const int32_t* index;
+  Ragged rag;
+  int64_t N, K;
+  const uint8_t *codes, *exps;
+  uint16_t* Y;
+  int64_t ldy;
+  int clear;
+};
+hipError_t launch_block_few(const BlockFew& a, hipStream_t stream);
+bool block_few_takes(int64_t rows, int64_t E, int64_t N, int64_t K);
+
+}  // namespace i8mp

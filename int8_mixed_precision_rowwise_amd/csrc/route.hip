@@ -1,0 +1,499 @@
+// Routing of tokens to experts and back: the top experts of each token with their weights, the
+// rows sorted by expert, the weighted sums of the experts' rows, and the gradients of both.
+//
+// Choosing: 16 lanes (up to 256 experts) or 64 share a token, each with 4 or 16 adjacent experts'
+// scores in registers; a round takes the largest score by DPP moves and, among the lanes that
+// have it, the lowest, whose experts come first.  Sorting is a counting sort that keeps the
+// tokens' order without an atomic whose order matters: a workgroup counts its block of tokens,
+// and in a second launch each adds up the blocks before it and ranks its own entries by ballots
+// over the bits of the expert's number.  One block of tokens needs one launch.
+#include "route.h"
+
+#include <algorithm>
+
+namespace i8mp {
+namespace {
+
+constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
+constexpr int64_t kRouteBlock = 256;      // tokens a workgroup, and at most this many blocks
+constexpr int64_t kRouteMaxBlocks = 256;
+
+template <int DT>
+__device__ __forceinline__ float load_as_float(const void* p, int64_t i) {
+  if constexpr (DT == I8MP_BF16) return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+  if constexpr (DT == I8MP_FP16) return (float)static_cast<const _Float16*>(p)[i];
+  return static_cast<const float*>(p)[i];
+}
+template <int DT>
+__device__ __forceinline__ void store_float(void* p, int64_t i, float v) {
+  if constexpr (DT == I8MP_BF16) static_cast<__bf16*>(p)[i] = (__bf16)v;
+  if constexpr (DT == I8MP_FP16) static_cast<_Float16*>(p)[i] = (_Float16)v;
+  if constexpr (DT == I8MP_FP32) static_cast<float*>(p)[i] = v;
+}
+
+// Over the 16 lanes of a DPP row (G = 16) or the wave (64); every lane gets the result.
+template <int G, typename F>
+__device__ __forceinline__ float over_lanes(float v, F f) {
+  const auto dpp = [&](int moved) { v = f(v, __int_as_float(moved)); };
+  dpp(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));
+  dpp(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));
+  dpp(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false));
+  dpp(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false));
+  if constexpr (G == 64) {
+    v = f(v, __shfl_xor(v, 16));
+    v = f(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// A token's scores: lane l of its G has experts l J .. l J + J - 1.  bad: one is NaN or +inf.
+template <int G, int J, int DT>
+__device__ __forceinline__ void load_scores(const RouteArgs& a, int64_t t, int lane, float (&x)[J]) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = lane * J + j;
+    x[j] = e < a.E ? load_as_float<DT>(a.logits, t * a.ld + e) : -INFINITY;
+  }
+}
+
+// The k choices of token t (G lanes, all of them here), written by the lanes that win; counts in LDS.
+template <int G, int J, int DT>
+__device__ __forceinline__ void choose(const RouteArgs& a, int64_t t, int lane, int32_t* counts) {
+  float x[J], left[J];
+  load_scores<G, J, DT>(a, t, lane, x);
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    bad |= !(x[j] < INFINITY);  // NaN, +inf
+    left[j] = x[j] == x[j] ? x[j] : -INFINITY;
+  }
+  const int shift = (threadIdx.x & 63) & ~(G - 1);  // the group's first lane in the wave
+  constexpr uint64_t kGroup = G == 64 ? ~uint64_t(0) : (uint64_t(1) << G) - 1;
+  bad = (__ballot(bad) >> shift) & kGroup;
+  constexpr int kKept = kRouteMaxK / G + (kRouteMaxK % G != 0);
+  float m = 0.0f, taken = 0.0f, kept[kKept];  // lane r % G keeps round r's score
+  for (int r = 0; r < a.k; ++r) {
+    float best = left[0];
+#pragma unroll
+    for (int j = 1; j < J; ++j) best = larger(best, left[j]);
+    const float top = over_lanes<G>(best, larger);
+    const uint64_t who = (__ballot(best == top) >> shift) & kGroup;
+    const bool some = top > -INFINITY;
+    if (r == 0) m = some ? top : 0.0f;
+    const float s = !some ? 0.0f : a.score == I8MP_SIGMOID ? sigmoid(top) : expf(top - m);
+    taken += s;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+      if (lane + G * i == r) kept[i] = s;
+    if (lane == __builtin_ctzll(who)) {
+      int at = J - 1;
+#pragma unroll
+      for (int j = J - 1; j >= 0; --j) at = left[j] == top ? j : at;
+      const int e = lane * J + at;
+      a.experts[t * a.k + r] = some ? e : -1;
+      if (some) atomicAdd(counts + e, 1);
+#pragma unroll
+      for (int j = 0; j < J; ++j) left[j] = j == at ? -INFINITY : left[j];
+    }
+  }
+  float total = taken;
+  if (!a.normalize) {
+    total = 1.0f;
+    if (a.score == I8MP_SOFTMAX) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) sum += expf(x[j] - m);
+      total = over_lanes<G>(sum, add);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (lane + G * i < a.k) a.weights[t * a.k + lane + G * i] = bad ? NAN : kept[i] > 0.0f ? kept[i] / total : 0.0f;
+}
+
+// Ranks of the block's entries and where they go.  base[e]: first row of the block's entries
+// for expert e; within[wave][e]: entries of a turn's waves, at most 64 each.
+__device__ __forceinline__ void place_entries(const RouteArgs& a, int64_t first, int64_t n, int32_t* base, uint16_t* within) {
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, E = (int)a.E;  // E <= kRouteThreads
+  const int bits = 32 - __builtin_clz(E);                                 // numbers 0 .. E
+  for (int64_t i0 = 0; i0 < n; i0 += kRouteThreads) {
+    for (int i = t; i < kRouteWaves * E; i += kRouteThreads) within[i] = 0;
+    __syncthreads();
+    const int64_t i = i0 + t;
+    const int e = i < n ? a.experts[first + i] : -1;
+    const int key = e < 0 ? E : e;
+    uint64_t same = ~uint64_t(0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot((key >> b) & 1);
+      same &= (key >> b) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+    if (e >= 0 && rank == 0) within[wave * E + e] = (uint16_t)__popcll(same);
+    __syncthreads();
+    int32_t turn = 0;  // entries of expert t
+    if (t < E) {
+#pragma unroll
+      for (int w = 0; w < kRouteWaves; ++w) {
+        const int32_t c = within[w * E + t];
+        within[w * E + t] = (uint16_t)turn;
+        turn += c;
+      }
+    }
+    __syncthreads();
+    if (i < n) {
+      int32_t at = -1;
+      if (e >= 0) {
+        at = base[e] + within[wave * E + e] + rank;
+        a.rows[at] = (int32_t)((first + i) / a.k);
+      }
+      a.places[first + i] = at;
+    }
+    __syncthreads();
+    if (t < E) base[t] += turn;
+  }
+}
+
+// Exclusive sums of counts[0 .. E - 1] into first[0 .. E], by the first wave.
+__device__ __forceinline__ void first_rows(const int32_t* counts, int32_t* first, int E) {
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int32_t before = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int32_t c = e0 + lane < E ? counts[e0 + lane] : 0;
+      int32_t s = c;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int32_t up = __shfl_up(s, o);
+        if (lane >= o) s += up;
+      }
+      if (e0 + lane < E) first[e0 + lane] = before + s - c;
+      before += __shfl(s, 63);
+    }
+    if (lane == 0) first[E] = before;
+  }
+}
+
+// LDS: counts [E], first [E + 1], within [waves][E] (16 bits).
+template <int G, int J, int DT, bool ONE>
+__global__ __launch_bounds__(kRouteThreads) void route_choose(RouteArgs a, int64_t per) {
+  extern __shared__ int32_t lds[];
+  const int E = (int)a.E, t = threadIdx.x;
+  int32_t *counts = lds, *first = lds + E;
+  uint16_t* within = reinterpret_cast<uint16_t*>(first + E + 1);
+  for (int e = t; e < E; e += kRouteThreads) counts[e] = 0;
+  __syncthreads();
+  const int64_t t0 = blockIdx.x * per, n = min(per, a.T - t0);
+  for (int64_t i = t / G; i < n; i += kRouteThreads / G) choose<G, J, DT>(a, t0 + i, t & (G - 1), counts);
+  __syncthreads();
+  if constexpr (!ONE) {
+    for (int e = t; e < E; e += kRouteThreads) a.hist[blockIdx.x * a.E + e] = counts[e];
+  } else {
+    first_rows(counts, first, E);
+    __threadfence_block();  // the choices, read again by other waves
+    __syncthreads();
+    for (int e = t; e <= E; e += kRouteThreads) a.offsets[e] = first[e];
+    const int32_t used = first[E];
+    __syncthreads();
+    place_entries(a, 0, a.T * a.k, first, within);
+    for (int64_t r = used + t; r < a.T * a.k; r += kRouteThreads) a.rows[r] = -1;
+  }
+}
+
+__global__ __launch_bounds__(kRouteThreads) void route_place(RouteArgs a, int64_t per, int blocks) {
+  extern __shared__ int32_t lds[];
+  const int E = (int)a.E, t = threadIdx.x;
+  int32_t *counts = lds, *first = lds + E, *before = first + E + 1;  // rows of the blocks before this one
+  uint16_t* within = reinterpret_cast<uint16_t*>(before + E);
+  for (int e = t; e < E; e += kRouteThreads) counts[e] = 0, before[e] = 0;
+  __syncthreads();
+  const int parts = kRouteThreads / E, e = t % E, part = t / E;  // E <= kRouteThreads
+  if (part < parts) {
+    int32_t all = 0, some = 0;
+    for (int b = part; b < blocks; b += parts) {
+      const int32_t c = a.hist[(int64_t)b * E + e];
+      all += c;
+      some += b < (int)blockIdx.x ? c : 0;
+    }
+    atomicAdd(counts + e, all);
+    atomicAdd(before + e, some);
+  }
+  __syncthreads();
+  first_rows(counts, first, E);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int x = t; x <= E; x += kRouteThreads) a.offsets[x] = first[x];
+  const int32_t used = first[E];
+  __syncthreads();
+  for (int x = t; x < E; x += kRouteThreads) first[x] += before[x];
+  __syncthreads();
+  const int64_t t0 = blockIdx.x * per, n = min(per, a.T - t0);
+  place_entries(a, t0 * a.k, n * a.k, first, within);
+  for (int64_t r = used + blockIdx.x * (int64_t)kRouteThreads + t; r < a.T * a.k; r += (int64_t)gridDim.x * kRouteThreads) a.rows[r] = -1;
+}
+
+// Gradient at a token's scores: with g the gradients of the taken weights w and S their sum,
+// <g, w> = inner, softmax gives p (g - inner) (over all, or the taken alone with their w), the
+// normalized sigmoid w (1 - s) (g - inner), the plain one g s (1 - s).
+template <int G, int J, int DT>
+__global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __restrict__ experts,
+                                                  const float* __restrict__ dw, void* __restrict__ d, int64_t ldd) {
+  const int64_t t = (blockIdx.x * (int64_t)256 + threadIdx.x) / G;
+  if (t >= a.T) return;  // whole groups
+  const int lane = threadIdx.x & (G - 1);
+  float x[J], g[J];
+  bool mine[J], bad = false;
+  load_scores<G, J, DT>(a, t, lane, x);
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    bad |= !(x[j] < INFINITY);
+    m = larger(m, x[j]);
+    g[j] = 0.0f, mine[j] = false;
+  }
+  for (int r = 0; r < a.k; ++r) {
+    const int e = experts[t * a.k + r] - lane * J;
+    const float v = dw[t * a.k + r];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (e == j) g[j] = v, mine[j] = true;
+  }
+  const int shift = (threadIdx.x & 63) & ~(G - 1);
+  constexpr uint64_t kGroup = G == 64 ? ~uint64_t(0) : (uint64_t(1) << G) - 1;
+  bad = (__ballot(bad) >> shift) & kGroup;
+  m = over_lanes<G>(m, larger);
+  m = m > -INFINITY ? m : 0.0f;
+  const bool sig = a.score == I8MP_SIGMOID;
+  float s[J], sum = 0.0f, inner = 0.0f;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    s[j] = sig ? sigmoid(x[j]) : expf(x[j] - m);
+    if (mine[j] || !(a.normalize || sig)) sum += s[j];
+    if (mine[j]) inner += g[j] * s[j];
+  }
+  sum = over_lanes<G>(sum, add);
+  inner = over_lanes<G>(inner, add);
+  const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+  inner *= r;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = lane * J + j;
+    if (e >= a.E) continue;
+    float v;
+    if (sig) {
+      const float slope = s[j] * (1.0f - s[j]);
+      v = !mine[j] ? 0.0f : a.normalize ? (g[j] - inner) * r * slope : g[j] * slope;
+    } else {
+      v = a.normalize && !mine[j] ? 0.0f : s[j] * r * (g[j] - inner);
+    }
+    store_float<DT>(d, t * ldd + e, bad ? NAN : v);
+  }
+}
+
+// ---- the weighted sums ------------------------------------------------------
+
+// Rows are read W elements at a time: 16 bytes, or one element.
+template <int DT, int W>
+__device__ __forceinline__ void read_chunk(const void* p, int64_t i, float (&v)[W]) {
+  if constexpr (W == 1) {
+    v[0] = load_as_float<DT>(p, i);
+  } else if constexpr (DT == I8MP_FP32) {
+    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (DT == I8MP_BF16) {
+        v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      } else {
+        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+        const h2 h = __builtin_bit_cast(h2, w[j]);
+        v[2 * j] = (float)h.x, v[2 * j + 1] = (float)h.y;
+      }
+    }
+  }
+}
+
+template <int DT, int W>
+__device__ __forceinline__ void write_chunk(void* p, int64_t i, const float (&v)[W]) {
+  if constexpr (W == 1) {
+    store_float<DT>(p, i, v[0]);
+  } else if constexpr (DT == I8MP_FP32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint16_t h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) store_float<DT>(h, j, v[j]);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = __builtin_bit_cast(uint4, h);
+  }
+}
+
+// A thread has one chunk of a token.
+template <int DT, int W>
+__global__ __launch_bounds__(256) void combine(CombineArgs a, int64_t chunks, int64_t first) {
+  const int64_t i = first + blockIdx.x * (int64_t)256 + threadIdx.x;
+  const int64_t t = i / chunks, c = (i - t * chunks) * W;
+  if (t >= a.T) return;
+  float s[W];
+  if (a.residual) {
+    read_chunk<DT, W>(a.residual, t * a.ldr + c, s);
+  } else {
+#pragma unroll
+    for (int j = 0; j < W; ++j) s[j] = 0.0f;
+  }
+#pragma unroll 4
+  for (int r = 0; r < a.k; ++r) {
+    const int64_t at = a.places[t * a.k + r];
+    if (at < 0 || at >= a.R) continue;
+    const float w = a.weights ? a.weights[t * a.k + r] : 1.0f;
+    float y[W];
+    read_chunk<DT, W>(a.Y, at * a.ldy + c, y);
+#pragma unroll
+    for (int j = 0; j < W; ++j) s[j] = __builtin_fmaf(w, y[j], s[j]);
+  }
+  write_chunk<DT, W>(a.out, t * a.ldo + c, s);
+}
+
+// A wave has one (token, choice): its row of dY and its weight's gradient; then, with `rows`, the
+// rows that nobody has.
+template <int DT, int W>
+__global__ __launch_bounds__(256) void combine_back(CombineArgs a, int64_t first) {
+  const int64_t i = first + blockIdx.x * (int64_t)4 + (threadIdx.x >> 6), pairs = a.T * a.k;
+  const int lane = threadIdx.x & 63;
+  if (i < pairs) {
+    const int64_t t = i / a.k, at = a.places[i];
+    const bool some = at >= 0 && at < a.R;
+    float dot = 0.0f;
+    if (some) {
+      const float w = a.weights ? a.weights[i] : 1.0f;
+      for (int64_t c = lane * W; c < a.N; c += 64 * W) {
+        float d[W], y[W];
+        read_chunk<DT, W>(a.dout, t * a.ldd + c, d);
+        if (a.dweights) {
+          read_chunk<DT, W>(a.Y, at * a.ldy + c, y);
+#pragma unroll
+          for (int j = 0; j < W; ++j) dot = __builtin_fmaf(d[j], y[j], dot);
+        }
+        if (a.dY) {
+#pragma unroll
+          for (int j = 0; j < W; ++j) d[j] *= w;
+          write_chunk<DT, W>(a.dY, at * a.ldg + c, d);
+        }
+      }
+    }
+    if (a.dweights) {
+      dot = over_lanes<64>(dot, add);
+      if (lane == 0) a.dweights[i] = dot;
+    }
+  } else if (a.rows && a.dY && i - pairs < a.R) {
+    const int64_t r = i - pairs;
+    if (a.rows[r] >= 0) return;
+    float z[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) z[j] = 0.0f;
+    for (int64_t c = lane * W; c < a.N; c += 64 * W) write_chunk<DT, W>(a.dY, r * a.ldg + c, z);
+  }
+}
+
+template <int G, int J, int DT>
+void choose_blocks(const RouteArgs& a, int64_t per, int blocks, hipStream_t stream) {
+  const size_t small = (size_t)(2 * a.E + 1) * 4, ranks = (size_t)kRouteWaves * a.E * 2;
+  if (blocks == 1) {
+    route_choose<G, J, DT, true><<<1, kRouteThreads, small + ranks, stream>>>(a, per);
+  } else {
+    route_choose<G, J, DT, false><<<(unsigned)blocks, kRouteThreads, small, stream>>>(a, per);
+    route_place<<<(unsigned)blocks, kRouteThreads, small + (size_t)a.E * 4 + ranks, stream>>>(a, per, blocks);
+  }
+}
+
+template <int DT>
+void route_as(const RouteArgs& a, int64_t per, int blocks, hipStream_t stream) {
+  if (a.E <= 64)
+    choose_blocks<16, 4, DT>(a, per, blocks, stream);
+  else if (a.E <= 256)
+    choose_blocks<16, 16, DT>(a, per, blocks, stream);
+  else
+    choose_blocks<64, 16, DT>(a, per, blocks, stream);
+}
+
+constexpr int64_t kMaxGrid = int64_t(1) << 23;  // workgroups of 256: fewer than 2^32 work items
+
+template <int DT>
+void route_back_as(const RouteArgs& a, const int32_t* experts, const float* dw, void* d, int64_t ldd, hipStream_t stream) {
+  if (a.E <= 64)
+    route_back<16, 4, DT><<<(unsigned)((a.T + 15) / 16), 256, 0, stream>>>(a, experts, dw, d, ldd);
+  else if (a.E <= 256)
+    route_back<16, 16, DT><<<(unsigned)((a.T + 15) / 16), 256, 0, stream>>>(a, experts, dw, d, ldd);
+  else
+    route_back<64, 16, DT><<<(unsigned)((a.T + 3) / 4), 256, 0, stream>>>(a, experts, dw, d, ldd);
+}
+
+template <int DT, int W>
+void combine_as(const CombineArgs& a, hipStream_t stream) {
+  const int64_t chunks = (a.N + W - 1) / W, n = (a.T * chunks + 255) / 256;
+  for (int64_t b = 0; b < n; b += kMaxGrid)
+    combine<DT, W><<<(unsigned)std::min(kMaxGrid, n - b), 256, 0, stream>>>(a, chunks, b * 256);
+}
+
+template <int DT, int W>
+void combine_back_as(const CombineArgs& a, hipStream_t stream) {
+  const int64_t n = (a.T * a.k + (a.rows && a.dY ? a.R : 0) + 3) / 4;
+  for (int64_t b = 0; b < n; b += kMaxGrid)
+    combine_back<DT, W><<<(unsigned)std::min(kMaxGrid, n - b), 256, 0, stream>>>(a, b * 4);
+}
+
+}  // namespace
+
+int64_t route_block_tokens(int64_t T) { return std::max(kRouteBlock, (T + kRouteMaxBlocks - 1) / kRouteMaxBlocks); }
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
+  const int64_t per = route_block_tokens(a.T);
+  const int blocks = (int)std::max<int64_t>(1, (a.T + per - 1) / per);
+  switch (a.dtype) {
+    case I8MP_BF16: route_as<I8MP_BF16>(a, per, blocks, stream); break;
+    case I8MP_FP16: route_as<I8MP_FP16>(a, per, blocks, stream); break;
+    default: route_as<I8MP_FP32>(a, per, blocks, stream);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_route_bwd(const RouteArgs& a, const int32_t* experts, const float* dw, void* d, int64_t ldd, hipStream_t stream) {
+  if (a.T == 0) return hipSuccess;
+  switch (a.dtype) {
+    case I8MP_BF16: route_back_as<I8MP_BF16>(a, experts, dw, d, ldd, stream); break;
+    case I8MP_FP16: route_back_as<I8MP_FP16>(a, experts, dw, d, ldd, stream); break;
+    default: route_back_as<I8MP_FP32>(a, experts, dw, d, ldd, stream);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const CombineArgs& a, hipStream_t stream) {
+  switch (2 * a.dtype + a.vec) {
+    case 2 * I8MP_BF16 + 1: combine_as<I8MP_BF16, 8>(a, stream); break;
+    case 2 * I8MP_BF16: combine_as<I8MP_BF16, 1>(a, stream); break;
+    case 2 * I8MP_FP16 + 1: combine_as<I8MP_FP16, 8>(a, stream); break;
+    case 2 * I8MP_FP16: combine_as<I8MP_FP16, 1>(a, stream); break;
+    case 2 * I8MP_FP32 + 1: combine_as<I8MP_FP32, 4>(a, stream); break;
+    default: combine_as<I8MP_FP32, 1>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_bwd(const CombineArgs& a, hipStream_t stream) {
+  switch (2 * a.dtype + a.vec) {
+    case 2 * I8MP_BF16 + 1: combine_back_as<I8MP_BF16, 8>(a, stream); break;
+    case 2 * I8MP_BF16: combine_back_as<I8MP_BF16, 1>(a, stream); break;
+    case 2 * I8MP_FP16 + 1: combine_back_as<I8MP_FP16, 8>(a, stream); break;
+    case 2 * I8MP_FP16: combine_back_as<I8MP_FP16, 1>(a, stream); break;
+    case 2 * I8MP_FP32 + 1: combine_back_as<I8MP_FP32, 4>(a, stream); break;
+    default: combine_back_as<I8MP_FP32, 1>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace i8mp

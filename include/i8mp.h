@@ -564,8 +564,8 @@ i8mp_status i8mp_quantize_block_weight(const uint16_t* W, int64_t E, int64_t N, 
  *   M: rows of Y and dY (and of X, unless rows is given)
  *   codes, exps: as written by i8mp_quantize_block_weight ([N][Kp] or [E][N][Kp])
  *   offsets: int32 or int64 (offset_bits) [experts + 1]
- *   rows: NULL, or int32 [M]: row r is X's row rows[r], of `tokens`; one outside
- *     them is a row of zeros
+ *   rows: NULL, or int32 [M]: row r is X's row rows[r], of `tokens` (at least 1); one
+ *     outside them is a row of zeros
  *   X: bf16 [tokens x K], rows 16-byte aligned
  *   Sizes: M < 2^28, N and K < 2^23, experts < 2^16.
  */

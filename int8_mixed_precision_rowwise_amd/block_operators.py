@@ -107,7 +107,7 @@ def _block(X, codes, exps, offsets, rows, K, N, M, dy=None, out=None, out_cols=0
         if offsets is not None:
             fine = fine and offsets.dtype in _OFFSETS and offsets.shape == (E + 1,) and offsets.is_contiguous()
         if rows is not None:
-            fine = fine and rows.dtype == _i32 and rows.shape == (M,) and rows.is_contiguous()
+            fine = fine and rows.dtype == _i32 and rows.shape == (M,) and rows.is_contiguous() and X.shape[0] > 0
         else:
             fine = fine and X.shape[0] == M
         if dy is not None:
@@ -146,6 +146,8 @@ def _block_checks(X, codes, exps, offsets, rows, K, N, M, E, dy, out, out_cols, 
         raise ValueError("offsets given without experts (codes are [N, K])")
     if rows is not None:
         _pkg._vec(rows, "rows", M, _i32)
+        if M and not X.shape[0]:
+            raise ValueError("X: at least one row expected where rows are read through an index")
     elif X.shape[0] != M:
         raise ValueError(f"X: {M} rows expected, got {tuple(X.shape)}")
     if dy is not None:

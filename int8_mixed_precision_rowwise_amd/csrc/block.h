@@ -84,6 +84,20 @@ __device__ __forceinline__ float inverse_scale(uint32_t byte) {
   return __uint_as_float(byte == 255u ? 0x7FC00000u : (254u - byte) << 23);
 }
 
+// 2^e (infinity for the byte 255, which makes codes that do not matter).
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Codes of four bf16 under one scale: the conversion divides by 2^e and rounds once (the same codes as x * 2^-e
+// converted, over every bf16 pattern and exponent).
+__device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float scale) {
+  typedef short s2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  s2 w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(b2, lo), scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(b2, hi), scale, true);
+  return __builtin_bit_cast(uint32_t, w);
+}
+
 }  // namespace
 #endif
 
@@ -134,8 +148,20 @@ struct BlockGemm {
   int64_t ldc, c_stride;
   Ragged rag;
   int clear;  // rows behind the last expert are written as zeros
+  // set by the launcher from the plan
+  uint32_t splits;
+  int64_t kchunk, plane, plane_ld;
+  float* planes;
 };
-hipError_t launch_block_gemm(BlockProduct what, const BlockGemm& g, hipStream_t stream);
+// Tile size and, for one matrix, the parts of the contraction (of kchunk each, a multiple of 128) and the pitch of
+// their planes.  rows, cols: C's; contraction as in BlockGemm (WEIGHT of one matrix: its rows); all_rows: ragged rows.
+struct BlockPlan {
+  bool big;
+  int64_t splits, kchunk, plane_ld;
+  size_t bytes(int64_t rows) const { return splits > 1 ? (size_t)(splits * rows * plane_ld) * 4 : 0; }
+};
+BlockPlan block_plan(BlockProduct what, int64_t rows, int64_t cols, int64_t contraction, int64_t E, int64_t all_rows);
+hipError_t launch_block_gemm(BlockProduct what, const BlockGemm& g, const BlockPlan& plan, float* planes, hipStream_t stream);
 
 // Few rows an expert against weight codes: bound by reading them, X quantized in the kernel.
 struct BlockFew {

@@ -30,8 +30,13 @@ bool block_dims_ok(int64_t M, int64_t N, int64_t K, int64_t E) {
 int64_t room16(int64_t M, int64_t E) { return E ? 16 * i8mp::ragged_units(M, E, 16) : pad16(M); }
 int64_t room128(int64_t M, int64_t E) { return E ? i8mp::ragged_units(M, E, kBlock) : blocks_of(M); }
 
+i8mp::BlockPlan plan_fwd(int64_t M, int64_t N, int64_t K, int64_t E) { return i8mp::block_plan(i8mp::kBlockForward, M, N, K, E, M); }
+i8mp::BlockPlan plan_dx(int64_t M, int64_t N, int64_t K, int64_t E) { return i8mp::block_plan(i8mp::kBlockInput, M, K, N, E, M); }
+i8mp::BlockPlan plan_dw(int64_t M, int64_t N, int64_t K, int64_t E) { return i8mp::block_plan(i8mp::kBlockWeight, N, K, M, E, M); }
+
 struct FwdWs {
   uint8_t *q, *s, *planes;
+  float* sums;
 };
 size_t carve_fwd(void* ws, int64_t M, int64_t N, int64_t K, int64_t E, FwdWs* out) {
   Carver c{static_cast<char*>(ws)};
@@ -39,6 +44,7 @@ size_t carve_fwd(void* ws, int64_t M, int64_t N, int64_t K, int64_t E, FwdWs* ou
   w.q = static_cast<uint8_t*>(c.take((size_t)(room16(M, E) * pad16(K))));
   w.s = static_cast<uint8_t*>(c.take((size_t)(blocks_of(K) * room16(M, E))));
   w.planes = static_cast<uint8_t*>(c.take((size_t)(std::max<int64_t>(E, 1) * blocks_of(K) * pad16(N))));
+  w.sums = static_cast<float*>(c.take(plan_fwd(M, N, K, E).bytes(M)));
   if (out) *out = w;
   return c.used;
 }
@@ -46,6 +52,7 @@ size_t carve_fwd(void* ws, int64_t M, int64_t N, int64_t K, int64_t E, FwdWs* ou
 struct BwdWs {
   uint8_t *q, *s, *planes;        // dY along N, the weights' exponents
   uint8_t *qd, *sd, *qx, *sx;     // dY and X down the rows
+  float* sums;                    // of one product after the other
 };
 size_t carve_bwd(void* ws, int64_t M, int64_t N, int64_t K, int64_t E, BwdWs* out) {
   Carver c{static_cast<char*>(ws)};
@@ -57,6 +64,7 @@ size_t carve_bwd(void* ws, int64_t M, int64_t N, int64_t K, int64_t E, BwdWs* ou
   w.sd = static_cast<uint8_t*>(c.take((size_t)(room128(M, E) * pad16(N))));
   w.qx = static_cast<uint8_t*>(c.take((size_t)(M * pad16(K))));
   w.sx = static_cast<uint8_t*>(c.take((size_t)(room128(M, E) * pad16(K))));
+  w.sums = static_cast<float*>(c.take(std::max(plan_dx(M, N, K, E).bytes(M), plan_dw(M, N, K, E).bytes(N))));
   if (out) *out = w;
   return c.used;
 }
@@ -86,7 +94,7 @@ i8mp_status block_inputs(const i8mp_block* p, bool need_w, bool need_x, BlockInp
   }
   if (need_x && M > 0 && K > 0) {
     if (p->rows) {
-      if (!aligned(p->rows, 4) || p->tokens < 0 || p->tokens >= kMaxRows) return I8MP_EINVAL;
+      if (!aligned(p->rows, 4) || p->tokens < 1 || p->tokens >= kMaxRows) return I8MP_EINVAL;
       in.rows = vec_range(p->rows, M, 4);
     } else if (p->tokens != M) {
       return I8MP_EINVAL;
@@ -211,7 +219,7 @@ i8mp_status i8mp_block_fwd(const i8mp_block* p, uint16_t* Y, int64_t ldy, int32_
   g.A = w.q, g.sA = w.s, g.lda = pad16(K), g.ldsa = room16(M, E);
   g.B = p->codes, g.sB = w.planes, g.ldb = pad16(K), g.ldsb = pad16(N), g.b_stride = N * pad16(K), g.sb_stride = blocks_of(K) * pad16(N);
   g.C = Y, g.ldc = ldy, g.rag = rag, g.clear = clear != 0;
-  return hip_status(i8mp::launch_block_gemm(i8mp::kBlockForward, g, s));
+  return hip_status(i8mp::launch_block_gemm(i8mp::kBlockForward, g, plan_fwd(M, N, K, E), w.sums, s));
 }
 
 i8mp_status i8mp_block_bwd(const i8mp_block* p, const uint16_t* dY, int64_t lddy, uint16_t* dX, int64_t lddx, uint16_t* dW,
@@ -256,7 +264,7 @@ i8mp_status i8mp_block_bwd(const i8mp_block* p, const uint16_t* dY, int64_t lddy
     g.A = w.q, g.sA = w.s, g.lda = np, g.ldsa = room16(M, E);
     g.B = p->codes, g.sB = w.planes, g.ldb = kp, g.ldsb = kp, g.b_stride = N * kp, g.sb_stride = blocks_of(N) * kp;
     g.C = dX, g.ldc = lddx, g.clear = clear != 0;
-    const hipError_t e = i8mp::launch_block_gemm(i8mp::kBlockInput, g, s);
+    const hipError_t e = i8mp::launch_block_gemm(i8mp::kBlockInput, g, plan_dx(M, N, K, E), w.sums, s);
     if (e != hipSuccess) return hip_status(e);
   }
   if (some_dw) {
@@ -264,7 +272,7 @@ i8mp_status i8mp_block_bwd(const i8mp_block* p, const uint16_t* dY, int64_t lddy
     g.A = w.qd, g.sA = w.sd, g.lda = np, g.ldsa = np;
     g.B = w.qx, g.sB = w.sx, g.ldb = kp, g.ldsb = kp, g.b_stride = 0, g.sb_stride = 0;
     g.C = dW, g.ldc = lddw, g.c_stride = N * lddw;
-    return hip_status(i8mp::launch_block_gemm(i8mp::kBlockWeight, g, s));
+    return hip_status(i8mp::launch_block_gemm(i8mp::kBlockWeight, g, plan_dw(M, N, K, E), w.sums, s));
   }
   return I8MP_OK;
 }

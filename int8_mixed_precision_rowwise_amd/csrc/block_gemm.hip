@@ -12,59 +12,92 @@
 namespace i8mp {
 namespace {
 
-// The tile of a workgroup among the rows that the experts have: tiles of BM rows, expert after
-// expert.  Every wave adds up the experts' tiles by itself (64 experts at a time).
-struct RaggedTile {
-  int64_t tiles;  // of all experts
-  Place p;        // of tile `tm`, if tm < tiles
-};
+// The tiles of the experts' rows: tiles of BM rows, expert after expert.  Every wave adds up the
+// experts' tiles by itself, 64 experts at a time.
+template <int BM>
+__device__ __forceinline__ int tiles_at(const Ragged& r, int64_t e) {
+  return e < r.E ? (int)(max((int64_t)0, offset_at(r, e + 1) - offset_at(r, e) + BM - 1) / BM) : 0;
+}
 
 template <int BM>
-__device__ __forceinline__ int64_t ragged_tiles(const Ragged& r) {
-  if (!r.off) return (r.rows + BM - 1) / BM;
-  int64_t n = 0;
-  for (int64_t e = threadIdx.x & 63; e < r.E; e += 64) n += max((int64_t)0, offset_at(r, e + 1) - offset_at(r, e) + BM - 1) / BM;
+__device__ __forceinline__ int ragged_tiles(const Ragged& r) {
+  if (!r.off) return (int)((r.rows + BM - 1) / BM);
+  int n = 0;
+  for (int64_t e = threadIdx.x & 63; e < r.E; e += 64) n += tiles_at<BM>(r, e);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
   return n;
 }
 
+__device__ __forceinline__ void expert_rows(const Ragged& r, int64_t e, Place& p) {
+  p.e = e, p.first = 0, p.count = r.rows, p.local = 0;
+  if (!r.off) return;
+  p.first = offset_at(r, e);
+  p.count = max((int64_t)0, offset_at(r, e + 1) - p.first);
+}
+
+// Where row tile tm lies.
 template <int BM>
-__device__ __forceinline__ void ragged_place(const Ragged& r, int64_t tm, Place& p) {
-  if (!r.off) {
-    p.e = 0, p.first = 0, p.count = r.rows, p.local = tm * BM;
-    return;
-  }
+__device__ __forceinline__ void ragged_place(const Ragged& r, int tm, Place& p) {
+  expert_rows(r, 0, p);
+  p.local = (int64_t)tm * BM;
+  if (!r.off) return;
   const int lane = threadIdx.x & 63;
-  int64_t before = 0;  // tiles of the experts before this turn's 64
+  int before = 0;  // tiles of the experts before this turn's 64
   for (int64_t e0 = 0; e0 < r.E; e0 += 64) {
-    const int64_t e = e0 + lane;
-    int64_t n = e < r.E ? max((int64_t)0, offset_at(r, e + 1) - offset_at(r, e) + BM - 1) / BM : 0;
+    int n = tiles_at<BM>(r, e0 + lane);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int64_t up = __shfl_up(n, o);
+      const int up = __shfl_up(n, o);
       if (lane >= o) n += up;
     }
     const uint64_t past = __ballot(before + n > tm);
     if (past) {
       const int at = __builtin_ctzll(past);
-      const int64_t start = at ? before + __shfl(n, at - 1) : before;
-      p.e = e0 + at;
-      p.first = offset_at(r, p.e);
-      p.count = offset_at(r, p.e + 1) - p.first;
-      p.local = (tm - start) * BM;
+      const int start = at ? before + __shfl(n, at - 1) : before;
+      expert_rows(r, e0 + at, p);
+      p.local = (int64_t)(tm - start) * BM;
       return;
     }
     before += __shfl(n, 63);
   }
-  p.e = 0, p.first = 0, p.count = 0, p.local = 0;  // not reached: tm is one of the experts' tiles
+  p.count = 0;  // not reached: tm is one of the experts' tiles
 }
 
-// Consecutive workgroups go to the 8 XCDs in turn; each XCD gets a contiguous run of n tiles.
-__device__ __forceinline__ int64_t xcd_run(int64_t wg, int64_t n) {
-  const int64_t x = wg & 7;
-  return x * (n >> 3) + min(x, n & 7) + (wg >> 3);
+// The i-th expert in falling order of rows (up to 64 experts; more: the i-th): the products that
+// contract over an expert's rows start with the longest.
+__device__ __forceinline__ int64_t by_size(const Ragged& r, int64_t i) {
+  if (!r.off || r.E > 64) return i;
+  const int lane = threadIdx.x & 63;
+  const int n = lane < r.E ? (int)max((int64_t)0, offset_at(r, lane + 1) - offset_at(r, lane)) : -1;
+  int rank = 0;
+  for (int l = 0; l < (int)r.E; ++l) {
+    const int other = __builtin_amdgcn_readlane(n, l);
+    rank += other > n || (other == n && l < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < r.E && rank == (int)i));
 }
+
+// Consecutive workgroups go to the 8 XCDs in turn.  Runs of kRun tiles go to one XCD, so that they share
+// panels in its L2; the XCDs take the runs in turn, so that experts of different sizes load them alike.
+// (With an eighth of all tiles to each, the dW of 16384 rows of 8 experts took 346 us, and 222 so.)
+constexpr uint32_t kRun = 32;
+__device__ __forceinline__ uint32_t xcd_runs(uint32_t wg, uint32_t n) {
+  const uint32_t whole = n / (8 * kRun) * (8 * kRun);
+  if (wg < whole) {
+    const uint32_t x = wg & 7, i = wg >> 3;
+    return (i / kRun * 8 + x) * kRun + i % kRun;
+  }
+  // the rest: each XCD a run of what is left
+  const uint32_t m = n - whole, k = wg - whole, x = k & 7;
+  return whole + x * (m >> 3) + min(x, m & 7) + (k >> 3);
+}
+
+// Tiles of 256 x 256, one to a CU at a time; a last round with at most a quarter of the CUs' number is
+// cut into quarter tiles, which together fill the CUs once (a quarter takes 0.42 to 0.47 of a whole one's
+// time).
+constexpr uint32_t kCUs = 256;
+__host__ __device__ inline uint32_t whole_tiles(uint32_t n) { return n % kCUs <= kCUs / 4 ? n - n % kCUs : n; }
 
 // bf16 of 32 x 32 accumulators through LDS, whole rows at a time (or element by element where
 // C's rows do not start every 16 bytes).
@@ -104,101 +137,176 @@ __device__ __forceinline__ void store_rows(const v16f (&acc)[TM][TN], int8_t* mi
   }
 }
 
-// Exponents of four blocks of one tile's rows and columns, (kind, block) at bytes
-// (4 kind + block) * BM of the buffer: each wave loads 256 of its bytes.
-template <int BM, int NW>
-struct Exponents {
-  const uint8_t* base;
-  int64_t ld, left;  // plane pitch, bytes from base to the end of the planes
-  int64_t first;     // of this lane within four planes
-  __device__ __forceinline__ void init(const uint8_t* a, int64_t lda, const uint8_t* b, int64_t ldb, int64_t a0, int64_t b0,
-                                       int64_t blocks, int wave, int lane) {
-    const bool is_b = wave >= NW / 2;
-    const int k = NW == 8 ? wave & 3 : 2 * (wave & 1) + (lane >> 5);
-    base = is_b ? b + b0 : a + a0;
-    ld = is_b ? ldb : lda;
-    left = blocks * ld - (is_b ? b0 : a0);
-    first = k * ld + 4 * (NW == 8 ? lane : lane & 31);
+template <int BM>
+constexpr int kLdsBytes = BM == 256 ? 4 * 512 * BK + 4096 : 4 * 256 * BK + 2048;
+
+// Slab loads of one operand, as Dma (gemm_pipelined.h) with less state in registers: a lane's chunks of a
+// slab's loads lie a fixed step apart (and, in tiles read down their rows, swap neighbours with every
+// second load of four waves).  Rows or columns past the operand are not looked at: a K-major operand's
+// lie past the descriptor's end and arrive as zeros, the others' are the next row's bytes or zeros, and
+// either only reach outputs that are not stored.
+template <int R, bool KMAJOR, int NW, bool REBASE>
+struct Slabs {
+  static constexpr int kInst = R * BK / 1024 / NW;
+  static constexpr int CPR = R / 16, KR = 64 / CPR;               // [k][n] tiles: chunks a row, rows a load
+  static constexpr bool kSwap = !KMAJOR && kInst > 1 && (NW * KR) % 32 == 16;
+  static_assert(KMAJOR || kInst == 1 || (NW * KR) % 16 == 0, "the swizzle repeats from load to load");
+  v4u rsrc;
+  uint32_t off, at;  // this lane's chunk in slab 0; its contraction index within a slab
+  int swap;          // what a swapped chunk's offset differs by
+  uint32_t step, ld;
+  const int8_t* base;
+  int64_t bytes;
+
+  __device__ __forceinline__ void init(const int8_t* p, int64_t ld_, int64_t mn0, int64_t MN, int64_t K, int wave, int lane) {
+    ld = (uint32_t)ld_;
+    swap = 0;
+    if constexpr (KMAJOR) {
+      base = p + mn0 * ld_;
+      bytes = min((int64_t)R, MN - mn0) * ld_;
+      const int c = (lane & 3) ^ ((lane >> 4) & 3);
+      at = 16 * c;
+      off = (16 * wave + (lane >> 2)) * ld + at;
+      step = 16 * NW * ld;
+    } else {
+      base = p + mn0;
+      bytes = (K - 1) * ld_ + min((int64_t)R, MN - mn0);
+      const int k = wave * KR + lane / CPR, c = (lane % CPR) ^ mnmajor_swz(R, k);
+      at = k;
+      off = k * ld + 16 * c;
+      if constexpr (kSwap) swap = c & 1 ? -16 : 16;
+      step = NW * KR * ld;
+    }
+    rsrc = Dma<64, true, NW>::make_rsrc(base, min(bytes, (int64_t)kOob));
   }
-  __device__ __forceinline__ void issue(int8_t* buf, int64_t group, int wave) const {
-    const int64_t skip = 4 * group * ld;
-    const v4u r = Dma<64, true, NW>::make_rsrc(reinterpret_cast<const int8_t*>(base + skip),
-                                               max((int64_t)0, min(left - skip, (int64_t)kOob)));
-    const uint32_t o = (uint32_t)first;
+  __device__ __forceinline__ void load(uint32_t o, const v4u& r, int8_t* dst, int j, int wave) const {
     const uint32_t l = (uint32_t)__builtin_amdgcn_readfirstlane(
-        (uint32_t)reinterpret_cast<uintptr_t>((lds_void*)(buf + wave * 256)));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+        (uint32_t)reinterpret_cast<uintptr_t>((lds_void*)(dst + (wave + NW * j) * 1024)));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(l), "v"(o), "s"(r)
                  : "memory", "m0");
   }
+  __device__ __forceinline__ void issue_one(int j, int8_t* dst, int slab, int64_t K, int wave) const {
+    const int64_t k0 = (int64_t)BK * slab;
+    const int limit = (int)min(K - k0, (int64_t)BK) - (KMAJOR ? 0 : NW * KR * j);
+    // the part that is the same in all lanes, added up in scalar registers
+    uint32_t ahead = j * step;
+    v4u r = rsrc;
+    if constexpr (REBASE && !KMAJOR) {
+      const int64_t sh = k0 * ld;
+      r = Dma<64, true, NW>::make_rsrc(base + sh, max((int64_t)0, min(bytes - sh, (int64_t)kOob)));
+    } else {
+      ahead += (uint32_t)k0 * (KMAJOR ? 1u : ld);
+    }
+    uint32_t o = off + (uint32_t)__builtin_amdgcn_readfirstlane(ahead);
+    if constexpr (kSwap) o += j & 1 ? swap : 0;
+    load((int)at < limit ? o : kOob, r, dst, j, wave);
+  }
+  __device__ __forceinline__ void issue(int8_t* dst, int slab, int64_t K, int wave) const {
+#pragma unroll
+    for (int j = 0; j < kInst; ++j) issue_one(j, dst, slab, K, wave);
+  }
+  // For a slab past the contraction, so that it counts in the waits: zeros into a buffer nobody reads.
+  __device__ __forceinline__ void issue_past_end(int j, int8_t* dst, int wave) const { load(kOob, rsrc, dst, j, wave); }
 };
 
-template <int BM, int WGN, BlockProduct WHAT, bool REBASE, bool VEC>
-__global__ __launch_bounds__(128 * WGN) void block_gemm(BlockGemm g) {
-  constexpr int BN = BM, NW = 2 * WGN, NT = 64 * NW;
-  constexpr int WM = BM / 2, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
+// Exponents of four blocks of one tile's rows (4 BM bytes, block after block) and columns (4 BN bytes
+// behind them): 256 bytes a load.
+template <int BM, int BN, int NW>
+struct Exponents {
+  static constexpr int kLoads = (BM + BN) / 64, kMine = (kLoads + NW - 1) / NW;  // of the workgroup, of a wave at most
+  const uint8_t *a, *b;         // at the tile's first row and column of the planes
+  int64_t lda, ldb, enda, endb; // plane pitches, bytes to the end of the planes
+  __device__ __forceinline__ void init(const uint8_t* sa, int64_t la, const uint8_t* sb, int64_t lb, int64_t a0, int64_t b0, int64_t blocks) {
+    a = sa + a0, b = sb + b0, lda = la, ldb = lb;
+    enda = blocks * la - a0, endb = blocks * lb - b0;
+  }
+  __device__ __forceinline__ void issue(int8_t* buf, int64_t group, int wave, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int load = wave + NW * i;
+      if (load >= kLoads) break;
+      const bool is_b = load >= BM / 64;
+      const int R = is_b ? BN : BM, k = (is_b ? load - BM / 64 : load) * (256 / R) + lane / (R / 4);
+      const int64_t ld = is_b ? ldb : lda, skip = 4 * group * ld, left = (is_b ? endb : enda) - skip;
+      const v4u r = Dma<64, true, NW>::make_rsrc(reinterpret_cast<const int8_t*>((is_b ? b : a) + skip),
+                                                 max((int64_t)0, min(left, (int64_t)kOob)));
+      const uint32_t o = (uint32_t)(k * ld + 4 * (lane % (R / 4)));
+      const uint32_t l = (uint32_t)__builtin_amdgcn_readfirstlane(
+          (uint32_t)reinterpret_cast<uintptr_t>((lds_void*)(buf + load * 256)));
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                   :
+                   : "s"(l), "v"(o), "s"(r)
+                   : "memory", "m0");
+    }
+  }
+};
+
+// The sums themselves, into a plane of partial sums (rows `ld` apart, a multiple of 4).
+template <int TM, int TN>
+__device__ __forceinline__ void store_sums(const v16f (&acc)[TM][TN], float* __restrict__ C, int64_t ld, int64_t rows, int64_t cols,
+                                           int lane) {
+  const int mr = lane & 31, nq = 4 * (lane >> 5);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    if (32 * i + mr >= rows) continue;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = 32 * j + 8 * q + nq;  // columns up to the next multiple of 4 are the plane's
+        if (n < cols)
+          *reinterpret_cast<float4*>(C + (32 * i + mr) * ld + n) =
+              make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+      }
+  }
+}
+
+// One tile: rows p.local on of the expert (WEIGHT: columns p.local on of A), columns n0 on; part `split` of the
+// contraction.
+template <int BM, int BN, int WR, int WGN, int STAGES, BlockProduct WHAT, bool REBASE, bool VEC>
+__device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int64_t n0, uint32_t split, int8_t* lds) {
+  constexpr int NW = WR * WGN;
+  constexpr int WM = BM / WR, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
   constexpr bool AK = WHAT != kBlockWeight, BKM = WHAT == kBlockForward;
   constexpr int A_BYTES = BM * BK, SLAB = A_BYTES + BN * BK;
-  constexpr int EXPS = 8 * BM;  // bytes of four blocks' exponents
-  typedef Dma<BM, AK, NW, REBASE && !AK> DA;
-  typedef Dma<BN, BKM, NW, REBASE && !BKM> DB;
+  constexpr int EXPS = 4 * (BM + BN);  // bytes of four blocks' exponents
+  typedef Slabs<BM, AK, NW, REBASE> DA;
+  typedef Slabs<BN, BKM, NW, REBASE> DB;
   constexpr int NA = DA::kInst, PER = NA + DB::kInst;
   using S = SlabSchedule<TM, TN, PER>;
   static_assert(NW * WM * WN * 2 <= STAGES * SLAB, "the outputs fit where the slabs were");
-  __shared__ __attribute__((aligned(1024))) int8_t lds[STAGES * SLAB + 2 * EXPS];
+  static_assert(STAGES * SLAB + 2 * EXPS <= kLdsBytes<NW == 8 ? 256 : 128>, "room in LDS");
   int8_t* const exps = lds + STAGES * SLAB;
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
 
-  const int64_t tiles_n = (g.cols_out + BN - 1) / BN;
-  int64_t tiles_m, tm, tn, wg = blockIdx.x;
-  Place p;
-  if constexpr (WHAT == kBlockWeight) {
-    tiles_m = (g.rows_out + BM - 1) / BM;
-    const int64_t each = tiles_m * tiles_n;
-    wg = xcd_run(wg, gridDim.x);
-    p.e = wg / each;
-    wg -= p.e * each;
-    p.local = 0, p.first = 0, p.count = g.rag.rows;
-    if (g.rag.off) {
-      p.first = offset_at(g.rag, p.e);
-      p.count = max((int64_t)0, offset_at(g.rag, p.e + 1) - p.first);
-    }
-  } else {
-    tiles_m = ragged_tiles<BM>(g.rag);
-    if (g.clear && g.rag.off) {
-      for (int64_t r = offset_at(g.rag, g.rag.E) + wg; r < g.rag.rows; r += gridDim.x)
-        for (int64_t c = t; c < g.cols_out; c += NT) g.C[r * g.ldc + c] = 0;
-    }
-    if (wg >= tiles_m * tiles_n) return;
-    wg = xcd_run(wg, tiles_m * tiles_n);
-  }
-  {  // groups of 4 tile rows, so that the tiles of an XCD share panels in its L2
-    const int64_t group = wg / (4 * tiles_n), first = 4 * group, rows = min(tiles_m - first, (int64_t)4);
-    const int64_t in = wg - group * 4 * tiles_n;
-    tm = first + in % rows;
-    tn = in / rows;
-  }
-  int64_t K = g.contraction, a_rows, c_rows;  // contraction; rows of A in this tile's operand; C's rows in this tile
+  int64_t K = g.contraction, m0, a_rows, c_rows;  // first and last of A's rows (columns), rows of C from here on
   const int8_t *A = reinterpret_cast<const int8_t*>(g.A), *B = reinterpret_cast<const int8_t*>(g.B);
   const uint8_t *sA = g.sA, *sB = g.sB;
-  int64_t m0 = tm * BM, n0 = tn * BN;
   uint16_t* C = g.C + n0;
   if constexpr (WHAT == kBlockWeight) {
     K = p.count;
     A += p.first * g.lda, B += p.first * g.ldb;
     sA += unit_of<kBlock>(p) * g.ldsa, sB += unit_of<kBlock>(p) * g.ldsb;
-    a_rows = g.lda;
-    c_rows = g.rows_out - m0;
-    C += p.e * g.c_stride + m0 * g.ldc;
+    m0 = p.local, a_rows = g.lda;
+    c_rows = g.rows_out - p.local;
+    C += p.e * g.c_stride + p.local * g.ldc;
   } else {
-    ragged_place<BM>(g.rag, tm, p);
     m0 = 16 * unit_of<16>(p) + p.local;
-    a_rows = m0 + p.count - p.local;
     c_rows = p.count - p.local;
+    a_rows = m0 + c_rows;
     B += p.e * g.b_stride, sB += p.e * g.sb_stride;
     C += (p.first + p.local) * g.ldc;
+  }
+  constexpr bool CAN_SPLIT = NW == 4;
+  if (CAN_SPLIT && g.splits > 1) {  // one matrix
+    const int64_t k0 = split * g.kchunk;
+    K = min(g.kchunk, K - k0);
+    A += AK ? k0 : k0 * g.lda;
+    B += BKM ? k0 : k0 * g.ldb;
+    sA += k0 / kBlock * g.ldsa, sB += k0 / kBlock * g.ldsb;
   }
   const int wm0 = (wave / WGN) * WM, wn0 = (wave % WGN) * WN;
   const int nk = (int)((K + BK - 1) / BK);
@@ -215,17 +323,17 @@ __global__ __launch_bounds__(128 * WGN) void block_gemm(BlockGemm g) {
     DB db;
     da.init(A, g.lda, m0, a_rows, K, wave, lane);
     db.init(B, g.ldb, n0, BKM ? g.cols_out : g.ldb, K, wave, lane);
-    Exponents<BM, NW> ex;
-    ex.init(sA, g.ldsa, sB, g.ldsb, m0, n0, blocks, wave, lane);
+    Exponents<BM, BN, NW> ex;
+    ex.init(sA, g.ldsa, sB, g.ldsb, m0, n0, blocks);
 
     v8i a[TM], b0[TN], b1[TN];
     int ea[TM], eb[TN], na[TM], nb[TN];  // exponents of this block and the next
     const auto read_exps = [&](int block) __attribute__((always_inline)) {
-      const int8_t* at = exps + ((block >> 2) & 1) * EXPS + (block & 3) * BM + (lane & 31);
+      const int8_t* at = exps + ((block >> 2) & 1) * EXPS + (lane & 31);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) na[i] = *reinterpret_cast<const uint8_t*>(at + wm0 + 32 * i);
+      for (int i = 0; i < TM; ++i) na[i] = *reinterpret_cast<const uint8_t*>(at + (block & 3) * BM + wm0 + 32 * i);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) nb[j] = *reinterpret_cast<const uint8_t*>(at + 4 * BM + wn0 + 32 * j);
+      for (int j = 0; j < TN; ++j) nb[j] = *reinterpret_cast<const uint8_t*>(at + 4 * BM + (block & 3) * BN + wn0 + 32 * j);
     };
     const auto next_exps = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -239,7 +347,7 @@ __global__ __launch_bounds__(128 * WGN) void block_gemm(BlockGemm g) {
     };
     // A group of exponents goes out ahead of the slab that starts it, so it has landed whenever that
     // slab has; the waits below count slab loads and are at most stricter for the loads between them.
-    ex.issue(exps, 0, wave);
+    ex.issue(exps, 0, wave, lane);
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
       da.issue(lds + s * SLAB, s, K, wave);
@@ -257,9 +365,11 @@ __global__ __launch_bounds__(128 * WGN) void block_gemm(BlockGemm g) {
     // One slab, as in gemm_pipelined.h: slab kt is multiplied from registers while slab kt + 1 is read
     // from LDS and slab kt + STAGES goes into slab kt's place.  ODD: the second half of a block, which
     // reads the next block's exponents.
+    int stage = 0;  // slab kt's place
     auto slab = [&](v8i(&bc)[TN], v8i(&bn)[TN], int kt, bool odd, bool tail) __attribute__((always_inline)) {
-      const int8_t* nxt = lds + ((kt + 1) % STAGES) * SLAB;
-      int8_t* dst = lds + (kt % STAGES) * SLAB;
+      int8_t* dst = lds + stage * SLAB;
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      const int8_t* nxt = lds + stage * SLAB;
       const int ns = kt + STAGES;
 #pragma unroll
       for (int m = 0; m < S::HA; ++m) {
@@ -269,7 +379,7 @@ __global__ __launch_bounds__(128 * WGN) void block_gemm(BlockGemm g) {
       __builtin_amdgcn_s_waitcnt(waitcnt_vm((STAGES - 2) * PER));  // slab kt + 1 has landed
       lds_barrier();
       if (odd) read_exps((kt + 1) >> 1);
-      if (!tail && (ns & 7) == 0 && ns < nk) ex.issue(exps + ((ns >> 3) & 1) * EXPS, ns >> 3, wave);
+      if (!tail && (ns & 7) == 0 && ns < nk) ex.issue(exps + ((ns >> 3) & 1) * EXPS, ns >> 3, wave, lane);
 #pragma unroll
       for (int m = S::HA; m < S::NM; ++m) {
         mma(bc[m % TN], a[m / TN], m / TN, m % TN);
@@ -308,58 +418,171 @@ __global__ __launch_bounds__(128 * WGN) void block_gemm(BlockGemm g) {
     for (int m = 0; m < S::NM; ++m) mma(odd ? b1[m % TN] : b0[m % TN], a[m / TN], m / TN, m % TN);
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));  // the trailing loads land before their place is used again
   }
+  if (CAN_SPLIT && g.splits > 1) {
+    const int64_t row = p.local + wm0, col = n0 + wn0;
+    store_sums<TM, TN>(acc, g.planes + split * g.plane + row * g.plane_ld + col, g.plane_ld, c_rows - wm0, g.cols_out - col, lane);
+    return;
+  }
   __syncthreads();
   store_rows<TM, TN, VEC>(acc, lds + wave * (WM * WN * 2), C + wm0 * g.ldc + wn0, g.ldc, c_rows - wm0, g.cols_out - n0 - wn0, lane);
 }
 
-template <int BM, int WGN, BlockProduct WHAT>
-void launch(const BlockGemm& g, bool rebase, bool vec, unsigned grid, hipStream_t stream) {
-  constexpr bool CAN = WHAT != kBlockForward;  // an operand read down its rows
-  if (CAN && rebase) {
-    if (vec)
-      block_gemm<BM, WGN, WHAT, CAN, true><<<grid, 128 * WGN, 0, stream>>>(g);
-    else
-      block_gemm<BM, WGN, WHAT, CAN, false><<<grid, 128 * WGN, 0, stream>>>(g);
-  } else if (vec) {
-    block_gemm<BM, WGN, WHAT, false, true><<<grid, 128 * WGN, 0, stream>>>(g);
+// The parts' sums added in order, rounded once.
+__global__ __launch_bounds__(256) void add_planes(BlockGemm g, int64_t rows) {
+  const uint32_t quads = (uint32_t)(g.plane_ld / 4);
+  const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x, r = i / quads, n = (i - r * quads) * 4;
+  if (r >= rows) return;
+  const float* at = g.planes + r * g.plane_ld + n;
+  float4 s = *reinterpret_cast<const float4*>(at);
+  for (int64_t k = 1; k < g.splits; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(at + k * g.plane);
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  __bf16* c = reinterpret_cast<__bf16*>(g.C) + r * g.ldc + n;
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < g.cols_out) c[e] = (__bf16)v[e];  // round to nearest even
+}
+
+template <int BM, BlockProduct WHAT, bool REBASE, bool VEC>
+__global__ __launch_bounds__(BM == 256 ? 512 : 256, 2) void block_gemm(BlockGemm g) {
+  constexpr int BN = BM, NT = BM == 256 ? 512 : 256;
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kLdsBytes<BM>];
+  const uint32_t wg = blockIdx.x, tiles_n = (uint32_t)((g.cols_out + BN - 1) / BN);
+  uint32_t tiles_m;
+  if constexpr (WHAT == kBlockWeight) {
+    tiles_m = (uint32_t)(g.rag.E * ((g.rows_out + BM - 1) / BM));  // of all experts
   } else {
-    block_gemm<BM, WGN, WHAT, false, false><<<grid, 128 * WGN, 0, stream>>>(g);
+    tiles_m = ragged_tiles<BM>(g.rag);
+    if (g.clear && g.rag.off) {
+      for (int64_t r = offset_at(g.rag, g.rag.E) + wg; r < g.rag.rows; r += gridDim.x)
+        for (int64_t c = threadIdx.x; c < g.cols_out; c += NT) g.C[r * g.ldc + c] = 0;
+    }
+  }
+  const uint32_t each = tiles_m * tiles_n, all = each * (BM == 128 ? g.splits : 1), whole = BM == 256 ? whole_tiles(all) : all;
+  uint32_t tile, quarter = 0;
+  if (wg < whole) {
+    tile = xcd_runs(wg, whole);
+  } else {  // the quarters of a tile to one XCD
+    const uint32_t i = wg - whole;
+    tile = whole + i / 32 * 8 + (i & 7);
+    quarter = i / 8 & 3;
+    if (tile >= all) return;
+  }
+  // the parts of the contraction one after another: an XCD's run of tiles reads the same part
+  const uint32_t split = BM == 128 && g.splits > 1 ? tile / each : 0;
+  tile -= split * each;
+  // groups of 4 tile rows (of an expert's tile rows), so that the tiles of an XCD share panels in its L2
+  int64_t e = 0;
+  if constexpr (WHAT == kBlockWeight) {
+    tiles_m = (uint32_t)((g.rows_out + BM - 1) / BM);
+    e = tile / (tiles_m * tiles_n);
+    tile -= (uint32_t)e * tiles_m * tiles_n;
+  }
+  const uint32_t group = tile / (4 * tiles_n), first = 4 * group, rows = min(tiles_m - first, 4u), in = tile - group * 4 * tiles_n;
+  const uint32_t tm = first + in % rows, tn = in / rows;
+  Place p;
+  if constexpr (WHAT == kBlockWeight) {
+    expert_rows(g.rag, by_size(g.rag, e), p);
+    p.local = (int64_t)tm * BM;
+  } else {
+    ragged_place<BM>(g.rag, tm, p);
+  }
+  int64_t n0 = (int64_t)tn * BN;
+  if constexpr (BM == 256) {
+    if (wg < whole) {
+      multiply<256, 256, 2, 4, 4, WHAT, REBASE, VEC>(g, p, n0, split, lds);
+    } else {
+      p.local += quarter & 1 ? 128 : 0;
+      n0 += quarter & 2 ? 128 : 0;
+      if (p.local >= (WHAT == kBlockWeight ? g.rows_out : p.count) || n0 >= g.cols_out) return;
+      multiply<128, 128, 2, 4, 8, WHAT, REBASE, VEC>(g, p, n0, split, lds);
+    }
+  } else {
+    multiply<128, 128, 2, 2, 4, WHAT, REBASE, VEC>(g, p, n0, split, lds);
   }
 }
 
+template <int BM, BlockProduct WHAT>
+void launch(const BlockGemm& g, bool rebase, bool vec, int64_t grid, hipStream_t stream) {
+  constexpr bool CAN = WHAT != kBlockForward;  // an operand read down its rows
+  constexpr int NT = BM == 256 ? 512 : 256;
+  if (CAN && rebase) {
+    if (vec)
+      block_gemm<BM, WHAT, CAN, true><<<(unsigned)grid, NT, 0, stream>>>(g);
+    else
+      block_gemm<BM, WHAT, CAN, false><<<(unsigned)grid, NT, 0, stream>>>(g);
+  } else if (vec) {
+    block_gemm<BM, WHAT, false, true><<<(unsigned)grid, NT, 0, stream>>>(g);
+  } else {
+    block_gemm<BM, WHAT, false, false><<<(unsigned)grid, NT, 0, stream>>>(g);
+  }
+}
+
+// At most: how many the experts' rows make, only the GPU knows.
+int64_t tiles_of(BlockProduct what, int64_t rows, int64_t cols, int64_t E, bool ragged, int64_t b) {
+  const int64_t tn = (cols + b - 1) / b;
+  if (what == kBlockWeight) return E * ((rows + b - 1) / b) * tn;
+  return (ragged ? ragged_units(rows, E, b) : (rows + b - 1) / b) * tn;
+}
+
 template <BlockProduct WHAT>
-hipError_t launch_tiles(const BlockGemm& g, hipStream_t stream) {
+hipError_t launch_tiles(const BlockGemm& g, const BlockPlan& plan, hipStream_t stream) {
   const bool ragged = g.rag.off != nullptr;
-  const int64_t E = ragged ? g.rag.E : 1;
-  const auto grid_of = [&](int64_t b) {
-    const int64_t tn = (g.cols_out + b - 1) / b;
-    if (WHAT == kBlockWeight) return E * ((g.rows_out + b - 1) / b) * tn;
-    return (ragged ? ragged_units(g.rag.rows, E, b) : (g.rag.rows + b - 1) / b) * tn;
-  };
   // bytes that an operand read down its rows spans
   const int64_t down = WHAT == kBlockForward ? 0 : WHAT == kBlockInput ? g.contraction * g.ldb : g.rag.rows * std::max(g.lda, g.ldb);
   const bool rebase = down >= (int64_t(1) << 31) - 1024;
   const bool vec = g.ldc % 8 == 0 && g.c_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(g.C) & 15) == 0;
-  // the rows an expert's tiles are filled with, on average; see kBigTileMin for the tiles' sizes
-  const bool full = WHAT == kBlockWeight || !ragged || g.rag.rows >= 192 * E;
-  const bool big = grid_of(256) >= kBigTileMin && full;
-  const int64_t n = grid_of(big ? 256 : 128);
+  const int64_t b = plan.big ? 256 : 128;
+  const int64_t n = tiles_of(WHAT, g.rows_out, g.cols_out, ragged ? g.rag.E : 1, ragged, b) * plan.splits;
   if (n == 0) return hipSuccess;
-  if (big)
-    launch<256, 4, WHAT>(g, rebase, vec, (unsigned)n, stream);
-  else
-    launch<128, 2, WHAT>(g, rebase, vec, (unsigned)n, stream);
+  if (plan.big) {
+    // The last round's r tiles are (r + 7) / 8 * 32 quarters: at most 24 * 7 + 31 workgroups more.
+    const bool known = WHAT == kBlockWeight || !ragged;
+    const int64_t rest = n - whole_tiles((uint32_t)n);
+    launch<256, WHAT>(g, rebase, vec, known ? n - rest + (rest + 7) / 8 * 32 : n + 199, stream);
+  } else {
+    launch<128, WHAT>(g, rebase, vec, n, stream);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_block_gemm(BlockProduct what, const BlockGemm& g, hipStream_t stream) {
-  switch (what) {
-    case kBlockForward: return launch_tiles<kBlockForward>(g, stream);
-    case kBlockInput: return launch_tiles<kBlockInput>(g, stream);
-    default: return launch_tiles<kBlockWeight>(g, stream);
-  }
+// Tiles of 256 x 256 where there are enough of them (kBigTileMin, gemm_pipelined.h) and the experts' rows fill
+// them, else of 128 x 128.  One matrix with few of those and a long contraction splits it, each part of at least
+// 512 into a plane of fp32 sums that a second launch adds up.  Both sides, all the call's kernels: 64 rows against
+// 4096 x 14336 65 us and 31, 128 rows 73 and 35, 64 against 4096 x 4096 25.5 and 20.0; dW of 32768 rows of 512 x 2048
+// 152 us and 55, of 8192 of 256 x 2048 40 and 18.  With two parts only it does not pay (64 rows against 14336 x
+// 4096 26.8 and 29.6), nor do parts over tiles of 256 x 256, whose planes are four times as many (the dW of
+// 32768 rows of 512 x 2048 in 16 parts 54 us, of 4096 of 2048 x 2048 in 4 parts 43 us and 25 unsplit).
+BlockPlan block_plan(BlockProduct what, int64_t rows, int64_t cols, int64_t contraction, int64_t E, int64_t all_rows) {
+  BlockPlan p{false, 1, 0, 0};
+  const bool ragged = E > 0;
+  const int64_t e = std::max<int64_t>(E, 1), small = tiles_of(what, rows, cols, e, ragged, 128);
+  p.big = tiles_of(what, rows, cols, e, ragged, 256) >= kBigTileMin && (what == kBlockWeight || !ragged || all_rows >= 192 * e);
+  if (ragged || p.big || small == 0) return p;
+  const int64_t s = std::min<int64_t>(kCUs / small, contraction / 512);
+  if (s < 3) return p;
+  p.kchunk = ((contraction + s - 1) / s + kBlock - 1) / kBlock * kBlock;
+  p.splits = (contraction + p.kchunk - 1) / p.kchunk;
+  p.plane_ld = (cols + 3) / 4 * 4;
+  return p;
+}
+
+hipError_t launch_block_gemm(BlockProduct what, const BlockGemm& gemm, const BlockPlan& plan, float* planes, hipStream_t stream) {
+  BlockGemm g = gemm;
+  g.splits = (uint32_t)plan.splits, g.kchunk = plan.kchunk;
+  g.planes = planes, g.plane_ld = plan.plane_ld, g.plane = g.rows_out * plan.plane_ld;
+  const hipError_t e = what == kBlockForward ? launch_tiles<kBlockForward>(g, plan, stream)
+                       : what == kBlockInput ? launch_tiles<kBlockInput>(g, plan, stream)
+                                             : launch_tiles<kBlockWeight>(g, plan, stream);
+  if (e != hipSuccess || plan.splits == 1) return e;
+  const int64_t quads = g.rows_out * (g.plane_ld / 4);
+  if (quads == 0) return hipSuccess;
+  add_planes<<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(g, g.rows_out);
+  return hipGetLastError();
 }
 
 }  // namespace i8mp

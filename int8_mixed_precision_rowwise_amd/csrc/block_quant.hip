@@ -24,12 +24,16 @@ __device__ __forceinline__ us2 max_of_row16(us2 m) {  // over 16 lanes
   return m;
 }
 
-// Eight codes of a chunk; inv: 2^-e of all of them or of each.
-template <bool EACH>
-__device__ __forceinline__ uint2 codes_of(const uint4& v, const float* inv) {
+// Eight codes of a chunk under one scale.
+__device__ __forceinline__ uint2 codes_of(const uint4& v, float scale) {
+  return make_uint2(codes4(v.x, v.y, scale), codes4(v.z, v.w, scale));
+}
+
+// Eight codes of a chunk, each under a scale of its own (the conversion above takes one for two): inv is 2^-e.
+__device__ __forceinline__ uint2 codes_of_columns(const uint4& v, const float* inv) {
   float f[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = elem(v, j) * inv[EACH ? j : 0];
+  for (int j = 0; j < 8; ++j) f[j] = elem(v, j) * inv[j];
   return make_uint2(pack_f8x4(f[0], f[1], f[2], f[3]), pack_f8x4(f[4], f[5], f[6], f[7]));
 }
 
@@ -87,10 +91,9 @@ __device__ __forceinline__ void quant_tile(const BlockQuant& q, int64_t slot, in
       for (int k = 0; k < 2; ++k) {
         const int r = g + kGroups * (i + k);
         const uint32_t byte = exponent_byte(k ? m.y : m.x);
-        const float inv = inverse_scale(byte);
         if ((c & 15) == 0) lds.byte[c >> 4][r] = (uint8_t)byte;
         if (r < rows && col < q.ldq) {
-          const uint2 w = codes_of<false>(v[i + k], &inv);
+          const uint2 w = codes_of(v[i + k], scale_of(byte));
           *reinterpret_cast<uint2*>(q.q_row + (16 * unit_of<16>(p) + p.local + r) * q.ldq + col) = w;
         }
       }
@@ -123,7 +126,7 @@ __device__ __forceinline__ void quant_tile(const BlockQuant& q, int64_t slot, in
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int r = g + kGroups * i;
-        if (r < rows) *reinterpret_cast<uint2*>(q.q_col + (r0 + r) * q.ldq + col) = codes_of<true>(v[i], inv);
+        if (r < rows) *reinterpret_cast<uint2*>(q.q_col + (r0 + r) * q.ldq + col) = codes_of_columns(v[i], inv);
       }
     }
   }
@@ -194,14 +197,14 @@ __global__ __launch_bounds__(kThreads) void quant_weight(const uint16_t* __restr
 #pragma unroll
   for (int i = 0; i < kThreads / 64; ++i) a = max(a, red[half][i]);
   const uint32_t byte = exponent_byte(a);
-  const float inv = inverse_scale(byte);
+  const float scale = scale_of(byte);
   if (g == 0 && (c & 15) == 0 && col < K) exps[(e * rts + rt) * kb + 2 * ct + half] = (uint8_t)byte;
   if (col >= Kp) return;
   uint8_t* dst = codes + (e * N + rt * kTileRows) * Kp + col;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = g + kGroups * i;
-    if (r < rows) *reinterpret_cast<uint2*>(dst + r * Kp) = codes_of<false>(v[i], &inv);
+    if (r < rows) *reinterpret_cast<uint2*>(dst + r * Kp) = codes_of(v[i], scale);
   }
 }
 

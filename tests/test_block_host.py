@@ -125,6 +125,8 @@ def test_expert_linear_checks(lib):
             f(*a, X, c[0], e[0], off)
         with pytest.raises(ValueError, match="at least one expert"):
             f(*a, X, c[:0], e[:0], t(1, dtype=i32))
+    with pytest.raises(ValueError, match="at least one row"):
+        i8.expert_linear_fwd(X[:0], c, e, off, rows)
     with pytest.raises(TypeError, match="rows: torch.int32"):
         i8.expert_linear_fwd(X, c, e, off, rows.long())
     with pytest.raises(ValueError, match="rows: 1-D tensor"):
@@ -217,7 +219,7 @@ def test_block_abi():
                 dict(codes=None), dict(exps=None), dict(codes=at(1, 8)), dict(X=None), dict(X=at(3, 8)), dict(ldx=64), dict(ldx=76),
                 dict(tokens=4), dict(experts=-1), dict(experts=1 << 16, offsets=at(6), bits=32), dict(experts=2), dict(offsets=at(6)),
                 dict(experts=2, offsets=at(6), bits=16), dict(experts=2, offsets=at(6, 4), bits=64), dict(rows=at(7, 2)),
-                dict(rows=at(7), tokens=-1)):
+                dict(rows=at(7), tokens=-1), dict(rows=at(7), tokens=0)):
         assert f(block(**bad)) == EINVAL, bad
     assert f(block(), Y=None) == EINVAL and f(block(), ldy=39) == EINVAL
     for over in (at(1, 16), at(2), at(3, 64)):

@@ -26,7 +26,7 @@ __device__ __forceinline__ int ragged_tiles(const Ragged& r) {
   for (int64_t e = threadIdx.x & 63; e < r.E; e += 64) n += tiles_at<BM>(r, e);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-  return n;
+  return __builtin_amdgcn_readfirstlane(n);  // what loops over it then stays in scalar registers
 }
 
 __device__ __forceinline__ void expert_rows(const Ragged& r, int64_t e, Place& p) {
@@ -138,7 +138,7 @@ __device__ __forceinline__ void store_rows(const v16f (&acc)[TM][TN], int8_t* mi
 }
 
 template <int BM>
-constexpr int kLdsBytes = BM == 256 ? 4 * 512 * BK + 4096 : 4 * 256 * BK + 2048;
+constexpr int kLdsBytes = BM == 256 ? 4 * 512 * BK + 10240 : 4 * 256 * BK + 2048;  // of a workgroup of 8 waves, of 4
 
 // Slab loads of one operand, as Dma (gemm_pipelined.h) with less state in registers: a lane's chunks of a
 // slab's loads lie a fixed step apart (and, in tiles read down their rows, swap neighbours with every
@@ -154,7 +154,7 @@ struct Slabs {
   v4u rsrc;
   uint32_t off, at;  // this lane's chunk in slab 0; its contraction index within a slab
   int swap;          // what a swapped chunk's offset differs by
-  uint32_t step, ld;
+  uint32_t ld;
   const int8_t* base;
   int64_t bytes;
 
@@ -167,7 +167,6 @@ struct Slabs {
       const int c = (lane & 3) ^ ((lane >> 4) & 3);
       at = 16 * c;
       off = (16 * wave + (lane >> 2)) * ld + at;
-      step = 16 * NW * ld;
     } else {
       base = p + mn0;
       bytes = (K - 1) * ld_ + min((int64_t)R, MN - mn0);
@@ -175,41 +174,47 @@ struct Slabs {
       at = k;
       off = k * ld + 16 * c;
       if constexpr (kSwap) swap = c & 1 ? -16 : 16;
-      step = NW * KR * ld;
     }
-    rsrc = Dma<64, true, NW>::make_rsrc(base, min(bytes, (int64_t)kOob));
+    rsrc = Dma<64, true, NW>::make_rsrc(base, max((int64_t)0, min(bytes, (int64_t)kOob)));  // an empty contraction: nothing
   }
-  __device__ __forceinline__ void load(uint32_t o, const v4u& r, int8_t* dst, int j, int wave) const {
-    const uint32_t l = (uint32_t)__builtin_amdgcn_readfirstlane(
-        (uint32_t)reinterpret_cast<uintptr_t>((lds_void*)(dst + (wave + NW * j) * 1024)));
+  // Into byte `to` of LDS and the 1023 behind it.
+  static __device__ __forceinline__ void load(uint32_t o, const v4u& r, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(l), "v"(o), "s"(r)
+                 : "s"((uint32_t)__builtin_amdgcn_readfirstlane(to)), "v"(o), "s"(r)
                  : "memory", "m0");
   }
-  __device__ __forceinline__ void issue_one(int j, int8_t* dst, int slab, int64_t K, int wave) const {
-    const int64_t k0 = (int64_t)BK * slab;
-    const int limit = (int)min(K - k0, (int64_t)BK) - (KMAJOR ? 0 : NW * KR * j);
-    // the part that is the same in all lanes, added up in scalar registers
-    uint32_t ahead = j * step;
+  // Load j of the slab at contraction index k0, `ahead` = k0 (k0 ld in tiles read down their rows) bytes on, of
+  // which `left` = K - k0 contraction indices are the operand's, into the operand's tile at byte `to` of LDS.
+  __device__ __forceinline__ void issue_at(int j, uint32_t to, int k0, uint32_t ahead, int left, int wave) const {
+    const int limit = min(left, BK) - (KMAJOR ? 0 : NW * KR * j);
+    ahead += j * ((KMAJOR ? 16 * NW : NW * KR) * ld);
     v4u r = rsrc;
     if constexpr (REBASE && !KMAJOR) {
-      const int64_t sh = k0 * ld;
+      const int64_t sh = (int64_t)k0 * ld;
       r = Dma<64, true, NW>::make_rsrc(base + sh, max((int64_t)0, min(bytes - sh, (int64_t)kOob)));
-    } else {
-      ahead += (uint32_t)k0 * (KMAJOR ? 1u : ld);
+      ahead -= (uint32_t)sh;
     }
+    // what is the same in all lanes is added up in scalar registers
     uint32_t o = off + (uint32_t)__builtin_amdgcn_readfirstlane(ahead);
     if constexpr (kSwap) o += j & 1 ? swap : 0;
-    load((int)at < limit ? o : kOob, r, dst, j, wave);
+    load((int)at < limit ? o : kOob, r, to + (wave + NW * j) * 1024);
   }
-  __device__ __forceinline__ void issue(int8_t* dst, int slab, int64_t K, int wave) const {
+  __device__ __forceinline__ void issue_one(int j, uint32_t to, int slab, int K, int wave) const {
+    const int k0 = BK * slab;
+    issue_at(j, to, k0, (uint32_t)k0 * (KMAJOR ? 1u : ld), K - k0, wave);
+  }
+  __device__ __forceinline__ void issue(uint32_t to, int slab, int K, int wave) const {
 #pragma unroll
-    for (int j = 0; j < kInst; ++j) issue_one(j, dst, slab, K, wave);
+    for (int j = 0; j < kInst; ++j) issue_one(j, to, slab, K, wave);
   }
   // For a slab past the contraction, so that it counts in the waits: zeros into a buffer nobody reads.
-  __device__ __forceinline__ void issue_past_end(int j, int8_t* dst, int wave) const { load(kOob, rsrc, dst, j, wave); }
+  __device__ __forceinline__ void issue_past_end(int j, uint32_t to, int wave) const { load(kOob, rsrc, to + (wave + NW * j) * 1024); }
 };
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>((lds_void*)const_cast<void*>(p)));
+}
 
 // Exponents of four blocks of one tile's rows (4 BM bytes, block after block) and columns (4 BN bytes
 // behind them): 256 bytes a load.
@@ -263,6 +268,34 @@ __device__ __forceinline__ void store_sums(const v16f (&acc)[TM][TN], float* __r
   }
 }
 
+// What a tile reads and writes: rows p.local on of the expert (WEIGHT: columns p.local on of A), columns n0 on.
+struct Operands {
+  const int8_t *A, *B;
+  const uint8_t *sA, *sB;
+  int64_t K, m0, a_rows;  // contraction, first of A's rows (columns) and the end of them
+  uint16_t* C;            // the tile's first output
+  int64_t c_rows;         // rows of C from there on
+};
+template <BlockProduct WHAT>
+__device__ __forceinline__ Operands operands(const BlockGemm& g, const Place& p, int64_t n0) {
+  Operands o{reinterpret_cast<const int8_t*>(g.A), reinterpret_cast<const int8_t*>(g.B), g.sA, g.sB, g.contraction, 0, 0, g.C + n0, 0};
+  if constexpr (WHAT == kBlockWeight) {
+    o.K = p.count;
+    o.A += p.first * g.lda, o.B += p.first * g.ldb;
+    o.sA += unit_of<kBlock>(p) * g.ldsa, o.sB += unit_of<kBlock>(p) * g.ldsb;
+    o.m0 = p.local, o.a_rows = g.lda;
+    o.c_rows = g.rows_out - p.local;
+    o.C += p.e * g.c_stride + p.local * g.ldc;
+  } else {
+    o.m0 = 16 * unit_of<16>(p) + p.local;
+    o.c_rows = p.count - p.local;
+    o.a_rows = o.m0 + o.c_rows;
+    o.B += p.e * g.b_stride, o.sB += p.e * g.sb_stride;
+    o.C += (p.first + p.local) * g.ldc;
+  }
+  return o;
+}
+
 // One tile: rows p.local on of the expert (WEIGHT: columns p.local on of A), columns n0 on; part `split` of the
 // contraction.
 template <int BM, int BN, int WR, int WGN, int STAGES, BlockProduct WHAT, bool REBASE, bool VEC>
@@ -282,24 +315,12 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
 
-  int64_t K = g.contraction, m0, a_rows, c_rows;  // first and last of A's rows (columns), rows of C from here on
-  const int8_t *A = reinterpret_cast<const int8_t*>(g.A), *B = reinterpret_cast<const int8_t*>(g.B);
-  const uint8_t *sA = g.sA, *sB = g.sB;
-  uint16_t* C = g.C + n0;
-  if constexpr (WHAT == kBlockWeight) {
-    K = p.count;
-    A += p.first * g.lda, B += p.first * g.ldb;
-    sA += unit_of<kBlock>(p) * g.ldsa, sB += unit_of<kBlock>(p) * g.ldsb;
-    m0 = p.local, a_rows = g.lda;
-    c_rows = g.rows_out - p.local;
-    C += p.e * g.c_stride + p.local * g.ldc;
-  } else {
-    m0 = 16 * unit_of<16>(p) + p.local;
-    c_rows = p.count - p.local;
-    a_rows = m0 + c_rows;
-    B += p.e * g.b_stride, sB += p.e * g.sb_stride;
-    C += (p.first + p.local) * g.ldc;
-  }
+  Operands o(operands<WHAT>(g, p, n0));
+  int64_t K = o.K;
+  const int8_t *A = o.A, *B = o.B;
+  const uint8_t *sA = o.sA, *sB = o.sB;
+  const int64_t m0 = o.m0, a_rows = o.a_rows, c_rows = o.c_rows;
+  uint16_t* const C = o.C;
   constexpr bool CAN_SPLIT = NW == 4;
   if (CAN_SPLIT && g.splits > 1) {  // one matrix
     const int64_t k0 = split * g.kchunk;
@@ -347,11 +368,13 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
     };
     // A group of exponents goes out ahead of the slab that starts it, so it has landed whenever that
     // slab has; the waits below count slab loads and are at most stricter for the loads between them.
+    const uint32_t lds0 = lds_address(lds);
+    const int k = (int)K;
     ex.issue(exps, 0, wave, lane);
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
-      da.issue(lds + s * SLAB, s, K, wave);
-      db.issue(lds + s * SLAB + A_BYTES, s, K, wave);
+      da.issue(lds0 + s * SLAB, s, k, wave);
+      db.issue(lds0 + s * SLAB + A_BYTES, s, k, wave);
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_vm((STAGES - 1) * PER));  // slab 0 has landed
     lds_barrier();
@@ -367,7 +390,7 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
     // reads the next block's exponents.
     int stage = 0;  // slab kt's place
     auto slab = [&](v8i(&bc)[TN], v8i(&bn)[TN], int kt, bool odd, bool tail) __attribute__((always_inline)) {
-      int8_t* dst = lds + stage * SLAB;
+      const uint32_t dst = lds0 + stage * SLAB;
       stage = stage + 1 == STAGES ? 0 : stage + 1;
       const int8_t* nxt = lds + stage * SLAB;
       const int ns = kt + STAGES;
@@ -396,8 +419,8 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
               if (d < NA) da.issue_past_end(d, dst, wave);
               else db.issue_past_end(d - NA, dst + A_BYTES, wave);
             } else {
-              if (d < NA) da.issue_one(d, dst, ns, K, wave);
-              else db.issue_one(d - NA, dst + A_BYTES, ns, K, wave);
+              if (d < NA) da.issue_one(d, dst, ns, k, wave);
+              else db.issue_one(d - NA, dst + A_BYTES, ns, k, wave);
             }
           }
         __builtin_amdgcn_sched_barrier(0);
@@ -427,6 +450,237 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
   store_rows<TM, TN, VEC>(acc, lds + wave * (WM * WN * 2), C + wm0 * g.ldc + wn0, g.ldc, c_rows - wm0, g.cols_out - n0 - wn0, lane);
 }
 
+// A wave's 128 x 64 outputs straight from its accumulators.  A lane has four adjacent columns of a row, and the
+// one 32 lanes on the next four; exchanging halves makes eight of each, 16 bytes.  What lies outside the
+// tile falls outside the descriptor.
+__device__ __forceinline__ void store_direct(const v16f (&acc)[4][2], uint16_t* C, uint32_t ldc, int rows, int cols, int lane) {
+  const int mr = lane & 31, half = lane >> 5;
+  rows = min(max(rows, 0), 128), cols = min(max(cols, 0), 64);
+  const int bytes = __builtin_amdgcn_readfirstlane(rows > 0 && cols > 0 ? (int)(2 * ((rows - 1) * ldc + cols)) : 0);
+  const uint64_t c = reinterpret_cast<uint64_t>(C);
+  const uint64_t c0 = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(c >> 32)) << 32 |
+                      (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)c);
+  const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(c0), 0, bytes, 0x00020000);
+  uint32_t at = 2 * (mr * ldc + 8 * half);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        uint32_t w[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          __bf16 h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = (__bf16)acc[i][j][4 * (q + k) + e];  // round to nearest even
+          const uint2 u = __builtin_bit_cast(uint2, h);
+          w[k][0] = u.x, w[k][1] = u.y;
+        }
+        const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+        const v4u v = {s0[0], s1[0], s0[1], s1[1]};
+        const int n = 32 * j + 8 * q;  // of lanes 0 .. 31; the others are 8 on
+        __builtin_amdgcn_raw_buffer_store_b128(v, out, n + 8 * half < cols ? at + 2 * n : kOob, 0, 0);
+      }
+    at += 64 * ldc;  // rows past the last one lie past the descriptor's end
+  }
+}
+
+constexpr int kBatch = 32;  // tiles whose places are worked out at a time
+
+struct BigLds {
+  int8_t slabs[4 * 512 * BK];
+  int8_t exps[5][4 * 512];  // four groups, and one that nobody reads
+  int info[kBatch][8];
+};
+
+// Tiles info[0 .. n - 1] of 256 x 256, one after another without a pause: the pipeline's slab loads run on into
+// the next tile while the last slabs of this one are multiplied, and its outputs leave while the next one's first
+// slabs arrive.  A tile's contraction is taken in whole blocks of 128, two slabs, and at least two of them; the loads
+// are two blocks ahead, so that they change to the next tile before the last two blocks, and the loop over a
+// tile's blocks has no branch in it (one would let the compiler move matrix instructions past the loads and reads that they
+// are to cover).
+template <BlockProduct WHAT, bool REBASE>
+__device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& lds) {
+  constexpr int BM = 256, BN = 256, WGN = 4, NW = 8, WM = 128, WN = 64, TM = 4, TN = 2;
+  constexpr bool AK = WHAT != kBlockWeight, BKM = WHAT == kBlockForward;
+  constexpr int A_BYTES = BM * BK, SLAB = A_BYTES + BN * BK;
+  typedef Slabs<BM, AK, NW, REBASE> DA;
+  typedef Slabs<BN, BKM, NW, REBASE> DB;
+  constexpr int NA = DA::kInst, PER = NA + DB::kInst;
+  using S = SlabSchedule<TM, TN, PER>;
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm0 = (wave / WGN) * WM, wn0 = (wave % WGN) * WN;
+  const uint32_t slabs0 = lds_address(lds.slabs), exps0 = lds_address(lds.exps);
+
+  const auto place = [&](int i, int64_t& n0) __attribute__((always_inline)) {
+    const int* q = lds.info[i];
+    Place p;
+    p.e = __builtin_amdgcn_readfirstlane(q[0]);
+    p.local = __builtin_amdgcn_readfirstlane(q[1]);
+    p.first = __builtin_amdgcn_readfirstlane(q[2]);
+    p.count = __builtin_amdgcn_readfirstlane(q[3]);
+    n0 = __builtin_amdgcn_readfirstlane(q[4]);
+    return p;
+  };
+
+  // What is being loaded: the slab at contraction index lk of a tile of K = lk + left, with the operands' bytes that
+  // lie before it.
+  DA da;
+  DB db;
+  int lk = 0, left = 0;
+  uint32_t ahead_a = 0, ahead_b = 0;
+  // Exponents of a group of four blocks: waves 0 .. 3 load A's, the others B's, of one block each; every block
+  // counts one load, those that start no group one of zeros into a place of its own.
+  const uint8_t* ex = nullptr;
+  int64_t ex_left = 0;
+  const uint32_t ex_ld = (uint32_t)(wave < 4 ? g.ldsa : g.ldsb), ex_at = (wave & 3) * ex_ld + 4 * lane;
+  int lgroup = 0;  // groups loaded so far
+  const auto open = [&](int i) __attribute__((always_inline)) {
+    lk = 0, ahead_a = 0, ahead_b = 0;
+    if (i < n) {
+      int64_t n0;
+      const Place p = place(i, n0);
+      const Operands o = operands<WHAT>(g, p, n0);
+      left = (int)o.K;
+      da.init(o.A, g.lda, o.m0, o.a_rows, o.K, wave, lane);
+      db.init(o.B, g.ldb, n0, BKM ? g.cols_out : g.ldb, o.K, wave, lane);
+      ex = wave < 4 ? o.sA + o.m0 : o.sB + n0;
+      ex_left = (o.K + kBlock - 1) / kBlock * ex_ld - (wave < 4 ? o.m0 : n0);
+    } else {
+      left = 0, ex_left = 0;  // nothing but zeros
+    }
+  };
+  const auto issue_exps = [&]() __attribute__((always_inline)) {  // before a block's slabs
+    const bool starts = (lk & (4 * kBlock - 1)) == 0;
+    const v4u r = Dma<64, true, NW>::make_rsrc(reinterpret_cast<const int8_t*>(ex), max((int64_t)0, min(ex_left, (int64_t)kOob)));
+    const uint32_t to = exps0 + (starts ? lgroup & 3 : 4) * (uint32_t)sizeof(lds.exps[0]) + wave * 256;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"((uint32_t)__builtin_amdgcn_readfirstlane(to)), "v"(starts ? ex_at : kOob), "s"(r)
+                 : "memory", "m0");
+    ex += starts ? 4 * (int64_t)ex_ld : 0;
+    ex_left -= starts ? 4 * (int64_t)ex_ld : 0;
+    lgroup += starts;
+  };
+  const auto issue = [&](int d, uint32_t dst) __attribute__((always_inline)) {
+    if (d < NA) da.issue_at(d, dst, lk, ahead_a, left, wave);
+    else db.issue_at(d - NA, dst + A_BYTES, lk, ahead_b, left, wave);
+  };
+  const auto issued = [&]() __attribute__((always_inline)) {
+    lk += BK, left -= BK;
+    ahead_a += BK * (AK ? 1u : da.ld), ahead_b += BK * (BKM ? 1u : db.ld);
+  };
+
+  v16f acc[TM][TN];
+  const auto clear_acc = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = Mma<1>::zero();
+  };
+  v8i a[TM], b0[TN], b1[TN];
+  int ea[TM], eb[TN], na[TM], nb[TN];  // exponents of this block and the next
+  int rgroup = 0, rblock = 0;          // where they are read: group, block of it
+  const auto read_exps = [&]() __attribute__((always_inline)) {
+    const int8_t* at = lds.exps[rgroup & 3] + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) na[i] = *reinterpret_cast<const uint8_t*>(at + rblock * BM + wm0 + 32 * i);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) nb[j] = *reinterpret_cast<const uint8_t*>(at + 4 * BM + rblock * BN + wn0 + 32 * j);
+  };
+  const auto next_exps = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) ea[i] = na[i];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) eb[j] = nb[j];
+  };
+  const auto mma = [&](const v8i& bf, const v8i& af, int i, int j) __attribute__((always_inline)) {
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf, af, acc[i][j], 0, 0, 0, eb[j], 0, ea[i]);
+  };
+
+  open(0);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    if ((s & 1) == 0) issue_exps();
+#pragma unroll
+    for (int d = 0; d < PER; ++d) issue(d, slabs0 + s * SLAB);
+    issued();
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(3 * PER));  // slab 0 has landed (and exponents a load for every block ahead of it)
+  lds_barrier();
+  read_exps();
+  next_exps();
+  clear_acc();
+#pragma unroll
+  for (int i = 0; i < TM; ++i) a[i] = frag32f8<BM, AK>(lds.slabs, wm0 + 32 * i, lane);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) b0[j] = frag32f8<BN, BKM>(lds.slabs + A_BYTES, wn0 + 32 * j, lane);
+
+  int stage = 0;  // this slab's place
+  // One slab, as in multiply; half: of the block.  The waits count slab loads and are at most stricter for the
+  // exponents' loads and the last tile's stores among them.
+  auto slab = [&](v8i(&bc)[TN], v8i(&bn)[TN], int half) __attribute__((always_inline)) {
+    const uint32_t dst = slabs0 + stage * SLAB;
+    stage = (stage + 1) & 3;
+    const int8_t* nxt = lds.slabs + stage * SLAB;
+#pragma unroll
+    for (int m = 0; m < S::HA; ++m) {
+      mma(bc[m % TN], a[m / TN], m / TN, m % TN);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(2 * PER));  // the next slab has landed
+    lds_barrier();
+    if (half) read_exps();
+    else issue_exps();
+#pragma unroll
+    for (int m = S::HA; m < S::NM; ++m) {
+      mma(bc[m % TN], a[m / TN], m / TN, m % TN);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        if (m == S::a_read(i)) a[i] = frag32f8<BM, AK>(nxt, wm0 + 32 * i, lane);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        if (m == S::b_read(j)) bn[j] = frag32f8<BN, BKM>(nxt + A_BYTES, wn0 + 32 * j, lane);
+#pragma unroll
+      for (int d = 0; d < PER; ++d)
+        if (m == S::dma_at(d)) issue(d, dst);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    issued();
+  };
+#pragma unroll 1
+  for (int ct = 0; ct < n; ++ct) {
+    const int K = WHAT == kBlockWeight ? __builtin_amdgcn_readfirstlane(lds.info[ct][3]) : (int)g.contraction;
+    const int blocks = max((K + kBlock - 1) / kBlock, 2);
+    int b = 0;
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+      const int end = part ? blocks : blocks - 2;
+      if (part) open(ct + 1);
+#pragma unroll 1
+      for (; b < end; ++b) {
+        slab(b0, b1, 0);
+        // the exponents of the next block: the next group's first after the group's fourth and after the tile's last
+        const bool last = b + 1 == blocks || rblock == 3;
+        rgroup += last;
+        rblock = last ? 0 : rblock + 1;
+        slab(b1, b0, 1);
+        next_exps();
+      }
+    }
+    int64_t n0;
+    const Place p = place(ct, n0);
+    const Operands o = operands<WHAT>(g, p, n0);
+    store_direct(acc, o.C + wm0 * g.ldc + wn0, (uint32_t)g.ldc, (int)min(o.c_rows - wm0, (int64_t)WM), (int)min(g.cols_out - n0 - wn0, (int64_t)WN), lane);
+    clear_acc();
+  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));  // the trailing loads land before their place is used again
+  __syncthreads();
+}
+
 // The parts' sums added in order, rounded once.
 __global__ __launch_bounds__(256) void add_planes(BlockGemm g, int64_t rows) {
   const uint32_t quads = (uint32_t)(g.plane_ld / 4);
@@ -445,43 +699,18 @@ __global__ __launch_bounds__(256) void add_planes(BlockGemm g, int64_t rows) {
     if (n + e < g.cols_out) c[e] = (__bf16)v[e];  // round to nearest even
 }
 
-template <int BM, BlockProduct WHAT, bool REBASE, bool VEC>
-__global__ __launch_bounds__(BM == 256 ? 512 : 256, 2) void block_gemm(BlockGemm g) {
-  constexpr int BN = BM, NT = BM == 256 ? 512 : 256;
-  __shared__ __attribute__((aligned(1024))) int8_t lds[kLdsBytes<BM>];
-  const uint32_t wg = blockIdx.x, tiles_n = (uint32_t)((g.cols_out + BN - 1) / BN);
-  uint32_t tiles_m;
+// Where a tile lies, in groups of 4 tile rows (of an expert's tile rows), so that the tiles of an XCD share panels
+// in its L2.  tiles_m: of all experts' rows (WEIGHT: of one expert's outputs).
+template <int BM, BlockProduct WHAT>
+__device__ __forceinline__ Place tile_place(const BlockGemm& g, uint32_t tile, uint32_t tiles_m, uint32_t tiles_n, int64_t& n0) {
+  uint32_t e = 0;
   if constexpr (WHAT == kBlockWeight) {
-    tiles_m = (uint32_t)(g.rag.E * ((g.rows_out + BM - 1) / BM));  // of all experts
-  } else {
-    tiles_m = ragged_tiles<BM>(g.rag);
-    if (g.clear && g.rag.off) {
-      for (int64_t r = offset_at(g.rag, g.rag.E) + wg; r < g.rag.rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < g.cols_out; c += NT) g.C[r * g.ldc + c] = 0;
-    }
-  }
-  const uint32_t each = tiles_m * tiles_n, all = each * (BM == 128 ? g.splits : 1), whole = BM == 256 ? whole_tiles(all) : all;
-  uint32_t tile, quarter = 0;
-  if (wg < whole) {
-    tile = xcd_runs(wg, whole);
-  } else {  // the quarters of a tile to one XCD
-    const uint32_t i = wg - whole;
-    tile = whole + i / 32 * 8 + (i & 7);
-    quarter = i / 8 & 3;
-    if (tile >= all) return;
-  }
-  // the parts of the contraction one after another: an XCD's run of tiles reads the same part
-  const uint32_t split = BM == 128 && g.splits > 1 ? tile / each : 0;
-  tile -= split * each;
-  // groups of 4 tile rows (of an expert's tile rows), so that the tiles of an XCD share panels in its L2
-  int64_t e = 0;
-  if constexpr (WHAT == kBlockWeight) {
-    tiles_m = (uint32_t)((g.rows_out + BM - 1) / BM);
     e = tile / (tiles_m * tiles_n);
-    tile -= (uint32_t)e * tiles_m * tiles_n;
+    tile -= e * tiles_m * tiles_n;
   }
   const uint32_t group = tile / (4 * tiles_n), first = 4 * group, rows = min(tiles_m - first, 4u), in = tile - group * 4 * tiles_n;
   const uint32_t tm = first + in % rows, tn = in / rows;
+  n0 = (int64_t)tn * BM;
   Place p;
   if constexpr (WHAT == kBlockWeight) {
     expert_rows(g.rag, by_size(g.rag, e), p);
@@ -489,35 +718,81 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256, 2) void block_gemm(BlockGemm
   } else {
     ragged_place<BM>(g.rag, tm, p);
   }
-  int64_t n0 = (int64_t)tn * BN;
-  if constexpr (BM == 256) {
-    if (wg < whole) {
-      multiply<256, 256, 2, 4, 4, WHAT, REBASE, VEC>(g, p, n0, split, lds);
-    } else {
-      p.local += quarter & 1 ? 128 : 0;
-      n0 += quarter & 2 ? 128 : 0;
-      if (p.local >= (WHAT == kBlockWeight ? g.rows_out : p.count) || n0 >= g.cols_out) return;
-      multiply<128, 128, 2, 4, 8, WHAT, REBASE, VEC>(g, p, n0, split, lds);
-    }
-  } else {
-    multiply<128, 128, 2, 2, 4, WHAT, REBASE, VEC>(g, p, n0, split, lds);
-  }
+  return p;
 }
 
 template <int BM, BlockProduct WHAT>
-void launch(const BlockGemm& g, bool rebase, bool vec, int64_t grid, hipStream_t stream) {
-  constexpr bool CAN = WHAT != kBlockForward;  // an operand read down its rows
-  constexpr int NT = BM == 256 ? 512 : 256;
-  if (CAN && rebase) {
-    if (vec)
-      block_gemm<BM, WHAT, CAN, true><<<(unsigned)grid, NT, 0, stream>>>(g);
-    else
-      block_gemm<BM, WHAT, CAN, false><<<(unsigned)grid, NT, 0, stream>>>(g);
-  } else if (vec) {
-    block_gemm<BM, WHAT, false, true><<<(unsigned)grid, NT, 0, stream>>>(g);
-  } else {
-    block_gemm<BM, WHAT, false, false><<<(unsigned)grid, NT, 0, stream>>>(g);
+__device__ __forceinline__ uint32_t tile_rows(const BlockGemm& g) {
+  return WHAT == kBlockWeight ? (uint32_t)((g.rows_out + BM - 1) / BM) : ragged_tiles<BM>(g.rag);
+}
+
+template <BlockProduct WHAT>
+__device__ __forceinline__ void clear_rows(const BlockGemm& g) {
+  if (WHAT == kBlockWeight || !g.clear || !g.rag.off) return;
+  for (int64_t r = offset_at(g.rag, g.rag.E) + blockIdx.x; r < g.rag.rows; r += gridDim.x)
+    for (int64_t c = threadIdx.x; c < g.cols_out; c += blockDim.x) g.C[r * g.ldc + c] = 0;
+}
+
+// Tiles of 128 x 128, two workgroups a CU.
+template <BlockProduct WHAT, bool REBASE, bool VEC>
+__global__ __launch_bounds__(256, 2) void block_gemm_small(BlockGemm g) {
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kLdsBytes<128>];
+  const uint32_t tiles_n = (uint32_t)((g.cols_out + 127) / 128), tiles_m = tile_rows<128, WHAT>(g);
+  clear_rows<WHAT>(g);
+  const uint32_t each = tiles_m * tiles_n, all = each * (WHAT == kBlockWeight ? (uint32_t)g.rag.E : 1) * g.splits;
+  if (blockIdx.x >= all) return;
+  uint32_t tile = xcd_runs(blockIdx.x, all);
+  // the parts of the contraction one after another: an XCD's run of tiles reads the same part
+  const uint32_t split = g.splits > 1 ? tile / each : 0;
+  int64_t n0;
+  const Place p = tile_place<128, WHAT>(g, tile - split * each, tiles_m, tiles_n, n0);
+  multiply<128, 128, 2, 2, 4, WHAT, REBASE, VEC>(g, p, n0, split, lds);
+}
+
+// Tiles of 256 x 256: a workgroup for each CU takes every 256th of them, then at most one quarter of the last ones.
+template <BlockProduct WHAT, bool REBASE>
+__global__ __launch_bounds__(512, 2) void block_gemm_big(BlockGemm g) {
+  __shared__ __attribute__((aligned(1024))) BigLds lds;
+  const uint32_t tiles_n = (uint32_t)((g.cols_out + 255) / 256), tiles_m = tile_rows<256, WHAT>(g);
+  clear_rows<WHAT>(g);
+  const uint32_t all = tiles_m * tiles_n * (WHAT == kBlockWeight ? (uint32_t)g.rag.E : 1), whole = whole_tiles(all);
+  const uint32_t wg = blockIdx.x, step = gridDim.x;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (uint32_t first = wg; first < whole; first += kBatch * step) {
+    const int n = (int)min((whole - first + step - 1) / step, (uint32_t)kBatch);
+    for (int i = wave; i < n; i += 8) {
+      int64_t n0;
+      const Place p = tile_place<256, WHAT>(g, xcd_runs(first + i * step, whole), tiles_m, tiles_n, n0);
+      if (lane == 0) {
+        int* q = lds.info[i];
+        q[0] = (int)p.e, q[1] = (int)p.local, q[2] = (int)p.first, q[3] = (int)p.count, q[4] = (int)n0;
+      }
+    }
+    __syncthreads();
+    multiply_all<WHAT, REBASE>(g, n, lds);
   }
+  // the quarters of a tile to one XCD
+  for (uint32_t i = wg; i < (all - whole + 7) / 8 * 32; i += step) {
+    const uint32_t tile = whole + i / 32 * 8 + (i & 7), quarter = i / 8 & 3;
+    if (tile >= all) continue;
+    int64_t n0;
+    Place p = tile_place<256, WHAT>(g, tile, tiles_m, tiles_n, n0);
+    p.local += quarter & 1 ? 128 : 0;
+    n0 += quarter & 2 ? 128 : 0;
+    if (p.local >= (WHAT == kBlockWeight ? g.rows_out : p.count) || n0 >= g.cols_out) continue;
+    multiply<128, 128, 2, 4, 8, WHAT, REBASE, true>(g, p, n0, 0, lds.slabs);
+    __syncthreads();  // the outputs have left LDS
+  }
+}
+
+template <BlockProduct WHAT, bool REBASE>
+void launch(const BlockGemm& g, bool big, bool vec, unsigned grid, hipStream_t stream) {
+  if (big)
+    block_gemm_big<WHAT, REBASE><<<grid, 512, 0, stream>>>(g);
+  else if (vec)
+    block_gemm_small<WHAT, REBASE, true><<<grid, 256, 0, stream>>>(g);
+  else
+    block_gemm_small<WHAT, REBASE, false><<<grid, 256, 0, stream>>>(g);
 }
 
 // At most: how many the experts' rows make, only the GPU knows.
@@ -534,17 +809,16 @@ hipError_t launch_tiles(const BlockGemm& g, const BlockPlan& plan, hipStream_t s
   const int64_t down = WHAT == kBlockForward ? 0 : WHAT == kBlockInput ? g.contraction * g.ldb : g.rag.rows * std::max(g.lda, g.ldb);
   const bool rebase = down >= (int64_t(1) << 31) - 1024;
   const bool vec = g.ldc % 8 == 0 && g.c_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(g.C) & 15) == 0;
-  const int64_t b = plan.big ? 256 : 128;
-  const int64_t n = tiles_of(WHAT, g.rows_out, g.cols_out, ragged ? g.rag.E : 1, ragged, b) * plan.splits;
+  // the big tiles' kernel writes whole chunks of 8 columns
+  const bool big = plan.big && vec && g.cols_out % 8 == 0 && g.ldc < (int64_t(1) << 22);
+  const int64_t n = tiles_of(WHAT, g.rows_out, g.cols_out, ragged ? g.rag.E : 1, ragged, big ? 256 : 128) * plan.splits;
   if (n == 0) return hipSuccess;
-  if (plan.big) {
-    // The last round's r tiles are (r + 7) / 8 * 32 quarters: at most 24 * 7 + 31 workgroups more.
-    const bool known = WHAT == kBlockWeight || !ragged;
-    const int64_t rest = n - whole_tiles((uint32_t)n);
-    launch<256, WHAT>(g, rebase, vec, known ? n - rest + (rest + 7) / 8 * 32 : n + 199, stream);
-  } else {
-    launch<128, WHAT>(g, rebase, vec, n, stream);
-  }
+  const bool cut = n > whole_tiles((uint32_t)n) || (ragged && WHAT != kBlockWeight);
+  const unsigned grid = (unsigned)(big ? cut ? kCUs : std::min<int64_t>(n, kCUs) : n);
+  if (WHAT != kBlockForward && rebase)  // an operand read down its rows
+    launch<WHAT, WHAT != kBlockForward>(g, big, vec, grid, stream);
+  else
+    launch<WHAT, false>(g, big, vec, grid, stream);
   return hipGetLastError();
 }
 

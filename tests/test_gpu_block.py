@@ -80,7 +80,8 @@ def test_weight_codes_of_views_and_given_outputs():
 # ------------------------------------------------------------------ products
 
 SIZES = [(1, 1, 8), (1, 16, 16), (1, 300, 2040), (5, 40, 24), (16, 130, 136), (17, 64, 128), (33, 129, 520), (64, 257, 264),
-         (65, 129, 264), (129, 136, 72), (200, 300, 1000), (300, 70, 128), (257, 520, 2040), (700, 520, 200)]
+         (65, 129, 264), (129, 136, 72), (200, 300, 1000), (300, 70, 128), (257, 520, 2040), (700, 520, 200),
+         (4100, 2056, 264), (4100, 2051, 72)]  # enough tiles for the big ones; columns that they do not take
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -97,7 +98,8 @@ def test_forward(M, N, K):
     assert bool((store[:, 0] == 7).all()) and bool((store[:, N + 1:] == 7).all())
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 8, 8), (5, 40, 24), (130, 136, 72), (65, 264, 136), (200, 304, 1000), (257, 520, 2040), (1000, 136, 128)])
+@pytest.mark.parametrize("M,N,K", [(1, 8, 8), (5, 40, 24), (130, 136, 72), (65, 264, 136), (200, 304, 1000), (257, 520, 2040), (1000, 136, 128),
+                                   (300, 4104, 2056), (4100, 264, 2056), (60, 4104, 2056)])
 def test_backward(M, N, K):
     X, W, dY = randn(M, M, K), randn(N, N, K, std=0.02), randn(K, M, N, std=1e-3)
     codes, exps = i8.quantize_block_weight(W)

@@ -21,7 +21,7 @@ def randn(seed, *shape, std=1.0):
 # rows of each expert; N; K
 CASES = [([0, 1, 0], 16, 16), ([3, 0, 0, 5, 1], 40, 24), ([0] * 70 + [2, 0, 1], 24, 40), ([17, 130, 0, 64], 136, 264),
          ([1] * 40, 264, 136), ([300, 0, 20, 129], 264, 136), ([128, 256, 127], 300, 200), ([600, 700], 264, 520),
-         ([2000], 40, 72), ([0, 0], 40, 72)]
+         ([2000], 40, 72), ([0, 0], 40, 72), ([700, 0, 300, 1500, 0, 130], 2056, 2056)]  # the last in big tiles
 
 
 def setup(counts, N, K, behind, dtype=i32, gather=False):

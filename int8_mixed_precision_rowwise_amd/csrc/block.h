@@ -103,8 +103,8 @@ __device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float scale
 
 // Codes of a bf16 matrix x [rows of rag][cols], read through `index` (row r is x's row
 // index[r], of n_src; a negative index or one past the end is a row of zeros) unless NULL.
-// Along the rows: codes at rows 16 * unit_of<16> + local of q_row, exponents s_row[block][that
-// row].  Down the rows, blocks starting at the expert's first row: codes at the rows
+// Along the rows: codes at rows 16 * unit_of<16> + local of q_row, exponents s_row[that row][block],
+// rows of which lie ld_srow (a multiple of 4) apart.  Down the rows, blocks starting at the expert's first row: codes at the rows
 // themselves of q_col, exponents s_col[unit_of<128> + block][column].  Pitch of codes: ldq
 // = cols rounded up to 16, zeros behind cols.
 struct BlockQuant {
@@ -136,12 +136,18 @@ hipError_t launch_block_quant_weight(const uint16_t* w, int64_t E, int64_t N, in
 // The products.  FORWARD: C[r][n] = sum_k A[r][k] B[e][n][k]; INPUT: C[r][k] = sum_n A[r][n]
 // B[e][n][k]; WEIGHT: C[e][n][k] = sum_r A[r][n] B[r][k] over the expert's rows.
 enum BlockProduct { kBlockForward = 0, kBlockInput = 1, kBlockWeight = 2 };
+// Exponents: B's (and WEIGHT's A's) in planes [block][row or column], ldsb (ldsa) apart; the others' A's in rows
+// [row][block], ldsa (a multiple of 4) apart.
 struct BlockGemm {
   int64_t rows_out;      // C's rows (WEIGHT: N); others: rag's
   int64_t cols_out;      // C's columns
   int64_t contraction;   // FORWARD: K, INPUT: N; WEIGHT: the expert's rows
-  const uint8_t *A, *sA; // codes and exponent planes
+  const uint8_t *A, *sA; // codes and exponents
   int64_t lda, ldsa;
+  // FORWARD: NULL, or row r of the experts' rows is A's row index[r], of n_src (another: a row of zeros); A then
+  // lies row by row, and n_src * lda is below 2^31 - 1024.  Otherwise A has each expert's rows at 16 * unit_of<16>.
+  const int32_t* index;
+  int64_t n_src;
   const uint8_t *B, *sB;
   int64_t ldb, ldsb, b_stride, sb_stride;  // strides between experts (FORWARD, INPUT)
   uint16_t* C;
@@ -153,7 +159,7 @@ struct BlockGemm {
   int64_t kchunk, plane, plane_ld;
   float* planes;
 };
-// Tile size and, for one matrix, the parts of the contraction (of kchunk each, a multiple of 128) and the pitch of
+// Tile size and, for one matrix, the parts of the contraction (of kchunk each, a multiple of 512) and the pitch of
 // their planes.  rows, cols: C's; contraction as in BlockGemm (WEIGHT of one matrix: its rows); all_rows: ragged rows.
 struct BlockPlan {
   bool big;

@@ -26,6 +26,9 @@ bool block_dims_ok(int64_t M, int64_t N, int64_t K, int64_t E) {
   return (M / kBlock + e + 1) * sides < limit && e * (blocks_of(N) + 1) * (blocks_of(K) + 1) < limit;
 }
 
+// Pitch of a row's exponents: whole words.
+int64_t pitch4(int64_t K) { return (blocks_of(K) + 3) / 4 * 4; }
+
 // Rows of the room in which each expert starts at a multiple of 16, and its blocks of 128.
 int64_t room16(int64_t M, int64_t E) { return E ? 16 * i8mp::ragged_units(M, E, 16) : pad16(M); }
 int64_t room128(int64_t M, int64_t E) { return E ? i8mp::ragged_units(M, E, kBlock) : blocks_of(M); }
@@ -42,7 +45,7 @@ size_t carve_fwd(void* ws, int64_t M, int64_t N, int64_t K, int64_t E, FwdWs* ou
   Carver c{static_cast<char*>(ws)};
   FwdWs w{};
   w.q = static_cast<uint8_t*>(c.take((size_t)(room16(M, E) * pad16(K))));
-  w.s = static_cast<uint8_t*>(c.take((size_t)(blocks_of(K) * room16(M, E))));
+  w.s = static_cast<uint8_t*>(c.take((size_t)(room16(M, E) * pitch4(K))));
   w.planes = static_cast<uint8_t*>(c.take((size_t)(std::max<int64_t>(E, 1) * blocks_of(K) * pad16(N))));
   w.sums = static_cast<float*>(c.take(plan_fwd(M, N, K, E).bytes(M)));
   if (out) *out = w;
@@ -58,7 +61,7 @@ size_t carve_bwd(void* ws, int64_t M, int64_t N, int64_t K, int64_t E, BwdWs* ou
   Carver c{static_cast<char*>(ws)};
   BwdWs w{};
   w.q = static_cast<uint8_t*>(c.take((size_t)(room16(M, E) * pad16(N))));
-  w.s = static_cast<uint8_t*>(c.take((size_t)(blocks_of(N) * room16(M, E))));
+  w.s = static_cast<uint8_t*>(c.take((size_t)(room16(M, E) * pitch4(N))));
   w.planes = static_cast<uint8_t*>(c.take((size_t)(std::max<int64_t>(E, 1) * blocks_of(N) * pad16(K))));
   w.qd = static_cast<uint8_t*>(c.take((size_t)(M * pad16(N))));
   w.sd = static_cast<uint8_t*>(c.take((size_t)(room128(M, E) * pad16(N))));
@@ -210,13 +213,20 @@ i8mp_status i8mp_block_fwd(const i8mp_block* p, uint16_t* Y, int64_t ldy, int32_
   }
   FwdWs w;
   carve_fwd(ws, M, N, K, E, &w);
-  const i8mp::BlockQuant q{p->X, p->ldx, K, p->tokens, p->rows, rag, w.q, w.s, nullptr, nullptr, pad16(K), room16(M, E), 0};
+  // Where tokens are fewer than the rows that are read through an index, they are quantized once each, and the product
+  // reads their codes through it (32768 rows of 8192 tokens of 2048: 12 us and the product's own time, 36 us for all
+  // rows' codes).
+  const bool gather = p->rows && p->tokens < M && p->tokens * pad16(K) < (int64_t(1) << 31) - 1024;
+  const i8mp::Ragged tokens{nullptr, 0, 1, p->tokens};
+  const i8mp::BlockQuant q{p->X, p->ldx, K, p->tokens, gather ? nullptr : p->rows, gather ? tokens : rag,
+                           w.q, w.s, nullptr, nullptr, pad16(K), pitch4(K), 0};
   const i8mp::SpreadJob sp{p->exps, rag.E, blocks_of(N), blocks_of(K), pad16(N), 0, w.planes};
   const hipError_t e = i8mp::launch_block_quant(q, nullptr, sp, s);
   if (e != hipSuccess) return hip_status(e);
   i8mp::BlockGemm g{};
   g.rows_out = M, g.cols_out = N, g.contraction = K;
-  g.A = w.q, g.sA = w.s, g.lda = pad16(K), g.ldsa = room16(M, E);
+  g.A = w.q, g.sA = w.s, g.lda = pad16(K), g.ldsa = pitch4(K);
+  g.index = gather ? p->rows : nullptr, g.n_src = p->tokens;
   g.B = p->codes, g.sB = w.planes, g.ldb = pad16(K), g.ldsb = pad16(N), g.b_stride = N * pad16(K), g.sb_stride = blocks_of(K) * pad16(N);
   g.C = Y, g.ldc = ldy, g.rag = rag, g.clear = clear != 0;
   return hip_status(i8mp::launch_block_gemm(i8mp::kBlockForward, g, plan_fwd(M, N, K, E), w.sums, s));
@@ -248,7 +258,7 @@ i8mp_status i8mp_block_bwd(const i8mp_block* p, const uint16_t* dY, int64_t lddy
   BwdWs w;
   carve_bwd(ws, M, N, K, E, &w);
   const int64_t np = pad16(N), kp = pad16(K);
-  i8mp::BlockQuant d{dY, lddy, N, M, nullptr, rag, nullptr, nullptr, nullptr, nullptr, np, room16(M, E), np};
+  i8mp::BlockQuant d{dY, lddy, N, M, nullptr, rag, nullptr, nullptr, nullptr, nullptr, np, pitch4(N), np};
   const i8mp::BlockQuant x{p->X, p->ldx, K, p->tokens, p->rows, rag, nullptr, nullptr, w.qx, w.sx, kp, 0, kp};
   i8mp::SpreadJob sp{p->exps, rag.E, blocks_of(N), blocks_of(K), kp, 1, nullptr};
   if (some_dx) d.q_row = w.q, d.s_row = w.s, sp.planes = w.planes;
@@ -261,7 +271,7 @@ i8mp_status i8mp_block_bwd(const i8mp_block* p, const uint16_t* dY, int64_t lddy
   g.cols_out = K, g.rag = rag;
   if (some_dx) {
     g.rows_out = M, g.contraction = N;
-    g.A = w.q, g.sA = w.s, g.lda = np, g.ldsa = room16(M, E);
+    g.A = w.q, g.sA = w.s, g.lda = np, g.ldsa = pitch4(N);
     g.B = p->codes, g.sB = w.planes, g.ldb = kp, g.ldsb = kp, g.b_stride = N * kp, g.sb_stride = blocks_of(N) * kp;
     g.C = dX, g.ldc = lddx, g.clear = clear != 0;
     const hipError_t e = i8mp::launch_block_gemm(i8mp::kBlockInput, g, plan_dx(M, N, K, E), w.sums, s);

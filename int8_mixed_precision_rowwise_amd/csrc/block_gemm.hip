@@ -4,8 +4,7 @@
 // memory straight into LDS, four deep, and feed v_mfma_scale_f32_32x32x64_f8f6f4.  That
 // instruction multiplies each lane's 32 contraction values by a power of two of its own, so the
 // blocks' scales cost no vector operation: a lane needs the exponent's byte of its row (or
-// column) of each 128, which lies in planes [block][row] and comes into LDS the same way as the
-// codes, four blocks at a time (one more load a wave for every eight slabs).
+// column) of each 128, which comes into LDS the same way as the codes, four blocks at a time.
 #include "block.h"
 #include "gemm_pipelined.h"
 
@@ -145,14 +144,15 @@ constexpr int kLdsBytes = BM == 256 ? 4 * 512 * BK + 10240 : 4 * 256 * BK + 2048
 // second load of four waves).  Rows or columns past the operand are not looked at: a K-major operand's
 // lie past the descriptor's end and arrive as zeros, the others' are the next row's bytes or zeros, and
 // either only reach outputs that are not stored.
-template <int R, bool KMAJOR, int NW, bool REBASE>
+// GATHER (K-major): rows from anywhere in the operand, each at an offset of its own.
+template <int R, bool KMAJOR, int NW, bool REBASE, bool GATHER = false>
 struct Slabs {
   static constexpr int kInst = R * BK / 1024 / NW;
   static constexpr int CPR = R / 16, KR = 64 / CPR;               // [k][n] tiles: chunks a row, rows a load
   static constexpr bool kSwap = !KMAJOR && kInst > 1 && (NW * KR) % 32 == 16;
   static_assert(KMAJOR || kInst == 1 || (NW * KR) % 16 == 0, "the swizzle repeats from load to load");
   v4u rsrc;
-  uint32_t off, at;  // this lane's chunk in slab 0; its contraction index within a slab
+  uint32_t off[GATHER ? kInst : 1], at;  // this lane's chunk in slab 0; its contraction index within a slab
   int swap;          // what a swapped chunk's offset differs by
   uint32_t ld;
   const int8_t* base;
@@ -166,17 +166,29 @@ struct Slabs {
       bytes = min((int64_t)R, MN - mn0) * ld_;
       const int c = (lane & 3) ^ ((lane >> 4) & 3);
       at = 16 * c;
-      off = (16 * wave + (lane >> 2)) * ld + at;
+      off[0] = (16 * wave + (lane >> 2)) * ld + at;
     } else {
       base = p + mn0;
       bytes = (K - 1) * ld_ + min((int64_t)R, MN - mn0);
       const int k = wave * KR + lane / CPR, c = (lane % CPR) ^ mnmajor_swz(R, k);
       at = k;
-      off = k * ld + 16 * c;
+      off[0] = k * ld + 16 * c;
       if constexpr (kSwap) swap = c & 1 ? -16 : 16;
     }
     rsrc = Dma<64, true, NW>::make_rsrc(base, max((int64_t)0, min(bytes, (int64_t)kOob)));  // an empty contraction: nothing
   }
+  // Row `row` of the tile for load j of this lane, and where it is: one outside [0, n) is a row of zeros.
+  static __device__ __forceinline__ int row_of(int j, int wave, int lane) { return 16 * (wave + NW * j) + (lane >> 2); }
+  __device__ __forceinline__ void init_rows(const int8_t* p, int64_t ld_, int64_t n, int lane) {
+    ld = (uint32_t)ld_;
+    base = p, bytes = n * ld_;
+    at = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
+    rsrc = Dma<64, true, NW>::make_rsrc(base, bytes);
+  }
+  __device__ __forceinline__ void set_row(int j, int64_t src, int64_t n) {
+    off[j] = src >= 0 && src < n ? (uint32_t)src * ld + at : kOob;
+  }
+
   // Into byte `to` of LDS and the 1023 behind it.
   static __device__ __forceinline__ void load(uint32_t o, const v4u& r, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
@@ -188,7 +200,7 @@ struct Slabs {
   // which `left` = K - k0 contraction indices are the operand's, into the operand's tile at byte `to` of LDS.
   __device__ __forceinline__ void issue_at(int j, uint32_t to, int k0, uint32_t ahead, int left, int wave) const {
     const int limit = min(left, BK) - (KMAJOR ? 0 : NW * KR * j);
-    ahead += j * ((KMAJOR ? 16 * NW : NW * KR) * ld);
+    if constexpr (!GATHER) ahead += j * ((KMAJOR ? 16 * NW : NW * KR) * ld);
     v4u r = rsrc;
     if constexpr (REBASE && !KMAJOR) {
       const int64_t sh = (int64_t)k0 * ld;
@@ -196,7 +208,7 @@ struct Slabs {
       ahead -= (uint32_t)sh;
     }
     // what is the same in all lanes is added up in scalar registers
-    uint32_t o = off + (uint32_t)__builtin_amdgcn_readfirstlane(ahead);
+    uint32_t o = off[GATHER ? j : 0] + (uint32_t)__builtin_amdgcn_readfirstlane(ahead);
     if constexpr (kSwap) o += j & 1 ? swap : 0;
     load((int)at < limit ? o : kOob, r, to + (wave + NW * j) * 1024);
   }
@@ -216,17 +228,24 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>((lds_void*)const_cast<void*>(p)));
 }
 
-// Exponents of four blocks of one tile's rows (4 BM bytes, block after block) and columns (4 BN bytes
-// behind them): 256 bytes a load.
-template <int BM, int BN, int NW>
+// Exponents of four blocks of one tile: A's 4 BM bytes, row after row (ROWS) or block after block, and B's 4 BN
+// behind them, block after block; 256 bytes a load.
+template <int BM, int BN, int NW, bool ROWS>
 struct Exponents {
   static constexpr int kLoads = (BM + BN) / 64, kMine = (kLoads + NW - 1) / NW;  // of the workgroup, of a wave at most
-  const uint8_t *a, *b;         // at the tile's first row and column of the planes
-  int64_t lda, ldb, enda, endb; // plane pitches, bytes to the end of the planes
-  __device__ __forceinline__ void init(const uint8_t* sa, int64_t la, const uint8_t* sb, int64_t lb, int64_t a0, int64_t b0, int64_t blocks) {
-    a = sa + a0, b = sb + b0, lda = la, ldb = lb;
-    enda = blocks * la - a0, endb = blocks * lb - b0;
+  const uint8_t *a, *b;          // at the tile's first row and column
+  int64_t lda, ldb, enda, endb;  // pitches, bytes to the end of the exponents
+  uint32_t row[kMine];           // ROWS: this lane's row of A
+  // a0, b0: the tile's first row and column; arows: ROWS: rows of A from there on
+  __device__ __forceinline__ void init(const uint8_t* sa, int64_t la, const uint8_t* sb, int64_t lb, int64_t a0, int64_t b0,
+                                       int64_t blocks, int64_t arows, int wave, int lane) {
+    a = sa + (ROWS ? a0 * la : a0), b = sb + b0, lda = la, ldb = lb;
+    enda = ROWS ? arows * la : blocks * la - a0, endb = blocks * lb - b0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) row[i] = (uint32_t)((64 * (wave + NW * i) + lane) * la);
   }
+  // Row r of the tile for load i of this lane, if the load is one of A's.
+  static __device__ __forceinline__ int row_of(int i, int wave, int lane) { return 64 * (wave + NW * i) + lane; }
   __device__ __forceinline__ void issue(int8_t* buf, int64_t group, int wave, int lane) const {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
@@ -234,10 +253,10 @@ struct Exponents {
       if (load >= kLoads) break;
       const bool is_b = load >= BM / 64;
       const int R = is_b ? BN : BM, k = (is_b ? load - BM / 64 : load) * (256 / R) + lane / (R / 4);
-      const int64_t ld = is_b ? ldb : lda, skip = 4 * group * ld, left = (is_b ? endb : enda) - skip;
+      const int64_t ld = is_b ? ldb : lda, skip = 4 * group * (ROWS && !is_b ? 1 : ld), left = (is_b ? endb : enda) - skip;
       const v4u r = Dma<64, true, NW>::make_rsrc(reinterpret_cast<const int8_t*>((is_b ? b : a) + skip),
                                                  max((int64_t)0, min(left, (int64_t)kOob)));
-      const uint32_t o = (uint32_t)(k * ld + 4 * (lane % (R / 4)));
+      const uint32_t o = ROWS && !is_b ? row[i] : (uint32_t)(k * ld + 4 * (lane % (R / 4)));
       const uint32_t l = (uint32_t)__builtin_amdgcn_readfirstlane(
           (uint32_t)reinterpret_cast<uintptr_t>((lds_void*)(buf + load * 256)));
       asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
@@ -298,14 +317,14 @@ __device__ __forceinline__ Operands operands(const BlockGemm& g, const Place& p,
 
 // One tile: rows p.local on of the expert (WEIGHT: columns p.local on of A), columns n0 on; part `split` of the
 // contraction.
-template <int BM, int BN, int WR, int WGN, int STAGES, BlockProduct WHAT, bool REBASE, bool VEC>
+template <int BM, int BN, int WR, int WGN, int STAGES, BlockProduct WHAT, bool REBASE, bool VEC, bool GATHER>
 __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int64_t n0, uint32_t split, int8_t* lds) {
   constexpr int NW = WR * WGN;
   constexpr int WM = BM / WR, WN = BN / WGN, TM = WM / 32, TN = WN / 32;
   constexpr bool AK = WHAT != kBlockWeight, BKM = WHAT == kBlockForward;
   constexpr int A_BYTES = BM * BK, SLAB = A_BYTES + BN * BK;
   constexpr int EXPS = 4 * (BM + BN);  // bytes of four blocks' exponents
-  typedef Slabs<BM, AK, NW, REBASE> DA;
+  typedef Slabs<BM, AK, NW, REBASE, GATHER> DA;
   typedef Slabs<BN, BKM, NW, REBASE> DB;
   constexpr int NA = DA::kInst, PER = NA + DB::kInst;
   using S = SlabSchedule<TM, TN, PER>;
@@ -327,7 +346,7 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
     K = min(g.kchunk, K - k0);
     A += AK ? k0 : k0 * g.lda;
     B += BKM ? k0 : k0 * g.ldb;
-    sA += k0 / kBlock * g.ldsa, sB += k0 / kBlock * g.ldsb;
+    sA += AK ? k0 / kBlock : k0 / kBlock * g.ldsa, sB += k0 / kBlock * g.ldsb;
   }
   const int wm0 = (wave / WGN) * WM, wn0 = (wave % WGN) * WN;
   const int nk = (int)((K + BK - 1) / BK);
@@ -342,17 +361,33 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
   if (nk > 0) {  // an expert without rows: workgroup-uniform
     DA da;
     DB db;
-    da.init(A, g.lda, m0, a_rows, K, wave, lane);
     db.init(B, g.ldb, n0, BKM ? g.cols_out : g.ldb, K, wave, lane);
-    Exponents<BM, BN, NW> ex;
-    ex.init(sA, g.ldsa, sB, g.ldsb, m0, n0, blocks);
+    Exponents<BM, BN, NW, AK> ex;
+    if constexpr (GATHER) {
+      da.init_rows(A, g.lda, g.n_src, lane);
+      ex.init(sA, g.ldsa, sB, g.ldsb, 0, n0, blocks, g.n_src, wave, lane);
+      const int32_t* index = g.index + p.first + p.local;
+      const int last = (int)min(c_rows, (int64_t)BM) - 1;  // rows past it repeat it: their outputs are not stored
+#pragma unroll
+      for (int j = 0; j < NA; ++j) da.set_row(j, index[min(DA::row_of(j, wave, lane), last)], g.n_src);
+#pragma unroll
+      for (int i = 0; i < decltype(ex)::kMine; ++i) {
+        const int64_t src = index[min(decltype(ex)::row_of(i, wave, lane), last)];
+        ex.row[i] = src >= 0 && src < g.n_src ? (uint32_t)(src * g.ldsa) : kOob;
+      }
+    } else {
+      da.init(A, g.lda, m0, a_rows, K, wave, lane);
+      ex.init(sA, g.ldsa, sB, g.ldsb, m0, n0, blocks, a_rows - m0, wave, lane);
+    }
 
     v8i a[TM], b0[TN], b1[TN];
     int ea[TM], eb[TN], na[TM], nb[TN];  // exponents of this block and the next
     const auto read_exps = [&](int block) __attribute__((always_inline)) {
       const int8_t* at = exps + ((block >> 2) & 1) * EXPS + (lane & 31);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) na[i] = *reinterpret_cast<const uint8_t*>(at + (block & 3) * BM + wm0 + 32 * i);
+      for (int i = 0; i < TM; ++i)
+        na[i] = AK ? *reinterpret_cast<const uint8_t*>(exps + ((block >> 2) & 1) * EXPS + 4 * (wm0 + 32 * i + (lane & 31)) + (block & 3))
+                   : *reinterpret_cast<const uint8_t*>(at + (block & 3) * BM + wm0 + 32 * i);
 #pragma unroll
       for (int j = 0; j < TN; ++j) nb[j] = *reinterpret_cast<const uint8_t*>(at + 4 * BM + (block & 3) * BN + wn0 + 32 * j);
     };
@@ -493,6 +528,7 @@ struct BigLds {
   int8_t slabs[4 * 512 * BK];
   int8_t exps[5][4 * 512];  // four groups, and one that nobody reads
   int info[kBatch][8];
+  int index[2][256];  // of this tile's rows and the next one's
 };
 
 // Tiles info[0 .. n - 1] of 256 x 256, one after another without a pause: the pipeline's slab loads run on into
@@ -501,12 +537,12 @@ struct BigLds {
 // are two blocks ahead, so that they change to the next tile before the last two blocks, and the loop over a
 // tile's blocks has no branch in it (one would let the compiler move matrix instructions past the loads and reads that they
 // are to cover).
-template <BlockProduct WHAT, bool REBASE>
+template <BlockProduct WHAT, bool REBASE, bool GATHER>
 __device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& lds) {
   constexpr int BM = 256, BN = 256, WGN = 4, NW = 8, WM = 128, WN = 64, TM = 4, TN = 2;
   constexpr bool AK = WHAT != kBlockWeight, BKM = WHAT == kBlockForward;
   constexpr int A_BYTES = BM * BK, SLAB = A_BYTES + BN * BK;
-  typedef Slabs<BM, AK, NW, REBASE> DA;
+  typedef Slabs<BM, AK, NW, REBASE, GATHER> DA;
   typedef Slabs<BN, BKM, NW, REBASE> DB;
   constexpr int NA = DA::kInst, PER = NA + DB::kInst;
   using S = SlabSchedule<TM, TN, PER>;
@@ -536,8 +572,25 @@ __device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& 
   // counts one load, those that start no group one of zeros into a place of its own.
   const uint8_t* ex = nullptr;
   int64_t ex_left = 0;
-  const uint32_t ex_ld = (uint32_t)(wave < 4 ? g.ldsa : g.ldsb), ex_at = (wave & 3) * ex_ld + 4 * lane;
+  const bool ex_rows = AK && wave < 4;  // of 64 rows, four blocks each; otherwise of one block
+  const uint32_t ex_ld = (uint32_t)(wave < 4 ? g.ldsa : g.ldsb), ex_step = ex_rows ? 4 : 4 * ex_ld;
+  uint32_t ex_at = ex_rows ? (64 * wave + lane) * ex_ld : (wave & 3) * ex_ld + 4 * lane;
   int lgroup = 0;  // groups loaded so far
+  // GATHER: the index of a tile's rows comes into LDS while the tile before it is multiplied (waves 0 .. 3, 64
+  // rows each); at least four slabs are loaded and waited for before it is looked at.
+  const auto fetch_index = [&](int i) __attribute__((always_inline)) {
+    if constexpr (GATHER) {
+      if (i >= n || wave >= 4) return;
+      int64_t n0;
+      const Place p = place(i, n0);
+      const int64_t from = p.first + p.local;
+      const v4u r = Dma<64, true, NW>::make_rsrc(reinterpret_cast<const int8_t*>(g.index + from), min((g.rag.rows - from) * 4, (int64_t)1024));
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                   :
+                   : "s"(lds_address(lds.index[i & 1]) + wave * 256), "v"(256 * wave + 4 * lane), "s"(r)
+                   : "memory", "m0");
+    }
+  };
   const auto open = [&](int i) __attribute__((always_inline)) {
     lk = 0, ahead_a = 0, ahead_b = 0;
     if (i < n) {
@@ -545,10 +598,25 @@ __device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& 
       const Place p = place(i, n0);
       const Operands o = operands<WHAT>(g, p, n0);
       left = (int)o.K;
-      da.init(o.A, g.lda, o.m0, o.a_rows, o.K, wave, lane);
       db.init(o.B, g.ldb, n0, BKM ? g.cols_out : g.ldb, o.K, wave, lane);
-      ex = wave < 4 ? o.sA + o.m0 : o.sB + n0;
-      ex_left = (o.K + kBlock - 1) / kBlock * ex_ld - (wave < 4 ? o.m0 : n0);
+      const int64_t planes = (o.K + kBlock - 1) / kBlock * ex_ld;
+      if (wave >= 4) ex = o.sB + n0, ex_left = planes - n0;
+      else if (!AK) ex = o.sA + o.m0, ex_left = planes - o.m0;
+      if constexpr (GATHER) {
+        da.init_rows(o.A, g.lda, g.n_src, lane);
+        const int* index = lds.index[i & 1];
+#pragma unroll
+        for (int j = 0; j < NA; ++j) da.set_row(j, index[DA::row_of(j, wave, lane)], g.n_src);
+        if (wave < 4) {
+          const int src = index[64 * wave + lane];
+          ex = o.sA, ex_left = g.n_src * g.ldsa;
+          ex_at = src >= 0 && src < g.n_src ? (uint32_t)src * ex_ld : kOob;
+        }
+        fetch_index(i + 1);
+      } else {
+        da.init(o.A, g.lda, o.m0, o.a_rows, o.K, wave, lane);
+        if (ex_rows) ex = o.sA + o.m0 * g.ldsa, ex_left = (o.a_rows - o.m0) * g.ldsa;
+      }
     } else {
       left = 0, ex_left = 0;  // nothing but zeros
     }
@@ -561,8 +629,8 @@ __device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& 
                  :
                  : "s"((uint32_t)__builtin_amdgcn_readfirstlane(to)), "v"(starts ? ex_at : kOob), "s"(r)
                  : "memory", "m0");
-    ex += starts ? 4 * (int64_t)ex_ld : 0;
-    ex_left -= starts ? 4 * (int64_t)ex_ld : 0;
+    ex += starts ? ex_step : 0;
+    ex_left -= starts ? ex_step : 0;
     lgroup += starts;
   };
   const auto issue = [&](int d, uint32_t dst) __attribute__((always_inline)) {
@@ -587,7 +655,9 @@ __device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& 
   const auto read_exps = [&]() __attribute__((always_inline)) {
     const int8_t* at = lds.exps[rgroup & 3] + (lane & 31);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) na[i] = *reinterpret_cast<const uint8_t*>(at + rblock * BM + wm0 + 32 * i);
+    for (int i = 0; i < TM; ++i)
+      na[i] = AK ? *reinterpret_cast<const uint8_t*>(lds.exps[rgroup & 3] + 4 * (wm0 + 32 * i + (lane & 31)) + rblock)
+                 : *reinterpret_cast<const uint8_t*>(at + rblock * BM + wm0 + 32 * i);
 #pragma unroll
     for (int j = 0; j < TN; ++j) nb[j] = *reinterpret_cast<const uint8_t*>(at + 4 * BM + rblock * BN + wn0 + 32 * j);
   };
@@ -601,6 +671,11 @@ __device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& 
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf, af, acc[i][j], 0, 0, 0, eb[j], 0, ea[i]);
   };
 
+  if constexpr (GATHER) {
+    fetch_index(0);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    lds_barrier();
+  }
   open(0);
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -734,7 +809,7 @@ __device__ __forceinline__ void clear_rows(const BlockGemm& g) {
 }
 
 // Tiles of 128 x 128, two workgroups a CU.
-template <BlockProduct WHAT, bool REBASE, bool VEC>
+template <BlockProduct WHAT, bool REBASE, bool VEC, bool GATHER>
 __global__ __launch_bounds__(256, 2) void block_gemm_small(BlockGemm g) {
   __shared__ __attribute__((aligned(1024))) int8_t lds[kLdsBytes<128>];
   const uint32_t tiles_n = (uint32_t)((g.cols_out + 127) / 128), tiles_m = tile_rows<128, WHAT>(g);
@@ -746,11 +821,11 @@ __global__ __launch_bounds__(256, 2) void block_gemm_small(BlockGemm g) {
   const uint32_t split = g.splits > 1 ? tile / each : 0;
   int64_t n0;
   const Place p = tile_place<128, WHAT>(g, tile - split * each, tiles_m, tiles_n, n0);
-  multiply<128, 128, 2, 2, 4, WHAT, REBASE, VEC>(g, p, n0, split, lds);
+  multiply<128, 128, 2, 2, 4, WHAT, REBASE, VEC, GATHER>(g, p, n0, split, lds);
 }
 
 // Tiles of 256 x 256: a workgroup for each CU takes every 256th of them, then at most one quarter of the last ones.
-template <BlockProduct WHAT, bool REBASE>
+template <BlockProduct WHAT, bool REBASE, bool GATHER>
 __global__ __launch_bounds__(512, 2) void block_gemm_big(BlockGemm g) {
   __shared__ __attribute__((aligned(1024))) BigLds lds;
   const uint32_t tiles_n = (uint32_t)((g.cols_out + 255) / 256), tiles_m = tile_rows<256, WHAT>(g);
@@ -769,7 +844,7 @@ __global__ __launch_bounds__(512, 2) void block_gemm_big(BlockGemm g) {
       }
     }
     __syncthreads();
-    multiply_all<WHAT, REBASE>(g, n, lds);
+    multiply_all<WHAT, REBASE, GATHER>(g, n, lds);
   }
   // the quarters of a tile to one XCD
   for (uint32_t i = wg; i < (all - whole + 7) / 8 * 32; i += step) {
@@ -780,19 +855,19 @@ __global__ __launch_bounds__(512, 2) void block_gemm_big(BlockGemm g) {
     p.local += quarter & 1 ? 128 : 0;
     n0 += quarter & 2 ? 128 : 0;
     if (p.local >= (WHAT == kBlockWeight ? g.rows_out : p.count) || n0 >= g.cols_out) continue;
-    multiply<128, 128, 2, 4, 8, WHAT, REBASE, true>(g, p, n0, 0, lds.slabs);
+    multiply<128, 128, 2, 4, 8, WHAT, REBASE, true, GATHER>(g, p, n0, 0, lds.slabs);
     __syncthreads();  // the outputs have left LDS
   }
 }
 
-template <BlockProduct WHAT, bool REBASE>
+template <BlockProduct WHAT, bool REBASE, bool GATHER>
 void launch(const BlockGemm& g, bool big, bool vec, unsigned grid, hipStream_t stream) {
   if (big)
-    block_gemm_big<WHAT, REBASE><<<grid, 512, 0, stream>>>(g);
+    block_gemm_big<WHAT, REBASE, GATHER><<<grid, 512, 0, stream>>>(g);
   else if (vec)
-    block_gemm_small<WHAT, REBASE, true><<<grid, 256, 0, stream>>>(g);
+    block_gemm_small<WHAT, REBASE, true, GATHER><<<grid, 256, 0, stream>>>(g);
   else
-    block_gemm_small<WHAT, REBASE, false><<<grid, 256, 0, stream>>>(g);
+    block_gemm_small<WHAT, REBASE, false, GATHER><<<grid, 256, 0, stream>>>(g);
 }
 
 // At most: how many the experts' rows make, only the GPU knows.
@@ -816,9 +891,11 @@ hipError_t launch_tiles(const BlockGemm& g, const BlockPlan& plan, hipStream_t s
   const bool cut = n > whole_tiles((uint32_t)n) || (ragged && WHAT != kBlockWeight);
   const unsigned grid = (unsigned)(big ? cut ? kCUs : std::min<int64_t>(n, kCUs) : n);
   if (WHAT != kBlockForward && rebase)  // an operand read down its rows
-    launch<WHAT, WHAT != kBlockForward>(g, big, vec, grid, stream);
+    launch<WHAT, WHAT != kBlockForward, false>(g, big, vec, grid, stream);
+  else if (WHAT == kBlockForward && g.index)
+    launch<WHAT, false, WHAT == kBlockForward>(g, big, vec, grid, stream);
   else
-    launch<WHAT, false>(g, big, vec, grid, stream);
+    launch<WHAT, false, false>(g, big, vec, grid, stream);
   return hipGetLastError();
 }
 
@@ -839,7 +916,7 @@ BlockPlan block_plan(BlockProduct what, int64_t rows, int64_t cols, int64_t cont
   if (ragged || p.big || small == 0) return p;
   const int64_t s = std::min<int64_t>(kCUs / small, contraction / 512);
   if (s < 3) return p;
-  p.kchunk = ((contraction + s - 1) / s + kBlock - 1) / kBlock * kBlock;
+  p.kchunk = ((contraction + s - 1) / s + 4 * kBlock - 1) / (4 * kBlock) * (4 * kBlock);  // whole groups of exponents
   p.splits = (contraction + p.kchunk - 1) / p.kchunk;
   p.plane_ld = (cols + 3) / 4 * 4;
   return p;

@@ -101,9 +101,9 @@ __device__ __forceinline__ void quant_tile(const BlockQuant& q, int64_t slot, in
   }
   __syncthreads();
   if constexpr (ROWS) {
-    const int half = t / kTileRows, r = t % kTileRows;
-    const int64_t block = 2 * ct + half;
-    if (r < rows && block * kBlock < q.cols) q.s_row[block * q.ld_srow + 16 * unit_of<16>(p) + p.local + r] = lds.byte[half][r];
+    if (t < rows)  // both blocks' exponents; the second one's place is there even where its columns are not
+      *reinterpret_cast<uint16_t*>(q.s_row + (16 * unit_of<16>(p) + p.local + t) * q.ld_srow + 2 * ct) =
+          (uint16_t)(lds.byte[0][t] | lds.byte[1][t] << 8);
   }
   if constexpr (COLS) {
     if (col < q.ldq) {

@@ -7,6 +7,11 @@
 // tokens' order without an atomic whose order matters: a workgroup counts its block of tokens,
 // and in a second launch each adds up the blocks before it and ranks its own entries by ballots
 // over the bits of the expert's number.  One block of tokens needs one launch.
+//
+// All of it is short work in waves that wait: 32768 tokens to 4 of 64 (bf16) choose in 6.9 us and
+// place in 6.5, where 13 MB need 2.5; scores loaded one by one, searched each round and turned to
+// weights one at a time took 10.2 to choose.  The gradient takes 7.7 us (7 MB of 32768 x 64), a
+// launch of 16 tokens to 4 of 64 4.7.
 #include "route.h"
 
 #include <algorithm>
@@ -15,8 +20,9 @@ namespace i8mp {
 namespace {
 
 constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
-constexpr int64_t kRouteBlock = 256;      // tokens a workgroup, and at most this many blocks
-constexpr int64_t kRouteMaxBlocks = 256;
+// Tokens a workgroup counts, at least, and workgroups at most: one for each CU.  (32768 tokens, 4 of 64 experts: choosing
+// took 12.8 us with 128 workgroups of 256 tokens and 10.2 with 256 of 128, placing 6.4 and 8.2.)
+constexpr int64_t kRouteBlock = 128, kRouteMaxBlocks = 256;
 
 template <int DT>
 __device__ __forceinline__ float load_as_float(const void* p, int64_t i) {
@@ -50,69 +56,160 @@ __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); 
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// A token's scores: lane l of its G has experts l J .. l J + J - 1.  bad: one is NaN or +inf.
-template <int G, int J, int DT>
+// A token's scores: lane l of its G has experts l J .. l J + J - 1.  VEC: J of them are there or none, and lie at a
+// multiple of their size (of 16 bytes at most).
+template <int DT, int J>
+struct Lanes {
+  static constexpr int kSize = DT == I8MP_FP32 ? 4 : 2, kPer = J * kSize > 16 ? 16 / kSize : J;  // elements of one load
+};
+template <int G, int J, int DT, bool VEC>
 __device__ __forceinline__ void load_scores(const RouteArgs& a, int64_t t, int lane, float (&x)[J]) {
+  typedef Lanes<DT, J> L;
+  if constexpr (VEC) {
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    const int e = lane * J + j;
-    x[j] = e < a.E ? load_as_float<DT>(a.logits, t * a.ld + e) : -INFINITY;
+    for (int j = 0; j < J; ++j) x[j] = -INFINITY;
+    if (lane * J < a.E) {
+      typedef uint32_t words __attribute__((ext_vector_type(L::kPer * L::kSize / 4)));
+      const char* p = static_cast<const char*>(a.logits) + (t * a.ld + lane * J) * L::kSize;
+#pragma unroll
+      for (int i = 0; i < J; i += L::kPer) {
+        const words w = *reinterpret_cast<const words*>(p + i * L::kSize);
+#pragma unroll
+        for (int j = 0; j < L::kPer; ++j) {
+          if constexpr (DT == I8MP_FP32) x[i + j] = __uint_as_float(w[j]);
+          if constexpr (DT == I8MP_BF16) x[i + j] = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+          if constexpr (DT == I8MP_FP16) x[i + j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[j / 2] >> (16 * (j & 1))));
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int e = lane * J + j;
+      x[j] = e < a.E ? load_as_float<DT>(a.logits, t * a.ld + e) : -INFINITY;
+    }
   }
 }
 
-// The k choices of token t (G lanes, all of them here), written by the lanes that win; counts in LDS.
-template <int G, int J, int DT>
-__device__ __forceinline__ void choose(const RouteArgs& a, int64_t t, int lane, int32_t* counts) {
-  float x[J], left[J];
-  load_scores<G, J, DT>(a, t, lane, x);
+template <int J, int DT, bool VEC>
+__device__ __forceinline__ void store_scores(const RouteArgs& a, void* d, int64_t at, int lane, const float (&v)[J]) {
+  typedef Lanes<DT, J> L;
+  if constexpr (VEC) {
+    if (lane * J >= a.E) return;
+    typedef uint32_t words __attribute__((ext_vector_type(L::kPer * L::kSize / 4)));
+    char* p = static_cast<char*>(d) + (at + lane * J) * L::kSize;
+#pragma unroll
+    for (int i = 0; i < J; i += L::kPer) {
+      __attribute__((aligned(16))) char buf[L::kPer * L::kSize];
+#pragma unroll
+      for (int j = 0; j < L::kPer; ++j) store_float<DT>(buf, j, v[i + j]);
+      *reinterpret_cast<words*>(p + i * L::kSize) = *reinterpret_cast<const words*>(buf);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (lane * J + j < a.E) store_float<DT>(d, at + lane * J + j, v[j]);
+  }
+}
+
+// Whether score (v, e) comes before (w, f).
+__device__ __forceinline__ bool before(float v, int e, float w, int f) { return v > w || (v == w && e < f); }
+
+// A lane's scores, of which the best is asked for again and again.  Four are sorted first, so that the best is
+// the first; sixteen are searched each time.
+template <int J>
+struct Best {
+  float v[J];
+  int e[J];
+  __device__ __forceinline__ void init(const float (&x)[J]) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) v[j] = x[j] == x[j] ? x[j] : -INFINITY, e[j] = j;  // NaN is never taken
+    if constexpr (J == 4) {
+      order(0, 1), order(2, 3), order(0, 2), order(1, 3), order(1, 2);
+    }
+  }
+  __device__ __forceinline__ void order(int i, int j) {
+    const bool swap = before(v[j], e[j], v[i], e[i]);
+    const float a = v[i], b = v[j];
+    const int c = e[i], d = e[j];
+    v[i] = swap ? b : a, v[j] = swap ? a : b;
+    e[i] = swap ? d : c, e[j] = swap ? c : d;
+  }
+  __device__ __forceinline__ float top() const {
+    float t = v[0];
+    if constexpr (J != 4) {
+#pragma unroll
+      for (int j = 1; j < J; ++j) t = fmaxf(t, v[j]);
+    }
+    return t;
+  }
+  // The first of the scores `t`, taken away.
+  __device__ __forceinline__ int pop(float t) {
+    if constexpr (J == 4) {
+      const int first = e[0];
+#pragma unroll
+      for (int j = 0; j < J - 1; ++j) v[j] = v[j + 1], e[j] = e[j + 1];
+      v[J - 1] = -INFINITY;
+      return first;
+    } else {
+      int at = J - 1;
+#pragma unroll
+      for (int j = J - 1; j >= 0; --j) at = v[j] == t ? j : at;
+#pragma unroll
+      for (int j = 0; j < J; ++j) v[j] = j == at ? -INFINITY : v[j];
+      return at;
+    }
+  }
+};
+
+// The k choices of token t (G lanes, all of them here), written by the lanes that have them; counts in LDS.  Lane
+// r % G keeps round r's score, so that exponentials and divisions are one for all rounds.
+template <int G, int J>
+__device__ __forceinline__ void choose(const RouteArgs& a, int64_t t, int lane, const float (&x)[J], int32_t* counts) {
   bool bad = false;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    bad |= !(x[j] < INFINITY);  // NaN, +inf
-    left[j] = x[j] == x[j] ? x[j] : -INFINITY;
-  }
+  for (int j = 0; j < J; ++j) bad |= !(x[j] < INFINITY);  // NaN, +inf
+  Best<J> best;
+  best.init(x);
   const int shift = (threadIdx.x & 63) & ~(G - 1);  // the group's first lane in the wave
   constexpr uint64_t kGroup = G == 64 ? ~uint64_t(0) : (uint64_t(1) << G) - 1;
   bad = (__ballot(bad) >> shift) & kGroup;
   constexpr int kKept = kRouteMaxK / G + (kRouteMaxK % G != 0);
-  float m = 0.0f, taken = 0.0f, kept[kKept];  // lane r % G keeps round r's score
-  for (int r = 0; r < a.k; ++r) {
-    float best = left[0];
+  float m = 0.0f, kept[kKept];
 #pragma unroll
-    for (int j = 1; j < J; ++j) best = larger(best, left[j]);
-    const float top = over_lanes<G>(best, larger);
-    const uint64_t who = (__ballot(best == top) >> shift) & kGroup;
+  for (int i = 0; i < kKept; ++i) kept[i] = -INFINITY;
+  for (int r = 0; r < a.k; ++r) {
+    const float mine = best.top(), top = over_lanes<G>(mine, larger);
+    const uint64_t who = (__ballot(mine == top) >> shift) & kGroup;
     const bool some = top > -INFINITY;
     if (r == 0) m = some ? top : 0.0f;
-    const float s = !some ? 0.0f : a.score == I8MP_SIGMOID ? sigmoid(top) : expf(top - m);
-    taken += s;
 #pragma unroll
     for (int i = 0; i < kKept; ++i)
-      if (lane + G * i == r) kept[i] = s;
+      if (lane + G * i == r) kept[i] = top;
     if (lane == __builtin_ctzll(who)) {
-      int at = J - 1;
-#pragma unroll
-      for (int j = J - 1; j >= 0; --j) at = left[j] == top ? j : at;
-      const int e = lane * J + at;
+      const int e = lane * J + best.pop(top);
       a.experts[t * a.k + r] = some ? e : -1;
       if (some) atomicAdd(counts + e, 1);
-#pragma unroll
-      for (int j = 0; j < J; ++j) left[j] = j == at ? -INFINITY : left[j];
     }
   }
-  float total = taken;
-  if (!a.normalize) {
-    total = 1.0f;
-    if (a.score == I8MP_SOFTMAX) {
-      float sum = 0.0f;
+  float s[kKept], taken = 0.0f;
 #pragma unroll
-      for (int j = 0; j < J; ++j) sum += expf(x[j] - m);
-      total = over_lanes<G>(sum, add);
-    }
+  for (int i = 0; i < kKept; ++i) {
+    s[i] = !(kept[i] > -INFINITY) ? 0.0f : a.score == I8MP_SIGMOID ? sigmoid(kept[i]) : expf(kept[i] - m);
+    taken += s[i];
+  }
+  float total = 1.0f;
+  if (a.normalize) {
+    total = over_lanes<G>(taken, add);
+  } else if (a.score == I8MP_SOFTMAX) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) sum += expf(x[j] - m);
+    total = over_lanes<G>(sum, add);
   }
 #pragma unroll
   for (int i = 0; i < kKept; ++i)
-    if (lane + G * i < a.k) a.weights[t * a.k + lane + G * i] = bad ? NAN : kept[i] > 0.0f ? kept[i] / total : 0.0f;
+    if (lane + G * i < a.k) a.weights[t * a.k + lane + G * i] = bad ? NAN : s[i] > 0.0f ? s[i] / total : 0.0f;
 }
 
 // Ranks of the block's entries and where they go.  base[e]: first row of the block's entries
@@ -178,7 +275,7 @@ __device__ __forceinline__ void first_rows(const int32_t* counts, int32_t* first
 }
 
 // LDS: counts [E], first [E + 1], within [waves][E] (16 bits).
-template <int G, int J, int DT, bool ONE>
+template <int G, int J, int DT, bool VEC, bool ONE>
 __global__ __launch_bounds__(kRouteThreads) void route_choose(RouteArgs a, int64_t per) {
   extern __shared__ int32_t lds[];
   const int E = (int)a.E, t = threadIdx.x;
@@ -187,7 +284,15 @@ __global__ __launch_bounds__(kRouteThreads) void route_choose(RouteArgs a, int64
   for (int e = t; e < E; e += kRouteThreads) counts[e] = 0;
   __syncthreads();
   const int64_t t0 = blockIdx.x * per, n = min(per, a.T - t0);
-  for (int64_t i = t / G; i < n; i += kRouteThreads / G) choose<G, J, DT>(a, t0 + i, t & (G - 1), counts);
+  constexpr int kAtOnce = kRouteThreads / G;
+  float x[J], next[J];
+  if (t / G < n) load_scores<G, J, DT, VEC>(a, t0 + t / G, t & (G - 1), x);
+  for (int64_t i = t / G; i < n; i += kAtOnce) {  // whole groups
+    if (i + kAtOnce < n) load_scores<G, J, DT, VEC>(a, t0 + i + kAtOnce, t & (G - 1), next);
+    choose<G, J>(a, t0 + i, t & (G - 1), x, counts);
+#pragma unroll
+    for (int j = 0; j < J; ++j) x[j] = next[j];
+  }
   __syncthreads();
   if constexpr (!ONE) {
     for (int e = t; e < E; e += kRouteThreads) a.hist[blockIdx.x * a.E + e] = counts[e];
@@ -213,6 +318,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_place(RouteArgs a, int64_
   const int parts = kRouteThreads / E, e = t % E, part = t / E;  // E <= kRouteThreads
   if (part < parts) {
     int32_t all = 0, some = 0;
+#pragma unroll 8
     for (int b = part; b < blocks; b += parts) {
       const int32_t c = a.hist[(int64_t)b * E + e];
       all += c;
@@ -238,7 +344,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_place(RouteArgs a, int64_
 // Gradient at a token's scores: with g the gradients of the taken weights w and S their sum,
 // <g, w> = inner, softmax gives p (g - inner) (over all, or the taken alone with their w), the
 // normalized sigmoid w (1 - s) (g - inner), the plain one g s (1 - s).
-template <int G, int J, int DT>
+template <int G, int J, int DT, bool VEC>
 __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __restrict__ experts,
                                                   const float* __restrict__ dw, void* __restrict__ d, int64_t ldd) {
   const int64_t t = (blockIdx.x * (int64_t)256 + threadIdx.x) / G;
@@ -246,7 +352,7 @@ __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __
   const int lane = threadIdx.x & (G - 1);
   float x[J], g[J];
   bool mine[J], bad = false;
-  load_scores<G, J, DT>(a, t, lane, x);
+  load_scores<G, J, DT, VEC>(a, t, lane, x);
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -278,19 +384,18 @@ __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __
   inner = over_lanes<G>(inner, add);
   const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
   inner *= r;
+  float v[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
-    const int e = lane * J + j;
-    if (e >= a.E) continue;
-    float v;
     if (sig) {
       const float slope = s[j] * (1.0f - s[j]);
-      v = !mine[j] ? 0.0f : a.normalize ? (g[j] - inner) * r * slope : g[j] * slope;
+      v[j] = !mine[j] ? 0.0f : a.normalize ? (g[j] - inner) * r * slope : g[j] * slope;
     } else {
-      v = a.normalize && !mine[j] ? 0.0f : s[j] * r * (g[j] - inner);
+      v[j] = a.normalize && !mine[j] ? 0.0f : s[j] * r * (g[j] - inner);
     }
-    store_float<DT>(d, t * ldd + e, bad ? NAN : v);
+    v[j] = bad ? NAN : v[j];
   }
+  store_scores<J, DT, VEC>(a, d, t * ldd, lane, v);
 }
 
 // ---- the weighted sums ------------------------------------------------------
@@ -400,37 +505,62 @@ __global__ __launch_bounds__(256) void combine_back(CombineArgs a, int64_t first
   }
 }
 
-template <int G, int J, int DT>
+template <int G, int J, int DT, bool VEC>
 void choose_blocks(const RouteArgs& a, int64_t per, int blocks, hipStream_t stream) {
   const size_t small = (size_t)(2 * a.E + 1) * 4, ranks = (size_t)kRouteWaves * a.E * 2;
   if (blocks == 1) {
-    route_choose<G, J, DT, true><<<1, kRouteThreads, small + ranks, stream>>>(a, per);
+    route_choose<G, J, DT, VEC, true><<<1, kRouteThreads, small + ranks, stream>>>(a, per);
   } else {
-    route_choose<G, J, DT, false><<<(unsigned)blocks, kRouteThreads, small, stream>>>(a, per);
+    route_choose<G, J, DT, VEC, false><<<(unsigned)blocks, kRouteThreads, small, stream>>>(a, per);
     route_place<<<(unsigned)blocks, kRouteThreads, small + (size_t)a.E * 4 + ranks, stream>>>(a, per, blocks);
   }
+}
+
+// Whether a lane's J scores of a matrix can be moved at once.
+template <int DT, int J>
+bool whole_lanes(const RouteArgs& a, const void* p, int64_t ld) {
+  typedef Lanes<DT, J> L;
+  constexpr int64_t kBytes = L::kPer * L::kSize;
+  return a.E % J == 0 && (reinterpret_cast<uintptr_t>(p) % kBytes) == 0 && ld * L::kSize % kBytes == 0;
+}
+
+template <int G, int J, int DT>
+void choose_lanes(const RouteArgs& a, int64_t per, int blocks, hipStream_t stream) {
+  if (whole_lanes<DT, J>(a, a.logits, a.ld))
+    choose_blocks<G, J, DT, true>(a, per, blocks, stream);
+  else
+    choose_blocks<G, J, DT, false>(a, per, blocks, stream);
 }
 
 template <int DT>
 void route_as(const RouteArgs& a, int64_t per, int blocks, hipStream_t stream) {
   if (a.E <= 64)
-    choose_blocks<16, 4, DT>(a, per, blocks, stream);
+    choose_lanes<16, 4, DT>(a, per, blocks, stream);
   else if (a.E <= 256)
-    choose_blocks<16, 16, DT>(a, per, blocks, stream);
+    choose_lanes<16, 16, DT>(a, per, blocks, stream);
   else
-    choose_blocks<64, 16, DT>(a, per, blocks, stream);
+    choose_lanes<64, 16, DT>(a, per, blocks, stream);
 }
 
 constexpr int64_t kMaxGrid = int64_t(1) << 23;  // workgroups of 256: fewer than 2^32 work items
 
+template <int G, int J, int DT>
+void route_back_lanes(const RouteArgs& a, const int32_t* experts, const float* dw, void* d, int64_t ldd, hipStream_t stream) {
+  const unsigned grid = (unsigned)((a.T + 256 / G - 1) / (256 / G));
+  if (whole_lanes<DT, J>(a, a.logits, a.ld) && whole_lanes<DT, J>(a, d, ldd))
+    route_back<G, J, DT, true><<<grid, 256, 0, stream>>>(a, experts, dw, d, ldd);
+  else
+    route_back<G, J, DT, false><<<grid, 256, 0, stream>>>(a, experts, dw, d, ldd);
+}
+
 template <int DT>
 void route_back_as(const RouteArgs& a, const int32_t* experts, const float* dw, void* d, int64_t ldd, hipStream_t stream) {
   if (a.E <= 64)
-    route_back<16, 4, DT><<<(unsigned)((a.T + 15) / 16), 256, 0, stream>>>(a, experts, dw, d, ldd);
+    route_back_lanes<16, 4, DT>(a, experts, dw, d, ldd, stream);
   else if (a.E <= 256)
-    route_back<16, 16, DT><<<(unsigned)((a.T + 15) / 16), 256, 0, stream>>>(a, experts, dw, d, ldd);
+    route_back_lanes<16, 16, DT>(a, experts, dw, d, ldd, stream);
   else
-    route_back<64, 16, DT><<<(unsigned)((a.T + 3) / 4), 256, 0, stream>>>(a, experts, dw, d, ldd);
+    route_back_lanes<64, 16, DT>(a, experts, dw, d, ldd, stream);
 }
 
 template <int DT, int W>

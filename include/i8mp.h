@@ -567,7 +567,9 @@ i8mp_status i8mp_quantize_block_weight(const uint16_t* W, int64_t E, int64_t N, 
  *   rows: NULL, or int32 [M]: row r is X's row rows[r], of `tokens` (at least 1); one
  *     outside them is a row of zeros
  *   X: bf16 [tokens x K], rows 16-byte aligned
- *   Sizes: M < 2^28, N and K < 2^23, experts < 2^16.
+ *   Sizes: M < 2^28, N and K < 2^23, experts < 2^16; with blocks of 128 rounded up,
+ *     (M / 128 + experts + 1) (N / 128 + K / 128 + 2) and experts (N / 128 + 1)
+ *     (K / 128 + 1) < 2^22 (2^23 rows of 2048 x 2048, 255 experts of 16256 x 16256).
  */
 typedef struct {
   int64_t M, N, K;

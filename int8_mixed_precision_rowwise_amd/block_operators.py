@@ -333,16 +333,16 @@ def expert_route(logits: torch.Tensor, k: int, score: str = "softmax", normalize
     rows behind offsets[E] are -1."""
     p, dev = _route(logits, k, score, normalize, workspace=workspace)
     T, E = p.T, p.E
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    ints = torch.empty(3 * T * k + E + 1, dtype=_i32, device=dev)
     n = T * k
-    experts, places, rows, offsets = ints[:n].view(T, k), ints[n:2 * n].view(T, k), ints[2 * n:3 * n], ints[3 * n:]
+    weights = torch.empty(T, k, dtype=torch.float32, device=dev)
+    ints = torch.empty(3 * n + E + 1, dtype=_i32, device=dev)
+    experts, places, rows, offsets = ints.split_with_sizes((n, n, n, E + 1))
     need = _pkg.lib.i8mp_expert_route_workspace_bytes(T, E, k)
     ws = _space(workspace, need, dev) if need else None
     at = ints.data_ptr()
     _call(dev, "i8mp_expert_route", p, _ptr(weights), at, at + 4 * n, at + 8 * n, at + 12 * n, None if ws is None else ws.data_ptr(),
           0 if ws is None else ws.numel())
-    return Route(weights, experts, places, rows, offsets)
+    return Route(weights, experts.view(T, k), places.view(T, k), rows, offsets)
 
 
 def expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
@@ -364,7 +364,7 @@ def _combine(Y, places, weights, same=(), rows=None):
         (R, N), (T, k) = Y.shape, places.shape
         sy = Y.stride()
         fine = (Y.dtype in _DTYPE and T > 0 and R > 0 and N > 0 and k > 0 and sy[1] == 1 and sy[0] >= N and places.dtype == _i32
-                and places.is_contiguous() and _on_gpu(Y, places, weights, rows, *(t for t, _ in same)))
+                and places.is_contiguous() and _on_gpu(Y, places, weights, rows))
         if weights is not None:
             fine = fine and weights.shape == (T, k) and weights.dtype == torch.float32 and weights.is_contiguous()
         if rows is not None:
@@ -372,7 +372,7 @@ def _combine(Y, places, weights, same=(), rows=None):
         for t, _ in same:
             if t is not None:
                 st = t.stride()
-                fine = fine and t.shape == (T, N) and t.dtype == Y.dtype and st[1] == 1 and st[0] >= N
+                fine = fine and t.shape == (T, N) and t.dtype == Y.dtype and st[1] == 1 and st[0] >= N and t.get_device() == Y.get_device()
     except (AttributeError, IndexError, TypeError, ValueError):
         fine = False
     if not fine:
@@ -403,7 +403,7 @@ def expert_combine(Y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor 
     rows read through expert_route's `rows`.  Sums are fp32, in the order of j, rounded
     once.  residual may be `out` itself."""
     p, dev = _combine(Y, places, weights, ((residual, "residual"), (out, "out")))
-    out = torch.empty((p.T, p.N), dtype=Y.dtype, device=dev) if out is None else out
+    out = torch.empty(p.T, p.N, dtype=Y.dtype, device=dev) if out is None else out
     _call(dev, "i8mp_expert_combine", p, _ptr(residual), 0 if residual is None else _ld2(residual), _ptr(out), _ld2(out))
     return out
 

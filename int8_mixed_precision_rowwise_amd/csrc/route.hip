@@ -23,6 +23,10 @@ constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
 // Tokens a workgroup counts, at least, and workgroups at most: one for each CU.  (32768 tokens, 4 of 64 experts: choosing
 // took 12.8 us with 128 workgroups of 256 tokens and 10.2 with 256 of 128, placing 6.4 and 8.2.)
 constexpr int64_t kRouteBlock = 128, kRouteMaxBlocks = 256;
+// Tokens that one workgroup takes alone, in one launch, up to 64 experts and beyond.  (Replayed, one launch and two: 256
+// tokens to 2 of 8 8.7 us and 8.4, to 4 of 64 11.0 and 9.5, to 8 of 256 33.4 and 21.8, 200 tokens to 4 of 64 9.3
+// either way; a second launch costs the host 2 us.)
+constexpr int64_t kRouteAlone = 256, kRouteAloneMany = 128;
 
 template <int DT>
 __device__ __forceinline__ float load_as_float(const void* p, int64_t i) {
@@ -346,8 +350,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_place(RouteArgs a, int64_
 // normalized sigmoid w (1 - s) (g - inner), the plain one g s (1 - s).
 template <int G, int J, int DT, bool VEC>
 __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __restrict__ experts,
-                                                  const float* __restrict__ dw, void* __restrict__ d, int64_t ldd) {
-  const int64_t t = (blockIdx.x * (int64_t)256 + threadIdx.x) / G;
+                                                  const float* __restrict__ dw, void* __restrict__ d, int64_t ldd, int64_t first) {
+  const int64_t t = first + (blockIdx.x * (int64_t)256 + threadIdx.x) / G;
   if (t >= a.T) return;  // whole groups
   const int lane = threadIdx.x & (G - 1);
   float x[J], g[J];
@@ -546,11 +550,16 @@ constexpr int64_t kMaxGrid = int64_t(1) << 23;  // workgroups of 256: fewer than
 
 template <int G, int J, int DT>
 void route_back_lanes(const RouteArgs& a, const int32_t* experts, const float* dw, void* d, int64_t ldd, hipStream_t stream) {
-  const unsigned grid = (unsigned)((a.T + 256 / G - 1) / (256 / G));
-  if (whole_lanes<DT, J>(a, a.logits, a.ld) && whole_lanes<DT, J>(a, d, ldd))
-    route_back<G, J, DT, true><<<grid, 256, 0, stream>>>(a, experts, dw, d, ldd);
-  else
-    route_back<G, J, DT, false><<<grid, 256, 0, stream>>>(a, experts, dw, d, ldd);
+  constexpr int64_t kTokens = 256 / G;  // of a workgroup
+  const int64_t n = (a.T + kTokens - 1) / kTokens;
+  const bool vec = whole_lanes<DT, J>(a, a.logits, a.ld) && whole_lanes<DT, J>(a, d, ldd);
+  for (int64_t b = 0; b < n; b += kMaxGrid) {
+    const unsigned grid = (unsigned)std::min(kMaxGrid, n - b);
+    if (vec)
+      route_back<G, J, DT, true><<<grid, 256, 0, stream>>>(a, experts, dw, d, ldd, b * kTokens);
+    else
+      route_back<G, J, DT, false><<<grid, 256, 0, stream>>>(a, experts, dw, d, ldd, b * kTokens);
+  }
 }
 
 template <int DT>
@@ -579,10 +588,13 @@ void combine_back_as(const CombineArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t route_block_tokens(int64_t T) { return std::max(kRouteBlock, (T + kRouteMaxBlocks - 1) / kRouteMaxBlocks); }
+int64_t route_block_tokens(int64_t T, int64_t E) {
+  const int64_t alone = E <= 64 ? kRouteAlone : kRouteAloneMany;
+  return T <= alone ? alone : std::max(kRouteBlock, (T + kRouteMaxBlocks - 1) / kRouteMaxBlocks);
+}
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
-  const int64_t per = route_block_tokens(a.T);
+  const int64_t per = route_block_tokens(a.T, a.E);
   const int blocks = (int)std::max<int64_t>(1, (a.T + per - 1) / per);
   switch (a.dtype) {
     case I8MP_BF16: route_as<I8MP_BF16>(a, per, blocks, stream); break;

@@ -44,12 +44,14 @@ from typing import Callable, Optional
 import torch
 
 from . import linear_bwd, linear_bwd_fp8, linear_fwd, linear_fwd_colmax, linear_fwd_fp8, linear_fwd_fp8_colmax
+from . import block_operators as _block
 from . import operators as _ops
 
 __all__ = ["Int8MixedPrecisionConfig", "Int8MixedPrecisionLinearFunction",
            "Int8MixedPrecisionLinear", "swap_linear_modules", "STEP_STRIDE", "STEPS_PER_KEY",
            "module_seed", "step_key_offset", "sr_checkpoint_contexts", "RotaryFunction", "rotary", "DistillFunction", "distill_loss",
-           "LinearActFunction", "linear_act", "Int8MixedPrecisionActLinear"]
+           "LinearActFunction", "linear_act", "Int8MixedPrecisionActLinear", "LinearBlockFunction", "linear_block",
+           "ExpertLinearFunction", "expert_linear", "ExpertRouteFunction", "expert_route", "ExpertCombineFunction", "expert_combine"]
 
 STEP_STRIDE = 8 << 40  # Philox blocks reserved per linear step (6 passes of 2**40 each, rounded up)
 STEPS_PER_KEY = (1 << 64) // STEP_STRIDE  # steps whose offsets fit the 64-bit block counter
@@ -474,3 +476,139 @@ class Int8MixedPrecisionActLinear(Int8MixedPrecisionLinear):
 
     def extra_repr(self) -> str:
         return super().extra_repr() + f", bias={self.bias is not None}, activation={self.activation}"
+
+
+class LinearBlockFunction(torch.autograd.Function):
+    """y = x @ weight.T with all three GEMMs over E4M3 codes with a scale for each 128 of
+    the contraction (block_operators).  Saved for backward: the input and the weight's
+    codes.  There is no second derivative: asking for one raises."""
+
+    @staticmethod
+    def forward(ctx, x, weight, codes, exponents):
+        x2 = _aligned_rows(x, x.shape[-1])
+        ctx.save_for_backward(x2, codes, exponents)
+        ctx.shape = x.shape
+        return _block.linear_block_fwd(x2, codes, exponents).reshape(*x.shape[:-1], codes.shape[0])
+
+    @staticmethod
+    def backward(ctx, dy):
+        x2, codes, exponents = ctx.saved_tensors
+        dx, dw = _block.linear_block_bwd(_aligned_rows(dy, codes.shape[0]), x2, codes, exponents,
+                                         ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        return _once("linear_block", None if dx is None else dx.reshape(ctx.shape)), _once("linear_block", dw), None, None
+
+
+def _weight_codes(weight: torch.Tensor, quantized):
+    """The codes given, or the weight's own."""
+    if quantized is not None:
+        codes, exponents = quantized
+        return codes, exponents
+    with torch.no_grad():
+        rows = _aligned_rows(weight, weight.shape[-1])
+        return _block.quantize_block_weight(rows if weight.dim() == 2 else rows.unflatten(0, weight.shape[:-1]))
+
+
+def linear_block(x: torch.Tensor, weight: torch.Tensor, quantized=None) -> torch.Tensor:
+    """operators.linear_block_fwd with a gradient: x [..., K], weight [N, K], bf16.
+
+    quantized: what quantize_block_weight gave for this weight, where several calls
+    share it between two updates; else the call quantizes the weight.  The backward
+    takes the same codes."""
+    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"shapes {tuple(x.shape)} and {tuple(weight.shape)} do not match")
+    codes, exponents = _weight_codes(weight, quantized)
+    if codes.shape[:-1] != weight.shape[:-1]:
+        raise ValueError(f"quantized: codes {tuple(codes.shape)} are not those of a weight {tuple(weight.shape)}")
+    return LinearBlockFunction.apply(x, weight, codes, exponents)
+
+
+class ExpertLinearFunction(torch.autograd.Function):
+    """linear_block for each of many experts over their rows.  Saved for backward: the
+    input, the weights' codes and what says whose the rows are.  There is no second
+    derivative: asking for one raises."""
+
+    @staticmethod
+    def forward(ctx, x, weight, codes, exponents, offsets, rows, places):
+        x2 = _aligned_rows(x, x.shape[1])
+        ctx.save_for_backward(x2, codes, exponents, offsets, rows, places)
+        return _block.expert_linear_fwd(x2, codes, exponents, offsets, rows)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x2, codes, exponents, offsets, rows, places = ctx.saved_tensors
+        dx, dw = _block.expert_linear_bwd(_aligned_rows(dy, codes.shape[1]), x2, codes, exponents, offsets, rows,
+                                          ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        if dx is not None and rows is not None:
+            dx = _block.expert_combine(dx, places)
+        return _once("expert_linear", dx), _once("expert_linear", dw), None, None, None, None, None
+
+
+def expert_linear(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                  places: Optional[torch.Tensor] = None, quantized=None) -> torch.Tensor:
+    """operators.expert_linear_fwd with a gradient: weight [E, N, K], bf16; `quantized` as in linear_block.
+
+    x [R, K] holds the rows sorted by expert, or, with `rows` and `places` of expert_route,
+    the tokens [T, K] (each token's gradient is the sum over its places)."""
+    if weight.dim() != 3 or x.dim() != 2 or x.shape[1] != weight.shape[2]:
+        raise ValueError(f"shapes {tuple(x.shape)} and {tuple(weight.shape)} do not match")
+    if (rows is None) != (places is None):
+        raise ValueError("rows and places are given together or not at all")
+    if places is not None and (places.dim() != 2 or places.shape[0] != x.shape[0]):
+        raise ValueError(f"places: a row for each of {x.shape[0]} tokens expected, got {tuple(places.shape)}")
+    codes, exponents = _weight_codes(weight, quantized)
+    if codes.shape[:-1] != weight.shape[:-1]:
+        raise ValueError(f"quantized: codes {tuple(codes.shape)} are not those of a weight {tuple(weight.shape)}")
+    return ExpertLinearFunction.apply(x, weight, codes, exponents, offsets, rows, places)
+
+
+class ExpertRouteFunction(torch.autograd.Function):
+    """Experts of each token (operators.expert_route); the gradient goes through the
+    weights, the choice taken as given.  There is no second derivative: asking for one
+    raises."""
+
+    @staticmethod
+    def forward(ctx, logits, k, score, normalize):
+        r = _block.expert_route(logits, k, score, normalize)
+        ctx.save_for_backward(logits, r.experts)
+        ctx.args = score, normalize
+        ctx.mark_non_differentiable(*r[1:])
+        return tuple(r)
+
+    @staticmethod
+    def backward(ctx, dweights, *_):
+        logits, experts = ctx.saved_tensors
+        d = _block.expert_route_bwd(logits, experts, dweights.contiguous(), *ctx.args)
+        return _once("expert_route", d), None, None, None
+
+
+def expert_route(logits: torch.Tensor, k: int, score: str = "softmax", normalize: bool = True) -> _block.Route:
+    """operators.expert_route with a gradient of the weights at the logits."""
+    return _block.Route(*ExpertRouteFunction.apply(logits, k, score, normalize))
+
+
+class ExpertCombineFunction(torch.autograd.Function):
+    """Weighted sums of the experts' rows (operators.expert_combine).  There is no second
+    derivative: asking for one raises."""
+
+    @staticmethod
+    def forward(ctx, y, places, weights, residual, rows):
+        ctx.save_for_backward(y, places, weights, rows)
+        return _block.expert_combine(y, places, weights, residual)
+
+    @staticmethod
+    def backward(ctx, dout):
+        y, places, weights, rows = ctx.saved_tensors
+        dy = dw = None
+        if ctx.needs_input_grad[0] or ctx.needs_input_grad[2]:
+            dy, dw = _block.expert_combine_bwd(_aligned_rows(dout, y.shape[1]), y, places, weights, rows,
+                                               ctx.needs_input_grad[0], ctx.needs_input_grad[2])
+        return (_once("expert_combine", dy), None, _once("expert_combine", dw),
+                dout if ctx.needs_input_grad[3] else None, None)
+
+
+def expert_combine(y: torch.Tensor, places: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """operators.expert_combine with gradients at y, weights and residual.  Each row of y
+    may have one place at most; with `rows` of expert_route the backward need not clear
+    the gradient of y first."""
+    return ExpertCombineFunction.apply(y, places, weights, residual, rows)

@@ -168,6 +168,7 @@ struct BlockPlan {
 };
 BlockPlan block_plan(BlockProduct what, int64_t rows, int64_t cols, int64_t contraction, int64_t E, int64_t all_rows);
 hipError_t launch_block_gemm(BlockProduct what, const BlockGemm& g, const BlockPlan& plan, float* planes, hipStream_t stream);
+hipError_t launch_block_gemms(const BlockGemm& dx, const BlockPlan& px, const BlockGemm& dw, const BlockPlan& pw, float* planes, hipStream_t stream);
 
 // Few rows an expert against weight codes: bound by reading them, X quantized in the kernel.
 struct BlockFew {

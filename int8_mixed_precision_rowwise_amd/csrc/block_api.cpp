@@ -267,24 +267,20 @@ i8mp_status i8mp_block_bwd(const i8mp_block* p, const uint16_t* dY, int64_t lddy
     const hipError_t e = i8mp::launch_block_quant(d, some_dw ? &x : nullptr, sp, s);
     if (e != hipSuccess) return hip_status(e);
   }
-  i8mp::BlockGemm g{};
-  g.cols_out = K, g.rag = rag;
-  if (some_dx) {
-    g.rows_out = M, g.contraction = N;
-    g.A = w.q, g.sA = w.s, g.lda = np, g.ldsa = pitch4(N);
-    g.B = p->codes, g.sB = w.planes, g.ldb = kp, g.ldsb = kp, g.b_stride = N * kp, g.sb_stride = blocks_of(N) * kp;
-    g.C = dX, g.ldc = lddx, g.clear = clear != 0;
-    const hipError_t e = i8mp::launch_block_gemm(i8mp::kBlockInput, g, plan_dx(M, N, K, E), w.sums, s);
-    if (e != hipSuccess) return hip_status(e);
-  }
-  if (some_dw) {
-    g.rows_out = N, g.clear = 0;
-    g.A = w.qd, g.sA = w.sd, g.lda = np, g.ldsa = np;
-    g.B = w.qx, g.sB = w.sx, g.ldb = kp, g.ldsb = kp, g.b_stride = 0, g.sb_stride = 0;
-    g.C = dW, g.ldc = lddw, g.c_stride = N * lddw;
-    return hip_status(i8mp::launch_block_gemm(i8mp::kBlockWeight, g, plan_dw(M, N, K, E), w.sums, s));
-  }
-  return I8MP_OK;
+  i8mp::BlockGemm gx{}, gw{};
+  gx.cols_out = gw.cols_out = K, gx.rag = gw.rag = rag;
+  gx.rows_out = M, gx.contraction = N;
+  gx.A = w.q, gx.sA = w.s, gx.lda = np, gx.ldsa = pitch4(N);
+  gx.B = p->codes, gx.sB = w.planes, gx.ldb = kp, gx.ldsb = kp, gx.b_stride = N * kp, gx.sb_stride = blocks_of(N) * kp;
+  gx.C = dX, gx.ldc = lddx, gx.clear = clear != 0;
+  gw.rows_out = N;
+  gw.A = w.qd, gw.sA = w.sd, gw.lda = np, gw.ldsa = np;
+  gw.B = w.qx, gw.sB = w.sx, gw.ldb = kp, gw.ldsb = kp;
+  gw.C = dW, gw.ldc = lddw, gw.c_stride = N * lddw;
+  const i8mp::BlockPlan px = plan_dx(M, N, K, E), pw = plan_dw(M, N, K, E);
+  if (some_dx && some_dw) return hip_status(i8mp::launch_block_gemms(gx, px, gw, pw, w.sums, s));
+  if (some_dx) return hip_status(i8mp::launch_block_gemm(i8mp::kBlockInput, gx, px, w.sums, s));
+  return hip_status(i8mp::launch_block_gemm(i8mp::kBlockWeight, gw, pw, w.sums, s));
 }
 
 size_t i8mp_expert_route_workspace_bytes(int64_t T, int64_t E, int32_t k) {

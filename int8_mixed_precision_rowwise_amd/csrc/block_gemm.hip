@@ -696,7 +696,8 @@ __device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& 
 
   int stage = 0;  // this slab's place
   // One slab, as in multiply; half: of the block.  The waits count slab loads and are at most stricter for the
-  // exponents' loads and the last tile's stores among them.
+  // exponents' loads and the last tile's stores among them.  (Waits that let a tile's stores go on for three more slabs
+  // made no difference.)
   auto slab = [&](v8i(&bc)[TN], v8i(&bn)[TN], int half) __attribute__((always_inline)) {
     const uint32_t dst = slabs0 + stage * SLAB;
     stage = (stage + 1) & 3;
@@ -801,22 +802,22 @@ __device__ __forceinline__ uint32_t tile_rows(const BlockGemm& g) {
   return WHAT == kBlockWeight ? (uint32_t)((g.rows_out + BM - 1) / BM) : ragged_tiles<BM>(g.rag);
 }
 
+// By workgroup wg of n.
 template <BlockProduct WHAT>
-__device__ __forceinline__ void clear_rows(const BlockGemm& g) {
+__device__ __forceinline__ void clear_rows(const BlockGemm& g, uint32_t wg, uint32_t n) {
   if (WHAT == kBlockWeight || !g.clear || !g.rag.off) return;
-  for (int64_t r = offset_at(g.rag, g.rag.E) + blockIdx.x; r < g.rag.rows; r += gridDim.x)
+  for (int64_t r = offset_at(g.rag, g.rag.E) + wg; r < g.rag.rows; r += n)
     for (int64_t c = threadIdx.x; c < g.cols_out; c += blockDim.x) g.C[r * g.ldc + c] = 0;
 }
 
-// Tiles of 128 x 128, two workgroups a CU.
+// Tiles of 128 x 128, two workgroups a CU; this is workgroup wg of n.
 template <BlockProduct WHAT, bool REBASE, bool VEC, bool GATHER>
-__global__ __launch_bounds__(256, 2) void block_gemm_small(BlockGemm g) {
-  __shared__ __attribute__((aligned(1024))) int8_t lds[kLdsBytes<128>];
+__device__ __forceinline__ void small_tile(const BlockGemm& g, uint32_t wg, uint32_t n, int8_t* lds) {
   const uint32_t tiles_n = (uint32_t)((g.cols_out + 127) / 128), tiles_m = tile_rows<128, WHAT>(g);
-  clear_rows<WHAT>(g);
+  clear_rows<WHAT>(g, wg, n);
   const uint32_t each = tiles_m * tiles_n, all = each * (WHAT == kBlockWeight ? (uint32_t)g.rag.E : 1) * g.splits;
-  if (blockIdx.x >= all) return;
-  uint32_t tile = xcd_runs(blockIdx.x, all);
+  if (wg >= all) return;
+  uint32_t tile = xcd_runs(wg, all);
   // the parts of the contraction one after another: an XCD's run of tiles reads the same part
   const uint32_t split = g.splits > 1 ? tile / each : 0;
   int64_t n0;
@@ -824,12 +825,28 @@ __global__ __launch_bounds__(256, 2) void block_gemm_small(BlockGemm g) {
   multiply<128, 128, 2, 2, 4, WHAT, REBASE, VEC, GATHER>(g, p, n0, split, lds);
 }
 
+template <BlockProduct WHAT, bool REBASE, bool VEC, bool GATHER>
+__global__ __launch_bounds__(256, 2) void block_gemm_small(BlockGemm g) {
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kLdsBytes<128>];
+  small_tile<WHAT, REBASE, VEC, GATHER>(g, blockIdx.x, gridDim.x, lds);
+}
+
+// Both products of a backward at once: nx workgroups (a multiple of 8, so that the XCDs' runs stay theirs) for dX, the
+// rest for dW.
+__global__ __launch_bounds__(256, 2) void block_gemm_both(BlockGemm dx, BlockGemm dw, uint32_t nx) {
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kLdsBytes<128>];
+  if (blockIdx.x < nx)
+    small_tile<kBlockInput, false, true, false>(dx, blockIdx.x, nx, lds);
+  else
+    small_tile<kBlockWeight, false, true, false>(dw, blockIdx.x - nx, gridDim.x - nx, lds);
+}
+
 // Tiles of 256 x 256: a workgroup for each CU takes every 256th of them, then at most one quarter of the last ones.
 template <BlockProduct WHAT, bool REBASE, bool GATHER>
 __global__ __launch_bounds__(512, 2) void block_gemm_big(BlockGemm g) {
   __shared__ __attribute__((aligned(1024))) BigLds lds;
   const uint32_t tiles_n = (uint32_t)((g.cols_out + 255) / 256), tiles_m = tile_rows<256, WHAT>(g);
-  clear_rows<WHAT>(g);
+  clear_rows<WHAT>(g, blockIdx.x, gridDim.x);
   const uint32_t all = tiles_m * tiles_n * (WHAT == kBlockWeight ? (uint32_t)g.rag.E : 1), whole = whole_tiles(all);
   const uint32_t wg = blockIdx.x, step = gridDim.x;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -877,20 +894,28 @@ int64_t tiles_of(BlockProduct what, int64_t rows, int64_t cols, int64_t E, bool 
   return (ragged ? ragged_units(rows, E, b) : (rows + b - 1) / b) * tn;
 }
 
+// An operand read down its rows that spans more bytes than a descriptor's offsets reach.
+bool needs_rebase(BlockProduct what, const BlockGemm& g) {
+  const int64_t down = what == kBlockForward ? 0 : what == kBlockInput ? g.contraction * g.ldb : g.rag.rows * std::max(g.lda, g.ldb);
+  return down >= (int64_t(1) << 31) - 1024;
+}
+// Whole chunks of 8 columns can be written.
+bool whole_chunks(const BlockGemm& g) {
+  return g.ldc % 8 == 0 && g.c_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(g.C) & 15) == 0;
+}
+// The big tiles' kernel writes nothing else.
+bool takes_big(const BlockGemm& g, const BlockPlan& plan) {
+  return plan.big && whole_chunks(g) && g.cols_out % 8 == 0 && g.ldc < (int64_t(1) << 22);
+}
+
 template <BlockProduct WHAT>
 hipError_t launch_tiles(const BlockGemm& g, const BlockPlan& plan, hipStream_t stream) {
-  const bool ragged = g.rag.off != nullptr;
-  // bytes that an operand read down its rows spans
-  const int64_t down = WHAT == kBlockForward ? 0 : WHAT == kBlockInput ? g.contraction * g.ldb : g.rag.rows * std::max(g.lda, g.ldb);
-  const bool rebase = down >= (int64_t(1) << 31) - 1024;
-  const bool vec = g.ldc % 8 == 0 && g.c_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(g.C) & 15) == 0;
-  // the big tiles' kernel writes whole chunks of 8 columns
-  const bool big = plan.big && vec && g.cols_out % 8 == 0 && g.ldc < (int64_t(1) << 22);
+  const bool ragged = g.rag.off != nullptr, rebase = needs_rebase(WHAT, g), vec = whole_chunks(g), big = takes_big(g, plan);
   const int64_t n = tiles_of(WHAT, g.rows_out, g.cols_out, ragged ? g.rag.E : 1, ragged, big ? 256 : 128) * plan.splits;
   if (n == 0) return hipSuccess;
   const bool cut = n > whole_tiles((uint32_t)n) || (ragged && WHAT != kBlockWeight);
   const unsigned grid = (unsigned)(big ? cut ? kCUs : std::min<int64_t>(n, kCUs) : n);
-  if (WHAT != kBlockForward && rebase)  // an operand read down its rows
+  if (WHAT != kBlockForward && rebase)
     launch<WHAT, WHAT != kBlockForward, false>(g, big, vec, grid, stream);
   else if (WHAT == kBlockForward && g.index)
     launch<WHAT, false, WHAT == kBlockForward>(g, big, vec, grid, stream);
@@ -899,10 +924,31 @@ hipError_t launch_tiles(const BlockGemm& g, const BlockPlan& plan, hipStream_t s
   return hipGetLastError();
 }
 
+BlockGemm with_plan(const BlockGemm& gemm, const BlockPlan& plan, float* planes) {
+  BlockGemm g = gemm;
+  g.splits = (uint32_t)plan.splits, g.kchunk = plan.kchunk;
+  g.planes = planes, g.plane_ld = plan.plane_ld, g.plane = g.rows_out * plan.plane_ld;
+  return g;
+}
+
+hipError_t join_parts(const BlockGemm& g, hipStream_t stream) {
+  const int64_t quads = g.rows_out * (g.plane_ld / 4);
+  if (g.splits == 1 || quads == 0) return hipSuccess;
+  add_planes<<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(g, g.rows_out);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-// Tiles of 256 x 256 where there are enough of them (kBigTileMin, gemm_pipelined.h) and the experts' rows fill
-// them, else of 128 x 128.  One matrix with few of those and a long contraction splits it, each part of at least
+// Tiles of 256 x 256, or of 128 x 128, which start and end sooner, of which two share a CU, and by which a backward's
+// two products go out together.  The bigger where they are more than half the CUs' number, the experts' rows fill
+// them, and their number squared times the contraction reaches kBigWork.  Time of the small ones over that of the big: 128
+// tiles 0.69 to 0.92 over contractions of 64 to 4096; 160 tiles 0.95 over 1024, 1.02 over 2048, 1.17 over 4096; 256
+// tiles 0.91 over 512, 1.02 over 1024, 1.1 over 2048; 320 tiles 0.88 over 512, 1.00 over 1024; 512 tiles 0.9 over 128,
+// 1.09 over 512; dW of 1024 tiles 1.2 over 64.
+constexpr double kBigWork = 256.0 * 256.0 * 1024.0;
+
+// One matrix with few tiles and a long contraction splits it, each part of at least
 // 512 into a plane of fp32 sums that a second launch adds up.  Both sides, all the call's kernels: 64 rows against
 // 4096 x 14336 65 us and 31, 128 rows 73 and 35, 64 against 4096 x 4096 25.5 and 20.0; dW of 32768 rows of 512 x 2048
 // 152 us and 55, of 8192 of 256 x 2048 40 and 18.  With two parts only it does not pay (64 rows against 14336 x
@@ -912,7 +958,8 @@ BlockPlan block_plan(BlockProduct what, int64_t rows, int64_t cols, int64_t cont
   BlockPlan p{false, 1, 0, 0};
   const bool ragged = E > 0;
   const int64_t e = std::max<int64_t>(E, 1), small = tiles_of(what, rows, cols, e, ragged, 128);
-  p.big = tiles_of(what, rows, cols, e, ragged, 256) >= kBigTileMin && (what == kBlockWeight || !ragged || all_rows >= 192 * e);
+  const int64_t big = tiles_of(what, rows, cols, e, ragged, 256), depth = what == kBlockWeight ? all_rows / e : contraction;
+  p.big = big > kCUs / 2 && (double)big * (double)big * (double)depth >= kBigWork && (what == kBlockWeight || !ragged || all_rows >= 192 * e);
   if (ragged || p.big || small == 0) return p;
   const int64_t s = std::min<int64_t>(kCUs / small, contraction / 512);
   if (s < 3) return p;
@@ -923,17 +970,33 @@ BlockPlan block_plan(BlockProduct what, int64_t rows, int64_t cols, int64_t cont
 }
 
 hipError_t launch_block_gemm(BlockProduct what, const BlockGemm& gemm, const BlockPlan& plan, float* planes, hipStream_t stream) {
-  BlockGemm g = gemm;
-  g.splits = (uint32_t)plan.splits, g.kchunk = plan.kchunk;
-  g.planes = planes, g.plane_ld = plan.plane_ld, g.plane = g.rows_out * plan.plane_ld;
+  const BlockGemm g = with_plan(gemm, plan, planes);
   const hipError_t e = what == kBlockForward ? launch_tiles<kBlockForward>(g, plan, stream)
                        : what == kBlockInput ? launch_tiles<kBlockInput>(g, plan, stream)
                                              : launch_tiles<kBlockWeight>(g, plan, stream);
-  if (e != hipSuccess || plan.splits == 1) return e;
-  const int64_t quads = g.rows_out * (g.plane_ld / 4);
-  if (quads == 0) return hipSuccess;
-  add_planes<<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(g, g.rows_out);
-  return hipGetLastError();
+  return e != hipSuccess ? e : join_parts(g, stream);
+}
+
+// In one launch where both take tiles of 128 x 128 and at most one has its contraction in parts (they share the
+// planes).  The whole backward of 300 rows of 2048 x 2048 in 24.4 us, 29.2 with a launch each; of 1000 of 1000 x 1000
+// 19.3 and 27.9; of 2048 of 4096 x 1024 39 and 49.
+hipError_t launch_block_gemms(const BlockGemm& dx, const BlockPlan& px, const BlockGemm& dw, const BlockPlan& pw, float* planes,
+                              hipStream_t stream) {
+  const BlockGemm x = with_plan(dx, px, planes), w = with_plan(dw, pw, planes);
+  const bool ragged = x.rag.off != nullptr;
+  const int64_t e = ragged ? x.rag.E : 1;
+  const int64_t nx = tiles_of(kBlockInput, x.rows_out, x.cols_out, e, ragged, 128) * px.splits;
+  const int64_t nw = tiles_of(kBlockWeight, w.rows_out, w.cols_out, e, ragged, 128) * pw.splits;
+  if (nx == 0 || nw == 0 || takes_big(x, px) || takes_big(w, pw) || !whole_chunks(x) || !whole_chunks(w) || (px.splits > 1 && pw.splits > 1) ||
+      needs_rebase(kBlockInput, x) || needs_rebase(kBlockWeight, w)) {
+    const hipError_t first = launch_block_gemm(kBlockInput, dx, px, planes, stream);
+    return first != hipSuccess ? first : launch_block_gemm(kBlockWeight, dw, pw, planes, stream);
+  }
+  const int64_t nx8 = (nx + 7) / 8 * 8;
+  block_gemm_both<<<(unsigned)(nx8 + nw), 256, 0, stream>>>(x, w, (uint32_t)nx8);
+  hipError_t st = hipGetLastError();
+  if (st == hipSuccess) st = join_parts(x, stream);
+  return st != hipSuccess ? st : join_parts(w, stream);
 }
 
 }  // namespace i8mp

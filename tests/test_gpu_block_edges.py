@@ -247,3 +247,78 @@ def test_two_threads_share_a_stream():
     for th in threads:
         th.join()
     assert not errors and wrong == [0, 0]
+
+
+# ------------------------------------------------------------------ big tiles
+
+
+@pytest.mark.parametrize("M,N,K", [(4100, 4104, 1000), (4100, 4104, 1160), (8195, 2568, 840)])
+def test_big_tiles(M, N, K):
+    """More tiles than CUs, of which the last are cut; the same rows in views."""
+    X, W = randn(M, M, K), randn(N, N, K, std=0.02)
+    codes, exps = i8.quantize_block_weight(W)
+    want, slack = ref.forward(ref.to64(X), ref.to64(W))
+    ref.close(i8.linear_block_fwd(X, codes, exps), want, slack, "Y")
+    store = torch.full((M + 1, N + 24), 7.0, dtype=bf, device="cuda")
+    i8.linear_block_fwd(far(X, K + 24), codes, exps, out=store[:M, 8:N + 8])
+    ref.close(store[:M, 8:N + 8], want, slack, "Y in a view")
+    assert bool((store[:, :8] == 7).all()) and bool((store[:, N + 8:] == 7).all()) and bool((store[M] == 7).all())
+
+
+@pytest.mark.parametrize("K", [8, 72, 128, 136, 264])
+def test_big_tiles_of_short_contractions(K):
+    """Contractions of one block, of two and a part: some rows of many."""
+    M, N = 8200, 8200
+    X, W, dY = randn(1, M, K), randn(2, N, K, std=0.02), randn(3, M, K)
+    codes, exps = i8.quantize_block_weight(W)
+    Y = i8.linear_block_fwd(X, codes, exps)
+    # the same sizes as gradients: dX over K columns of dY, dW over K rows
+    Wt = randn(4, K, N, std=0.02)
+    dX, none = i8.linear_block_bwd(dY, torch.zeros(M, N, dtype=bf, device="cuda"), *i8.quantize_block_weight(Wt), want_dw=False)
+    dYt, Xt = randn(5, K, M), randn(6, K, N)
+    none, dW = i8.linear_block_bwd(dYt, Xt, torch.zeros(M, (N + 15) // 16 * 16, dtype=u8, device="cuda"),
+                                   torch.zeros((M + 127) // 128, (N + 127) // 128, dtype=u8, device="cuda"), want_dx=False)
+    for s in (slice(0, 60), slice(4090, 4110), slice(M - 60, M)):
+        ref.close(Y[s], *ref.forward(ref.to64(X[s]), ref.to64(W)), "Y")
+        ref.close(dX[s], *ref.grad_input(ref.to64(dY[s]), ref.to64(Wt)), "dX")
+        ref.close(dW[s], *ref.grad_weight(ref.to64(dYt[:, s]), ref.to64(Xt)), "dW")
+
+
+@pytest.mark.parametrize("M,N,K", [(4100, 1000, 4104), (1000, 4104, 4104), (2100, 2056, 2056)])
+def test_big_tiles_backward(M, N, K):
+    X, W, dY = randn(M, M, K), randn(N, N, K, std=0.02), randn(K, M, N, std=1e-3)
+    codes, exps = i8.quantize_block_weight(W)
+    dX, dW = i8.linear_block_bwd(dY, X, codes, exps)
+    dy = ref.to64(dY)
+    ref.close(dX, *ref.grad_input(dy, ref.to64(W)), "dX")
+    ref.close(dW, *ref.grad_weight(dy, ref.to64(X)), "dW")
+    only_x, _ = i8.linear_block_bwd(dY, X, codes, exps, want_dw=False)
+    _, only_w = i8.linear_block_bwd(dY, X, codes, exps, want_dx=False)
+    assert torch.equal(only_x, dX) and torch.equal(only_w, dW)
+
+
+@pytest.mark.parametrize("counts,N,K", [([1400, 0, 600, 3000, 0, 260], 2056, 2056), ([70, 0, 1, 200, 129, 64, 0, 130] * 8, 1032, 1032)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_big_tiles_of_experts(counts, N, K, gather):
+    used, E = sum(counts), len(counts)
+    R, tokens = used + 5, 777
+    W, dY = randn(2, E, N, K, std=0.02), randn(3, R, N, std=1e-3)
+    X = randn(1, tokens if gather else R, K)
+    rows = torch.randint(-1, tokens + 1, (R,), generator=torch.Generator().manual_seed(1)).to(i32).cuda() if gather else None
+    x = ref.to64(X)
+    if gather:
+        r = rows.cpu().numpy()
+        x = np.where(((r >= 0) & (r < tokens))[:, None], x[np.clip(r, 0, tokens - 1)], 0)
+    codes, exps = i8.quantize_block_weight(W)
+    offsets = torch.tensor([0, *np.cumsum(counts)], dtype=i32, device="cuda")
+    Y = i8.expert_linear_fwd(X, codes, exps, offsets, rows)
+    dX, dW = i8.expert_linear_bwd(dY, X, codes, exps, offsets, rows)
+    w, dy, a = ref.to64(W), ref.to64(dY), 0
+    for e, n in enumerate(counts):
+        at, a = slice(a, a + n), a + n
+        if E > 8 and e % 7:
+            continue  # some of many
+        ref.close(Y[at], *ref.forward(x[at], w[e]), f"Y of expert {e}")
+        ref.close(dX[at], *ref.grad_input(dy[at], w[e]), f"dX of expert {e}")
+        ref.close(dW[e], *ref.grad_weight(dy[at], x[at]), f"dW of expert {e}")
+    assert not bool(Y[used:].any()) and not bool(dX[used:].any())

@@ -52,16 +52,27 @@ __device__ __forceinline__ void quant_tile(const BlockQuant& q, int64_t slot, in
   const int64_t col = ct * kTileCols + 8 * c;
   const int rows = (int)min((int64_t)kTileRows, p.count - p.local);
   const int64_t r0 = p.first + p.local;
+  // Rows and columns past the tile's read its last row and first columns, and become zeros below: loads without
+  // branches, so that all of a thread's are under way together.
   uint4 v[kPer];
+  int64_t src[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) src[i] = r0 + min(g + kGroups * i, rows - 1);
+  if (q.index) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) src[i] = q.index[src[i]];
+  }
+  const uint16_t* x = q.x + (col < q.cols ? col : 0);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int r = g + kGroups * i;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (r < rows && col < q.cols) {
-      int64_t src = r0 + r;
-      if (q.index) src = q.index[src];
-      if (!q.index || (src >= 0 && src < q.n_src)) v[i] = *reinterpret_cast<const uint4*>(q.x + src * q.ldx + col);
-    }
+    const bool there = !q.index || (src[i] >= 0 && src[i] < q.n_src);
+    v[i] = *reinterpret_cast<const uint4*>(x + (there ? src[i] : 0) * q.ldx);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const bool there = !q.index || (src[i] >= 0 && src[i] < q.n_src);
+    if (!there || g + kGroups * i >= rows) v[i] = make_uint4(0, 0, 0, 0);
   }
   if (col + 8 > q.cols) {
     const int keep = (int)max((int64_t)0, q.cols - col);
@@ -172,15 +183,17 @@ __global__ __launch_bounds__(kThreads) void quant_weight(const uint16_t* __restr
   const int64_t ct = blockIdx.x % cts, rt = blockIdx.x / cts % rts, e = blockIdx.x / (cts * rts);
   const int64_t col = ct * kTileCols + 8 * c, Kp = (K + 15) / 16 * 16, kb = (K + kBlock - 1) / kBlock;
   const int rows = (int)min((int64_t)kTileRows, N - rt * kTileRows);
-  w += e * stride + rt * kTileRows * ldw + col;
+  w += e * stride + rt * kTileRows * ldw + (col < K ? col : 0);
   uint4 v[kPer];
   us2 m = {0, 0};
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int r = g + kGroups * i;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (r < rows && col < K) v[i] = *reinterpret_cast<const uint4*>(w + r * ldw);
+    v[i] = *reinterpret_cast<const uint4*>(w + min(g + kGroups * i, rows - 1) * ldw);  // as in quant_tile
   }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (g + kGroups * i >= rows) v[i] = make_uint4(0, 0, 0, 0);
   if (col + 8 > K) {
     const int keep = (int)max((int64_t)0, K - col);
 #pragma unroll

@@ -182,15 +182,21 @@ void launch(const BlockFew& a, hipStream_t stream) {
 // and 8.0; 1 against 4096 x 14336 16.2 and 21.4, 4 against 4096 x 4096 6.6 and 9.6.
 constexpr int64_t kFewWide = 16 * 256;
 
-// Rows an expert, on average, that this kernel takes: against the tiles' kernel and the quantization before it, 16 rows
-// against 4096 x 14336 33.8 us and 64.3; 17 against 5632 x 2048 8.3 and 17.1; 32 against 14336 x 4096 28.4 and 25.9, 33
-// against 5632 x 2048 11.6 and 17.2 (64 rows 42.3 and 26.8 of 14336 x 4096).
+// Rows of one matrix, or of an expert on average, that this kernel takes: against the tiles' kernel and the quantization
+// before it, 16 rows against 4096 x 14336 33.8 us and 64.3; 17 against 5632 x 2048 8.3 and 17.1; 32 against 14336 x 4096
+// 28.4 and 25.9, 33 against 5632 x 2048 11.6 and 17.2 (64 rows 42.3 and 26.8 of 14336 x 4096).
 constexpr int64_t kFewRows = 32;
+
+// Rows of all experts, which may lie unevenly: an expert's rows beyond 32 read its codes again.  This kernel's time and the
+// tiles' over experts of 1024 x 2048, 8 of 2048 x 2048 or 128 of 768 x 2048: 64 rows of 8 10.3 us and 20.1, 128 of 8 17.4
+// and 20.2 (22.3 and 19.9 with 34 of them in one), 128 of 32 17.7 and 21.5 (43 and 20 with all in one), 128 of 128 30.3 and
+// 31.9, 256 of 32 20.0 and 21.9 (24.7 and 21.9 with 27 in one), 512 of 32 30 and 22 (52 and 23 with 111 in one).
+constexpr int64_t kFewAll = 128;
 
 bool block_few_takes(int64_t rows, int64_t E, int64_t N, int64_t K) {
   if (N < 1 || K < 1 || rows < 1) return false;
   const int64_t e = std::max<int64_t>(E, 1);
-  return rows <= kFewRows * e && e * ((N + 15) / 16) < (int64_t(1) << 22);
+  return rows <= (E > 0 ? std::min(kFewRows * e, kFewAll) : kFewRows) && e * ((N + 15) / 16) < (int64_t(1) << 22);
 }
 
 // Blocks a wave has in flight: 2, or 4 where only one tile is held and the contraction is long enough for 4

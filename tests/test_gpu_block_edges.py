@@ -40,6 +40,21 @@ def test_few_rows(M, N, K):
     ref.close(i8.linear_block_fwd(X, codes, exps), *ref.forward(ref.to64(X), ref.to64(W)), "Y")
 
 
+@pytest.mark.parametrize("counts", [[100, 0, 0, 28], [33, 0, 0, 0, 0, 0, 0, 0], [17, 16, 15, 0, 1], [64, 64], [0, 128, 0, 0], [100, 1, 0, 28],
+                                    [2] * 64, [2] * 65])
+def test_few_rows_of_experts(counts):
+    """All of them few, one expert's not, on either side of 128 rows."""
+    E, N, K = len(counts), 136, 264
+    R = sum(counts)
+    X, W = randn(1, R, K), randn(2, E, N, K, std=0.02)
+    offsets = torch.tensor([0, *np.cumsum(counts)], dtype=i32, device="cuda")
+    Y = i8.expert_linear_fwd(X, *i8.quantize_block_weight(W), offsets)
+    x, w, a = ref.to64(X), ref.to64(W), 0
+    for e, n in enumerate(counts):
+        ref.close(Y[a:a + n], *ref.forward(x[a:a + n], w[e]), f"Y of expert {e}")
+        a += n
+
+
 @pytest.mark.parametrize("M,N,K", [(128, 200, 4096), (100, 136, 1544), (70, 1000, 12296)])
 def test_split_contractions(M, N, K):
     """Few tiles over a long contraction: its parts are summed apart and joined; forward and both gradients."""

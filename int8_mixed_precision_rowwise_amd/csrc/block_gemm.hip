@@ -7,10 +7,11 @@
 // column) of each 128, which comes into LDS the same way as the codes, four blocks at a time.
 //
 // 8192 x 5632 x 2048 takes 92 us (2.05 PFLOP/s), 8192^3 430 to 475 (2.3 to 2.55; the library's row-wise FP8
-// product 2.74).
-// Of the 92, the last of three rounds of tiles is three quarters full (7 us), and a tile's outputs cost 3 us each round in
-// which its CU multiplies little: without any stores it took 83, with stores of whole lines 88, which would need the outputs
-// exchanged among four lanes.  On codes of zero, at the same clock limits, it takes 77: the rest is power.
+// product 2.74).  Of the 92, 64 are 96 slabs (three rounds of tiles, the last three quarters full) of 0.67 us each, where
+// the matrix instructions alone take 0.60 on random codes, which is what the card's power lets them (0.45 on zeros).  A
+// tile's end takes 6: a store writes 16 bytes of each of 64 rows' places, and the next slabs' loads queue behind
+// it (whole lines would save 1.5, before the exchange of outputs among four lanes that they need).  The kernel's start and
+// end take 9.
 #include "block.h"
 #include "gemm_pipelined.h"
 

@@ -429,13 +429,10 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
 
     // One slab, as in gemm_pipelined.h: slab kt is multiplied from registers while slab kt + 1 is read
     // from LDS and slab kt + STAGES goes into slab kt's place.  ODD: the second half of a block, which
-    // reads the next block's exponents.
+    // reads the next block's exponents.  A slab's first instructions, up to the barrier, end the turn of the loop before
+    // it: there nothing of LDS is under way, which the compiler would otherwise wait for at the loop's head.
     int stage = 0;  // slab kt's place
-    auto slab = [&](v8i(&bc)[TN], v8i(&bn)[TN], int kt, bool odd, bool tail) __attribute__((always_inline)) {
-      const uint32_t dst = lds0 + stage * SLAB;
-      stage = stage + 1 == STAGES ? 0 : stage + 1;
-      const int8_t* nxt = lds + stage * SLAB;
-      const int ns = kt + STAGES;
+    const auto first_half = [&](v8i(&bc)[TN]) __attribute__((always_inline)) {
 #pragma unroll
       for (int m = 0; m < S::HA; ++m) {
         mma(bc[m % TN], a[m / TN], m / TN, m % TN);
@@ -443,6 +440,12 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
       }
       __builtin_amdgcn_s_waitcnt(waitcnt_vm((STAGES - 2) * PER));  // slab kt + 1 has landed
       lds_barrier();
+    };
+    const auto second_half = [&](v8i(&bc)[TN], v8i(&bn)[TN], int kt, bool odd, bool tail) __attribute__((always_inline)) {
+      const uint32_t dst = lds0 + stage * SLAB;
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      const int8_t* nxt = lds + stage * SLAB;
+      const int ns = kt + STAGES;
       if (odd) read_exps((kt + 1) >> 1);
       if (!tail && (ns & 7) == 0 && ns < nk) ex.issue(exps + ((ns >> 3) & 1) * EXPS, ns >> 3, wave, lane);
 #pragma unroll
@@ -470,17 +473,21 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
       if (odd) next_exps();
     };
     int kt = 0;
+    first_half(b0);
     for (; kt + 2 < nk; kt += 2) {
-      slab(b0, b1, kt, false, false);
-      slab(b1, b0, kt + 1, true, false);
+      second_half(b0, b1, kt, false, false);
+      first_half(b1);
+      second_half(b1, b0, kt + 1, true, false);
+      first_half(b0);
     }
     if (kt + 1 < nk) {
-      slab(b0, b1, kt, false, true);
-      ++kt;
-    }
-    const bool odd = kt & 1;
+      second_half(b0, b1, kt, false, true);
 #pragma unroll
-    for (int m = 0; m < S::NM; ++m) mma(odd ? b1[m % TN] : b0[m % TN], a[m / TN], m / TN, m % TN);
+      for (int m = 0; m < S::NM; ++m) mma(b1[m % TN], a[m / TN], m / TN, m % TN);
+    } else {
+#pragma unroll
+      for (int m = S::HA; m < S::NM; ++m) mma(b0[m % TN], a[m / TN], m / TN, m % TN);
+    }
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));  // the trailing loads land before their place is used again
   }
   if (CAN_SPLIT && g.splits > 1) {
@@ -702,7 +709,7 @@ __device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& 
   for (int j = 0; j < TN; ++j) b0[j] = frag32f8<BN, BKM>(lds.slabs + A_BYTES, wn0 + 32 * j, lane);
 
   int stage = 0;  // this slab's place
-  // One slab, as in multiply; half: of the block.  The waits count slab loads and are at most stricter for the
+  // One slab, as in multiply (whole, since this loop keeps its order only without a branch in it); half: of the block.  The waits count slab loads and are at most stricter for the
   // exponents' loads and the last tile's stores among them.  (Waits that let a tile's stores go on for three more slabs
   // made no difference.)
   auto slab = [&](v8i(&bc)[TN], v8i(&bn)[TN], int half) __attribute__((always_inline)) {

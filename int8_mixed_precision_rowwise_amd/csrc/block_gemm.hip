@@ -709,9 +709,9 @@ __device__ __forceinline__ void multiply_all(const BlockGemm& g, int n, BigLds& 
   for (int j = 0; j < TN; ++j) b0[j] = frag32f8<BN, BKM>(lds.slabs + A_BYTES, wn0 + 32 * j, lane);
 
   int stage = 0;  // this slab's place
-  // One slab, as in multiply (whole, since this loop keeps its order only without a branch in it); half: of the block.  The waits count slab loads and are at most stricter for the
-  // exponents' loads and the last tile's stores among them.  (Waits that let a tile's stores go on for three more slabs
-  // made no difference.)
+  // One slab, both halves of multiply's; half: of the block.  The waits count slab loads and are at most stricter for the
+  // exponents' loads and the last tile's stores among them.  (Waits that let a tile's stores go on for three more slabs, and
+  // a loop head that waits for less of the last turn's reads, made no difference.)
   auto slab = [&](v8i(&bc)[TN], v8i(&bn)[TN], int half) __attribute__((always_inline)) {
     const uint32_t dst = slabs0 + stage * SLAB;
     stage = (stage + 1) & 3;

@@ -87,6 +87,28 @@ def test_one_token_in_every_row(counts):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("counts", [[3, 0, 9, 2], [130, 0, 77, 50], [1400, 0, 600, 3000, 0, 260]])
+def test_what_no_expert_has_reaches_nothing(counts):
+    """Rows behind the last expert's, and tokens that no row names, hold NaN."""
+    used, E, N, K, tokens = sum(counts), len(counts), 264, 520, 60
+    R = used + 70
+    W, X, Xt, dY = randn(2, E, N, K, std=0.02), randn(1, R, K), randn(4, tokens, K), randn(3, R, N)
+    rows = (torch.arange(R, dtype=i32, device="cuda") * 7) % (tokens - 11)
+    rows[used:] = -1
+    offsets = torch.tensor([0, *np.cumsum(counts)], dtype=i32, device="cuda")
+    q = i8.quantize_block_weight(W)
+
+    def run():
+        return [*(i8.expert_linear_fwd(x, *q, offsets, r) for x, r in ((X, None), (Xt, rows))),
+                *(t for x, r in ((X, None), (Xt, rows)) for t in i8.expert_linear_bwd(dY, x, *q, offsets, r))]
+
+    want = run()
+    nan = float("nan")
+    X[used:], Xt[tokens - 11:], dY[used:] = nan, nan, nan
+    got = run()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and not any(bool(t.isnan().any()) for t in got)
+
+
 @pytest.mark.parametrize("T", [128, 129, 255, 256, 257, 32768, 32769])
 @pytest.mark.parametrize("E", [40, 65])
 def test_blocks_of_tokens(T, E):

@@ -134,3 +134,20 @@ def test_replayed_from_a_graph():
         torch.cuda.synchronize()
         mine = [t.clone() for t in got]
         assert all(torch.equal(a, b) for a, b in zip(mine, step()))
+
+
+@pytest.mark.parametrize("tokens,padding", [(0, False), (20, True)])
+def test_a_layer_without_rows(tokens, padding):
+    """No tokens at all, and padding alone: what comes in goes out, and the weights' gradients are zeros."""
+    E, k, D, H = 4, 2, 40, 24
+    x = randn(1, tokens, D).requires_grad_()
+    w1, w2 = randn(2, E, H, D).requires_grad_(), randn(3, E, D, H).requires_grad_()
+    logits = torch.full((tokens, E), -float("inf"), device="cuda").requires_grad_()
+    r = T.expert_route(logits, k)
+    y = T.expert_linear(T.expert_linear(x, w1, r.offsets, r.rows, r.places), w2, r.offsets)
+    out = T.expert_combine(y, r.places, r.weights, residual=x, rows=r.rows)
+    assert torch.equal(out, x)
+    g = randn(4, tokens, D)
+    dx, dw1, dw2, dl = torch.autograd.grad(out, (x, w1, w2, logits), g)
+    assert torch.equal(dx, g) and not dw1.any() and not dw2.any() and not dl.any()
+    assert dw1.shape == w1.shape and dl.shape == logits.shape

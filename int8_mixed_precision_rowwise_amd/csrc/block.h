@@ -42,6 +42,28 @@ struct Place {
   int64_t e, local, first, count;
 };
 
+// First row and number of rows of this lane's expert e; no rows past the last expert.  What a wave needs of one of them
+// it then reads from that lane, not from memory again: the way to a first load is a chain of such reads (the backward of
+// 1551 rows of 13 experts 23.9 us, 24.7 with offsets read again).
+struct LaneRows {
+  int first, count;
+};
+__device__ __forceinline__ LaneRows lane_rows(const Ragged& r, int64_t e) {
+  LaneRows l{(int)r.rows, 0};
+  if (e < r.E) {
+    l.first = (int)offset_at(r, e);
+    l.count = max(0, (int)offset_at(r, e + 1) - l.first);
+  }
+  return l;
+}
+// Those of expert e0 + at, at the same in all lanes.
+__device__ __forceinline__ void take_lane(const LaneRows& l, int64_t e0, int at, Place& p) {
+  at = __builtin_amdgcn_readfirstlane(at);
+  p.e = e0 + at;
+  p.first = __builtin_amdgcn_readlane(l.first, at);
+  p.count = __builtin_amdgcn_readlane(l.count, at);
+}
+
 template <int UNIT>
 __device__ __forceinline__ bool locate(const Ragged& r, int64_t s, Place& p) {
   if (!r.off) {
@@ -50,18 +72,15 @@ __device__ __forceinline__ bool locate(const Ragged& r, int64_t s, Place& p) {
   }
   // the last expert whose first unit is at most s; a wave looks at 64 experts at a time
   const int lane = threadIdx.x & 63;
-  int64_t below = 0;
+  bool some = false;
   for (int64_t e0 = 0; e0 < r.E; e0 += 64) {
-    const int64_t e = e0 + lane;
-    const bool in = e < r.E && offset_at(r, e) / UNIT + e <= s;
-    const uint64_t m = __ballot(in);
-    below += __popcll(m);
+    const LaneRows l = lane_rows(r, e0 + lane);
+    const uint64_t m = __ballot(e0 + lane < r.E && l.first / UNIT + e0 + lane <= s);
+    const int here = __popcll(m);
+    if (here) take_lane(l, e0, here - 1, p), some = true;
     if (m != ~uint64_t(0)) break;
   }
-  if (below == 0) return false;
-  p.e = below - 1;
-  p.first = offset_at(r, p.e);
-  p.count = offset_at(r, p.e + 1) - p.first;
+  if (!some) return false;
   p.local = (s - (p.first / UNIT + p.e)) * UNIT;
   return p.local >= 0 && p.local < p.count;
 }

@@ -21,67 +21,62 @@ namespace {
 // The tiles of the experts' rows: tiles of BM rows, expert after expert.  Every wave adds up the
 // experts' tiles by itself, 64 experts at a time.
 template <int BM>
-__device__ __forceinline__ int tiles_at(const Ragged& r, int64_t e) {
-  return e < r.E ? (int)(max((int64_t)0, offset_at(r, e + 1) - offset_at(r, e) + BM - 1) / BM) : 0;
-}
-
-template <int BM>
 __device__ __forceinline__ int ragged_tiles(const Ragged& r) {
   if (!r.off) return (int)((r.rows + BM - 1) / BM);
   int n = 0;
-  for (int64_t e = threadIdx.x & 63; e < r.E; e += 64) n += tiles_at<BM>(r, e);
+  for (int64_t e = threadIdx.x & 63; e < r.E; e += 64) n += (lane_rows(r, e).count + BM - 1) / BM;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
   return __builtin_amdgcn_readfirstlane(n);  // what loops over it then stays in scalar registers
 }
 
-__device__ __forceinline__ void expert_rows(const Ragged& r, int64_t e, Place& p) {
-  p.e = e, p.first = 0, p.count = r.rows, p.local = 0;
-  if (!r.off) return;
-  p.first = offset_at(r, e);
-  p.count = max((int64_t)0, offset_at(r, e + 1) - p.first);
-}
-
 // Where row tile tm lies.
 template <int BM>
 __device__ __forceinline__ void ragged_place(const Ragged& r, int tm, Place& p) {
-  expert_rows(r, 0, p);
-  p.local = (int64_t)tm * BM;
+  p.e = 0, p.first = 0, p.count = r.off ? 0 : r.rows, p.local = (int64_t)tm * BM;
   if (!r.off) return;
   const int lane = threadIdx.x & 63;
   int before = 0;  // tiles of the experts before this turn's 64
   for (int64_t e0 = 0; e0 < r.E; e0 += 64) {
-    int n = tiles_at<BM>(r, e0 + lane);
+    const LaneRows l = lane_rows(r, e0 + lane);
+    int n = (l.count + BM - 1) / BM;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int up = __shfl_up(n, o);
       if (lane >= o) n += up;
     }
     const uint64_t past = __ballot(before + n > tm);
-    if (past) {
+    if (past) {  // always, in the end: tm is one of the experts' tiles
       const int at = __builtin_ctzll(past);
       const int start = at ? before + __shfl(n, at - 1) : before;
-      expert_rows(r, e0 + at, p);
+      if constexpr (BM == 128) {
+        take_lane(l, e0, at, p);
+      } else {  // registers are scarcer than time there (32768 rows of 32 experts through an index 93 us, 90 so)
+        p.e = e0 + at;
+        p.first = offset_at(r, p.e);
+        p.count = max((int64_t)0, offset_at(r, p.e + 1) - p.first);
+      }
       p.local = (int64_t)(tm - start) * BM;
       return;
     }
     before += __shfl(n, 63);
   }
-  p.count = 0;  // not reached: tm is one of the experts' tiles
 }
 
 // The i-th expert in falling order of rows (up to 64 experts; more: the i-th): the products that
 // contract over an expert's rows start with the longest.
-__device__ __forceinline__ int64_t by_size(const Ragged& r, int64_t i) {
-  if (!r.off || r.E > 64) return i;
+__device__ __forceinline__ void by_size(const Ragged& r, int64_t i, Place& p) {
+  p.e = 0, p.first = 0, p.count = r.rows;
+  if (!r.off) return;
   const int lane = threadIdx.x & 63;
-  const int n = lane < r.E ? (int)max((int64_t)0, offset_at(r, lane + 1) - offset_at(r, lane)) : -1;
+  if (r.E > 64) return take_lane(lane_rows(r, i), i, 0, p);
+  const LaneRows l = lane_rows(r, lane);
   int rank = 0;
-  for (int l = 0; l < (int)r.E; ++l) {
-    const int other = __builtin_amdgcn_readlane(n, l);
-    rank += other > n || (other == n && l < lane);
+  for (int k = 0; k < (int)r.E; ++k) {
+    const int other = __builtin_amdgcn_readlane(l.count, k);
+    rank += other > l.count || (other == l.count && k < lane);
   }
-  return __builtin_ctzll(__ballot(lane < r.E && rank == (int)i));
+  take_lane(l, 0, __builtin_ctzll(__ballot(lane < r.E && rank == (int)i)), p);
 }
 
 // Consecutive workgroups go to the 8 XCDs in turn.  Runs of kRun tiles go to one XCD, so that they share
@@ -803,7 +798,7 @@ __device__ __forceinline__ Place tile_place(const BlockGemm& g, uint32_t tile, u
   n0 = (int64_t)tn * BM;
   Place p;
   if constexpr (WHAT == kBlockWeight) {
-    expert_rows(g.rag, by_size(g.rag, e), p);
+    by_size(g.rag, e, p);
     p.local = (int64_t)tm * BM;
   } else {
     ragged_place<BM>(g.rag, tm, p);

@@ -353,7 +353,7 @@ def expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, dweights: torc
         raise TypeError(f"experts: torch.Tensor expected, got {type(experts).__name__}")
     k = experts.shape[-1] if experts.dim() else 0
     p, dev = _route(logits, k, score, normalize, experts, dweights, out, backward=True)
-    d = torch.empty((p.T, p.E), dtype=logits.dtype, device=dev) if out is None else out
+    d = torch.empty(*logits.shape, dtype=logits.dtype, device=dev) if out is None else out
     _call(dev, "i8mp_expert_route_bwd", p, _ptr(experts), _ptr(dweights), _ptr(d), _ld2(d))
     return d
 
@@ -424,9 +424,9 @@ def expert_combine_bwd(dout: torch.Tensor, Y: torch.Tensor, places: torch.Tensor
         _pkg._mat(dY, "dY", Y.dtype, tuple(Y.shape))
         _pkg._device(Y, dY)
     if want_dy and dY is None:
-        dY = (torch.zeros if rows is None else torch.empty)((p.R, p.N), dtype=Y.dtype, device=dev)
+        dY = (torch.zeros if rows is None else torch.empty)(*Y.shape, dtype=Y.dtype, device=dev)
     dY = dY if want_dy else None
-    dw = torch.empty((p.T, p.k), dtype=torch.float32, device=dev) if want_dweights else None
+    dw = torch.empty(*places.shape, dtype=torch.float32, device=dev) if want_dweights else None
     _call(dev, "i8mp_expert_combine_bwd", p, _ptr(dout), _ld2(dout), None if rows is None else _ptr(rows), _ptr(dY),
           0 if dY is None else _ld2(dY), _ptr(dw))
     return dY, dw

@@ -284,9 +284,8 @@ i8mp_status i8mp_block_bwd(const i8mp_block* p, const uint16_t* dY, int64_t lddy
 }
 
 size_t i8mp_expert_route_workspace_bytes(int64_t T, int64_t E, int32_t k) {
-  (void)k;
   if (T < 0 || E < 1 || E > i8mp::kRouteMaxExperts) return 0;
-  const int64_t per = i8mp::route_block_tokens(T, E);
+  const int64_t per = i8mp::route_block_tokens(T, E, k);
   return T <= per ? 0 : up((size_t)((T + per - 1) / per * E * 4));
 }
 

@@ -14,7 +14,7 @@ struct RouteArgs {
   int32_t* hist;  // [blocks][E], for more than one block of tokens
 };
 constexpr int kRouteMaxExperts = 1024, kRouteMaxK = 32;
-int64_t route_block_tokens(int64_t T, int64_t E);  // tokens a workgroup counts
+int64_t route_block_tokens(int64_t T, int64_t E, int64_t k);  // tokens a workgroup counts
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 hipError_t launch_route_bwd(const RouteArgs& a, const int32_t* experts, const float* dweights, void* d, int64_t ldd,
                             hipStream_t stream);

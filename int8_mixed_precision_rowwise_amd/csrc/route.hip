@@ -1,7 +1,7 @@
 // Routing of tokens to experts and back: the top experts of each token with their weights, the
 // rows sorted by expert, the weighted sums of the experts' rows, and the gradients of both.
 //
-// Choosing: 16 lanes (up to 256 experts) or 64 share a token, each with 4 or 16 adjacent experts'
+// Choosing: 16 lanes (up to 256 experts) or 64 share a token, each with 4, 8 or 16 adjacent experts'
 // scores in registers; a round takes the largest score by DPP moves and, among the lanes that
 // have it, the lowest, whose experts come first.  Sorting is a counting sort that keeps the
 // tokens' order without an atomic whose order matters: a workgroup counts its block of tokens,
@@ -9,9 +9,9 @@
 // over the bits of the expert's number.  One block of tokens needs one launch.
 //
 // All of it is short work in waves that wait: 32768 tokens to 4 of 64 (fp32) choose in 6.9 us and
-// place in 6.5, where 13 MB need 2.5; scores loaded one by one, searched each round and turned to
-// weights one at a time took 10.2 to choose.  The gradient takes 7.7 us (7 MB of 32768 x 64), a
-// launch of 16 tokens to 4 of 64 4.7.
+// place in 6.1, where 13 MB need 2.5; to 8 of 256 (bf16) both take 28.  The gradient takes 4.5 us at 32768 x 64 (bf16, 8
+// taken; 8 MB) and 14.7 at 256: sums over the taken alone, and one exponential a score where the weights are
+// shares of all.
 #include "route.h"
 
 #include <algorithm>
@@ -20,13 +20,18 @@ namespace i8mp {
 namespace {
 
 constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
-// Tokens a workgroup counts, at least, and workgroups at most: one for each CU.  (32768 tokens, 4 of 64 experts: choosing
-// took 12.8 us with 128 workgroups of 256 tokens and 10.2 with 256 of 128, placing 6.4 and 8.2.)
-constexpr int64_t kRouteBlock = 128, kRouteMaxBlocks = 256;
-// Tokens that one workgroup takes alone, in one launch, up to 64 experts and beyond.  (Replayed, one launch and two: 256
-// tokens to 2 of 8 8.7 us and 8.4, to 4 of 64 11.0 and 9.5, to 8 of 256 33.4 and 21.8, 200 tokens to 4 of 64 9.3
-// either way; a second launch costs the host 2 us.)
-constexpr int64_t kRouteAlone = 256, kRouteAloneMany = 128;
+// Lanes of a token: a row of 16, or the wave for more than 256 experts.  Tokens a workgroup takes at least (what its lanes
+// take at a time), and workgroups at most, one for each CU.  (Whole calls, replayed: 512 tokens to 8 of 64 9.7 us with 64
+// tokens a workgroup, 13.0 with 128; to 8 of 512 24 with 32 and 37 with 64.)
+constexpr int route_lanes(int64_t E) { return E <= 256 ? 16 : 64; }
+constexpr int64_t route_block(int64_t E) { return kRouteThreads / route_lanes(E); }
+constexpr int64_t kRouteMaxBlocks = 256;
+// Whether one workgroup takes all tokens, in one launch: a second costs the host 2 us.  (Replayed, one launch and two: 64
+// tokens to 8 of 64 6.9 us and 9.5, 128 10.0 and 9.6, 256 17.2 and 9.7; 256 to 2 of 8 8.7 and 8.4; 64 to 8 of 128 8.8 and
+// 10.7, to 8 of 256 11.3 and 13.5; 32 to 8 of 512 15.2 and 14.3.)
+constexpr bool route_alone(int64_t T, int64_t E, int64_t k) {
+  return E <= 64 ? T <= 256 && T * k <= 512 : T <= (E <= 256 ? 64 : 32);
+}
 
 template <int DT>
 __device__ __forceinline__ float load_as_float(const void* p, int64_t i) {
@@ -49,9 +54,9 @@ __device__ __forceinline__ float over_lanes(float v, F f) {
   dpp(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));
   dpp(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false));
   dpp(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false));
-  if constexpr (G == 64) {
-    v = f(v, __shfl_xor(v, 16));
-    v = f(v, __shfl_xor(v, 32));
+  if constexpr (G == 64) {  // the whole wave is here
+    const auto row = [&](int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); };
+    v = f(f(row(0), row(16)), f(row(32), row(48)));
   }
   return v;
 }
@@ -116,53 +121,49 @@ __device__ __forceinline__ void store_scores(const RouteArgs& a, void* d, int64_
   }
 }
 
-// Whether score (v, e) comes before (w, f).
-__device__ __forceinline__ bool before(float v, int e, float w, int f) { return v > w || (v == w && e < f); }
-
-// A lane's scores, of which the best is asked for again and again.  Four are sorted first, so that the best is
-// the first; sixteen are searched each time.
+// A lane's J scores, of which the best is asked for again and again: lists of four, each sorted, so that a best is among
+// their firsts.  Exchanging neighbours only where the later is larger keeps equal ones in order.  (Searching 16 of them
+// each round: 512 tokens to 8 of 128 21.5 us, 15.5 so and with 8 a lane; to 8 of 256 22.6 and 20.7.)
 template <int J>
 struct Best {
-  float v[J];
-  int e[J];
+  static constexpr int kLists = J / 4;
+  float v[kLists][4];
+  int e[kLists][4];
   __device__ __forceinline__ void init(const float (&x)[J]) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) v[j] = x[j] == x[j] ? x[j] : -INFINITY, e[j] = j;  // NaN is never taken
-    if constexpr (J == 4) {
-      order(0, 1), order(2, 3), order(0, 2), order(1, 3), order(1, 2);
+    for (int l = 0; l < kLists; ++l) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[l][i] = x[4 * l + i] == x[4 * l + i] ? x[4 * l + i] : -INFINITY, e[l][i] = 4 * l + i;  // NaN is never taken
+      order(l, 0), order(l, 2), order(l, 1), order(l, 0), order(l, 2), order(l, 1);
     }
   }
-  __device__ __forceinline__ void order(int i, int j) {
-    const bool swap = before(v[j], e[j], v[i], e[i]);
-    const float a = v[i], b = v[j];
-    const int c = e[i], d = e[j];
-    v[i] = swap ? b : a, v[j] = swap ? a : b;
-    e[i] = swap ? d : c, e[j] = swap ? c : d;
+  __device__ __forceinline__ void order(int l, int i) {
+    const bool swap = v[l][i + 1] > v[l][i];
+    const float a = v[l][i], b = v[l][i + 1];
+    const int c = e[l][i], d = e[l][i + 1];
+    v[l][i] = swap ? b : a, v[l][i + 1] = swap ? a : b;
+    e[l][i] = swap ? d : c, e[l][i + 1] = swap ? c : d;
   }
   __device__ __forceinline__ float top() const {
-    float t = v[0];
-    if constexpr (J != 4) {
+    float t = v[0][0];
 #pragma unroll
-      for (int j = 1; j < J; ++j) t = fmaxf(t, v[j]);
-    }
+    for (int l = 1; l < kLists; ++l) t = fmaxf(t, v[l][0]);
     return t;
   }
   // The first of the scores `t`, taken away.
   __device__ __forceinline__ int pop(float t) {
-    if constexpr (J == 4) {
-      const int first = e[0];
+    int first = 0;
+    bool done = false;
 #pragma unroll
-      for (int j = 0; j < J - 1; ++j) v[j] = v[j + 1], e[j] = e[j + 1];
-      v[J - 1] = -INFINITY;
-      return first;
-    } else {
-      int at = J - 1;
+    for (int l = 0; l < kLists; ++l) {
+      const bool here = kLists == 1 || (!done && v[l][0] == t);
+      done |= here;
+      first = here ? e[l][0] : first;
 #pragma unroll
-      for (int j = J - 1; j >= 0; --j) at = v[j] == t ? j : at;
-#pragma unroll
-      for (int j = 0; j < J; ++j) v[j] = j == at ? -INFINITY : v[j];
-      return at;
+      for (int i = 0; i < 3; ++i) v[l][i] = here ? v[l][i + 1] : v[l][i], e[l][i] = here ? e[l][i + 1] : e[l][i];
+      v[l][3] = here ? -INFINITY : v[l][3];
     }
+    return first;
   }
 };
 
@@ -347,58 +348,66 @@ __global__ __launch_bounds__(kRouteThreads) void route_place(RouteArgs a, int64_
 
 // Gradient at a token's scores: with g the gradients of the taken weights w and S their sum,
 // <g, w> = inner, softmax gives p (g - inner) (over all, or the taken alone with their w), the
-// normalized sigmoid w (1 - s) (g - inner), the plain one g s (1 - s).
+// normalized sigmoid w (1 - s) (g - inner), the plain one g s (1 - s).  Lane r % G has the r-th taken expert and its
+// score; what it gets goes among the lanes' adjacent scores through LDS.
 template <int G, int J, int DT, bool VEC>
 __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __restrict__ experts,
                                                   const float* __restrict__ dw, void* __restrict__ d, int64_t ldd, int64_t first) {
+  __shared__ __attribute__((aligned(16))) float row_lds[256 / G][G * J];
   const int64_t t = first + (blockIdx.x * (int64_t)256 + threadIdx.x) / G;
   if (t >= a.T) return;  // whole groups
   const int lane = threadIdx.x & (G - 1);
-  float x[J], g[J];
-  bool mine[J], bad = false;
+  float x[J], v[J];
+  constexpr int kKept = kRouteMaxK / G + (kRouteMaxK % G != 0);
+  int e[kKept];
+  float g[kKept], s[kKept];
+  bool bad = false;
   load_scores<G, J, DT, VEC>(a, t, lane, x);
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const int r = lane + G * i;
+    e[i] = r < a.k ? experts[t * a.k + r] : -1;
+    g[i] = r < a.k ? dw[t * a.k + r] : 0.0f;
+    if (e[i] >= a.E) e[i] = -1;
+    s[i] = e[i] >= 0 ? load_as_float<DT>(a.logits, t * a.ld + e[i]) : -INFINITY;
+  }
   float m = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    bad |= !(x[j] < INFINITY);
-    m = larger(m, x[j]);
-    g[j] = 0.0f, mine[j] = false;
-  }
-  for (int r = 0; r < a.k; ++r) {
-    const int e = experts[t * a.k + r] - lane * J;
-    const float v = dw[t * a.k + r];
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (e == j) g[j] = v, mine[j] = true;
-  }
+  for (int j = 0; j < J; ++j) bad |= !(x[j] < INFINITY), m = larger(m, x[j]);
   const int shift = (threadIdx.x & 63) & ~(G - 1);
   constexpr uint64_t kGroup = G == 64 ? ~uint64_t(0) : (uint64_t(1) << G) - 1;
   bad = (__ballot(bad) >> shift) & kGroup;
   m = over_lanes<G>(m, larger);
   m = m > -INFINITY ? m : 0.0f;
-  const bool sig = a.score == I8MP_SIGMOID;
-  float s[J], sum = 0.0f, inner = 0.0f;
+  const bool sig = a.score == I8MP_SIGMOID, all = !sig && !a.normalize;
+  float sum = 0.0f, inner = 0.0f;
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    s[j] = sig ? sigmoid(x[j]) : expf(x[j] - m);
-    if (mine[j] || !(a.normalize || sig)) sum += s[j];
-    if (mine[j]) inner += g[j] * s[j];
+  for (int i = 0; i < kKept; ++i) {
+    s[i] = e[i] < 0 ? 0.0f : sig ? sigmoid(s[i]) : expf(s[i] - m);
+    sum += s[i];
+    inner += e[i] < 0 ? 0.0f : g[i] * s[i];
+  }
+  if (all) {
+    sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) v[j] = expf(x[j] - m), sum += v[j];
   }
   sum = over_lanes<G>(sum, add);
   inner = over_lanes<G>(inner, add);
   const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
   inner *= r;
-  float v[J];
+  float* const row = row_lds[threadIdx.x / G];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    if (sig) {
-      const float slope = s[j] * (1.0f - s[j]);
-      v[j] = !mine[j] ? 0.0f : a.normalize ? (g[j] - inner) * r * slope : g[j] * slope;
-    } else {
-      v[j] = a.normalize && !mine[j] ? 0.0f : s[j] * r * (g[j] - inner);
-    }
-    v[j] = bad ? NAN : v[j];
+  for (int j = 0; j < J; ++j) row[lane * J + j] = all ? v[j] * r * (0.0f - inner) : 0.0f;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a token's lanes are one wave's, whose accesses of LDS stay in order
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const float slope = s[i] * (1.0f - s[i]);
+    if (e[i] >= 0) row[e[i]] = sig ? (a.normalize ? (g[i] - inner) * r * slope : g[i] * slope) : s[i] * r * (g[i] - inner);
   }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+  for (int j = 0; j < J; ++j) v[j] = bad ? NAN : row[lane * J + j];
   store_scores<J, DT, VEC>(a, d, t * ldd, lane, v);
 }
 
@@ -543,8 +552,12 @@ template <int DT>
 void route_as(const RouteArgs& a, int64_t per, int blocks, hipStream_t stream) {
   if (a.E <= 64)
     choose_lanes<16, 4, DT>(a, per, blocks, stream);
+  else if (a.E <= 128)
+    choose_lanes<16, 8, DT>(a, per, blocks, stream);
   else if (a.E <= 256)
     choose_lanes<16, 16, DT>(a, per, blocks, stream);
+  else if (a.E <= 512)
+    choose_lanes<64, 8, DT>(a, per, blocks, stream);
   else
     choose_lanes<64, 16, DT>(a, per, blocks, stream);
 }
@@ -569,8 +582,12 @@ template <int DT>
 void route_back_as(const RouteArgs& a, const int32_t* experts, const float* dw, void* d, int64_t ldd, hipStream_t stream) {
   if (a.E <= 64)
     route_back_lanes<16, 4, DT>(a, experts, dw, d, ldd, stream);
+  else if (a.E <= 128)
+    route_back_lanes<16, 8, DT>(a, experts, dw, d, ldd, stream);
   else if (a.E <= 256)
     route_back_lanes<16, 16, DT>(a, experts, dw, d, ldd, stream);
+  else if (a.E <= 512)
+    route_back_lanes<64, 8, DT>(a, experts, dw, d, ldd, stream);
   else
     route_back_lanes<64, 16, DT>(a, experts, dw, d, ldd, stream);
 }
@@ -591,13 +608,13 @@ void combine_back_as(const CombineArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t route_block_tokens(int64_t T, int64_t E) {
-  const int64_t alone = E <= 64 ? kRouteAlone : kRouteAloneMany;
-  return T <= alone ? alone : std::max(kRouteBlock, (T + kRouteMaxBlocks - 1) / kRouteMaxBlocks);
+int64_t route_block_tokens(int64_t T, int64_t E, int64_t k) {
+  if (route_alone(T, E, k)) return std::max<int64_t>(T, 1);
+  return std::max(route_block(E), (T + kRouteMaxBlocks - 1) / kRouteMaxBlocks);
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
-  const int64_t per = route_block_tokens(a.T, a.E);
+  const int64_t per = route_block_tokens(a.T, a.E, a.k);
   const int blocks = (int)std::max<int64_t>(1, (a.T + per - 1) / per);
   switch (a.dtype) {
     case I8MP_BF16: route_as<I8MP_BF16>(a, per, blocks, stream); break;

@@ -53,6 +53,26 @@ def test_route(T, E, k, dtype):
             check_route(x, k, score, normalize)
 
 
+@pytest.mark.parametrize("E", [68, 72, 128, 132, 208, 264, 512, 516, 528, 1000])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_lanes_of_many_experts(E, dtype):
+    """Each number of scores a lane, read whole and one by one, with ties; gradients against the formula."""
+    T, k = 45, 6
+    x = (4 * randn(E, T, E)).round().div(4).to(dtype)
+    x[3], x[4, 5:] = -inf, -inf
+    g = randn(E + 1, T, k)
+    for score, normalize in (("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)):
+        r = check_route(x, k, score, normalize)
+        d = i8.expert_route_bwd(x, r.experts, g, score=score, normalize=normalize)
+        e, dw = r.experts.cpu().numpy(), ref.to64(g)
+        want = ref.route_grad(ref.to64(x), e, dw, score, normalize)
+        # as in test_route_gradient: differences of terms of size |g| w, then one rounding
+        scale = np.abs(dw).sum(1, keepdims=True)
+        p = np.abs(ref.route_grad(ref.to64(x), e, np.abs(dw), "sigmoid", False)) if score == "sigmoid" else 1.0
+        err = np.abs(ref.to64(d) - want)
+        assert (err <= half_step(dtype) * np.abs(want) + 4 * REL * scale * np.maximum(p, 1.0) + (2.0**-25 if dtype == torch.float16 else 0)).all()
+
+
 def test_many_tokens():
     check_route(randn(1, 70001, 8), 2, "softmax", True)  # blocks of more than 256 tokens
 

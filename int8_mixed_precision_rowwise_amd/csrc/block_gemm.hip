@@ -6,12 +6,10 @@
 // blocks' scales cost no vector operation: a lane needs the exponent's byte of its row (or
 // column) of each 128, which comes into LDS the same way as the codes, four blocks at a time.
 //
-// 8192 x 5632 x 2048 takes 92 us (2.05 PFLOP/s), 8192^3 430 to 475 (2.3 to 2.55; the library's row-wise FP8
-// product 2.74).  Of the 92, 64 are 96 slabs (three rounds of tiles, the last three quarters full) of 0.67 us each, where
+// 8192 x 5632 x 2048 takes 90 us (2.1 PFLOP/s), 8192^3 415 to 465 (2.35 to 2.65; the library's row-wise FP8
+// product 2.74).  Of the 90, 64 are 96 slabs (three rounds of tiles, the last three quarters full) of 0.67 us each, where
 // the matrix instructions alone take 0.60 on random codes, which is what the card's power lets them (0.45 on zeros).  A
-// tile's end takes 6: a store writes 16 bytes of each of 64 rows' places, and the next slabs' loads queue behind
-// it (whole lines would save 1.5, before the exchange of outputs among four lanes that they need).  The kernel's start and
-// end take 9.
+// tile's end takes 5: its stores, and the next slabs' loads that queue behind them.  The kernel's start and end take 9.
 #include "block.h"
 #include "gemm_pipelined.h"
 
@@ -494,9 +492,20 @@ __device__ __forceinline__ void multiply(const BlockGemm& g, const Place& p, int
   store_rows<TM, TN, VEC>(acc, lds + wave * (WM * WN * 2), C + wm0 * g.ldc + wn0, g.ldc, c_rows - wm0, g.cols_out - n0 - wn0, lane);
 }
 
-// A wave's 128 x 64 outputs straight from its accumulators.  A lane has four adjacent columns of a row, and the
-// one 32 lanes on the next four; exchanging halves makes eight of each, 16 bytes.  What lies outside the
-// tile falls outside the descriptor.
+// What two lanes exchange in a transposition: b of the first and a of the second.
+template <int QUAD_PERM>
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b, bool second) {
+  const uint32_t t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(second ? a : b), QUAD_PERM, 0xF, 0xF, false);
+  a = second ? t : a;
+  b = second ? b : t;
+}
+
+// A wave's 128 x 64 outputs straight from its accumulators.  A lane has four adjacent columns of a row here and there, and
+// the one 32 lanes on the next four; exchanging halves makes 32 columns in a row of one lane, four pieces of 16 bytes, and
+// transposing these among four adjacent lanes puts 64 bytes of one row into them: a store takes a row's piece from four
+// lanes at a time, or 16 bytes where they have different rows.  (8192 x 5632 x 2048 89.6 us, 92.6 with 16 bytes of a row each;
+// 8192 x 8192 x 1024 with X's quantization 82 and 93, the backward of 32768 rows of 32 experts 278 and 292.)  What lies
+// outside the tile falls outside the descriptor.
 __device__ __forceinline__ void store_direct(const v16f (&acc)[4][2], uint16_t* C, uint32_t ldc, int rows, int cols, int lane) {
   const int mr = lane & 31, half = lane >> 5;
   rows = min(max(rows, 0), 128), cols = min(max(cols, 0), 64);
@@ -505,29 +514,39 @@ __device__ __forceinline__ void store_direct(const v16f (&acc)[4][2], uint16_t* 
   const uint64_t c0 = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(c >> 32)) << 32 |
                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)c);
   const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(c0), 0, bytes, 0x00020000);
-  uint32_t at = 2 * (mr * ldc + 8 * half);
+  const int s = lane & 3;
+  const bool odd = s & 1, high = s & 2;
+  const uint32_t col = 32 * half + 8 * s;
+  uint32_t at = (int)col < cols ? 2 * (4 * (mr >> 2) * ldc + col) : kOob;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    uint32_t v[4][4];  // chunk q of 8 columns of this lane's row and half
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[2][2];
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        uint32_t w[2][2];
+      for (int j = 0; j < 2; ++j) {
+        __bf16 h[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          __bf16 h[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = (__bf16)acc[i][j][4 * (q + k) + e];  // round to nearest even
-          const uint2 u = __builtin_bit_cast(uint2, h);
-          w[k][0] = u.x, w[k][1] = u.y;
-        }
-        const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
-        const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
-        const v4u v = {s0[0], s1[0], s0[1], s1[1]};
-        const int n = 32 * j + 8 * q;  // of lanes 0 .. 31; the others are 8 on
-        __builtin_amdgcn_raw_buffer_store_b128(v, out, n + 8 * half < cols ? at + 2 * n : kOob, 0, 0);
+        for (int e = 0; e < 4; ++e) h[e] = (__bf16)acc[i][j][4 * q + e];  // round to nearest even
+        const uint2 u = __builtin_bit_cast(uint2, h);
+        w[j][0] = u.x, w[j][1] = u.y;
       }
-    at += 64 * ldc;  // rows past the last one lie past the descriptor's end
+      const auto s0 = __builtin_amdgcn_permlane32_swap(w[0][0], w[1][0], false, false);
+      const auto s1 = __builtin_amdgcn_permlane32_swap(w[0][1], w[1][1], false, false);
+      v[q][0] = s0[0], v[q][1] = s1[0], v[q][2] = s0[1], v[q][3] = s1[1];
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      exchange<0xB1>(v[0][d], v[1][d], odd), exchange<0xB1>(v[2][d], v[3][d], odd);
+      exchange<0x4E>(v[0][d], v[2][d], high), exchange<0x4E>(v[1][d], v[3][d], high);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const v4u c = {v[t][0], v[t][1], v[t][2], v[t][3]};
+      __builtin_amdgcn_raw_buffer_store_b128(c, out, at == kOob ? kOob : at + 2 * t * ldc, 0, 0);
+    }
+    at = at == kOob ? kOob : at + 64 * ldc;  // rows past the last one lie past the descriptor's end
   }
 }
 

@@ -559,7 +559,7 @@ i8mp_status i8mp_quantize_block_weight(const uint16_t* W, int64_t E, int64_t N, 
 /*
  * One linear layer (experts = 0), or one for each of many experts whose rows lie
  * one expert after another: expert e has rows offsets[e] .. offsets[e + 1] - 1 of
- * M.  The offsets are read on the GPU: they must not fall and must lie in [0, M];
+ * M (offsets[0] may lie behind 0: a slice of all experts' offsets).  The offsets are read on the GPU: they must not fall and must lie in [0, M];
  * others give outputs without meaning, but nothing outside the tensors is touched.
  *   M: rows of Y and dY (and of X, unless rows is given)
  *   codes, exps: as written by i8mp_quantize_block_weight ([N][Kp] or [E][N][Kp])
@@ -586,8 +586,9 @@ typedef struct {
  * looked at (few rows, whose kernel quantizes X by itself). */
 size_t i8mp_block_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t experts, int32_t backward);
 /*
- * Y = X W^T, bf16 [M x N].  clear: rows behind the last expert's (from
- * offsets[experts] on) are written as zeros; otherwise they are left as they were.
+ * Y = X W^T, bf16 [M x N].  clear: rows that no expert has (in front of
+ * offsets[0], and from offsets[experts] on) are written as zeros; otherwise they are
+ * left as they were.
  */
 i8mp_status i8mp_block_fwd(const i8mp_block* p, uint16_t* Y, int64_t ldy, int32_t clear, void* ws, size_t ws_bytes,
                            void* stream);

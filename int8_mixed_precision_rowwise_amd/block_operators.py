@@ -251,8 +251,9 @@ def expert_linear_fwd(X: torch.Tensor, codes: torch.Tensor, exponents: torch.Ten
     has rows offsets[e] .. offsets[e + 1] - 1 (int32 or int64 [E + 1] on the GPU, which
     the host never reads).  rows (int32 [R]): the row of X that each row is, as
     expert_route gives them; then X holds the tokens and is not copied into the experts'
-    order.  Without it R is X's own number of rows.  Rows behind the last expert's are
-    zero, or, in a given `out`, left as they were."""
+    order.  Without it R is X's own number of rows.  The offsets may be a slice of all
+    experts' offsets, [lo : hi + 1], with codes[lo:hi].  Rows that none of the experts
+    has, in front and behind, are zero, or, in a given `out`, left as they were."""
     if offsets is None:
         raise TypeError("offsets: torch.int32 or torch.int64 tensor expected")
     return _forward(X, codes, exponents, offsets, rows, out, workspace, True)
@@ -265,7 +266,7 @@ def expert_linear_bwd(dY: torch.Tensor, X: torch.Tensor, codes: torch.Tensor, ex
 
     dX has a row for each row of dY; where the rows were read through `rows`,
     expert_combine adds a token's rows up.  An expert without rows has a gradient of
-    zeros; rows of dX behind the last expert's as in the forward."""
+    zeros; rows of dX that no expert has as in the forward."""
     if offsets is None:
         raise TypeError("offsets: torch.int32 or torch.int64 tensor expected")
     return _backward(dY, X, codes, exponents, offsets, rows, want_dx, want_dw, dX, dW, workspace, True)

@@ -36,6 +36,17 @@ __device__ __forceinline__ int64_t offset_at(const Ragged& r, int64_t e) {
   return min(max(v, (int64_t)0), r.rows);  // whatever the offsets hold, rows stay within the tensors
 }
 
+// The rows that no expert has: those in front of the first one's and those behind the last one's.
+struct OtherRows {
+  int64_t front, end, count;
+  __device__ __forceinline__ int64_t row(int64_t i) const { return i < front ? i : end + (i - front); }
+};
+__device__ __forceinline__ OtherRows other_rows(const Ragged& r) {
+  if (!r.off) return {0, 0, 0};
+  const int64_t front = offset_at(r, 0), end = offset_at(r, r.E);
+  return {front, end, front + (r.rows - end)};
+}
+
 // Block `s` of the room in units of UNIT rows: the expert it belongs to (e), its first row
 // within that expert (local), and the expert's first row and number of rows.  false: none.
 struct Place {
@@ -172,7 +183,7 @@ struct BlockGemm {
   uint16_t* C;
   int64_t ldc, c_stride;
   Ragged rag;
-  int clear;  // rows behind the last expert are written as zeros
+  int clear;  // rows that no expert has are written as zeros
   // set by the launcher from the plan
   uint32_t splits;
   int64_t kchunk, plane, plane_ld;

@@ -42,10 +42,10 @@ __global__ __launch_bounds__(kFewThreads, 4) void block_few(BlockFew a, uint32_t
     count = offset_at(a.rag, e + 1) - first;
   }
   // Behind everything that is read: a store before would keep the offsets and the index out of scalar loads.
-  const int64_t clear_from = a.clear && a.rag.off ? offset_at(a.rag, a.rag.E) + wg : a.rag.rows;
+  const OtherRows other = a.clear ? other_rows(a.rag) : OtherRows{0, 0, 0};
   const auto clear = [&]() __attribute__((always_inline)) {
-    for (int64_t r = clear_from; r < a.rag.rows; r += gridDim.x)
-      for (int64_t c = t; c < a.N; c += kFewThreads) a.Y[r * a.ldy + c] = 0;
+    for (int64_t i = wg; i < other.count; i += gridDim.x)
+      for (int64_t c = t; c < a.N; c += kFewThreads) a.Y[other.row(i) * a.ldy + c] = 0;
   };
   if (count <= 0) return clear();  // workgroup-uniform
   const int64_t n0 = (int64_t)tile * (16 * CT);

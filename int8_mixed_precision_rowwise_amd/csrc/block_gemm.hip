@@ -833,9 +833,10 @@ __device__ __forceinline__ uint32_t tile_rows(const BlockGemm& g) {
 // By workgroup wg of n.
 template <BlockProduct WHAT>
 __device__ __forceinline__ void clear_rows(const BlockGemm& g, uint32_t wg, uint32_t n) {
-  if (WHAT == kBlockWeight || !g.clear || !g.rag.off) return;
-  for (int64_t r = offset_at(g.rag, g.rag.E) + wg; r < g.rag.rows; r += n)
-    for (int64_t c = threadIdx.x; c < g.cols_out; c += blockDim.x) g.C[r * g.ldc + c] = 0;
+  if (WHAT == kBlockWeight || !g.clear) return;
+  const OtherRows other = other_rows(g.rag);
+  for (int64_t i = wg; i < other.count; i += n)
+    for (int64_t c = threadIdx.x; c < g.cols_out; c += blockDim.x) g.C[other.row(i) * g.ldc + c] = 0;
 }
 
 // Tiles of 128 x 128, two workgroups a CU; this is workgroup wg of n.

@@ -932,9 +932,10 @@ bool needs_rebase(BlockProduct what, const BlockGemm& g) {
 bool whole_chunks(const BlockGemm& g) {
   return g.ldc % 8 == 0 && g.c_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(g.C) & 15) == 0;
 }
-// The big tiles' kernel writes nothing else.
+// The big tiles' kernel writes nothing else, and reads 256 rows of codes at offsets that stay below kOob, which stands
+// for "nothing": the last chunk of rows 2^23 apart (contractions from 2^23 - 15 on) would be taken for it.
 bool takes_big(const BlockGemm& g, const BlockPlan& plan) {
-  return plan.big && whole_chunks(g) && g.cols_out % 8 == 0 && g.ldc < (int64_t(1) << 22);
+  return plan.big && whole_chunks(g) && g.cols_out % 8 == 0 && g.ldc < (int64_t(1) << 22) && 256 * std::max(g.lda, g.ldb) <= kOob;
 }
 
 template <BlockProduct WHAT>

@@ -64,6 +64,9 @@ __device__ __forceinline__ float add(float a, float b) { return a + b; }
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// 1 - sigmoid(x) = sigmoid(-x): formed from the score, since 1 - s has no digits left where s is near 1 (6 % off at 16, 0
+// from 17 on).
+__device__ __forceinline__ float rest_of_sigmoid(float x) { return 1.0f / (1.0f + expf(x)); }
 
 // A token's scores: lane l of its G has experts l J .. l J + J - 1.  VEC: J of them are there or none, and lie at a
 // multiple of their size (of 16 bytes at most).
@@ -360,7 +363,7 @@ __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __
   float x[J], v[J];
   constexpr int kKept = kRouteMaxK / G + (kRouteMaxK % G != 0);
   int e[kKept];
-  float g[kKept], s[kKept];
+  float g[kKept], s[kKept], rest[kKept];
   bool bad = false;
   load_scores<G, J, DT, VEC>(a, t, lane, x);
 #pragma unroll
@@ -383,6 +386,7 @@ __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __
   float sum = 0.0f, inner = 0.0f;
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
+    rest[i] = sig ? rest_of_sigmoid(s[i]) : 0.0f;
     s[i] = e[i] < 0 ? 0.0f : sig ? sigmoid(s[i]) : expf(s[i] - m);
     sum += s[i];
     inner += e[i] < 0 ? 0.0f : g[i] * s[i];
@@ -402,7 +406,7 @@ __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a token's lanes are one wave's, whose accesses of LDS stay in order
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
-    const float slope = s[i] * (1.0f - s[i]);
+    const float slope = s[i] * rest[i];
     if (e[i] >= 0) row[e[i]] = sig ? (a.normalize ? (g[i] - inner) * r * slope : g[i] * slope) : s[i] * r * (g[i] - inner);
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

@@ -610,8 +610,8 @@ i8mp_status i8mp_block_bwd(const i8mp_block* p, const uint16_t* dY, int64_t lddy
  *   experts[t][j], in falling order of their scores; -1 for none
  *   weights[t][j]: I8MP_SOFTMAX: exp(x) over the sum of all (normalize = 0) or of the
  *     taken (1) exponentials; I8MP_SIGMOID: 1 / (1 + exp(-x)), over the sum of the
- *     taken ones (1; 0 where that is 0) or itself (0).  0 for none.  A score of NaN or +inf
- *     makes its token's weights NaN.
+ *     taken ones (1; 0 where all of these scores lie below -700) or itself (0).  0 for
+ *     none.  A score of NaN or +inf makes its token's weights NaN.
  *   offsets[0 .. E]: first row of each expert among the rows sorted by expert and,
  *     within one, by token; offsets[E] is the number of rows taken
  *   places[t][j]: the row of token t's j-th expert; -1 for none

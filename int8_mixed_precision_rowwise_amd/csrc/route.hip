@@ -68,6 +68,12 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-
 // from 17 on).
 __device__ __forceinline__ float rest_of_sigmoid(float x) { return 1.0f / (1.0f + expf(x)); }
 
+// For shares of a sum of sigmoids, of which the largest is that of m: sigmoid(x) / e^min(m, 0), so that the shares of
+// scores far below zero, whose sigmoids fp32 does not hold, are there.  Below -700 a sigmoid is 0.
+__device__ __forceinline__ float scaled_sigmoid(float x, float m) {
+  return m < -700.0f ? 0.0f : m < 0.0f ? expf(x - m) / (1.0f + expf(x)) : sigmoid(x);
+}
+
 // A token's scores: lane l of its G has experts l J .. l J + J - 1.  VEC: J of them are there or none, and lie at a
 // multiple of their size (of 16 bytes at most).
 template <int DT, int J>
@@ -203,7 +209,9 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int64_t t, int lane, 
   float s[kKept], taken = 0.0f;
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
-    s[i] = !(kept[i] > -INFINITY) ? 0.0f : a.score == I8MP_SIGMOID ? sigmoid(kept[i]) : expf(kept[i] - m);
+    s[i] = !(kept[i] > -INFINITY) ? 0.0f
+           : a.score != I8MP_SIGMOID ? expf(kept[i] - m)
+           : a.normalize ? scaled_sigmoid(kept[i], m) : sigmoid(kept[i]);
     taken += s[i];
   }
   float total = 1.0f;
@@ -374,20 +382,24 @@ __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __
     if (e[i] >= a.E) e[i] = -1;
     s[i] = e[i] >= 0 ? load_as_float<DT>(a.logits, t * a.ld + e[i]) : -INFINITY;
   }
-  float m = -INFINITY;
+  const bool sig = a.score == I8MP_SIGMOID, all = !sig && !a.normalize;
+  float m = -INFINITY;  // the largest score of all, or of the taken ones
 #pragma unroll
-  for (int j = 0; j < J; ++j) bad |= !(x[j] < INFINITY), m = larger(m, x[j]);
+  for (int j = 0; j < J; ++j) bad |= !(x[j] < INFINITY), m = sig ? m : larger(m, x[j]);
+  if (sig) {
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) m = larger(m, s[i]);
+  }
   const int shift = (threadIdx.x & 63) & ~(G - 1);
   constexpr uint64_t kGroup = G == 64 ? ~uint64_t(0) : (uint64_t(1) << G) - 1;
   bad = (__ballot(bad) >> shift) & kGroup;
   m = over_lanes<G>(m, larger);
   m = m > -INFINITY ? m : 0.0f;
-  const bool sig = a.score == I8MP_SIGMOID, all = !sig && !a.normalize;
   float sum = 0.0f, inner = 0.0f;
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
     rest[i] = sig ? rest_of_sigmoid(s[i]) : 0.0f;
-    s[i] = e[i] < 0 ? 0.0f : sig ? sigmoid(s[i]) : expf(s[i] - m);
+    s[i] = e[i] < 0 ? 0.0f : !sig ? expf(s[i] - m) : a.normalize ? scaled_sigmoid(s[i], m) : sigmoid(s[i]);
     sum += s[i];
     inner += e[i] < 0 ? 0.0f : g[i] * s[i];
   }

@@ -628,7 +628,8 @@ typedef struct {
 size_t i8mp_expert_route_workspace_bytes(int64_t T, int64_t E, int32_t k);
 i8mp_status i8mp_expert_route(const i8mp_route* p, float* weights, int32_t* experts, int32_t* places, int32_t* rows,
                               int32_t* offsets, void* ws, size_t ws_bytes, void* stream);
-/* The gradient of sum(dweights * weights) at the logits, in their type, for the given choice. */
+/* The gradient of sum(dweights * weights) at the logits, in their type, for the given choice: that of
+ * i8mp_expert_route or another, whose experts of a token are distinct (-1: none). */
 i8mp_status i8mp_expert_route_bwd(const i8mp_route* p, const int32_t* experts, const float* dweights, void* dlogits,
                                   int64_t ld, void* stream);
 

@@ -349,7 +349,8 @@ def expert_route(logits: torch.Tensor, k: int, score: str = "softmax", normalize
 def expert_route_bwd(logits: torch.Tensor, experts: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
                      normalize: bool = True, out: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of sum(dweights * weights) at the logits [T, E], in their type, the choice
-    of experts (from expert_route, with the same score and normalize) taken as given."""
+    of experts taken as given: expert_route's with the same score and normalize, or another
+    of distinct experts for each token (-1: none)."""
     if not isinstance(experts, torch.Tensor):
         raise TypeError(f"experts: torch.Tensor expected, got {type(experts).__name__}")
     k = experts.shape[-1] if experts.dim() else 0

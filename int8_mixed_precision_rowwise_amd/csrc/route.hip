@@ -385,8 +385,8 @@ __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __
   const bool sig = a.score == I8MP_SIGMOID, all = !sig && !a.normalize;
   float m = -INFINITY;  // the largest score of all, or of the taken ones
 #pragma unroll
-  for (int j = 0; j < J; ++j) bad |= !(x[j] < INFINITY), m = sig ? m : larger(m, x[j]);
-  if (sig) {
+  for (int j = 0; j < J; ++j) bad |= !(x[j] < INFINITY), m = all ? larger(m, x[j]) : m;
+  if (!all) {  // a choice that is given need not have the largest score
 #pragma unroll
     for (int i = 0; i < kKept; ++i) m = larger(m, s[i]);
   }

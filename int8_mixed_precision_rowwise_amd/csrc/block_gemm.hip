@@ -17,14 +17,20 @@ namespace i8mp {
 namespace {
 
 // The tiles of the experts' rows: tiles of BM rows, expert after expert.  Every wave adds up the
-// experts' tiles by itself, 64 experts at a time.
+// experts' tiles by itself, 64 experts at a time.  Sums stop at the number that offsets which do not fall can make:
+// others of many experts would take them past 32 bits, and tiles to rows that nobody has.
+template <int BM>
+__device__ __forceinline__ int most_tiles(const Ragged& r) {
+  return (int)(r.rows / BM + r.E);
+}
 template <int BM>
 __device__ __forceinline__ int ragged_tiles(const Ragged& r) {
   if (!r.off) return (int)((r.rows + BM - 1) / BM);
+  const int most = most_tiles<BM>(r);
   int n = 0;
-  for (int64_t e = threadIdx.x & 63; e < r.E; e += 64) n += (lane_rows(r, e).count + BM - 1) / BM;
+  for (int64_t e = threadIdx.x & 63; e < r.E; e += 64) n = min(n + (lane_rows(r, e).count + BM - 1) / BM, most);
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+  for (int o = 32; o > 0; o >>= 1) n = min(n + __shfl_xor(n, o), most);
   return __builtin_amdgcn_readfirstlane(n);  // what loops over it then stays in scalar registers
 }
 
@@ -34,6 +40,7 @@ __device__ __forceinline__ void ragged_place(const Ragged& r, int tm, Place& p) 
   p.e = 0, p.first = 0, p.count = r.off ? 0 : r.rows, p.local = (int64_t)tm * BM;
   if (!r.off) return;
   const int lane = threadIdx.x & 63;
+  const int most = most_tiles<BM>(r);
   int before = 0;  // tiles of the experts before this turn's 64
   for (int64_t e0 = 0; e0 < r.E; e0 += 64) {
     const LaneRows l = lane_rows(r, e0 + lane);
@@ -41,7 +48,7 @@ __device__ __forceinline__ void ragged_place(const Ragged& r, int tm, Place& p) 
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int up = __shfl_up(n, o);
-      if (lane >= o) n += up;
+      if (lane >= o) n = min(n + up, most);
     }
     const uint64_t past = __ballot(before + n > tm);
     if (past) {  // always, in the end: tm is one of the experts' tiles
@@ -57,7 +64,7 @@ __device__ __forceinline__ void ragged_place(const Ragged& r, int tm, Place& p) 
       p.local = (int64_t)(tm - start) * BM;
       return;
     }
-    before += __shfl(n, 63);
+    before = min(before + __shfl(n, 63), most);
   }
 }
 

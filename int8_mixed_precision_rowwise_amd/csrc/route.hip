@@ -64,10 +64,6 @@ __device__ __forceinline__ float add(float a, float b) { return a + b; }
 __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
-// 1 - sigmoid(x) = sigmoid(-x): formed from the score, since 1 - s has no digits left where s is near 1 (6 % off at 16, 0
-// from 17 on).
-__device__ __forceinline__ float rest_of_sigmoid(float x) { return 1.0f / (1.0f + expf(x)); }
-
 // For shares of a sum of sigmoids, of which the largest is that of m: sigmoid(x) / e^min(m, 0), so that the shares of
 // scores far below zero, whose sigmoids fp32 does not hold, are there.  Below -700 a sigmoid is 0.
 __device__ __forceinline__ float scaled_sigmoid(float x, float m) {
@@ -383,23 +379,37 @@ __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __
     s[i] = e[i] >= 0 ? load_as_float<DT>(a.logits, t * a.ld + e[i]) : -INFINITY;
   }
   const bool sig = a.score == I8MP_SIGMOID, all = !sig && !a.normalize;
-  float m = -INFINITY;  // the largest score of all, or of the taken ones
+  float m = -INFINITY;  // the largest score, of all or of the taken ones, which need not be the largest of all
 #pragma unroll
-  for (int j = 0; j < J; ++j) bad |= !(x[j] < INFINITY), m = all ? larger(m, x[j]) : m;
-  if (!all) {  // a choice that is given need not have the largest score
+  for (int j = 0; j < J; ++j) bad |= !(x[j] < INFINITY), m = larger(m, x[j]);
+  if (!all) {
+    m = s[0];
 #pragma unroll
-    for (int i = 0; i < kKept; ++i) m = larger(m, s[i]);
+    for (int i = 1; i < kKept; ++i) m = larger(m, s[i]);
   }
   const int shift = (threadIdx.x & 63) & ~(G - 1);
   constexpr uint64_t kGroup = G == 64 ? ~uint64_t(0) : (uint64_t(1) << G) - 1;
   bad = (__ballot(bad) >> shift) & kGroup;
   m = over_lanes<G>(m, larger);
   m = m > -INFINITY ? m : 0.0f;
+  if (sig) {
+    // 1 - sigmoid(x) is formed from the score: 1 - s has no digits left where s is near 1 (6 % off at 16, 0 from 17 on).
+    // Shares of a sum whose largest score lies below zero are formed as in scaled_sigmoid, where all scores have x < 0.
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      const float z = s[i], t = expf(-fabsf(z)), q = 1.0f / (1.0f + t);
+      rest[i] = z < 0.0f ? q : t * q;
+      s[i] = z < 0.0f ? t * q : q;
+      if (a.normalize && m < 0.0f) s[i] = m < -700.0f ? 0.0f : expf(z - m) * q;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) s[i] = expf(s[i] - m);
+  }
   float sum = 0.0f, inner = 0.0f;
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
-    rest[i] = sig ? rest_of_sigmoid(s[i]) : 0.0f;
-    s[i] = e[i] < 0 ? 0.0f : !sig ? expf(s[i] - m) : a.normalize ? scaled_sigmoid(s[i], m) : sigmoid(s[i]);
+    s[i] = e[i] < 0 ? 0.0f : s[i];
     sum += s[i];
     inner += e[i] < 0 ? 0.0f : g[i] * s[i];
   }
@@ -418,8 +428,7 @@ __global__ __launch_bounds__(256) void route_back(RouteArgs a, const int32_t* __
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a token's lanes are one wave's, whose accesses of LDS stay in order
 #pragma unroll
   for (int i = 0; i < kKept; ++i) {
-    const float slope = s[i] * rest[i];
-    if (e[i] >= 0) row[e[i]] = sig ? (a.normalize ? (g[i] - inner) * r * slope : g[i] * slope) : s[i] * r * (g[i] - inner);
+    if (e[i] >= 0) row[e[i]] = sig ? (a.normalize ? (g[i] - inner) * r : g[i]) * (s[i] * rest[i]) : s[i] * r * (g[i] - inner);
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll

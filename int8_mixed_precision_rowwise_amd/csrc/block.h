@@ -47,8 +47,8 @@ __device__ __forceinline__ OtherRows other_rows(const Ragged& r) {
   return {front, end, front + (r.rows - end)};
 }
 
-// Block `s` of the room in units of UNIT rows: the expert it belongs to (e), its first row
-// within that expert (local), and the expert's first row and number of rows.  false: none.
+// Where a tile of an expert's rows lies: the expert (e), the tile's first row within it (local), the expert's first row and
+// number of rows.
 struct Place {
   int64_t e, local, first, count;
 };
@@ -75,6 +75,7 @@ __device__ __forceinline__ void take_lane(const LaneRows& l, int64_t e0, int at,
   p.count = __builtin_amdgcn_readlane(l.count, at);
 }
 
+// Block `s` of the room in units of UNIT rows.  false: no expert's.
 template <int UNIT>
 __device__ __forceinline__ bool locate(const Ragged& r, int64_t s, Place& p) {
   if (!r.off) {

@@ -147,8 +147,7 @@ template <int BM>
 constexpr int kLdsBytes = BM == 256 ? 4 * 512 * BK + 10240 : 4 * 256 * BK + 2048;  // of a workgroup of 8 waves, of 4
 
 // Slab loads of one operand, as Dma (gemm_pipelined.h) with less state in registers: a lane's chunks of a
-// slab's loads lie a fixed step apart (and, in tiles read down their rows, swap neighbours with every
-// second load of four waves).  Rows or columns past the operand are not looked at: a K-major operand's
+// slab's loads lie a fixed step apart.  Rows or columns past the operand are not looked at: a K-major operand's
 // lie past the descriptor's end and arrive as zeros, the others' are the next row's bytes or zeros, and
 // either only reach outputs that are not stored.
 // GATHER (K-major): rows from anywhere in the operand, each at an offset of its own.
@@ -156,18 +155,15 @@ template <int R, bool KMAJOR, int NW, bool REBASE, bool GATHER = false>
 struct Slabs {
   static constexpr int kInst = R * BK / 1024 / NW;
   static constexpr int CPR = R / 16, KR = 64 / CPR;               // [k][n] tiles: chunks a row, rows a load
-  static constexpr bool kSwap = !KMAJOR && kInst > 1 && (NW * KR) % 32 == 16;
-  static_assert(KMAJOR || kInst == 1 || (NW * KR) % 16 == 0, "the swizzle repeats from load to load");
+  static_assert(KMAJOR || kInst == 1 || (NW * KR) % 32 == 0, "the swizzle repeats from load to load");
   v4u rsrc;
   uint32_t off[GATHER ? kInst : 1], at;  // this lane's chunk in slab 0; its contraction index within a slab
-  int swap;          // what a swapped chunk's offset differs by
   uint32_t ld;
   const int8_t* base;
   int64_t bytes;
 
   __device__ __forceinline__ void init(const int8_t* p, int64_t ld_, int64_t mn0, int64_t MN, int64_t K, int wave, int lane) {
     ld = (uint32_t)ld_;
-    swap = 0;
     if constexpr (KMAJOR) {
       base = p + mn0 * ld_;
       bytes = min((int64_t)R, MN - mn0) * ld_;
@@ -180,7 +176,6 @@ struct Slabs {
       const int k = wave * KR + lane / CPR, c = (lane % CPR) ^ mnmajor_swz(R, k);
       at = k;
       off[0] = k * ld + 16 * c;
-      if constexpr (kSwap) swap = c & 1 ? -16 : 16;
     }
     rsrc = Dma<64, true, NW>::make_rsrc(base, max((int64_t)0, min(bytes, (int64_t)kOob)));  // an empty contraction: nothing
   }
@@ -216,7 +211,6 @@ struct Slabs {
     }
     // what is the same in all lanes is added up in scalar registers
     uint32_t o = off[GATHER ? j : 0] + (uint32_t)__builtin_amdgcn_readfirstlane(ahead);
-    if constexpr (kSwap) o += j & 1 ? swap : 0;
     load((int)at < limit ? o : kOob, r, to + (wave + NW * j) * 1024);
   }
   __device__ __forceinline__ void issue_one(int j, uint32_t to, int slab, int K, int wave) const {

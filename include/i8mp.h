@@ -652,8 +652,9 @@ i8mp_status i8mp_expert_combine(const i8mp_combine* p, const void* residual, int
 /*
  * Its gradients: dY[places[t][j]] = weights[t][j] dout[t] and dweights[t][j] = <dout[t],
  * Y[places[t][j]]> (fp32; 0 without a place).  Either output may be NULL.  Places other
- * than the negative ones must be distinct.  rows: NULL, or int32 [R] as above: rows r with
- * rows[r] < 0 of dY are written as zeros; without it rows that no place names are left.
+ * than the negative ones must be distinct.  rows: NULL, or int32 [R] as above, which for
+ * every place in use has its token: rows of dY that no place names are written as zeros;
+ * without it they are left.
  */
 i8mp_status i8mp_expert_combine_bwd(const i8mp_combine* p, const void* dout, int64_t ldd, const int32_t* rows, void* dY,
                                     int64_t ldg, float* dweights, void* stream);

@@ -417,8 +417,8 @@ def expert_combine_bwd(dout: torch.Tensor, Y: torch.Tensor, places: torch.Tensor
     is not wanted (the residual's gradient is dout itself).
 
     places must be distinct but for those that add nothing.  rows (int32 [R], from
-    expert_route): rows that no token has (a negative entry) are written as zeros; without
-    it a new dY is cleared first, and a given one keeps them."""
+    expert_route; places may have been taken away since): rows that no place names are
+    written as zeros; without it a new dY is cleared first, and a given one keeps them."""
     p, dev = _combine(Y, places, weights, ((dout, "dout"),), rows)
     if dout is None:
         raise TypeError("dout: torch.Tensor expected, got NoneType")

@@ -506,7 +506,9 @@ __global__ __launch_bounds__(256) void combine(CombineArgs a, int64_t chunks, in
 }
 
 // A wave has one (token, choice): its row of dY and its weight's gradient; then, with `rows`, the
-// rows that nobody has.
+// rows that nobody has, of no token or of one whose places do not name them (any more): eight a wave, of which
+// eight lanes each look at a row's token (8192 tokens, 4 rows of 2048 each, with the sums: 94.5 us, 95.4 with a wave for each row).
+constexpr int kFreeRows = 8;
 template <int DT, int W>
 __global__ __launch_bounds__(256) void combine_back(CombineArgs a, int64_t first) {
   const int64_t i = first + blockIdx.x * (int64_t)4 + (threadIdx.x >> 6), pairs = a.T * a.k;
@@ -536,13 +538,21 @@ __global__ __launch_bounds__(256) void combine_back(CombineArgs a, int64_t first
       dot = over_lanes<64>(dot, add);
       if (lane == 0) a.dweights[i] = dot;
     }
-  } else if (a.rows && a.dY && i - pairs < a.R) {
-    const int64_t r = i - pairs;
-    if (a.rows[r] >= 0) return;
+  } else if (a.rows && a.dY) {
+    constexpr int kLook = 64 / kFreeRows;
+    const int64_t r0 = (i - pairs) * kFreeRows, r = r0 + lane / kLook;
+    const int64_t t = r < a.R ? a.rows[r] : -1;
+    bool named = r >= a.R;
+    if (t >= 0 && t < a.T)
+      for (int j = lane % kLook; j < a.k; j += kLook) named |= a.places[t * a.k + j] == r;
+    const uint64_t who = __ballot(named);
     float z[W];
 #pragma unroll
     for (int j = 0; j < W; ++j) z[j] = 0.0f;
-    for (int64_t c = lane * W; c < a.N; c += 64 * W) write_chunk<DT, W>(a.dY, r * a.ldg + c, z);
+    for (int n = 0; n < kFreeRows; ++n) {
+      if (who >> (kLook * n) & ((1 << kLook) - 1)) continue;
+      for (int64_t c = lane * W; c < a.N; c += 64 * W) write_chunk<DT, W>(a.dY, (r0 + n) * a.ldg + c, z);
+    }
   }
 }
 
@@ -626,7 +636,7 @@ void combine_as(const CombineArgs& a, hipStream_t stream) {
 
 template <int DT, int W>
 void combine_back_as(const CombineArgs& a, hipStream_t stream) {
-  const int64_t n = (a.T * a.k + (a.rows && a.dY ? a.R : 0) + 3) / 4;
+  const int64_t n = (a.T * a.k + (a.rows && a.dY ? (a.R + kFreeRows - 1) / kFreeRows : 0) + 3) / 4;
   for (int64_t b = 0; b < n; b += kMaxGrid)
     combine_back<DT, W><<<(unsigned)std::min(kMaxGrid, n - b), 256, 0, stream>>>(a, b * 4);
 }

@@ -184,7 +184,9 @@ constexpr int64_t kFewWide = 16 * 256;
 
 // Rows of one matrix, or of an expert on average, that this kernel takes: against the tiles' kernel and the quantization
 // before it, 16 rows against 4096 x 14336 33.8 us and 64.3; 17 against 5632 x 2048 8.3 and 17.1; 32 against 14336 x 4096
-// 28.4 and 25.9, 33 against 5632 x 2048 11.6 and 17.2 (64 rows 42.3 and 26.8 of 14336 x 4096).
+// 28.4 and 25.9, 33 against 5632 x 2048 11.6 and 17.2 (64 rows 42.3 and 26.8 of 14336 x 4096).  The border moves with the
+// codes' number, which the rule leaves out: near it the worse of the two is taken, at 2.5 us more for 32 rows of the
+// larger weight and 5.6 for 33 of the smaller.
 constexpr int64_t kFewRows = 32;
 
 // Rows of all experts, which may lie unevenly: an expert's rows beyond 32 read its codes again.  This kernel's time and the

@@ -7,9 +7,14 @@
 // column) of each 128, which comes into LDS the same way as the codes, four blocks at a time.
 //
 // 8192 x 5632 x 2048 takes 90 us (2.1 PFLOP/s), 8192^3 415 to 465 (2.35 to 2.65; the library's row-wise FP8
-// product 2.74).  Of the 90, 64 are 96 slabs (three rounds of tiles, the last three quarters full) of 0.67 us each, where
-// the matrix instructions alone take 0.60 on random codes, which is what the card's power lets them (0.45 on zeros).  A
-// tile's end takes 5: its stores, and the next slabs' loads that queue behind them.  The kernel's start and end take 9.
+// product 2.74).  Of the 90, 64 are 96 slabs (three rounds of tiles, the last three quarters full) of 0.67 us each, whose
+// matrix instructions are 1024 cycles of each SIMD: 0.61 us at the 1.69 GHz that the card holds under this load (0.45 measured
+// on zeros, at a higher clock).  They are busy 0.59 of the kernel's time.  A tile's end takes 5: its stores, and the next
+// slabs' loads that queue behind them.  The kernel's start and end take 9.
+//
+// The big tiles' kernels take all 256 registers, half of them accumulators, and where a tile is opened or closed a few more
+// vector and some tens of scalar ones, which go to memory and to lanes there (vector and scalar: forward 5 and 68, through an
+// index 9 and 90, dX 17 and 79, dW 3 and 34); a tile's loop over its blocks has none of that.
 #include "block.h"
 #include "gemm_pipelined.h"
 

@@ -8,10 +8,10 @@
 // and in a second launch each adds up the blocks before it and ranks its own entries by ballots
 // over the bits of the expert's number.  One block of tokens needs one launch.
 //
-// All of it is short work in waves that wait: 32768 tokens to 4 of 64 (fp32) choose in 6.9 us and
-// place in 6.1, where 13 MB need 2.5; to 8 of 256 (bf16) both take 28.  The gradient takes 4.5 us at 32768 x 64 (bf16, 8
-// taken; 8 MB) and 14.7 at 256: sums over the taken alone, and one exponential a score where the weights are
-// shares of all.
+// All of it is short work in waves that wait: 32768 tokens to 4 of 64 (fp32) choose in 7.1 us and
+// place in 6.4, where 13 MB need 2.5; to 8 of 256 (bf16) both take 28, of 512 60.  The gradient takes 5.1 us at 32768 x 64
+// (bf16, 8 taken; 8 MB), 14.9 at 256 and 15.4 at 512: sums over the taken alone; where the weights are shares of all
+// there is one exponential a score (5.7, 15.5 and 18.9).
 #include "route.h"
 
 #include <algorithm>

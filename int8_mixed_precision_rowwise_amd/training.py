@@ -568,11 +568,14 @@ class ExpertRouteFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, k, score, normalize):
-        r = _block.expert_route(logits, k, score, normalize)
-        ctx.save_for_backward(logits, r.experts)
+        weights, experts, *rest = _block.expert_route(logits, k, score, normalize)
+        # They are parts of one allocation, and its views count changes in place together: .data gives each a count of
+        # its own, so that places taken away in place are no change of the experts saved here.
+        rest = [t.data for t in rest]
+        ctx.save_for_backward(logits, experts)
         ctx.args = score, normalize
-        ctx.mark_non_differentiable(*r[1:])
-        return tuple(r)
+        ctx.mark_non_differentiable(experts, *rest)
+        return (weights, experts, *rest)
 
     @staticmethod
     def backward(ctx, dweights, *_):

@@ -41,3 +41,22 @@ def test_places_taken_away(T, E, k, N, dtype):
     blocks = [torch.full((R, N), nan, dtype=dtype, device="cuda") for _ in range(3)]
     del blocks
     assert torch.equal(torch.autograd.grad(out, y, dout)[0], want)
+
+
+def test_a_layer_whose_places_are_taken_away_in_place():
+    """As expert by expert over the rows that are left; the experts' weights see nothing of the others."""
+    tokens, E, k, D = 90, 5, 2, 40
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.randn(tokens, E, generator=g, device="cuda").requires_grad_()
+    y_of = torch.randn(tokens * k, D, generator=g, device="cuda")
+    dout = torch.randn(tokens, D, generator=g, device="cuda")
+    drop = torch.rand(tokens, k, generator=g, device="cuda") < 0.3
+    grads = []
+    for in_place in (True, False):
+        y = y_of.clone().requires_grad_()
+        r = training.expert_route(logits, k)
+        places = r.places.masked_fill_(drop, -1) if in_place else r.places.masked_fill(drop, -1)
+        out = training.expert_combine(y, places, r.weights, rows=r.rows)
+        grads.append(torch.autograd.grad(out, (logits, y), dout))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+    assert bool(grads[0][0].any()) and not bool(grads[0][1][r.places[drop].long()].any())
